@@ -65,7 +65,8 @@ extern "C" {
 #define ZS_ABI_VERSION 7
 #define ZS_MAX_WORLD 64
 
-typedef enum { ZS_BF16 = 0, ZS_FP16 = 1 } zs_dtype;
+/* ZS_FP32 is accepted only where a call says so. */
+typedef enum { ZS_BF16 = 0, ZS_FP16 = 1, ZS_FP32 = 2 } zs_dtype;
 
 /* Precision of the partial sums the ring reduction passes between ranks.
  * ZS_WIRE_FP32 (0, the default) carries them in fp32 ([Notes] 三: the owner
@@ -477,6 +478,149 @@ int zs_device_scaler_make(const zs_loss_scaler *s, float beta1, float beta2,
  * not write its input set and runs again at the same epoch). */
 int zs_step_device(const zs_step_args *a, zs_device_scaler *dev, void *stream, void *ev_start,
                    void *ev_stop);
+
+/* ------------------------------------------------------------------------
+ * Operators of the output end of a model trained in low precision: what
+ * makes the loss-scaled 16-bit gradients that the shard step above takes in,
+ * and what uses a 4-bit copy of the parameters that it gives out
+ * ([Intro] 一.3 items (1) and (3): low-precision copies for forward and
+ * backward, fp32 master weights, loss scaling). The conventions above hold:
+ * device pointers, caller's buffers and workspaces, work enqueued on
+ * `stream`, argument errors before anything is enqueued, no wait. All of
+ * them can be captured into a HIP graph. Outputs that overlap an input or
+ * each other are refused (ZS_ERR_ALIAS) except where stated. The same
+ * inputs give the same bits on every call.
+ *
+ * Microscaled rows. A matrix of `rows` x K elements is kept as codes and
+ * scales. K is padded with zeros to Kp = whole groups of ZS_MX_GROUP (128)
+ * elements; each ZS_MX_BLOCK (32) elements share a scale byte b that stands
+ * for 2^(b - 127), and an element for its code's value times that.
+ *   codes : ZS_MX_E4M3: uint8[rows][Kp], one element a byte;
+ *           ZS_MX_E2M1: uint8[rows][Kp/2], the even element in the low half.
+ *           16-byte aligned.
+ *   scales: uint8[rows][Kp/32], 4-byte aligned.
+ *   b = max(1, E - emax), E the biased fp32 exponent of the largest
+ *   magnitude in the block, emax = 2 (E2M1) or 8 (E4M3); elements are
+ *   rounded to nearest, ties to even, and saturate at 6 or 448. A block with
+ *   an infinity or NaN has b = 255: every value in it is NaN.
+ * ---------------------------------------------------------------------- */
+#define ZS_MX_BLOCK 32
+#define ZS_MX_GROUP 128
+typedef enum { ZS_MX_E2M1 = 0, ZS_MX_E4M3 = 1 } zs_mx_format;
+
+/* Microscaled copy of a matrix, along its rows (weights and activations for
+ * the forward product) or along its columns (the transposed operands of the
+ * backward products).
+ *   src    : src_dtype (bf16, fp16 or fp32)[rows][cols], rows `ld` elements
+ *            apart, any element alignment; e.g. a slice of the fp32 master
+ *            weights or of the 16-bit gather buffer.
+ *   columns: 0: codes and scales of `rows` rows of K = cols; otherwise of
+ *            `cols` rows of K = rows (the transposed matrix).
+ *   values : NULL, or values_dtype (bf16, fp16)[rows][cols], contiguous: the
+ *            values that the codes stand for, laid out as src (what a layer
+ *            without a 4-bit product multiplies by).
+ * Errors: ZS_ERR_INVALID_ARG (null pointers, dtypes, format, ld < cols),
+ * ZS_ERR_UNSUPPORTED (alignment of codes and scales, more than 2^48
+ * elements, more than 8 388 480 rows along the columns). */
+int zs_mx_quantize(const void *src, int src_dtype, uint64_t rows, uint64_t cols, uint64_t ld,
+                   int format, int columns, uint8_t *codes, uint8_t *scales, void *values,
+                   int values_dtype, void *stream);
+
+/* C[i][j] = sum over k of A[i][k] * B[j][k] on the matrix cores, fp32 sums,
+ * rounded once to c_dtype.
+ *   A : m rows of k elements in a_format (ZS_MX_E4M3 or ZS_MX_E2M1).
+ *   B : n rows of k elements in ZS_MX_E2M1.
+ *   c : c_dtype[m][n], rows `ldc` elements apart. fp32 results are offered
+ *       for 4-bit A only: those products and their sums are exact to fp32,
+ *       while with 8-bit elements the matrix unit aligns each step's
+ *       products to the largest (about 2^-18 of the sum), which 16-bit
+ *       results do not show.
+ *   workspace: NULL, or device memory (16-byte aligned) for partial sums.
+ *       No variant needs it yet.
+ * k == 0 gives zeros. Errors: ZS_ERR_INVALID_ARG (null pointers, dtype,
+ * format, ldc < n), ZS_ERR_UNSUPPORTED (dimensions above 2^30, alignment,
+ * fp32 with an 8-bit A). */
+int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
+                 const uint8_t *b_codes, const uint8_t *b_scales, uint64_t m, uint64_t n,
+                 uint64_t k, void *c, int c_dtype, uint64_t ldc, void *workspace,
+                 uint64_t workspace_bytes, void *stream);
+
+/* Root-mean-square norm with the residual's addition and an 8-bit output:
+ *   h = R16(x + residual);  rstd = 1 / sqrt(mean(h^2) + eps);
+ *   y = h * rstd * gain
+ * per row, fp32 between the roundings; the statistics are those of the
+ * rounded h, which zs_rmsnorm_backward reads.
+ *   x, residual: dtype (bf16, fp16)[rows][cols]; residual may be NULL.
+ *   gain       : dtype[cols].
+ *   h          : dtype[rows][cols], the new residual stream; may be x's or
+ *                residual's own buffer; NULL only without a residual.
+ *   rstd       : fp32[rows] or NULL.
+ *   codes, scales: y as ZS_MX_E4M3 rows (K = cols), or both NULL.
+ *   y          : dtype[rows][cols] or NULL; codes or y must be given.
+ * Errors: ZS_ERR_INVALID_ARG (null pointers, dtype, eps not finite or < 0),
+ * ZS_ERR_UNSUPPORTED (cols > 65536, alignment of codes and scales). */
+int zs_rmsnorm_forward(const void *x, const void *residual, const void *gain, int dtype,
+                       uint64_t rows, uint64_t cols, float eps, void *h, float *rstd,
+                       uint8_t *codes, uint8_t *scales, void *y, void *stream);
+
+/* Gradient of zs_rmsnorm_forward (the 8-bit rounding passes it through):
+ *   dx = R16(dres + rstd * (gain*dy - h * rstd^2 * mean(gain*dy*h)))
+ *   dgain = sum over rows of dy * h * rstd
+ * dx is the gradient of x and of the residual alike.
+ *   dy, h, gain, rstd: as the forward call's y, h, gain and rstd.
+ *   dres : dtype[rows][cols], what h receives from elsewhere, or NULL.
+ *   dx   : dtype[rows][cols]; may be dy's, h's or dres's own buffer.
+ *   dgain: fp32[cols] (zs_cast_gather puts it into a 16-bit gradient
+ *          buffer); zeros when rows == 0.
+ *   workspace: zs_rmsnorm_backward_workspace(rows, cols) bytes, 4-byte
+ *          aligned.
+ * Errors: as zs_rmsnorm_forward; a workspace too small is
+ * ZS_ERR_INVALID_ARG. */
+uint64_t zs_rmsnorm_backward_workspace(uint64_t rows, uint64_t cols);
+int zs_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const void *gain,
+                        const void *dres, int dtype, uint64_t rows, uint64_t cols, void *dx,
+                        float *dgain, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* Distillation from a teacher's top logits: loss and the logits' gradient in
+ * one call. Per row, with u = logits / temperature, q = softmax(u) over the
+ * vocabulary, and slots k = 0 .. slots-1 holding a token id and the
+ * teacher's logit t:
+ *   without teacher_lse: p = softmax of t / temperature over the row's slots,
+ *     loss = w * temperature^2 * sum p * (log p - log q[id]);
+ *   with it: p = exp(t / temperature - teacher_lse), and the teacher's mass
+ *     off the slots, pr = 1 - sum p (0 if that is below 2^-20, where fp32
+ *     says nothing any more), is one more outcome against the student's,
+ *     qr: loss += w * temperature^2 * pr * (log pr - log qr).
+ *   grad = S * d loss / d logits: S * w * temperature * (q - p) on the slots,
+ *     and off them S * w * temperature * q, times (1 - pr / qr) with
+ *     teacher_lse. S = dev->scale, or loss_scale without dev: the factor that
+ *     the shard step divides out again. An overflow of it is data, as there.
+ *   logits : dtype (bf16, fp16, fp32)[rows][vocab], rows `ld` apart.
+ *   ids    : int32[rows][slots]; an id outside [0, vocab) is an empty slot.
+ *            Slots of the same token add up.
+ *   teacher: dtype[rows][slots]; -inf: no mass.
+ *   teacher_lse: NULL, or fp32[rows]: logsumexp of the teacher's logits /
+ *            temperature over its whole vocabulary.
+ *   row_weight: NULL (all 1), or fp32[rows]. A row of weight 0, one without
+ *            a filled slot and, without teacher_lse, one whose slots hold no
+ *            mass give loss 0 and a zero gradient, whatever their logits.
+ *   loss   : fp32[rows]. grad: NULL (loss only), or dtype[rows][vocab], rows
+ *            `grad_ld` apart; may be the logits' own buffer.
+ *   workspace: zs_distill_workspace(rows, vocab, slots, dtype) bytes,
+ *            16-byte aligned; NULL if that is 0.
+ * Logits of -inf are tokens that cannot be chosen (q = 0); a NaN, +inf or a
+ * row of -inf gives a NaN row.
+ * Errors: ZS_ERR_INVALID_ARG (null pointers, dtype, temperature or
+ * loss_scale not finite and > 0, vocab 0 or above 2^31 - 1, rows closer
+ * than vocab, workspace too small), ZS_ERR_UNSUPPORTED (slots > 1024,
+ * alignment). */
+#define ZS_DISTILL_MAX_SLOTS 1024
+uint64_t zs_distill_workspace(uint64_t rows, uint64_t vocab, uint32_t slots, int dtype);
+int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
+               const int32_t *ids, const void *teacher, uint32_t slots, float temperature,
+               const float *teacher_lse, const float *row_weight, float loss_scale,
+               const zs_device_scaler *dev, float *loss, void *grad, uint64_t grad_ld,
+               void *workspace, uint64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

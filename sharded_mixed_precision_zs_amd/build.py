@@ -1,6 +1,7 @@
 """Build the in-tree shared libraries of the package.
 
   libzeroshard.so        the shard-step library (HIP, gfx950)  <- csrc/zeroshard.hip
+                         + the operators of the model's output end <- csrc/zs_ops.hip
                          + its host-side offload update (gcc) <- csrc/offload_cpu.cpp
   synth/libzssynth_dev.so   device twin of the input generator (HIP, gfx950)
   synth/libzssynth_host.so  host twin of the input generator (gcc)
@@ -105,8 +106,13 @@ def build_zeroshard(verbose=False):
     obj = os.path.join(PKG, "csrc", "offload_cpu.o")
     _run(["g++", *CPU_FLAGS, "-I", INCLUDE, "-c", os.path.join(PKG, "csrc", "offload_cpu.cpp"),
           "-o", obj], verbose)
-    _hip_lib(os.path.join(PKG, "csrc", "zeroshard.hip"), LIB, verbose, extra=[obj, "-pthread"])
+    ops = os.path.join(PKG, "csrc", "zs_ops.o")
+    _run([HIPCC, *HIP_FLAGS, "-I", INCLUDE, "-c", os.path.join(PKG, "csrc", "zs_ops.hip"),
+          "-o", ops], verbose)
+    _hip_lib(os.path.join(PKG, "csrc", "zeroshard.hip"), LIB, verbose,
+             extra=[obj, ops, "-pthread"])
     os.remove(obj)
+    os.remove(ops)
     return LIB
 
 

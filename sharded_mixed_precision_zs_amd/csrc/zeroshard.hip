@@ -21,6 +21,7 @@
 #include "zeroshard.h"
 
 #include "zs_aux_kernels.h"
+#include "zs_host_common.h"
 #include "zs_hparams.h"
 #include "zs_host_powers.h"
 #include "zs_host_setup.h"
@@ -45,27 +46,13 @@ using namespace zs;
  * Host side: validation, scalar preparation, launch.
  * ---------------------------------------------------------------------- */
 
-thread_local char g_err[512] = "";
-
-int fail(int status, const char *fmt, const char *detail = "") {
-  snprintf(g_err, sizeof g_err, fmt, detail);
-  return status;
-}
-
-int launch_result() {
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(ZS_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
-  g_err[0] = 0;
-  return ZS_OK;
-}
+using zs_host::fail;
+using zs_host::g_err;
+using zs_host::launch_result;
+using zs_host::overlaps;
+using zs_host::too_big;
 
 bool valid_dtype(int dt) { return dt == ZS_BF16 || dt == ZS_FP16; }
-
-/* Element counts and offsets above 2^48 are refused before any size
- * arithmetic (byte extents below are 4 * n and must not wrap). */
-constexpr uint64_t kMaxElems = 1ull << 48;
-
-bool too_big(uint64_t n) { return n > kMaxElems; }
 
 bool valid_wire(int w) { return w == ZS_WIRE_FP32 || w == ZS_WIRE_BF16 || w == ZS_WIRE_FP16; }
 
@@ -381,12 +368,6 @@ int fill_ring(const void *const *worker_grads, uint32_t world, uint32_t rank,
   }
   for (uint32_t j = world; j < ZS_MAX_WORLD; ++j) g->p[j] = nullptr;
   return ZS_OK;
-}
-
-bool overlaps(const void *a, uint64_t abytes, const void *b, uint64_t bbytes) {
-  if (!a || !b || !abytes || !bbytes) return false;
-  uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-  return a0 < b0 + bbytes && b0 < a0 + abytes;
 }
 
 /* ------------------------------------------------------------------------

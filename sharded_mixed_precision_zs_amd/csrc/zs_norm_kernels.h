@@ -1,0 +1,188 @@
+/*
+ * zs_norm_kernels.h -- root-mean-square norm with the residual's addition
+ * and an 8-bit microscaled output, forward and backward (gfx950).
+ *
+ *   h = R16(x + r);  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * g
+ *   dx = R16(dres + rstd * (g*dy - h * rstd^2 * mean(g*dy*h)))
+ *   dg = sum over rows of dy * h * rstd
+ *
+ * Both are bound by HBM: every element is read once, kept in registers
+ * between the row's sum and its use, and written once. Sums are fp32. The
+ * statistics are those of the rounded h, which is what the backward pass
+ * reads, so both passes see the same row.
+ */
+#ifndef ZS_NORM_KERNELS_H
+#define ZS_NORM_KERNELS_H
+
+#include "zs_mx.h"
+
+namespace zs {
+
+struct NormArgs {
+  const void *x, *res, *gain;
+  uint16_t *h, *y;           /* optional outputs */
+  float *rstd;               /* optional */
+  uint8_t *codes, *scales;   /* both or neither */
+  uint64_t rows;
+  uint32_t cols, padded;     /* padded: cols rounded up to whole groups */
+  float eps;
+};
+
+/* G threads per row (64: four rows per 256-thread block), ITEMS vectors of
+ * eight elements per thread. */
+template <int DT, bool AL, int G, int ITEMS>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
+  constexpr int kRows = G < 256 ? 256 / G : 1;
+  __shared__ float part[G / 64];
+  const uint32_t t = threadIdx.x % G;
+  const uint64_t row = (uint64_t)blockIdx.x * kRows + threadIdx.x / G;
+  if (row >= a.rows) return;   /* a whole wave; blocks of one row never take it */
+  const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.cols;
+  const uint16_t *r = a.res ? static_cast<const uint16_t *>(a.res) + row * a.cols : nullptr;
+  float h[ITEMS][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) load8<DT, AL>(x, (uint64_t)(i * G + t) * 8, a.cols, h[i]);
+  if (r) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      float b[8];
+      load8<DT, AL>(r, (uint64_t)(i * G + t) * 8, a.cols, b);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const uint32_t w = pack2<DT>(h[i][j] + b[j], h[i][j + 1] + b[j + 1]);
+        h[i][j] = up_lo<DT>(w);
+        h[i][j + 1] = up_hi<DT>(w);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    if (a.h) store8<DT, AL>(a.h + row * a.cols, (uint64_t)(i * G + t) * 8, a.cols, h[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+  }
+  ss = group_sum<G>(ss, part);
+  const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+  if (a.rstd && t == 0) a.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t v = i * G + t;
+    if (v * 8 >= a.padded) break;   /* whole quads: padded is a multiple of 128 */
+    float g[8], y[8];
+    load8<DT, AL>(a.gain, (uint64_t)v * 8, a.cols, g);
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      y[j] = v * 8 + j < a.cols ? h[i][j] * rstd * g[j] : 0.0f;
+      top = umax(top, mag_bits(y[j]));
+    }
+    if (a.y) store8<DT, AL>(a.y + row * a.cols, (uint64_t)v * 8, a.cols, y);
+    if (a.codes) {
+      const uint32_t byte = mx_scale_byte<ZS_MX_E4M3>(quad_max(top));
+      uint32_t code[2];
+      mx_encode<ZS_MX_E4M3>(y, byte, code);
+      *reinterpret_cast<u32x2 *>(a.codes + row * a.padded + v * 8) = u32x2{code[0], code[1]};
+      if ((v & 3) == 0) a.scales[row * (a.padded / kMxBlock) + v / 4] = (uint8_t)byte;
+    }
+  }
+}
+
+struct NormGradArgs {
+  const void *dy, *h, *gain, *dres;   /* dres optional */
+  const float *rstd;
+  uint16_t *dx;
+  float *part;                        /* [parts][cols] */
+  uint64_t rows;
+  uint32_t cols, parts;
+};
+
+/* Each of `parts` groups of G threads walks rows p, p + parts, ... and keeps
+ * its share of dg in registers; norm_gain_kernel adds the shares in order,
+ * so the result does not depend on scheduling. */
+template <int DT, bool AL, int G, int ITEMS>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void norm_grad_kernel(NormGradArgs a) {
+  constexpr int kRows = G < 256 ? 256 / G : 1;
+  __shared__ float sums[2][G / 64];
+  const uint32_t t = threadIdx.x % G;
+  const uint32_t p = blockIdx.x * kRows + threadIdx.x / G;
+  if (p >= a.parts) return;
+  float dg[ITEMS][8];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
+  int turn = 0;
+  for (uint64_t row = p; row < a.rows; row += a.parts, turn ^= 1) {
+    const uint16_t *dy = static_cast<const uint16_t *>(a.dy) + row * a.cols;
+    const uint16_t *hp = static_cast<const uint16_t *>(a.h) + row * a.cols;
+    const float rstd = a.rstd[row];
+    float h[ITEMS][8], d[ITEMS][8];
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const uint64_t c = (uint64_t)(i * G + t) * 8;
+      load8<DT, AL>(dy, c, a.cols, d[i]);
+      load8<DT, AL>(hp, c, a.cols, h[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      float g[8];
+      load8<DT, AL>(a.gain, (uint64_t)(i * G + t) * 8, a.cols, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dg[i][j] = fmaf(d[i][j], h[i][j] * rstd, dg[i][j]);
+        d[i][j] *= g[j];
+        dot = fmaf(d[i][j], h[i][j], dot);
+      }
+    }
+    const float s = group_sum<G>(dot, sums[turn]) / (float)a.cols * rstd * rstd;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const uint64_t c = (uint64_t)(i * G + t) * 8;
+      float o[8];
+      if (a.dres) {
+        load8<DT, AL>(static_cast<const uint16_t *>(a.dres) + row * a.cols, c, a.cols, o);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = fmaf(rstd, fmaf(-h[i][j], s, d[i][j]), o[j]);
+      store8<DT, AL>(a.dx + row * a.cols, c, a.cols, o);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t c = (i * G + t) * 8 + j;
+      if (c < a.cols) a.part[(uint64_t)p * a.cols + c] = dg[i][j];
+    }
+}
+
+/* dg[c] = sum of part[p][c] over p: 64 columns per block, 16 waves that
+ * take every 16th share, joined in wave order. */
+constexpr int kGainWaves = 16;
+
+__global__ __launch_bounds__(64 * kGainWaves) void norm_gain_kernel(const float *part,
+                                                                    uint32_t parts, uint32_t cols,
+                                                                    float *dgain) {
+  __shared__ float sums[kGainWaves][64];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t c = blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (c < cols)
+    for (uint32_t p = wave; p < parts; p += kGainWaves) s += part[(uint64_t)p * cols + c];
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kGainWaves; ++w) s += sums[w][lane];
+    dgain[c] = s;
+  }
+}
+
+}  // namespace zs
+#endif  // ZS_NORM_KERNELS_H

@@ -1,0 +1,448 @@
+/*
+ * zs_ops.hip -- libzeroshard's operators for the output end of a model
+ * trained in low precision (gfx950): the norm, the microscaled formats'
+ * quantisation and product, and the distillation loss. Host side: argument
+ * validation, choice of the kernel variant, launches. The device code is in
+ * zs_norm_kernels.h, zs_quantize_kernels.h, zs_matmul_kernels.h and
+ * zs_distill_kernels.h, over zs_mx.h.
+ */
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "zeroshard.h"
+
+#include "zs_distill_kernels.h"
+#include "zs_host_common.h"
+#include "zs_matmul_kernels.h"
+#include "zs_norm_kernels.h"
+#include "zs_quantize_kernels.h"
+
+namespace {
+
+using namespace zs;
+using zs_host::fail;
+using zs_host::launch_result;
+using zs_host::overlaps;
+using zs_host::too_big;
+
+constexpr uint64_t kMaxGrid = 0x7fffffffull;
+
+bool valid16(int dt) { return dt == ZS_BF16 || dt == ZS_FP16; }
+bool valid_any(int dt) { return valid16(dt) || dt == ZS_FP32; }
+bool valid_format(int f) { return f == ZS_MX_E2M1 || f == ZS_MX_E4M3; }
+
+uint64_t esize(int dt) { return dt == ZS_FP32 ? 4 : 2; }
+uint64_t padded_of(uint64_t k) { return (k + ZS_MX_GROUP - 1) / ZS_MX_GROUP * ZS_MX_GROUP; }
+uint64_t code_bytes(int format, uint64_t padded) { return format == ZS_MX_E2M1 ? padded / 2 : padded; }
+
+bool aligned(const void *p, uint64_t bytes) { return (uintptr_t)p % bytes == 0; }
+
+/* Bytes from the first to the last element of `rows` rows of `cols`, `ld` apart. */
+uint64_t extent(uint64_t rows, uint64_t cols, uint64_t ld, uint64_t esz) {
+  return rows ? ((rows - 1) * ld + cols) * esz : 0;
+}
+
+/* A matrix whose element counts stay below 2^48. */
+bool matrix_too_big(uint64_t rows, uint64_t cols) {
+  return too_big(rows) || too_big(cols) || (cols && rows > zs_host::kMaxElems / cols);
+}
+
+/* Calls f with std::integral_constant-like tags chosen at run time. */
+template <int V>
+struct Tag {
+  static constexpr int value = V;
+};
+
+template <class F>
+void with16(int dt, F f) {
+  if (dt == ZS_BF16) f(Tag<ZS_BF16>{});
+  else f(Tag<ZS_FP16>{});
+}
+
+template <class F>
+void with_any(int dt, F f) {
+  if (dt == ZS_FP32) f(Tag<ZS_FP32>{});
+  else with16(dt, f);
+}
+
+template <class F>
+void with_format(int fmt, F f) {
+  if (fmt == ZS_MX_E2M1) f(Tag<ZS_MX_E2M1>{});
+  else f(Tag<ZS_MX_E4M3>{});
+}
+
+template <class F>
+void with_bool(bool b, F f) {
+  if (b) f(Tag<1>{});
+  else f(Tag<0>{});
+}
+
+/* ------------------------------------------------------------------------
+ * The norm's threads per row and vectors of eight per thread: one wave per
+ * row where its registers hold the row and there are rows enough to fill the
+ * chip that way; otherwise a block.
+ * ---------------------------------------------------------------------- */
+constexpr uint64_t kMaxNormCols = 65536;
+
+template <class F>
+void with_items(uint32_t need, F f) {
+  if (need <= 1) f(Tag<1>{});
+  else if (need <= 2) f(Tag<2>{});
+  else if (need <= 4) f(Tag<4>{});
+  else f(Tag<8>{});
+}
+
+template <class F>
+void with_norm_shape(uint64_t rows, uint64_t padded, F f) {
+  const uint32_t vecs = (uint32_t)(padded / 8);
+  if (padded <= 512 || (padded <= 4096 && rows >= 1024))
+    with_items((vecs + 63) / 64, [&](auto i) { f(Tag<64>{}, i); });
+  else if (padded <= 16384)
+    with_items((vecs + 255) / 256, [&](auto i) { f(Tag<256>{}, i); });
+  else
+    with_items((vecs + 1023) / 1024, [&](auto i) { f(Tag<1024>{}, i); });
+}
+
+/* Groups that share the rows of a backward pass. */
+constexpr uint32_t kNormParts = 1024;
+
+uint32_t norm_parts(uint64_t rows) { return rows < kNormParts ? (uint32_t)rows : kNormParts; }
+
+}  // namespace
+
+extern "C" {
+
+int zs_rmsnorm_forward(const void *x, const void *residual, const void *gain, int dtype,
+                       uint64_t rows, uint64_t cols, float eps, void *h, float *rstd,
+                       uint8_t *codes, uint8_t *scales, void *y, void *stream) {
+  if (!valid16(dtype)) return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_forward: bad dtype%s");
+  if (!(eps >= 0.0f) || !isfinite(eps))
+    return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_forward: eps must be finite and >= 0%s");
+  if (!codes != !scales)
+    return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_forward: codes and scales go together%s");
+  if (!codes && !y) return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_forward: no output asked for%s");
+  if (!h && residual)
+    return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_forward: a residual needs h%s");
+  if (matrix_too_big(rows, cols))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: more than 2^48 elements%s");
+  if (cols > kMaxNormCols)
+    return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: rows of more than 65536 elements%s");
+  if (rows == 0 || cols == 0) return ZS_OK;
+  if (!x || !gain) return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_forward: null x or gain%s");
+  if (codes && (!aligned(codes, 16) || !aligned(scales, 4)))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: codes or scales not aligned%s");
+  const uint64_t padded = padded_of(cols), bytes = rows * cols * 2;
+  const void *outs[] = {h, y, codes, scales, rstd};
+  const uint64_t out_bytes[] = {bytes, bytes, rows * padded, rows * padded / ZS_MX_BLOCK, rows * 4};
+  for (int i = 0; i < 5; ++i) {
+    /* h may take the place of x or of the residual */
+    if ((overlaps(outs[i], out_bytes[i], x, bytes) && !(i == 0 && h == x)) ||
+        (overlaps(outs[i], out_bytes[i], residual, bytes) && !(i == 0 && h == residual)) ||
+        overlaps(outs[i], out_bytes[i], gain, cols * 2))
+      return fail(ZS_ERR_ALIAS, "zs_rmsnorm_forward: an output overlaps an input%s");
+    for (int j = i + 1; j < 5; ++j)
+      if (overlaps(outs[i], out_bytes[i], outs[j], out_bytes[j]))
+        return fail(ZS_ERR_ALIAS, "zs_rmsnorm_forward: two outputs overlap%s");
+  }
+  NormArgs a{x, residual, gain, static_cast<uint16_t *>(h), static_cast<uint16_t *>(y), rstd,
+             codes, scales, rows, (uint32_t)cols, (uint32_t)padded, eps};
+  const bool al = cols % 8 == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(gain, 16) &&
+                  aligned(h, 16) && aligned(y, 16);
+  if (rows > kMaxGrid) return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: too many rows%s");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  with16(dtype, [&](auto dt) {
+    with_bool(al, [&](auto v) {
+      with_norm_shape(rows, padded, [&](auto g, auto items) {
+        constexpr int G = decltype(g)::value, block = G < 256 ? 256 : G, per = block / G;
+        hipLaunchKernelGGL((norm_kernel<decltype(dt)::value, decltype(v)::value, G,
+                                        decltype(items)::value>),
+                           dim3((unsigned)((rows + per - 1) / per)), dim3(block), 0, s, a);
+      });
+    });
+  });
+  return launch_result();
+}
+
+uint64_t zs_rmsnorm_backward_workspace(uint64_t rows, uint64_t cols) {
+  return cols > kMaxNormCols ? 0 : (uint64_t)norm_parts(rows) * cols * 4;
+}
+
+int zs_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const void *gain,
+                        const void *dres, int dtype, uint64_t rows, uint64_t cols, void *dx,
+                        float *dgain, void *workspace, uint64_t workspace_bytes, void *stream) {
+  if (!valid16(dtype)) return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_backward: bad dtype%s");
+  if (matrix_too_big(rows, cols))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_backward: more than 2^48 elements%s");
+  if (cols > kMaxNormCols)
+    return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_backward: rows of more than 65536 elements%s");
+  if (cols == 0) return ZS_OK;
+  if (!dgain) return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_backward: null dgain%s");
+  const uint64_t bytes = rows * cols * 2, need = zs_rmsnorm_backward_workspace(rows, cols);
+  if (rows) {
+    if (!dy || !h || !rstd || !gain || !dx)
+      return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_backward: null pointer%s");
+    if (!workspace || workspace_bytes < need)
+      return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_backward: workspace too small%s");
+    if (!aligned(workspace, 4))
+      return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_backward: workspace not aligned%s");
+    const void *outs[] = {dx, dgain, workspace};
+    const uint64_t out_bytes[] = {bytes, cols * 4, need};
+    const void *ins[] = {dy, h, dres, rstd, gain};
+    const uint64_t in_bytes[] = {bytes, bytes, bytes, rows * 4, cols * 2};
+    for (int i = 0; i < 3; ++i) {
+      /* dx may take the place of dy, h or dres */
+      for (int j = 0; j < 5; ++j)
+        if (overlaps(outs[i], out_bytes[i], ins[j], in_bytes[j]) &&
+            !(i == 0 && j < 3 && dx == ins[j]))
+          return fail(ZS_ERR_ALIAS, "zs_rmsnorm_backward: an output overlaps an input%s");
+      for (int j = i + 1; j < 3; ++j)
+        if (overlaps(outs[i], out_bytes[i], outs[j], out_bytes[j]))
+          return fail(ZS_ERR_ALIAS, "zs_rmsnorm_backward: two outputs overlap%s");
+    }
+  }
+  const uint32_t parts = norm_parts(rows);
+  NormGradArgs a{dy, h, gain, dres, rstd, static_cast<uint16_t *>(dx),
+                 static_cast<float *>(workspace), rows, (uint32_t)cols, parts};
+  const bool al = cols % 8 == 0 && aligned(dy, 16) && aligned(h, 16) && aligned(gain, 16) &&
+                  aligned(dres, 16) && aligned(dx, 16);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (rows) {
+    with16(dtype, [&](auto dt) {
+      with_bool(al, [&](auto v) {
+        with_norm_shape(rows, padded_of(cols), [&](auto g, auto items) {
+          constexpr int G = decltype(g)::value, block = G < 256 ? 256 : G, per = block / G;
+          hipLaunchKernelGGL((norm_grad_kernel<decltype(dt)::value, decltype(v)::value, G,
+                                               decltype(items)::value>),
+                             dim3((parts + per - 1) / per), dim3(block), 0, s, a);
+        });
+      });
+    });
+    if (int rc = launch_result()) return rc;
+  }
+  hipLaunchKernelGGL(norm_gain_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(64 * kGainWaves),
+                     0, s, a.part, parts, (uint32_t)cols, dgain);
+  return launch_result();
+}
+
+int zs_mx_quantize(const void *src, int src_dtype, uint64_t rows, uint64_t cols, uint64_t ld,
+                   int format, int columns, uint8_t *codes, uint8_t *scales, void *values,
+                   int values_dtype, void *stream) {
+  if (!valid_any(src_dtype) || (values && !valid16(values_dtype)))
+    return fail(ZS_ERR_INVALID_ARG, "zs_mx_quantize: bad dtype%s");
+  if (!valid_format(format)) return fail(ZS_ERR_INVALID_ARG, "zs_mx_quantize: bad format%s");
+  if (ld < cols) return fail(ZS_ERR_INVALID_ARG, "zs_mx_quantize: ld below cols%s");
+  if (matrix_too_big(rows, ld))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: more than 2^48 elements%s");
+  if (rows == 0 || cols == 0) return ZS_OK;
+  if (!src || !codes || !scales)
+    return fail(ZS_ERR_INVALID_ARG, "zs_mx_quantize: null pointer%s");
+  if (!aligned(codes, 16) || !aligned(scales, 4))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: codes or scales not aligned%s");
+  const uint64_t orows = columns ? cols : rows, padded = padded_of(columns ? rows : cols);
+  if (matrix_too_big(orows, padded))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: more than 2^48 elements%s");
+  const uint64_t src_bytes = extent(rows, cols, ld, esize(src_dtype));
+  const void *outs[] = {codes, scales, values};
+  const uint64_t out_bytes[] = {orows * code_bytes(format, padded), orows * padded / ZS_MX_BLOCK,
+                                rows * cols * 2};
+  for (int i = 0; i < 3; ++i) {
+    if (overlaps(outs[i], out_bytes[i], src, src_bytes))
+      return fail(ZS_ERR_ALIAS, "zs_mx_quantize: an output overlaps the source%s");
+    for (int j = i + 1; j < 3; ++j)
+      if (overlaps(outs[i], out_bytes[i], outs[j], out_bytes[j]))
+        return fail(ZS_ERR_ALIAS, "zs_mx_quantize: two outputs overlap%s");
+  }
+  QuantArgs a{src, rows, cols, ld, codes, scales, static_cast<uint16_t *>(values), padded,
+              rows * (padded / 8)};
+  const bool al = cols % 8 == 0 && aligned(src, 16) && ld * esize(src_dtype) % 16 == 0 &&
+                  aligned(values, 16);
+  uint64_t grid_x, grid_y = 1;
+  if (columns) {
+    grid_x = (cols + kColTileC - 1) / kColTileC;
+    grid_y = padded / kColTileR;
+  } else {
+    grid_x = (a.vecs + kBlock - 1) / kBlock;
+  }
+  if (grid_x > kMaxGrid || grid_y > 65535)
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: too large for one launch%s");
+  const dim3 grid((unsigned)grid_x, (unsigned)grid_y);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  with_any(src_dtype, [&](auto dt) {
+    with16(values ? values_dtype : ZS_BF16, [&](auto vdt) {
+      with_bool(al, [&](auto v) {
+        with_format(format, [&](auto f) {
+          if (columns)
+            hipLaunchKernelGGL((quant_cols_kernel<decltype(dt)::value, decltype(v)::value,
+                                                  decltype(f)::value, decltype(vdt)::value>),
+                               grid, dim3(kBlock), 0, s, a);
+          else
+            hipLaunchKernelGGL((quant_rows_kernel<decltype(dt)::value, decltype(v)::value,
+                                                  decltype(f)::value, decltype(vdt)::value>),
+                               grid, dim3(kBlock), 0, s, a);
+        });
+      });
+    });
+  });
+  return launch_result();
+}
+
+int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
+                 const uint8_t *b_codes, const uint8_t *b_scales, uint64_t m, uint64_t n,
+                 uint64_t k, void *c, int c_dtype, uint64_t ldc, void *workspace,
+                 uint64_t workspace_bytes, void *stream) {
+  if (!valid_format(a_format)) return fail(ZS_ERR_INVALID_ARG, "zs_mx_matmul: bad format%s");
+  if (!valid_any(c_dtype)) return fail(ZS_ERR_INVALID_ARG, "zs_mx_matmul: bad dtype%s");
+  if (c_dtype == ZS_FP32 && a_format == ZS_MX_E4M3)
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: fp32 results need 4-bit operands%s");
+  if (ldc < n) return fail(ZS_ERR_INVALID_ARG, "zs_mx_matmul: ldc below n%s");
+  constexpr uint64_t kMaxDim = 1ull << 30;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxDim || matrix_too_big(m, ldc))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: a dimension above 2^30%s");
+  if (m == 0 || n == 0) return ZS_OK;
+  if (!c || (k && (!a_codes || !a_scales || !b_codes || !b_scales)))
+    return fail(ZS_ERR_INVALID_ARG, "zs_mx_matmul: null pointer%s");
+  if (!aligned(a_codes, 16) || !aligned(b_codes, 16) || !aligned(a_scales, 4) ||
+      !aligned(b_scales, 4) || !aligned(c, esize(c_dtype)))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: an operand is not aligned%s");
+  const uint64_t padded = padded_of(k), c_bytes = extent(m, n, ldc, esize(c_dtype));
+  const void *ins[] = {a_codes, a_scales, b_codes, b_scales};
+  const uint64_t in_bytes[] = {m * code_bytes(a_format, padded), m * padded / ZS_MX_BLOCK,
+                               n * padded / 2, n * padded / ZS_MX_BLOCK};
+  for (int i = 0; i < 4; ++i)
+    if (overlaps(c, c_bytes, ins[i], in_bytes[i]) ||
+        overlaps(workspace, workspace_bytes, ins[i], in_bytes[i]))
+      return fail(ZS_ERR_ALIAS, "zs_mx_matmul: an output overlaps an input%s");
+  if (overlaps(c, c_bytes, workspace, workspace_bytes))
+    return fail(ZS_ERR_ALIAS, "zs_mx_matmul: the result overlaps the workspace%s");
+  MatmulArgs a{a_codes, a_scales, b_codes, b_scales, c, ldc,
+               (uint32_t)m, (uint32_t)n, (uint32_t)padded};
+  /* four results of a lane in one store */
+  const int vec = aligned(c, 4 * esize(c_dtype)) && ldc % 4 == 0;
+  const dim3 grid((unsigned)((n + 63) / 64), (unsigned)((m + 63) / 64));
+  if (grid.y > 65535) return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: too many rows%s");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  with_format(a_format, [&](auto f) {
+    with_any(c_dtype, [&](auto dt) {
+      hipLaunchKernelGGL((matmul_kernel<decltype(f)::value, decltype(dt)::value>), grid,
+                         dim3(kBlock), 0, s, a, vec);
+    });
+  });
+  return launch_result();
+}
+
+namespace {
+
+/* A row is split over several blocks where there are few rows. */
+constexpr uint32_t kDistillThreads = 256;
+
+struct DistillSplit {
+  uint32_t parts, part_vecs;
+};
+
+DistillSplit distill_split(uint64_t rows, uint64_t vocab, int dtype) {
+  const uint64_t vecs = vocab * esize(dtype) / 16;
+  uint64_t parts = rows < 1024 ? 1024 / rows : 1;
+  const uint64_t most = (vecs + kDistillThreads - 1) / kDistillThreads;
+  if (parts > most) parts = most;
+  if (parts < 1) parts = 1;
+  return {(uint32_t)parts, (uint32_t)((vecs + parts - 1) / parts)};
+}
+
+}  // namespace
+
+uint64_t zs_distill_workspace(uint64_t rows, uint64_t vocab, uint32_t slots, int dtype) {
+  if (rows == 0 || !valid_any(dtype) || matrix_too_big(rows, vocab)) return 0;
+  return rows * (distill_split(rows, vocab, dtype).parts * sizeof(DistillPart) + slots * 4ull);
+}
+
+int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
+               const int32_t *ids, const void *teacher, uint32_t slots, float temperature,
+               const float *teacher_lse, const float *row_weight, float loss_scale,
+               const zs_device_scaler *dev, float *loss, void *grad, uint64_t grad_ld,
+               void *workspace, uint64_t workspace_bytes, void *stream) {
+  if (!valid_any(dtype)) return fail(ZS_ERR_INVALID_ARG, "zs_distill: bad dtype%s");
+  if (!(temperature > 0.0f) || !isfinite(temperature))
+    return fail(ZS_ERR_INVALID_ARG, "zs_distill: temperature must be finite and > 0%s");
+  if (!dev && (!(loss_scale > 0.0f) || !isfinite(loss_scale)))
+    return fail(ZS_ERR_INVALID_ARG, "zs_distill: loss_scale must be finite and > 0%s");
+  if (vocab == 0 || vocab > kMaxGrid || ld < vocab || (grad && grad_ld < vocab))
+    return fail(ZS_ERR_INVALID_ARG,
+                "zs_distill: need 0 < vocab < 2^31 and rows at least vocab apart%s");
+  if (slots > kMaxSlots) return fail(ZS_ERR_UNSUPPORTED, "zs_distill: more than 1024 slots%s");
+  if (matrix_too_big(rows, ld) || (grad && matrix_too_big(rows, grad_ld)))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_distill: more than 2^48 elements%s");
+  if (rows == 0) return ZS_OK;
+  if (!logits || !loss || (slots && (!ids || !teacher)))
+    return fail(ZS_ERR_INVALID_ARG, "zs_distill: null pointer%s");
+  const uint64_t esz = esize(dtype);
+  const DistillSplit sp = distill_split(rows, vocab, dtype);
+  const uint64_t need = zs_distill_workspace(rows, vocab, slots, dtype);
+  if (!workspace || workspace_bytes < need)
+    return fail(ZS_ERR_INVALID_ARG, "zs_distill: workspace too small%s");
+  if (!aligned(logits, esz) || (grad && !aligned(grad, esz)) || !aligned(workspace, 16) ||
+      !aligned(dev, 8))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_distill: an operand is not aligned%s");
+  const uint64_t z_bytes = extent(rows, vocab, ld, esz);
+  const uint64_t g_bytes = grad ? extent(rows, vocab, grad_ld, esz) : 0;
+  const void *outs[] = {grad, loss, workspace};
+  const uint64_t out_bytes[] = {g_bytes, rows * 4, need};
+  const void *ins[] = {logits, ids, teacher, teacher_lse, row_weight, dev};
+  const uint64_t in_bytes[] = {z_bytes, rows * slots * 4, rows * slots * esz, rows * 4, rows * 4,
+                               sizeof(zs_device_scaler)};
+  for (int i = 0; i < 3; ++i) {
+    /* the gradient may take the logits' place */
+    for (int j = 0; j < 6; ++j)
+      if (overlaps(outs[i], out_bytes[i], ins[j], in_bytes[j]) &&
+          !(i == 0 && j == 0 && grad == logits && grad_ld == ld))
+        return fail(ZS_ERR_ALIAS, "zs_distill: an output overlaps an input%s");
+    for (int j = i + 1; j < 3; ++j)
+      if (overlaps(outs[i], out_bytes[i], outs[j], out_bytes[j]))
+        return fail(ZS_ERR_ALIAS, "zs_distill: two outputs overlap%s");
+  }
+  if (rows * sp.parts > kMaxGrid) return fail(ZS_ERR_UNSUPPORTED, "zs_distill: too many rows%s");
+  DistillArgs a{};
+  a.z = logits;
+  a.ids = ids;
+  a.teacher = teacher;
+  a.lse = teacher_lse;
+  a.weight = row_weight;
+  a.dev = dev;
+  a.loss = loss;
+  a.grad = grad;
+  a.ws = static_cast<DistillPart *>(workspace);
+  a.ws_z = reinterpret_cast<float *>(a.ws + rows * sp.parts);
+  a.rows = rows;
+  a.ld = ld;
+  a.gld = grad_ld;
+  a.vocab = (uint32_t)vocab;
+  a.slots = slots;
+  a.parts = sp.parts;
+  a.part_vecs = sp.part_vecs;
+  a.tau = temperature;
+  a.inv_tau = 1.0f / temperature;
+  a.log2_scale = (float)(1.4426950408889634 / temperature);
+  a.scale = loss_scale;
+  a.vec_store = grad && (((uintptr_t)grad ^ (uintptr_t)logits) & 15) == 0 &&
+                (grad_ld - ld) * esz % 16 == 0;
+  const uint32_t blocks = grad ? sp.parts : 1;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  int rc = ZS_OK;
+  with_any(dtype, [&](auto dt) {
+    with_bool(teacher_lse != nullptr, [&](auto tail) {
+      constexpr int DT = decltype(dt)::value, NT = kDistillThreads;
+      constexpr bool TAIL = decltype(tail)::value;
+      hipLaunchKernelGGL((distill_stats_kernel<DT, TAIL, NT>), dim3((unsigned)(rows * sp.parts)),
+                         dim3(NT), 0, s, a);
+      rc = launch_result();
+      if (rc != ZS_OK) return;
+      hipLaunchKernelGGL((distill_grad_kernel<DT, TAIL, NT>), dim3((unsigned)(rows * blocks)),
+                         dim3(NT), 0, s, a, blocks);
+      rc = launch_result();
+    });
+  });
+  return rc;
+}
+
+}  /* extern "C" */

@@ -17,10 +17,13 @@ from . import build as _build
 
 ZS_ABI_VERSION = 7
 ZS_MAX_WORLD = 64
-ZS_BF16, ZS_FP16 = 0, 1
+ZS_BF16, ZS_FP16, ZS_FP32 = 0, 1, 2
 ZS_WIRE_FP32, ZS_WIRE_BF16, ZS_WIRE_FP16 = 0, 1, 2
 ZS_STATE_SPLIT, ZS_STATE_GROUPED = 0, 1
 ZS_STATE_GROUP = 1024
+ZS_MX_E2M1, ZS_MX_E4M3 = 0, 1
+ZS_MX_BLOCK, ZS_MX_GROUP = 32, 128
+ZS_DISTILL_MAX_SLOTS = 1024
 ZS_OK, ZS_ERR_INVALID_ARG, ZS_ERR_UNSUPPORTED, ZS_ERR_ALIAS, ZS_ERR_HIP = range(5)
 
 LIB_PATH = _build.LIB
@@ -103,6 +106,14 @@ def _load():
         "zs_device_scaler_make": ([C.POINTER(zs_loss_scaler), f32, f32,
                                    C.POINTER(zs_device_scaler)], i32),
         "zs_step_device": ([C.POINTER(zs_step_args), vp, vp, vp, vp], i32),
+        "zs_mx_quantize": ([vp, i32, u64, u64, u64, i32, i32, vp, vp, vp, i32, vp], i32),
+        "zs_mx_matmul": ([vp, vp, i32, vp, vp, u64, u64, u64, vp, i32, u64, vp, u64, vp], i32),
+        "zs_rmsnorm_forward": ([vp, vp, vp, i32, u64, u64, f32, vp, vp, vp, vp, vp, vp], i32),
+        "zs_rmsnorm_backward_workspace": ([u64, u64], u64),
+        "zs_rmsnorm_backward": ([vp, vp, vp, vp, vp, i32, u64, u64, vp, vp, vp, u64, vp], i32),
+        "zs_distill_workspace": ([u64, u64, u32, i32], u64),
+        "zs_distill": ([vp, i32, u64, u64, u64, vp, vp, u32, f32, vp, vp, f32, vp, vp, vp, u64,
+                        vp, u64, vp], i32),
         "zs_offload_step": ([vp, vp, vp, vp, vp, vp, vp, u64, C.POINTER(zs_adamw_hparams), i32,
                              vp, vp, i32, i32, vp, C.POINTER(C.c_int)], i32),
     }
@@ -457,3 +468,171 @@ def zs_offload_step(grad_dev, grad_host, master, m, v, params_host, params_dev,
         C.byref(committed))
     _check("zs_offload_step", rc)
     return bool(committed.value)
+
+
+# ---- operators of a low-precision model's output end --------------------------
+
+_FLOAT_CODES = {}
+
+
+def _float_code(t, what, fp32=False):
+    """zs_dtype of a tensor's element type."""
+    if not _FLOAT_CODES:
+        torch = _torch()
+        _FLOAT_CODES.update({torch.bfloat16: ZS_BF16, torch.float16: ZS_FP16,
+                             torch.float32: ZS_FP32})
+    code = _FLOAT_CODES.get(t.dtype)
+    if code is None or (code == ZS_FP32 and not fp32):
+        raise TypeError(f"{what}: {'float32, ' if fp32 else ''}bfloat16 or float16 tensor "
+                        f"expected, got {t.dtype}")
+    return code
+
+
+def _rows(x, what, shape=None):
+    """(address, rows, cols, row stride) of a 2-D CUDA tensor with contiguous rows."""
+    if not x.is_cuda:
+        raise ValueError(f"{what}: CUDA tensor expected")
+    if x.dim() != 2 or (shape is not None and tuple(x.shape) != shape):
+        raise ValueError(f"{what}: {'2-D' if shape is None else shape} tensor expected, "
+                         f"got {tuple(x.shape)}")
+    r, c = x.shape
+    ld = x.stride(0) if r > 1 else c
+    if (c > 1 and x.stride(1) != 1) or ld < c:
+        raise ValueError(f"{what}: rows must be contiguous and must not overlap")
+    return x.data_ptr(), r, c, ld
+
+
+def _dense(x, shape, dtype, what):
+    """Address of a contiguous CUDA tensor of that shape and type (None stays None)."""
+    if x is None:
+        return None
+    if not x.is_cuda or not x.is_contiguous() or tuple(x.shape) != shape or x.dtype != dtype:
+        raise ValueError(f"{what}: contiguous {dtype} CUDA tensor of shape {shape} expected, "
+                         f"got {x.dtype} {tuple(x.shape)}")
+    return x.data_ptr()
+
+
+def _workspace(x):
+    if x is None:
+        return None, 0
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("workspace: contiguous CUDA tensor expected")
+    return x.data_ptr(), x.numel() * x.element_size()
+
+
+def mx_padded(k):
+    """Elements of a microscaled row of k elements: whole groups."""
+    return -(-k // ZS_MX_GROUP) * ZS_MX_GROUP
+
+
+def mx_shapes(rows, k, fmt):
+    """Shapes of the codes and scales (both uint8) of `rows` microscaled rows of k elements."""
+    p = mx_padded(k)
+    return (rows, p // 2 if fmt == ZS_MX_E2M1 else p), (rows, p // ZS_MX_BLOCK)
+
+
+def mx_empty(rows, k, fmt, device="cuda"):
+    """Uninitialised codes and scales for `rows` microscaled rows of k elements."""
+    torch = _torch()
+    return tuple(torch.empty(s, dtype=torch.uint8, device=device)
+                 for s in mx_shapes(rows, k, fmt))
+
+
+def _mx_ptrs(codes, scales, rows, k, fmt, what):
+    cs, ss = mx_shapes(rows, k, fmt)
+    u8 = _torch().uint8
+    return (_dense(codes, cs, u8, f"{what} codes"), _dense(scales, ss, u8, f"{what} scales"))
+
+
+def zs_mx_quantize(src, fmt, codes, scales, columns=False, values=None, stream=None):
+    """Microscaled copy of the 2-D tensor src, along its rows or its columns
+    (codes and scales: mx_empty of src's rows, or columns, by the other)."""
+    p, r, c, ld = _rows(src, "src")
+    cp, sp = _mx_ptrs(codes, scales, c if columns else r, r if columns else c, fmt, "mx")
+    vp, vdt = None, ZS_BF16
+    if values is not None:
+        vdt = _float_code(values, "values")
+        vp = _dense(values, (r, c), values.dtype, "values")
+    _check("zs_mx_quantize", _lib.zs_mx_quantize(
+        p, _float_code(src, "src", fp32=True), r, c, ld, fmt, 1 if columns else 0, cp, sp, vp,
+        vdt, _stream(stream)))
+
+
+def zs_mx_matmul(a_codes, a_scales, a_format, b_codes, b_scales, out, k, workspace=None,
+                 stream=None):
+    """out[m][n] = A B^T: A m microscaled rows of k elements in a_format, B n in ZS_MX_E2M1."""
+    p, m, n, ld = _rows(out, "out")
+    ac, asc = _mx_ptrs(a_codes, a_scales, m, k, a_format, "A")
+    bc, bsc = _mx_ptrs(b_codes, b_scales, n, k, ZS_MX_E2M1, "B")
+    wp, wb = _workspace(workspace)
+    _check("zs_mx_matmul", _lib.zs_mx_matmul(
+        ac, asc, a_format, bc, bsc, m, n, k, p, _float_code(out, "out", fp32=True), ld, wp, wb,
+        _stream(stream)))
+
+
+def zs_rmsnorm_forward(x, gain, eps, h=None, rstd=None, residual=None, codes=None, scales=None,
+                       y=None, stream=None):
+    """Norm of x (+ residual, the sum going to h) into 8-bit microscaled rows
+    (codes, scales) and / or a 16-bit y."""
+    if x.dim() != 2:
+        raise ValueError("x: 2-D tensor expected")
+    shape, dt = tuple(x.shape), x.dtype
+    cp = sp = None
+    if codes is not None or scales is not None:
+        if codes is None or scales is None:
+            raise ValueError("codes and scales go together")
+        cp, sp = _mx_ptrs(codes, scales, *shape, ZS_MX_E4M3, "y")
+    _check("zs_rmsnorm_forward", _lib.zs_rmsnorm_forward(
+        _dense(x, shape, dt, "x"), _dense(residual, shape, dt, "residual"),
+        _dense(gain, shape[1:], dt, "gain"), _float_code(x, "x"), *shape, eps,
+        _dense(h, shape, dt, "h"), _dense(rstd, shape[:1], _torch().float32, "rstd"), cp, sp,
+        _dense(y, shape, dt, "y"), _stream(stream)))
+
+
+def zs_rmsnorm_backward_workspace(rows, cols):
+    """Bytes of workspace that zs_rmsnorm_backward needs."""
+    return _lib.zs_rmsnorm_backward_workspace(rows, cols)
+
+
+def zs_rmsnorm_backward(dy, h, rstd, gain, dx, dgain, workspace, dres=None, stream=None):
+    """Gradients of zs_rmsnorm_forward: dx (of x and of the residual alike) and the fp32 dgain."""
+    if dy.dim() != 2:
+        raise ValueError("dy: 2-D tensor expected")
+    shape, dt, f32 = tuple(dy.shape), dy.dtype, _torch().float32
+    wp, wb = _workspace(workspace)
+    _check("zs_rmsnorm_backward", _lib.zs_rmsnorm_backward(
+        _dense(dy, shape, dt, "dy"), _dense(h, shape, dt, "h"),
+        _dense(rstd, shape[:1], f32, "rstd"), _dense(gain, shape[1:], dt, "gain"),
+        _dense(dres, shape, dt, "dres"), _float_code(dy, "dy"), *shape,
+        _dense(dx, shape, dt, "dx"), _dense(dgain, shape[1:], f32, "dgain"), wp, wb,
+        _stream(stream)))
+
+
+def zs_distill_workspace(rows, vocab, slots, dtype):
+    """Bytes of workspace that zs_distill needs; dtype: the logits' zs_dtype."""
+    return _lib.zs_distill_workspace(rows, vocab, slots, dtype)
+
+
+def zs_distill(logits, ids, teacher, temperature, loss, grad=None, teacher_lse=None,
+               row_weight=None, loss_scale=1.0, dev_scaler=None, workspace=None, stream=None):
+    """Loss per row against a teacher's top logits and, with grad, the logits'
+    gradient times the loss scale (loss_scale, or dev_scaler's: the buffer of
+    device_scaler_upload). grad may be logits itself."""
+    p, rows, vocab, ld = _rows(logits, "logits")
+    torch = _torch()
+    f32 = torch.float32
+    slots = ids.shape[1] if ids.dim() == 2 else -1
+    gp, gld = None, 0
+    if grad is not None:
+        if grad.dtype != logits.dtype:
+            raise ValueError("grad: the logits' dtype expected")
+        gp, _, _, gld = _rows(grad, "grad", (rows, vocab))
+    wp, wb = _workspace(workspace)
+    _check("zs_distill", _lib.zs_distill(
+        p, _float_code(logits, "logits", fp32=True), rows, vocab, ld,
+        _dense(ids, (rows, slots), torch.int32, "ids"),
+        _dense(teacher, (rows, slots), logits.dtype, "teacher"), slots, temperature,
+        _dense(teacher_lse, (rows,), f32, "teacher_lse"),
+        _dense(row_weight, (rows,), f32, "row_weight"), loss_scale,
+        None if dev_scaler is None else _dev_scaler_ptr(dev_scaler),
+        _dense(loss, (rows,), f32, "loss"), gp, gld, wp, wb, _stream(stream)))
