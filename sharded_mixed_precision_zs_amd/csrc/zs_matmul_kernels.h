@@ -52,34 +52,471 @@ __device__ __forceinline__ void store_c4(void *c, uint64_t at, uint32_t col, uin
   }
 }
 
-/* One 32 x 32 tile of C per wave, operands straight from global memory. */
-template <int AF, int CDT>
-__global__ __launch_bounds__(kBlock) void matmul_kernel(MatmulArgs p, int vec) {
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t r = lane & 31, g = lane >> 5;
-  const uint32_t m0 = blockIdx.y * 64 + (wave >> 1) * 32, n0 = blockIdx.x * 64 + (wave & 1) * 32;
-  const uint64_t ra = m0 + r < p.m ? m0 + r : p.m - 1, rb = n0 + r < p.n ? n0 + r : p.n - 1;
-  const uint8_t *a = p.a + ra * mx_bytes<AF>(p.padded), *b = p.b + rb * (p.padded / 2);
-  const uint8_t *as = p.as + ra * (p.padded / 32), *bs = p.bs + rb * (p.padded / 32);
-  f32x16 acc = {};
-  for (uint32_t k = 0; k < p.padded; k += 64) {
-    i32x8 fa = {}, fb = {};
-    const u32x4 wb = *reinterpret_cast<const u32x4 *>(b + k / 2 + g * 16);
-    fb[0] = wb.x; fb[1] = wb.y; fb[2] = wb.z; fb[3] = wb.w;
-    const u32x4 wa = *reinterpret_cast<const u32x4 *>(a + mx_bytes<AF>(k) + g * 16);
-    fa[0] = wa.x; fa[1] = wa.y; fa[2] = wa.z; fa[3] = wa.w;
-    if constexpr (AF == ZS_MX_E4M3) {
-      const u32x4 wh = *reinterpret_cast<const u32x4 *>(a + k + 32 + g * 16);
-      fa[4] = wh.x; fa[5] = wh.y; fa[6] = wh.z; fa[7] = wh.w;
-    }
-    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb, fa, acc, 4, kMfmaFormat<AF>, 0,
-                                                          bs[k / 32 + g], 0, as[k / 32 + g]);
-  }
-  if (m0 + r >= p.m) return;
+/* ------------------------------------------------------------------------
+ * Tiles of C through LDS. A block of four waves (two by two) computes
+ * BM x BN, in stages of 256 elements of K that two LDS buffers hold in turn:
+ * while the matrix cores work on one, the loads of the next stage go
+ * straight to the other, so a stage's arithmetic hides its loads.
+ *
+ * LDS rows are 128 bytes: 256 E2M1 elements, or 128 E4M3 elements (A then
+ * has two planes). A wave's load fills 8 such rows, 16 bytes a lane, whole
+ * lines of memory; the 16-byte piece c of row r lies at c ^ x(r), x(r) =
+ * r % 8 with its lowest bit flipped in every other 8 rows, so that the lanes of a fragment, which read the same piece
+ * of 32 rows, meet no bank twice in any 8 or 16 of them.
+ *
+ * Scales: a thread fetches 16 bytes of a row or two, those of 512 elements,
+ * and puts them into LDS a chunk ahead; a fragment's lane then reads the 8
+ * bytes of a stage.
+ * ---------------------------------------------------------------------- */
+constexpr uint32_t kStageK = 256;                 /* elements of K per stage */
+constexpr uint32_t kStageGroups = kStageK / kMxGroup;
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void global_void;
+
+__device__ __forceinline__ uint32_t swizzle(uint32_t row) { return (row ^ (row >> 3 & 1)) & 7; }
+
+/* 16 bytes per lane from memory to LDS: lane l's go to dst + 16 l. */
+__device__ __forceinline__ void load_lds16(const uint8_t *src, uint8_t *dst) {
+  __builtin_amdgcn_global_load_lds((global_void *)src, (lds_void *)dst, 16, 0, 0);
+}
+
+template <int AF>
+__device__ __forceinline__ f32x16 mfma(const i32x8 &b, const i32x8 &a, f32x16 acc, uint32_t sb,
+                                       uint32_t sa, bool high) {
+  /* the lane's scale is byte 0 (first 64 elements of a group) or 2 of a word */
+  return high ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, 4, kMfmaFormat<AF>, 2,
+                                                                sb, 2, sa)
+              : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, 4, kMfmaFormat<AF>, 0,
+                                                                sb, 0, sa);
+}
+
+__device__ __forceinline__ void put4(i32x8 &f, int at, const u32x4 &w) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float x[4] = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-    store_c4<CDT>(p.c, (uint64_t)(m0 + r) * p.ldc, n0 + q * 8 + g * 4, p.n, x, vec);
+  for (int j = 0; j < 4; ++j) f[at + j] = (int)w[j];
+}
+
+/* One step's operands: 64 elements of K of a wave's rows, as read. */
+template <int AF>
+constexpr int kHalves = AF == ZS_MX_E2M1 ? 1 : 2;   /* 16-byte pieces of A */
+
+template <int AF, int FM, int FN>
+struct Fragments {
+  u32x4 a[FM][kHalves<AF>], b[FN];
+};
+
+/* 16-byte piece c of LDS row `row` (128 bytes); x = swizzle(row). */
+__device__ __forceinline__ u32x4 piece(const uint8_t *lds, uint32_t row, uint32_t c, uint32_t x) {
+  return *reinterpret_cast<const u32x4 *>(lds + row * 128 + ((c ^ x) * 16));
+}
+
+template <int AF, int FM, int FN>
+__device__ __forceinline__ void read_step(const uint8_t *sa, const uint8_t *sb, int ks,
+                                          uint32_t plane, uint32_t row, uint32_t g, uint32_t x,
+                                          Fragments<AF, FM, FN> &f) {
+#pragma unroll
+  for (int j = 0; j < FN; ++j) f.b[j] = piece(sb, j * 32 + row, 2 * ks + g, x);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    if constexpr (AF == ZS_MX_E2M1) {
+      f.a[i][0] = piece(sa, i * 32 + row, 2 * ks + g, x);
+    } else {
+      const uint8_t *q = sa + (ks >> 1) * plane;
+      f.a[i][0] = piece(q, i * 32 + row, 4 * (ks & 1) + g, x);
+      f.a[i][1] = piece(q, i * 32 + row, 4 * (ks & 1) + 2 + g, x);
+    }
+  }
+}
+
+/* A stage's scales of a wave's rows, a word per group. */
+template <int FM, int FN>
+struct StageScales {
+  uint32_t a[FM][2], b[FN][2];
+};
+
+template <int FM, int FN>
+__device__ __forceinline__ void read_scales(const uint8_t *sa, const uint8_t *sb, uint32_t row,
+                                            uint32_t g, StageScales<FM, FN> &w) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const u32x2 v = *reinterpret_cast<const u32x2 *>(sa + (i * 32 + row) * 16);
+    w.a[i][0] = v.x >> (8 * g);
+    w.a[i][1] = v.y >> (8 * g);
+  }
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const u32x2 v = *reinterpret_cast<const u32x2 *>(sb + (j * 32 + row) * 16);
+    w.b[j][0] = v.x >> (8 * g);
+    w.b[j][1] = v.y >> (8 * g);
+  }
+}
+
+template <int AF, int FM, int FN>
+__device__ __forceinline__ void multiply_step(const Fragments<AF, FM, FN> &f, int ks,
+                                              const StageScales<FM, FN> &w,
+                                              f32x16 (&acc)[FM][FN]) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    i32x8 a{};
+    put4(a, 0, f.a[i][0]);
+    if constexpr (AF == ZS_MX_E4M3) put4(a, 4, f.a[i][1]);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      i32x8 b{};
+      put4(b, 0, f.b[j]);
+      acc[i][j] = mfma<AF>(b, a, acc[i][j], w.b[j][ks >> 1], w.a[i][ks >> 1], ks & 1);
+    }
+  }
+}
+
+/* Asks the scheduler to spread a step's LDS reads among the matrix
+ * instructions of the step before. */
+template <int AF, int FM, int FN>
+__device__ __forceinline__ void interleave() {
+  constexpr int reads = FN + FM * (AF == ZS_MX_E2M1 ? 1 : 2), products = FM * FN;
+  constexpr int each = products / reads > 0 ? products / reads : 1;
+#pragma unroll
+  for (int i = 0; i < reads; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, each, 0);   /* matrix instructions */
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      /* an LDS read */
+  }
+  __builtin_amdgcn_sched_barrier(0);   /* nothing moves into another step */
+}
+
+/* Result element types by their size and rounding. */
+template <int CDT>
+__device__ __forceinline__ void put_c4(uint8_t *lds, const float (&x)[4]) {
+  if constexpr (CDT == ZS_FP32)
+    *reinterpret_cast<float4 *>(lds) = make_float4(x[0], x[1], x[2], x[3]);
+  else
+    *reinterpret_cast<u32x2 *>(lds) = u32x2{pack2<CDT>(x[0], x[1]), pack2<CDT>(x[2], x[3])};
+}
+
+template <bool V>
+struct Const {
+  static constexpr bool value = V;
+};
+
+template <int AF, int CDT, int BM, int BN>
+__global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
+  constexpr int FM = BM / 64, FN = BN / 64;           /* 32 x 32 fragments per wave */
+  constexpr uint32_t kPlanes = AF == ZS_MX_E2M1 ? 1 : 2, kPlane = BM * 128;
+  __shared__ __align__(16) uint8_t sa0[kPlanes * kPlane], sa1[kPlanes * kPlane];
+  __shared__ __align__(16) uint8_t sb0[BN * 128], sb1[BN * 128];
+  __shared__ __align__(16) uint8_t scales[2 * (BM + BN) * 16];   /* two chunks' */
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const uint32_t r = lane & 31, g = lane >> 5;
+  const uint32_t tm = (wave >> 1) * (BM / 2), tn = (wave & 1) * (BN / 2);   /* the wave's corner */
+
+  /* Blocks go round the eight XCDs; each XCD takes a run of tiles, and runs
+   * walk groups of eight tile rows, so that its L2 sees the same operands
+   * again soon. */
+  const uint32_t tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.n + BN - 1) / BN;
+  const uint32_t total = tiles_m * tiles_n;
+  uint32_t id = blockIdx.x;
+  {
+    const uint32_t per = total / 8, extra = total % 8, xcd = id % 8, at = id / 8;
+    id = xcd * per + (xcd < extra ? xcd : extra) + at;
+  }
+  constexpr uint32_t kBand = 8;
+  const uint32_t band = id / (kBand * tiles_n), in_band = id % (kBand * tiles_n);
+  const uint32_t high = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
+  const uint32_t m0 = (band * kBand + in_band % high) * BM, n0 = (in_band / high) * BN;
+
+  const uint64_t row_a = mx_bytes<AF>(p.padded), row_b = p.padded / 2;
+  const uint32_t groups = p.padded / kMxGroup, scale_row = p.padded / kMxBlock;
+  const uint8_t *ta = p.a + m0 * row_a, *tb = p.b + n0 * row_b;
+
+  /* Rows past the last are read as the last; their results are not stored. */
+  const uint32_t last_a = p.m - 1 - m0, last_b = p.n - 1 - n0;
+  uint32_t off_a[BM / 32], off_b[BN / 32];
+#pragma unroll
+  for (int i = 0; i < BM / 32; ++i) {
+    const uint32_t row = (wave * (BM / 32) + i) * 8 + lane / 8;
+    off_a[i] = (row < last_a ? row : last_a) * (uint32_t)row_a + ((lane & 7) ^ swizzle(row)) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < BN / 32; ++i) {
+    const uint32_t row = (wave * (BN / 32) + i) * 8 + lane / 8;
+    off_b[i] = (row < last_b ? row : last_b) * (uint32_t)row_b + ((lane & 7) ^ swizzle(row)) * 16;
+  }
+  /* this thread's rows of scales: A's, then B's */
+  constexpr int kScaleRows = (BM + BN + 255) / 256;
+  const uint8_t *scale_of[kScaleRows];
+#pragma unroll
+  for (int i = 0; i < kScaleRows; ++i) {
+    const uint32_t t = threadIdx.x + i * 256, rb = t - BM;
+    scale_of[i] = t < BM ? p.as + (uint64_t)(m0 + (t < last_a ? t : last_a)) * scale_row
+                         : p.bs + (uint64_t)(n0 + (rb < last_b ? rb : last_b)) * scale_row;
+  }
+
+  /* Bit i: the lane's piece of its i-th row lies in the upper half of a line. */
+  uint32_t upper_a = 0, upper_b = 0;
+#pragma unroll
+  for (int i = 0; i < BM / 32; ++i)
+    upper_a |= ((((lane & 7) ^ swizzle((wave * (BM / 32) + i) * 8 + lane / 8)) >> 2) & 1) << i;
+#pragma unroll
+  for (int i = 0; i < BN / 32; ++i)
+    upper_b |= ((((lane & 7) ^ swizzle((wave * (BN / 32) + i) * 8 + lane / 8)) >> 2) & 1) << i;
+
+  /* A stage of one group only (the last, where the groups are odd) loads the
+   * half of each row that it has twice, rather than past the row's end. A
+   * stage past the last loads the last again: no branch parts the loop. */
+  const uint32_t stages = (groups + kStageGroups - 1) / kStageGroups;
+  auto load = [&](uint32_t stage, uint8_t *sa, uint8_t *sb) {
+    stage = stage < stages ? stage : stages - 1;
+    const bool half = (stage + 1) * kStageGroups > groups;
+    const uint8_t *qa = ta + mx_bytes<AF>((uint64_t)stage * kStageK);
+    const uint8_t *qb = tb + (uint64_t)stage * (kStageK / 2);
+    const uint32_t mask = half ? ~0u : 0u;
+    const uint32_t ua = kPlanes == 1 ? upper_a & mask : 0, ub = upper_b & mask;
+#pragma unroll
+    for (uint32_t pl = 0; pl < kPlanes; ++pl)
+#pragma unroll
+      for (int i = 0; i < BM / 32; ++i)
+        load_lds16((half ? qa : qa + pl * 128) + (off_a[i] - ((ua >> i) & 1) * 64),
+                   sa + pl * kPlane + (wave * (BM / 32) + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < BN / 32; ++i)
+      load_lds16(qb + (off_b[i] - ((ub >> i) & 1) * 64), sb + (wave * (BN / 32) + i) * 1024);
+  };
+
+  f32x16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+  /* Scales go a chunk of four groups at a time, from no further than the
+   * row's last four; a last chunk that starts later is shifted down. */
+  struct __attribute__((packed, aligned(4))) W4 { uint32_t w[4]; };
+  uint32_t raw[kScaleRows][4];
+  auto fetch_scales = [&](uint32_t group) {
+    const uint32_t at = group + 4 <= groups ? group : groups >= 4 ? groups - 4 : 0;
+#pragma unroll
+    for (int i = 0; i < kScaleRows; ++i) {
+      if ((BM + BN) % 256 && threadIdx.x + i * 256 >= BM + BN) break;
+      const W4 v = *reinterpret_cast<const W4 *>(scale_of[i] + at * 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) raw[i][k] = v.w[k];
+    }
+  };
+  auto put_scales = [&](uint32_t group, uint32_t chunk) {
+    const uint32_t late = group + 4 > groups && groups >= 4 ? group + 4 - groups : 0;   /* <= 3 */
+#pragma unroll
+    for (int i = 0; i < kScaleRows; ++i) {
+      if ((BM + BN) % 256 && threadIdx.x + i * 256 >= BM + BN) break;
+      u32x4 v = {raw[i][0], raw[i][1], raw[i][2], raw[i][3]};
+      v = late & 1 ? u32x4{v.y, v.z, v.w, v.w} : v;
+      v = late & 2 ? u32x4{v.z, v.w, v.w, v.w} : v;
+      *reinterpret_cast<u32x4 *>(scales + chunk + (threadIdx.x + i * 256) * 16) = v;
+    }
+  };
+
+  /* Fragments start at multiples of 16 rows, which leave x(r) as it is. The
+   * operands of step k + 1 are read while step k multiplies. A stage's last
+   * step stands behind the barrier: by then every wave holds what it needs
+   * of this buffer, and the other one, asked for a stage ago, is complete;
+   * so the next stage's first operands and the loads after it are on their
+   * way before this stage's last products. */
+  const uint32_t x = swizzle(r);
+  const uint32_t full = groups / kStageGroups;    /* stages of two groups */
+  Fragments<AF, FM, FN> f0, f1;
+  StageScales<FM, FN> w0, w1;
+  constexpr uint32_t kChunk = (BM + BN) * 16;
+  const uint32_t srow_a = tm * 16, srow_b = (BM + tn) * 16;   /* the wave's rows of scales */
+  auto run_stage = [&](uint8_t *sa, uint8_t *sb, const uint8_t *next_sa, const uint8_t *next_sb,
+                       uint32_t next_sc, uint32_t stage, const StageScales<FM, FN> &w,
+                       StageScales<FM, FN> &next_w, auto first, uint32_t put_sc) {
+    const uint8_t *qa = sa + tm * 128, *qb = sb + tn * 128;
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (decltype(first)::value) fetch_scales((stage + 2) * kStageGroups);
+    read_step<AF, FM, FN>(qa, qb, 1, kPlane, r, g, x, f1);
+    multiply_step<AF, FM, FN>(f0, 0, w, acc);
+    interleave<AF, FM, FN>();
+    read_step<AF, FM, FN>(qa, qb, 2, kPlane, r, g, x, f0);
+    multiply_step<AF, FM, FN>(f1, 1, w, acc);
+    interleave<AF, FM, FN>();
+    read_step<AF, FM, FN>(qa, qb, 3, kPlane, r, g, x, f1);
+    multiply_step<AF, FM, FN>(f0, 2, w, acc);
+    interleave<AF, FM, FN>();
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    /* past the last stage, what is loaded and read here is not used */
+    read_step<AF, FM, FN>(next_sa + tm * 128, next_sb + tn * 128, 0, kPlane, r, g, x, f0);
+    read_scales<FM, FN>(scales + next_sc + srow_a, scales + next_sc + srow_b, r, g, next_w);
+    load(stage + 2, sa, sb);
+    if constexpr (decltype(first)::value) put_scales((stage + 2) * kStageGroups, put_sc);
+    multiply_step<AF, FM, FN>(f1, 3, w, acc);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  if (stages) {
+    load(0, sa0, sb0);
+    if (groups >= 4) {
+      fetch_scales(0);
+    } else {   /* shorter rows, of a single chunk, a word at a time */
+#pragma unroll
+      for (int i = 0; i < kScaleRows; ++i) {
+        if ((BM + BN) % 256 && threadIdx.x + i * 256 >= BM + BN) break;
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+          raw[i][k] = *reinterpret_cast<const uint32_t *>(scale_of[i] +
+                                                          4 * (k < groups ? k : groups - 1));
+        scale_of[i] = p.a;   /* what the loop fetches is not used: 16 bytes that are there */
+      }
+    }
+    put_scales(0, 0);
+    __syncthreads();
+    load(1, sa1, sb1);
+    read_scales<FM, FN>(scales + srow_a, scales + srow_b, r, g, w0);
+    read_step<AF, FM, FN>(sa0 + tm * 128, sb0 + tn * 128, 0, kPlane, r, g, x, f0);
+  }
+  uint32_t sc = 0, s = 0;   /* a chunk's scales: two stages' */
+  for (; s + 1 < full; s += 2, sc ^= kChunk) {
+    run_stage(sa0, sb0, sa1, sb1, sc + 8, s, w0, w1, Const<true>{}, sc ^ kChunk);
+    run_stage(sa1, sb1, sa0, sb0, sc ^ kChunk, s + 1, w1, w0, Const<false>{}, 0);
+  }
+  if (s < full) run_stage(sa0, sb0, sa1, sb1, sc + 8, s, w0, w1, Const<true>{}, sc ^ kChunk);
+  if (groups % kStageGroups) {   /* half a stage left: its first operands are in f0 */
+    const bool odd = full & 1;
+    read_step<AF, FM, FN>((odd ? sa1 : sa0) + tm * 128, (odd ? sb1 : sb0) + tn * 128, 1, kPlane, r,
+                          g, x, f1);
+    if (odd) w0 = w1;
+    multiply_step<AF, FM, FN>(f0, 0, w0, acc);
+    multiply_step<AF, FM, FN>(f1, 1, w0, acc);
+  }
+  __syncthreads();
+
+  /* Each wave turns strips of 32 rows round in its own part of LDS, so that
+   * rows of C go out in runs: 16-byte pieces, swizzled as above. */
+  constexpr uint32_t kEsz = CDT == ZS_FP32 ? 4 : 2, kRow = FN * 32 * kEsz, kPieces = kRow / 16;
+  static_assert(32 * kRow * 2 <= sizeof(sa0) && 32 * kRow * 2 <= sizeof(sb0), "strips fit");
+  uint8_t *strip = (wave & 2 ? sb0 : sa0) + (wave & 1) * 32 * kRow;
+  const bool vec = ((uintptr_t)p.c & 15) == 0 && p.ldc * kEsz % 16 == 0;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                            acc[i][j][4 * q + 3]};
+        const uint32_t byte = (j * 32 + q * 8 + g * 4) * kEsz;
+        put_c4<CDT>(strip + r * kRow + (((byte / 16) ^ (r % kPieces)) * 16) + byte % 16, v);
+      }
+    __builtin_amdgcn_wave_barrier();
+    const uint32_t col0 = n0 + tn;
+    if (vec) {
+      constexpr uint32_t kRowsAtOnce = 64 / kPieces > 0 ? 64 / kPieces : 1;
+#pragma unroll
+      for (uint32_t k = 0; k < 32 / kRowsAtOnce; ++k) {
+        const uint32_t lr = k * kRowsAtOnce + lane / kPieces, c = lane % kPieces;
+        const uint32_t row = m0 + tm + i * 32 + lr, col = col0 + c * (16 / kEsz);
+        const u32x4 w = *reinterpret_cast<const u32x4 *>(strip + lr * kRow +
+                                                         ((c ^ (lr % kPieces)) * 16));
+        if (row >= p.m) continue;
+        uint8_t *out = static_cast<uint8_t *>(p.c) + ((uint64_t)row * p.ldc + col) * kEsz;
+        if (col + 16 / kEsz <= p.n) {
+          *reinterpret_cast<u32x4 *>(out) = w;
+        } else {
+          const uint8_t *b = strip + lr * kRow + ((c ^ (lr % kPieces)) * 16);
+          for (uint32_t e = 0; col + e < p.n; ++e) {
+            if constexpr (kEsz == 4)
+              reinterpret_cast<uint32_t *>(out)[e] = reinterpret_cast<const uint32_t *>(b)[e];
+            else
+              reinterpret_cast<uint16_t *>(out)[e] = reinterpret_cast<const uint16_t *>(b)[e];
+          }
+        }
+      }
+    } else {
+      for (uint32_t lr = 0; lr < 32; ++lr) {
+        const uint32_t row = m0 + tm + i * 32 + lr;
+        if (row >= p.m) break;
+#pragma unroll
+        for (uint32_t h = 0; h < FN * 32 / 64 + (FN == 1); ++h) {
+          const uint32_t lc = h * 64 + lane, col = col0 + lc;
+          if (lc >= FN * 32 || col >= p.n) continue;
+          const uint8_t *b = strip + lr * kRow + (((lc * kEsz / 16) ^ (lr % kPieces)) * 16) +
+                             lc * kEsz % 16;
+          uint8_t *out = static_cast<uint8_t *>(p.c) + ((uint64_t)row * p.ldc + col) * kEsz;
+          if constexpr (kEsz == 4)
+            *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(b);
+          else
+            *reinterpret_cast<uint16_t *>(out) = *reinterpret_cast<const uint16_t *>(b);
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+/* ------------------------------------------------------------------------
+ * Few rows of A (m <= 32 MF): bound by reading B once. A block owns 32 rows
+ * of B; its eight waves share K in pieces of 256 elements (whole lines of
+ * memory), operands straight to registers, and join in wave order.
+ * ---------------------------------------------------------------------- */
+constexpr int kThinWaves = 8;
+
+template <int AF, int CDT, int MF>
+__global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs p, int vec) {
+  __shared__ float sums[kThinWaves][MF][16][64];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t r = lane & 31, g = lane >> 5, n0 = blockIdx.x * 32;
+  const uint64_t rb = n0 + r < p.n ? n0 + r : p.n - 1;
+  const uint8_t *b = p.b + rb * (p.padded / 2), *bs = p.bs + rb * (p.padded / kMxBlock);
+  const uint8_t *a[MF], *as[MF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i) {
+    const uint64_t ra = i * 32 + r < p.m ? i * 32 + r : p.m - 1;
+    a[i] = p.a + ra * mx_bytes<AF>(p.padded);
+    as[i] = p.as + ra * (p.padded / kMxBlock);
+  }
+  f32x16 acc[MF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i) acc[i] = f32x16{};
+  const uint32_t groups = p.padded / kMxGroup;
+  for (uint32_t gr = wave * 2; gr < groups; gr += kThinWaves * 2) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (gr + h >= groups) break;
+      const uint32_t k = (gr + h) * kMxGroup;
+      const uint32_t wb = *reinterpret_cast<const uint32_t *>(bs + (gr + h) * 4) >> (8 * g);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        i32x8 fb{};
+        put4(fb, 0, *reinterpret_cast<const u32x4 *>(b + k / 2 + ks * 32 + g * 16));
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          const uint32_t wa = *reinterpret_cast<const uint32_t *>(as[i] + (gr + h) * 4) >> (8 * g);
+          i32x8 fa{};
+          if constexpr (AF == ZS_MX_E2M1) {
+            put4(fa, 0, *reinterpret_cast<const u32x4 *>(a[i] + k / 2 + ks * 32 + g * 16));
+          } else {
+            put4(fa, 0, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 64 + g * 16));
+            put4(fa, 4, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 64 + 32 + g * 16));
+          }
+          acc[i] = mfma<AF>(fb, fa, acc[i], wb, wa, ks & 1);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sums[wave][i][e][lane] = acc[i][e];
+  __syncthreads();
+  /* a thread takes four neighbouring results: fragment i, quarter q, lane l */
+  for (uint32_t t = threadIdx.x; t < MF * 4 * 64; t += 64 * kThinWaves) {
+    const uint32_t i = t / 256, q = (t / 64) & 3, l = t & 63;
+    float x[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kThinWaves; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] += sums[w][i][q * 4 + e][l];
+    const uint32_t row = i * 32 + (l & 31);
+    if (row < p.m)
+      store_c4<CDT>(p.c, (uint64_t)row * p.ldc, n0 + q * 8 + (l >> 5) * 4, p.n, x, vec);
   }
 }
 

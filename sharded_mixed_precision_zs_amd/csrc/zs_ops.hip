@@ -105,6 +105,33 @@ void with_norm_shape(uint64_t rows, uint64_t padded, F f) {
     with_items((vecs + 1023) / 1024, [&](auto i) { f(Tag<1024>{}, i); });
 }
 
+/* ------------------------------------------------------------------------
+ * The product's variant: up to 64 rows of A, bound by B, the thin kernel;
+ * the large tiles where they occupy every CU, else 128 x 128.
+ * ---------------------------------------------------------------------- */
+template <int AF, int CDT, int BM, int BN>
+void launch_tile(const MatmulArgs &a, hipStream_t s) {
+  const uint64_t tiles = (uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN);
+  hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN>), dim3((unsigned)tiles), dim3(256), 0, s,
+                     a);
+}
+
+template <int AF, int CDT>
+void launch_matmul(const MatmulArgs &a, hipStream_t s) {
+  constexpr uint64_t esz = CDT == ZS_FP32 ? 4 : 2;
+  if (a.m <= 64) {
+    /* four results of a lane in one store */
+    const int vec = aligned(a.c, 4 * esz) && a.ldc % 4 == 0;
+    const dim3 grid((a.n + 31) / 32), block(64 * kThinWaves);
+    if (a.m <= 32) hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, 1>), grid, block, 0, s, a, vec);
+    else hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, 2>), grid, block, 0, s, a, vec);
+    return;
+  }
+  constexpr int BM = AF == ZS_MX_E2M1 ? 256 : 128, BN = 256;
+  if ((uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN) >= 256) launch_tile<AF, CDT, BM, BN>(a, s);
+  else launch_tile<AF, CDT, 128, 128>(a, s);
+}
+
 /* Groups that share the rows of a backward pass. */
 constexpr uint32_t kNormParts = 1024;
 
@@ -297,9 +324,11 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
   if (c_dtype == ZS_FP32 && a_format == ZS_MX_E4M3)
     return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: fp32 results need 4-bit operands%s");
   if (ldc < n) return fail(ZS_ERR_INVALID_ARG, "zs_mx_matmul: ldc below n%s");
-  constexpr uint64_t kMaxDim = 1ull << 30;
-  if (m > kMaxDim || n > kMaxDim || k > kMaxDim || matrix_too_big(m, ldc))
-    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: a dimension above 2^30%s");
+  /* within a tile of 256 rows, byte offsets are 32 bits */
+  constexpr uint64_t kMaxDim = 1ull << 30, kMaxMatmulK = 1ull << 22;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxMatmulK || matrix_too_big(m, ldc) ||
+      m / 128 * (n / 128) > kMaxGrid / 4)
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: m or n above 2^30, or k above 2^22%s");
   if (m == 0 || n == 0) return ZS_OK;
   if (!c || (k && (!a_codes || !a_scales || !b_codes || !b_scales)))
     return fail(ZS_ERR_INVALID_ARG, "zs_mx_matmul: null pointer%s");
@@ -318,15 +347,10 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
     return fail(ZS_ERR_ALIAS, "zs_mx_matmul: the result overlaps the workspace%s");
   MatmulArgs a{a_codes, a_scales, b_codes, b_scales, c, ldc,
                (uint32_t)m, (uint32_t)n, (uint32_t)padded};
-  /* four results of a lane in one store */
-  const int vec = aligned(c, 4 * esize(c_dtype)) && ldc % 4 == 0;
-  const dim3 grid((unsigned)((n + 63) / 64), (unsigned)((m + 63) / 64));
-  if (grid.y > 65535) return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: too many rows%s");
   hipStream_t s = static_cast<hipStream_t>(stream);
   with_format(a_format, [&](auto f) {
     with_any(c_dtype, [&](auto dt) {
-      hipLaunchKernelGGL((matmul_kernel<decltype(f)::value, decltype(dt)::value>), grid,
-                         dim3(kBlock), 0, s, a, vec);
+      launch_matmul<decltype(f)::value, decltype(dt)::value>(a, s);
     });
   });
   return launch_result();
