@@ -356,29 +356,69 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
   return launch_result();
 }
 
+}  /* extern "C" */
+
 namespace {
 
-/* A row is split over several blocks where there are few rows. */
-constexpr uint32_t kDistillThreads = 256;
+/* ------------------------------------------------------------------------
+ * A row per block where its registers hold it (256 threads up to 4096
+ * vectors of 16 bytes, 1024 up to 16384) and there are rows enough; else in
+ * parts, so many that some 1024 blocks run.
+ * ---------------------------------------------------------------------- */
+constexpr int kDistillThreads = 256, kRowItems = 16;
+constexpr uint64_t kDistillFewRows = 64, kDistillShortVecs = 4096;
 
 struct DistillSplit {
-  uint32_t parts, part_vecs;
+  uint32_t parts;      /* 0: a row per block */
+  uint32_t part_vecs, vecs;
 };
 
 DistillSplit distill_split(uint64_t rows, uint64_t vocab, int dtype) {
   const uint64_t vecs = vocab * esize(dtype) / 16;
+  if (vecs <= 1024 * kRowItems && (rows >= kDistillFewRows || vecs <= kDistillShortVecs))
+    return {0, 0, (uint32_t)vecs};
   uint64_t parts = rows < 1024 ? 1024 / rows : 1;
   const uint64_t most = (vecs + kDistillThreads - 1) / kDistillThreads;
   if (parts > most) parts = most;
   if (parts < 1) parts = 1;
-  return {(uint32_t)parts, (uint32_t)((vecs + parts - 1) / parts)};
+  return {(uint32_t)parts, (uint32_t)((vecs + parts - 1) / parts), (uint32_t)vecs};
+}
+
+template <int DT, bool TAIL, int NT, int ITEMS>
+void launch_rows(const DistillArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL((distill_row_kernel<DT, TAIL, NT, ITEMS>), dim3((unsigned)a.rows), dim3(NT), 0,
+                     s, a);
+}
+
+template <int DT, bool TAIL>
+int launch_distill(const DistillArgs &a, const DistillSplit &sp, hipStream_t s) {
+  if (!sp.parts) {
+    if (sp.vecs <= 256) launch_rows<DT, TAIL, 256, 1>(a, s);
+    else if (sp.vecs <= 1024) launch_rows<DT, TAIL, 256, 4>(a, s);
+    else if (sp.vecs <= 2048) launch_rows<DT, TAIL, 256, 8>(a, s);
+    else if (sp.vecs <= 4096) launch_rows<DT, TAIL, 256, 16>(a, s);
+    else if (sp.vecs <= 8192) launch_rows<DT, TAIL, 1024, 8>(a, s);
+    else launch_rows<DT, TAIL, 1024, kRowItems>(a, s);
+    return launch_result();
+  }
+  constexpr int NT = kDistillThreads;
+  const uint32_t blocks = a.grad ? sp.parts : 1;
+  hipLaunchKernelGGL((distill_stats_kernel<DT, NT>), dim3((unsigned)(a.rows * sp.parts)), dim3(NT),
+                     0, s, a);
+  if (int rc = launch_result()) return rc;
+  hipLaunchKernelGGL((distill_grad_kernel<DT, TAIL, NT>), dim3((unsigned)(a.rows * blocks)),
+                     dim3(NT), 0, s, a, blocks);
+  return launch_result();
 }
 
 }  // namespace
 
+extern "C" {
+
 uint64_t zs_distill_workspace(uint64_t rows, uint64_t vocab, uint32_t slots, int dtype) {
   if (rows == 0 || !valid_any(dtype) || matrix_too_big(rows, vocab)) return 0;
-  return rows * (distill_split(rows, vocab, dtype).parts * sizeof(DistillPart) + slots * 4ull);
+  const DistillSplit sp = distill_split(rows, vocab, dtype);
+  return sp.parts ? rows * (sp.parts * sizeof(DistillPart) + slots * 4ull) : 0;
 }
 
 int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
@@ -403,7 +443,7 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   const uint64_t esz = esize(dtype);
   const DistillSplit sp = distill_split(rows, vocab, dtype);
   const uint64_t need = zs_distill_workspace(rows, vocab, slots, dtype);
-  if (!workspace || workspace_bytes < need)
+  if (need && (!workspace || workspace_bytes < need))
     return fail(ZS_ERR_INVALID_ARG, "zs_distill: workspace too small%s");
   if (!aligned(logits, esz) || (grad && !aligned(grad, esz)) || !aligned(workspace, 16) ||
       !aligned(dev, 8))
@@ -425,7 +465,8 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
       if (overlaps(outs[i], out_bytes[i], outs[j], out_bytes[j]))
         return fail(ZS_ERR_ALIAS, "zs_distill: two outputs overlap%s");
   }
-  if (rows * sp.parts > kMaxGrid) return fail(ZS_ERR_UNSUPPORTED, "zs_distill: too many rows%s");
+  if (rows > kMaxGrid || rows * sp.parts > kMaxGrid)
+    return fail(ZS_ERR_UNSUPPORTED, "zs_distill: too many rows%s");
   DistillArgs a{};
   a.z = logits;
   a.ids = ids;
@@ -450,20 +491,11 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   a.scale = loss_scale;
   a.vec_store = grad && (((uintptr_t)grad ^ (uintptr_t)logits) & 15) == 0 &&
                 (grad_ld - ld) * esz % 16 == 0;
-  const uint32_t blocks = grad ? sp.parts : 1;
   hipStream_t s = static_cast<hipStream_t>(stream);
   int rc = ZS_OK;
   with_any(dtype, [&](auto dt) {
     with_bool(teacher_lse != nullptr, [&](auto tail) {
-      constexpr int DT = decltype(dt)::value, NT = kDistillThreads;
-      constexpr bool TAIL = decltype(tail)::value;
-      hipLaunchKernelGGL((distill_stats_kernel<DT, TAIL, NT>), dim3((unsigned)(rows * sp.parts)),
-                         dim3(NT), 0, s, a);
-      rc = launch_result();
-      if (rc != ZS_OK) return;
-      hipLaunchKernelGGL((distill_grad_kernel<DT, TAIL, NT>), dim3((unsigned)(rows * blocks)),
-                         dim3(NT), 0, s, a, blocks);
-      rc = launch_result();
+      rc = launch_distill<decltype(dt)::value, decltype(tail)::value>(a, sp, s);
     });
   });
   return rc;

@@ -472,17 +472,41 @@ def zs_offload_step(grad_dev, grad_host, master, m, v, params_host, params_dev,
 
 # ---- operators of a low-precision model's output end --------------------------
 
-_FLOAT_CODES = {}
+class _Torch:
+    """torch's names that every call looks up, found once."""
+
+    def __init__(self):
+        import torch
+        self.u8, self.i32, self.f32 = torch.uint8, torch.int32, torch.float32
+        self.codes = {torch.bfloat16: ZS_BF16, torch.float16: ZS_FP16}
+        self.codes32 = {**self.codes, torch.float32: ZS_FP32}
+        try:    # the current stream's handle without an object around it
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            self.stream = lambda: raw(device())
+        except AttributeError:
+            self.stream = lambda: torch.cuda.current_stream().cuda_stream
+
+
+_names = None
+
+
+def _t():
+    global _names
+    if _names is None:
+        _names = _Torch()
+    return _names
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return _t().stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _float_code(t, what, fp32=False):
     """zs_dtype of a tensor's element type."""
-    if not _FLOAT_CODES:
-        torch = _torch()
-        _FLOAT_CODES.update({torch.bfloat16: ZS_BF16, torch.float16: ZS_FP16,
-                             torch.float32: ZS_FP32})
-    code = _FLOAT_CODES.get(t.dtype)
-    if code is None or (code == ZS_FP32 and not fp32):
+    code = (_t().codes32 if fp32 else _t().codes).get(t.dtype)
+    if code is None:
         raise TypeError(f"{what}: {'float32, ' if fp32 else ''}bfloat16 or float16 tensor "
                         f"expected, got {t.dtype}")
     return code
@@ -492,10 +516,12 @@ def _rows(x, what, shape=None):
     """(address, rows, cols, row stride) of a 2-D CUDA tensor with contiguous rows."""
     if not x.is_cuda:
         raise ValueError(f"{what}: CUDA tensor expected")
-    if x.dim() != 2 or (shape is not None and tuple(x.shape) != shape):
+    if x.dim() != 2 or (shape is not None and x.shape != shape):
         raise ValueError(f"{what}: {'2-D' if shape is None else shape} tensor expected, "
                          f"got {tuple(x.shape)}")
     r, c = x.shape
+    if x.is_contiguous():
+        return x.data_ptr(), r, c, c
     ld = x.stride(0) if r > 1 else c
     if (c > 1 and x.stride(1) != 1) or ld < c:
         raise ValueError(f"{what}: rows must be contiguous and must not overlap")
@@ -506,9 +532,9 @@ def _dense(x, shape, dtype, what):
     """Address of a contiguous CUDA tensor of that shape and type (None stays None)."""
     if x is None:
         return None
-    if not x.is_cuda or not x.is_contiguous() or tuple(x.shape) != shape or x.dtype != dtype:
-        raise ValueError(f"{what}: contiguous {dtype} CUDA tensor of shape {shape} expected, "
-                         f"got {x.dtype} {tuple(x.shape)}")
+    if x.shape != shape or x.dtype != dtype or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{what}: contiguous {dtype} CUDA tensor of shape {tuple(shape)} "
+                         f"expected, got {x.dtype} {tuple(x.shape)} on {x.device}")
     return x.data_ptr()
 
 
@@ -517,7 +543,7 @@ def _workspace(x):
         return None, 0
     if not x.is_cuda or not x.is_contiguous():
         raise ValueError("workspace: contiguous CUDA tensor expected")
-    return x.data_ptr(), x.numel() * x.element_size()
+    return x.data_ptr(), x.nbytes
 
 
 def mx_padded(k):
@@ -540,7 +566,7 @@ def mx_empty(rows, k, fmt, device="cuda"):
 
 def _mx_ptrs(codes, scales, rows, k, fmt, what):
     cs, ss = mx_shapes(rows, k, fmt)
-    u8 = _torch().uint8
+    u8 = _t().u8
     return (_dense(codes, cs, u8, f"{what} codes"), _dense(scales, ss, u8, f"{what} scales"))
 
 
@@ -555,7 +581,7 @@ def zs_mx_quantize(src, fmt, codes, scales, columns=False, values=None, stream=N
         vp = _dense(values, (r, c), values.dtype, "values")
     _check("zs_mx_quantize", _lib.zs_mx_quantize(
         p, _float_code(src, "src", fp32=True), r, c, ld, fmt, 1 if columns else 0, cp, sp, vp,
-        vdt, _stream(stream)))
+        vdt, _raw_stream(stream)))
 
 
 def zs_mx_matmul(a_codes, a_scales, a_format, b_codes, b_scales, out, k, workspace=None,
@@ -567,7 +593,7 @@ def zs_mx_matmul(a_codes, a_scales, a_format, b_codes, b_scales, out, k, workspa
     wp, wb = _workspace(workspace)
     _check("zs_mx_matmul", _lib.zs_mx_matmul(
         ac, asc, a_format, bc, bsc, m, n, k, p, _float_code(out, "out", fp32=True), ld, wp, wb,
-        _stream(stream)))
+        _raw_stream(stream)))
 
 
 def zs_rmsnorm_forward(x, gain, eps, h=None, rstd=None, residual=None, codes=None, scales=None,
@@ -576,7 +602,7 @@ def zs_rmsnorm_forward(x, gain, eps, h=None, rstd=None, residual=None, codes=Non
     (codes, scales) and / or a 16-bit y."""
     if x.dim() != 2:
         raise ValueError("x: 2-D tensor expected")
-    shape, dt = tuple(x.shape), x.dtype
+    shape, dt = x.shape, x.dtype
     cp = sp = None
     if codes is not None or scales is not None:
         if codes is None or scales is None:
@@ -585,8 +611,8 @@ def zs_rmsnorm_forward(x, gain, eps, h=None, rstd=None, residual=None, codes=Non
     _check("zs_rmsnorm_forward", _lib.zs_rmsnorm_forward(
         _dense(x, shape, dt, "x"), _dense(residual, shape, dt, "residual"),
         _dense(gain, shape[1:], dt, "gain"), _float_code(x, "x"), *shape, eps,
-        _dense(h, shape, dt, "h"), _dense(rstd, shape[:1], _torch().float32, "rstd"), cp, sp,
-        _dense(y, shape, dt, "y"), _stream(stream)))
+        _dense(h, shape, dt, "h"), _dense(rstd, shape[:1], _t().f32, "rstd"), cp, sp,
+        _dense(y, shape, dt, "y"), _raw_stream(stream)))
 
 
 def zs_rmsnorm_backward_workspace(rows, cols):
@@ -598,14 +624,14 @@ def zs_rmsnorm_backward(dy, h, rstd, gain, dx, dgain, workspace, dres=None, stre
     """Gradients of zs_rmsnorm_forward: dx (of x and of the residual alike) and the fp32 dgain."""
     if dy.dim() != 2:
         raise ValueError("dy: 2-D tensor expected")
-    shape, dt, f32 = tuple(dy.shape), dy.dtype, _torch().float32
+    shape, dt, f32 = dy.shape, dy.dtype, _t().f32
     wp, wb = _workspace(workspace)
     _check("zs_rmsnorm_backward", _lib.zs_rmsnorm_backward(
         _dense(dy, shape, dt, "dy"), _dense(h, shape, dt, "h"),
         _dense(rstd, shape[:1], f32, "rstd"), _dense(gain, shape[1:], dt, "gain"),
         _dense(dres, shape, dt, "dres"), _float_code(dy, "dy"), *shape,
         _dense(dx, shape, dt, "dx"), _dense(dgain, shape[1:], f32, "dgain"), wp, wb,
-        _stream(stream)))
+        _raw_stream(stream)))
 
 
 def zs_distill_workspace(rows, vocab, slots, dtype):
@@ -619,8 +645,8 @@ def zs_distill(logits, ids, teacher, temperature, loss, grad=None, teacher_lse=N
     gradient times the loss scale (loss_scale, or dev_scaler's: the buffer of
     device_scaler_upload). grad may be logits itself."""
     p, rows, vocab, ld = _rows(logits, "logits")
-    torch = _torch()
-    f32 = torch.float32
+    names = _t()
+    f32 = names.f32
     slots = ids.shape[1] if ids.dim() == 2 else -1
     gp, gld = None, 0
     if grad is not None:
@@ -630,9 +656,9 @@ def zs_distill(logits, ids, teacher, temperature, loss, grad=None, teacher_lse=N
     wp, wb = _workspace(workspace)
     _check("zs_distill", _lib.zs_distill(
         p, _float_code(logits, "logits", fp32=True), rows, vocab, ld,
-        _dense(ids, (rows, slots), torch.int32, "ids"),
+        _dense(ids, (rows, slots), names.i32, "ids"),
         _dense(teacher, (rows, slots), logits.dtype, "teacher"), slots, temperature,
         _dense(teacher_lse, (rows,), f32, "teacher_lse"),
         _dense(row_weight, (rows,), f32, "row_weight"), loss_scale,
         None if dev_scaler is None else _dev_scaler_ptr(dev_scaler),
-        _dense(loss, (rows,), f32, "loss"), gp, gld, wp, wb, _stream(stream)))
+        _dense(loss, (rows,), f32, "loss"), gp, gld, wp, wb, _raw_stream(stream)))
