@@ -608,7 +608,7 @@ int zs_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const 
  *   loss   : fp32[rows]. grad: NULL (loss only), or dtype[rows][vocab], rows
  *            `grad_ld` apart; may be the logits' own buffer.
  *   workspace: zs_distill_workspace(rows, vocab, slots, dtype) bytes,
- *            16-byte aligned; NULL if that is 0.
+ *            16-byte aligned.
  * Logits of -inf are tokens that cannot be chosen (q = 0); a NaN, +inf or a
  * row of -inf gives a NaN row.
  * Errors: ZS_ERR_INVALID_ARG (null pointers, dtype, temperature or

@@ -45,7 +45,7 @@ struct DistillArgs {
   float *loss;
   void *grad;                      /* optional */
   DistillPart *ws;                 /* rows in parts: [rows][parts] */
-  float *ws_z;                     /* and their slots' logits: [rows][slots] */
+  float *ws_z;                     /* their slots' logits, [rows][slots], or NULL */
   uint64_t rows, ld, gld;
   uint32_t vocab, slots, parts, part_vecs;
   float tau, inv_tau, log2_scale, scale;   /* log2_scale = log2(e) / tau */
@@ -58,6 +58,27 @@ template <int DT>
 __device__ __forceinline__ float load1(const void *p, uint64_t i) {
   if constexpr (DT == ZS_FP32) return static_cast<const float *>(p)[i];
   else return up_lo<DT>(static_cast<const uint16_t *>(p)[i]);
+}
+
+/* An element as it lies in memory, and its value: apart, so that nothing
+ * waits for the element before its value is used. */
+template <int DT>
+__device__ __forceinline__ uint32_t load_raw(const void *p, uint64_t i) {
+  if constexpr (DT == ZS_FP32) return static_cast<const uint32_t *>(p)[i];
+  else return static_cast<const uint16_t *>(p)[i];
+}
+
+template <int DT>
+__device__ __forceinline__ float raw_value(uint32_t w) {
+  if constexpr (DT == ZS_FP32) return __uint_as_float(w);
+  else return up_lo<DT>(w);
+}
+
+/* A value that nothing writes while the kernel runs, by the scalar unit:
+ * vector loads return in order, and this one must not wait for a row. */
+__device__ __forceinline__ float load_scalar(const float *p, uint32_t i) {
+  return reinterpret_cast<const __attribute__((address_space(4))) float *>(
+      reinterpret_cast<uintptr_t>(p))[i];
 }
 
 template <int DT>
@@ -137,11 +158,30 @@ struct SumOf {
   __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
 };
 
+/* A value of another lane of the same 16, by the lane pattern CTRL. */
+template <int CTRL>
+__device__ __forceinline__ float lane_move(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double lane_move(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf,
+                                                         true);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+/* Within groups of `width` lanes: neighbours, pairs, then the mirrored half
+ * of 8 and of 16 lanes (equal within each half by then), then across. */
 template <class T, class Op>
 __device__ __forceinline__ T wave_reduce(T v, Op op, int width) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1)
-    if (m < width) v = op(v, __shfl_xor(v, m, 64));
+  v = op(v, lane_move<0xB1>(v));
+  v = op(v, lane_move<0x4E>(v));
+  if (width > 4) v = op(v, lane_move<0x141>(v));
+  if (width > 8) v = op(v, lane_move<0x140>(v));
+  if (width > 16) v = op(v, __shfl_xor(v, 16, 64));
+  if (width > 32) v = op(v, __shfl_xor(v, 32, 64));
   return v;
 }
 
@@ -154,6 +194,8 @@ __device__ __forceinline__ void reduce_put(T v, Op op, T *part) {
 
 template <int NT, class T, class Op>
 __device__ __forceinline__ T reduce_get(Op op, const T *part) {
+  if constexpr (NT == 64) return part[0];
+  if constexpr (NT == 128) return op(part[0], part[1]);
   return wave_reduce(part[threadIdx.x & (NT / 64 - 1)], op, NT / 64);
 }
 
@@ -185,24 +227,76 @@ __device__ __forceinline__ float term(float z, const Shift &s) {
  * The slots of one row, by a whole block of NT threads: the teacher's
  * probabilities and what the loss sums over them.
  * ---------------------------------------------------------------------- */
+struct SlotLds {           /* as many slots as the call has, to a multiple of four */
+  int32_t *id;
+  float *w, *z;
+};
+
+/* Bytes of LDS for the slots of a row; the launch asks for them. */
+__host__ __device__ inline uint32_t slot_bytes(uint32_t slots) { return (slots + 3) / 4 * 4 * 12; }
+
+__device__ __forceinline__ SlotLds slot_lds(uint32_t slots) {
+  extern __shared__ __align__(16) char lds[];
+  const uint32_t n = (slots + 3) / 4 * 4;
+  SlotLds s;
+  s.id = reinterpret_cast<int32_t *>(lds);
+  s.w = reinterpret_cast<float *>(lds + n * 4);
+  s.z = reinterpret_cast<float *>(lds + n * 8);
+  return s;
+}
+
+/* The slots that round their number up: empty. */
+__device__ __forceinline__ void pad_slots(uint32_t slots, const SlotLds &s) {
+  const uint32_t k = slots + threadIdx.x;
+  if (k < (slots + 3) / 4 * 4) {
+    s.id[k] = -1;
+    s.w[k] = 0.0f;
+  }
+}
+
+/* What the reductions over a block pass between its waves. */
 template <int NT>
-struct SlotLds {
-  int32_t id[kMaxSlots];
-  float w[kMaxSlots], z[kMaxSlots];
+struct ReduceLds {
   float part[5][NT / 64];
   double dpart[2][NT / 64];
 };
 
-/* Ids and the teacher's logits over the temperature; returns their maximum
+/* Sum of the weights of token id's slots. */
+__device__ __forceinline__ float slot_weight(const SlotLds &s, uint32_t slots, int32_t id) {
+  float w = 0.0f;
+  for (uint32_t j = 0; j < slots; j += 4) {
+    const int4 o = *reinterpret_cast<const int4 *>(s.id + j);
+    const float4 v = *reinterpret_cast<const float4 *>(s.w + j);
+    w += o.x == id ? v.x : 0.0f;
+    w += o.y == id ? v.y : 0.0f;
+    w += o.z == id ? v.z : 0.0f;
+    w += o.w == id ? v.w : 0.0f;
+  }
+  return w;
+}
+
+/* Whether an earlier slot holds slot k's token. */
+__device__ __forceinline__ bool slot_seen(const SlotLds &s, uint32_t k, int32_t id) {
+  bool seen = false;
+  for (uint32_t j = 0; j < k; j += 4) {
+    const int4 o = *reinterpret_cast<const int4 *>(s.id + j);
+    seen |= o.x == id || (j + 1 < k && o.y == id) || (j + 2 < k && o.z == id) ||
+            (j + 3 < k && o.w == id);
+  }
+  return seen;
+}
+
+/* From slot `first` on: ids and the teacher's logits over the temperature; returns their maximum
  * (+inf for a NaN) and whether a slot is filled. */
 struct SlotTop {
   float top, any;
 };
 
 template <int DT, int NT>
-__device__ __forceinline__ SlotTop slot_ids(const DistillArgs &a, uint64_t row, SlotLds<NT> &s) {
+__device__ __forceinline__ SlotTop slot_ids(const DistillArgs &a, uint64_t row, uint32_t first,
+                                            const SlotLds &s) {
   SlotTop r{-INFINITY, 0.0f};
-  for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
+  for (uint32_t k = first + threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = a.ids[row * a.slots + k];
     const bool ok = id >= 0 && (uint32_t)id < a.vocab;
     const float t = ok ? load1<DT>(a.teacher, row * a.slots + k) * a.inv_tau : -INFINITY;
@@ -218,8 +312,8 @@ __device__ __forceinline__ SlotTop slot_ids(const DistillArgs &a, uint64_t row, 
  * written over the logits, and another block may have begun to). */
 template <int DT, int NT>
 __device__ __forceinline__ void slot_logits(const DistillArgs &a, uint64_t row, const void *z,
-                                            const float *saved, SlotLds<NT> &s) {
-  for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
+                                            const float *saved, uint32_t first, const SlotLds &s) {
+  for (uint32_t k = first + threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = s.id[k];
     s.z[k] = id < 0 ? 0.0f : saved ? saved[row * a.slots + k] : load1<DT>(z, id);
   }
@@ -236,7 +330,7 @@ struct SlotSums {
  * with the very bits that it has in the row's sum. */
 template <bool TAIL, int NT, class F>
 __device__ __forceinline__ SlotSums slot_weights(const DistillArgs &a, float ref, const Shift &sh,
-                                                 SlotLds<NT> &s, F term_of) {
+                                                 const SlotLds &s, F term_of) {
   SlotSums r{0.0f, 0.0f, 0.0};
   for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = s.id[k];
@@ -247,9 +341,7 @@ __device__ __forceinline__ SlotSums slot_weights(const DistillArgs &a, float ref
       r.mass += w;
       if (!(w == 0.0f)) r.cross += w * ((t - ref) - (zk - sh.max) * a.inv_tau);
       if constexpr (TAIL) {
-        bool seen = false;
-        for (uint32_t j = 0; j < k; ++j) seen |= s.id[j] == id;
-        if (!seen) r.terms += term_of((uint32_t)id, zk);
+        if (!slot_seen(s, k, id)) r.terms += term_of((uint32_t)id, zk);
       }
     }
     s.w[k] = w;
@@ -291,14 +383,13 @@ __device__ __forceinline__ RowResult row_result(const SlotSums &s, const Shift &
 /* The slots' gradients, after the sweep over the row (and a barrier): this
  * block's share [first, last) of the vocabulary. */
 template <int DT, bool TAIL, int NT>
-__device__ __forceinline__ void store_slots(const DistillArgs &a, void *g, const SlotLds<NT> &s,
+__device__ __forceinline__ void store_slots(const DistillArgs &a, void *g, const SlotLds &s,
                                             const Shift &sh, float total, float mass, float coef,
                                             uint32_t first, uint32_t last) {
   for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = s.id[k];
     if (id < 0 || (uint32_t)id < first || (uint32_t)id >= last) continue;
-    float w = 0.0f;
-    for (uint32_t j = 0; j < a.slots; ++j) w += s.id[j] == id ? s.w[j] : 0.0f;
+    const float w = slot_weight(s, a.slots, id);
     const float p = TAIL ? w : w / mass;
     store1<DT>(g, id, (term(s.z[k], sh) / total - p) * coef);
   }
@@ -326,28 +417,6 @@ __device__ __forceinline__ RowFactors finish_row(const DistillArgs &a, uint64_t 
   return f;
 }
 
-/* A vector of terms times the factor, or zeros. */
-template <int DT>
-__device__ __forceinline__ void store_grad(const DistillArgs &a, char *g, uint32_t head, uint32_t v,
-                                           const float (&x)[kVecElems<DT>]) {
-  constexpr uint32_t ve = kVecElems<DT>;
-  constexpr uint32_t esz = DT == ZS_FP32 ? 4 : 2;
-  if (a.vec_store) {
-    *reinterpret_cast<u32x4 *>(g + (head + (uint64_t)v * ve) * esz) = pack_vec<DT>(x);
-  } else {
-#pragma unroll
-    for (uint32_t j = 0; j < ve; ++j) store1<DT>(g, head + (uint64_t)v * ve + j, x[j]);
-  }
-}
-
-/* Keeps the compiler from carrying unpacked values from one sweep over the
- * registers to the next, which would take twice the registers. */
-template <int ITEMS>
-__device__ __forceinline__ void unpack_again(u32x4 (&x)[ITEMS]) {
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) asm volatile("" : "+v"(x[i]));
-}
-
 /* A thread's sum of terms: binary64 where slots' terms are taken out of it. */
 template <bool TAIL>
 struct Sum { typedef float type; };
@@ -365,94 +434,239 @@ __device__ __forceinline__ u32x4 empty_vec() {   /* -inf */
   return u32x4{w, w, w, w};
 }
 
-template <int DT, bool TAIL, int NT, int ITEMS>
-__global__ __launch_bounds__(NT) void distill_row_kernel(DistillArgs a) {
-  constexpr uint32_t ve = kVecElems<DT>, esz = DT == ZS_FP32 ? 4 : 2;
-  __shared__ SlotLds<NT> lds;
-  const uint64_t row = blockIdx.x;
-  const uint32_t t = threadIdx.x;
-  const char *z = static_cast<const char *>(a.z) + row * a.ld * esz;
-  char *g = a.grad ? static_cast<char *>(a.grad) + row * a.gld * esz : nullptr;
-  const float weight = a.weight ? a.weight[row] : 1.0f;
-  const RowShape sh = row_shape<DT>(z, a.vocab);
-  const uint32_t edge = edge_index<DT>(sh, t, true, true, a.vocab);
-  u32x4 x[ITEMS];
-  float single = -INFINITY;
-  RowFactors f{1.0f, 0.0f, 0.0f, false};
-  SlotSums sums{};
-  Shift shift{};
-  if (weight != 0.0f) {   /* uniform over the block */
-    const SlotTop top = slot_ids<DT, NT>(a, row, lds);
-    const u32x4 *zv = reinterpret_cast<const u32x4 *>(z + sh.head * esz);
+/* A buffer that hardware checks the bounds of: reads past `bytes` give 0 and
+ * writes there are dropped, without a branch in the code. Only the vector
+ * offset is checked, so all of an offset goes there. The description is that
+ * of plain 32-bit data. */
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const void *p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
+}
+
+constexpr int kNonTemporal = 2;
+
+/* What a block knows of a row before it holds it. A row without weight is
+ * not read: its buffer is empty. */
+struct RowIn {
+  const char *z;
+  RowShape shape;
+  uint32_t edge;
+  float weight, lse;
+};
+
+template <int DT, bool TAIL>
+__device__ __forceinline__ RowIn open_row(const DistillArgs &a, uint32_t row) {
+  constexpr uint64_t esz = DT == ZS_FP32 ? 4 : 2;
+  RowIn r;
+  r.z = static_cast<const char *>(a.z) + (uint64_t)row * a.ld * esz;
+  r.shape = row_shape<DT>(r.z, a.vocab);
+  r.weight = a.weight ? load_scalar(a.weight, row) : 1.0f;
+  r.lse = TAIL ? load_scalar(a.lse, row) : 0.0f;
+  r.edge = r.weight != 0.0f ? edge_index<DT>(r.shape, threadIdx.x, true, true, a.vocab) : a.vocab;
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const RowIn &r) {
+  return bounded(r.z + r.shape.head * (DT == ZS_FP32 ? 4 : 2),
+                 r.weight != 0.0f ? r.shape.vecs * 16 : 0);
+}
+
+/* The vector at byte `at`, or the row's last for a thread past it: one that
+ * the maximum may count twice and the sum leaves out. */
+template <int DT>
+__device__ __forceinline__ u32x4 fetch_vec(__amdgpu_buffer_rsrc_t row, const RowIn &r, uint32_t at) {
+  const uint32_t last = (r.shape.vecs - 1) * 16, mine = at + threadIdx.x * 16;
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                       row, (int)(mine < last ? mine : last), 0, 0));
+}
+
+/* Running maximum of whole vectors. Written in instructions for two reasons:
+ * the compiler would quiet every operand first, and it would carry the
+ * values unpacked here to the sums, at twice the registers. What a NaN does
+ * to the row, its sum does anyway. */
+template <int DT>
+struct VecMax {
+  uint32_t m = DT == ZS_FP16 ? 0xfc00fc00u : 0xff800000u;   /* -inf, two of them in fp16 */
+
+  __device__ __forceinline__ void add(const u32x4 &x) {
+    if constexpr (DT == ZS_FP16) {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const uint32_t v = i * NT + t;
-      x[i] = v < sh.vecs ? __builtin_nontemporal_load(zv + v) : empty_vec<DT>();
+      for (int j = 0; j < 4; ++j) asm("v_pk_max_f16 %0, %0, %1" : "+v"(m) : "v"(x[j]));
+    } else if constexpr (DT == ZS_FP32) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2)
+        asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[j]), "v"(x[j + 1]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t lo, hi;
+        asm("v_lshlrev_b32 %0, 16, %1" : "=v"(lo) : "v"(x[j]));
+        asm("v_and_b32 %0, 0xffff0000, %1" : "=v"(hi) : "v"(x[j]));
+        asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(lo), "v"(hi));
+      }
     }
-    if (edge < a.vocab) single = load1<DT>(z, edge);
-    slot_logits<DT, NT>(a, row, z, nullptr, lds);
-    float max = single;
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      float e[ve];
-      unpack_vec<DT>(x[i], e);
-#pragma unroll
-      for (uint32_t j = 0; j < ve; j += 2) max = fmaxf(max, fmaxf(e[j], e[j + 1]));
-    }
-    unpack_again(x);
-    reduce_put(max, MaxOf{}, lds.part[0]);
-    reduce_put(top.top, MaxOf{}, lds.part[1]);
-    reduce_put(top.any, MaxOf{}, lds.part[2]);
-    __syncthreads();
-    shift = shift_of(reduce_get<NT>(MaxOf{}, lds.part[0]), a.log2_scale);
-    const float highest = reduce_get<NT>(MaxOf{}, lds.part[1]);
-    const float ref = TAIL ? a.lse[row] : highest;
-    const bool live = TAIL ? reduce_get<NT>(MaxOf{}, lds.part[2]) > 0.0f : highest > -INFINITY;
-    typename Sum<TAIL>::type sum = edge < a.vocab ? term(single, shift) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      float e[ve];
-      unpack_vec<DT>(x[i], e);
-#pragma unroll
-      for (uint32_t j = 0; j < ve; ++j) sum += term(e[j], shift);
-    }
-    unpack_again(x);
-    sums = slot_weights<TAIL, NT>(a, ref, shift, lds, [&](uint32_t, float zk) {
-      return (double)term(zk, shift);
-    });
-    reduce_put(sums.mass, SumOf{}, lds.part[3]);
-    reduce_put(sums.cross, SumOf{}, lds.part[4]);
-    reduce_put((double)sum, SumOf{}, lds.dpart[0]);
-    if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, lds.dpart[1]);
-    __syncthreads();
-    sums.mass = reduce_get<NT>(SumOf{}, lds.part[3]);
-    sums.cross = reduce_get<NT>(SumOf{}, lds.part[4]);
-    if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, lds.dpart[1]);
-    f = finish_row<TAIL>(a, row, weight, live, sums, shift, reduce_get<NT>(SumOf{}, lds.dpart[0]),
-                         t == 0);
-  } else if (t == 0) {
-    a.loss[row] = 0.0f;
   }
-  if (!g) return;
-  if (edge < a.vocab) store1<DT>(g, edge, f.live ? term(single, shift) * f.factor : 0.0f);
+
+  __device__ __forceinline__ float get() const {
+    if constexpr (DT == ZS_FP16) return fmaxf(up_lo<DT>(m), up_hi<DT>(m));
+    else return __uint_as_float(m);
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t fetch_edge(const DistillArgs &a, const RowIn &r) {
+  uint32_t w = empty_vec<DT>()[0];
+  if (r.edge < a.vocab) w = load_raw<DT>(r.z, r.edge);
+  return w;
+}
+
+/* Holds the first NT slots of a row in a register each, fetched ahead, as
+ * they lie in memory. */
+struct SlotAhead {
+  int32_t id;
+  uint32_t t, z;
+};
+
+/* A block walks rows blockIdx, + gridDim, ... While it writes a row's
+ * gradient it fetches the next row into the registers that fall free. Loads
+ * return in order, so what is wanted early is asked for early: the next row's
+ * slots before its vectors, their logits after. */
+template <int DT, bool TAIL, int NT, int ITEMS>
+__global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(DistillArgs a) {
+  constexpr uint32_t ve = kVecElems<DT>, esz = DT == ZS_FP32 ? 4 : 2;
+  __shared__ ReduceLds<NT> red;
+  const SlotLds lds = slot_lds(a.slots);
+  pad_slots(a.slots, lds);
+  const uint32_t t = threadIdx.x;
+  uint32_t row = blockIdx.x;
+  RowIn in = open_row<DT, TAIL>(a, row);
+  auto slots_ahead = [&](uint32_t r, const RowIn &q, SlotAhead &s) {
+    s.id = -1;
+    s.t = 0;
+    if (t < a.slots && q.weight != 0.0f) {
+      s.id = a.ids[(uint64_t)r * a.slots + t];
+      s.t = load_raw<DT>(a.teacher, (uint64_t)r * a.slots + t);
+    }
+  };
+  auto logits_ahead = [&](const RowIn &q, SlotAhead &s) {
+    s.z = 0;
+    if ((uint32_t)s.id < a.vocab) s.z = load_raw<DT>(q.z, s.id);
+  };
+  SlotAhead slot;
+  slots_ahead(row, in, slot);
+  u32x4 x[ITEMS];
+  {
+    const __amdgpu_buffer_rsrc_t buf = row_buffer<DT>(in);
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const uint32_t v = i * NT + t;
-    if (v >= sh.vecs) break;
-    float e[ve];
-    if (f.live) {
+    for (int i = 0; i < ITEMS; ++i) x[i] = fetch_vec<DT>(buf, in, i * (NT * 16));
+  }
+  uint32_t raw_single = fetch_edge<DT>(a, in);
+  logits_ahead(in, slot);
+  for (;;) {
+    /* rows are told apart by a scalar that the compiler cannot follow: it would
+     * keep a pointer of its own in vector registers for every use */
+    asm volatile("" : "+s"(row));
+    const uint32_t next = row + gridDim.x;
+    const RowIn after = open_row<DT, TAIL>(a, next < a.rows ? next : row);
+    RowFactors f{1.0f, 0.0f, 0.0f, false};
+    SlotSums sums{};
+    Shift shift{};
+    float single = -INFINITY;
+    if (in.weight != 0.0f) {   /* uniform over the block */
+      VecMax<DT> max;
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) max.add(x[i]);
+      single = raw_value<DT>(raw_single);
+      SlotTop top{-INFINITY, 0.0f};
+      if (t < a.slots) {
+        const bool ok = (uint32_t)slot.id < a.vocab;
+        const float v = ok ? raw_value<DT>(slot.t) * a.inv_tau : -INFINITY;
+        lds.id[t] = ok ? slot.id : -1;
+        lds.w[t] = v;
+        lds.z[t] = raw_value<DT>(slot.z);
+        if (ok) top = {v != v ? INFINITY : v, 1.0f};
+      }
+      if (a.slots > NT) {   /* the others */
+        const SlotTop more = slot_ids<DT, NT>(a, row, NT, lds);
+        slot_logits<DT, NT>(a, row, in.z, nullptr, NT, lds);
+        top = {fmaxf(top.top, more.top), fmaxf(top.any, more.any)};
+      }
+      reduce_put(fmaxf(max.get(), single), MaxOf{}, red.part[0]);
+      reduce_put(top.top, MaxOf{}, red.part[1]);
+      reduce_put(top.any, MaxOf{}, red.part[2]);
+      __syncthreads();
+      shift = shift_of(reduce_get<NT>(MaxOf{}, red.part[0]), a.log2_scale);
+      const float highest = reduce_get<NT>(MaxOf{}, red.part[1]);
+      const float ref = TAIL ? in.lse : highest;
+      const bool live = TAIL ? reduce_get<NT>(MaxOf{}, red.part[2]) > 0.0f : highest > -INFINITY;
+      typename Sum<TAIL>::type sum = in.edge < a.vocab ? term(single, shift) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        float e[ve];
+        unpack_vec<DT>(x[i], e);
+        typename Sum<TAIL>::type some = 0;
+#pragma unroll
+        for (uint32_t j = 0; j < ve; ++j) some += term(e[j], shift);
+        sum += (int)t < (int)in.shape.vecs - i * NT ? some : 0;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      sums = slot_weights<TAIL, NT>(a, ref, shift, lds, [&](uint32_t, float zk) {
+        return (double)term(zk, shift);
+      });
+      reduce_put(sums.mass, SumOf{}, red.part[3]);
+      reduce_put(sums.cross, SumOf{}, red.part[4]);
+      reduce_put((double)sum, SumOf{}, red.dpart[0]);
+      if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.dpart[1]);
+      __syncthreads();
+      sums.mass = reduce_get<NT>(SumOf{}, red.part[3]);
+      sums.cross = reduce_get<NT>(SumOf{}, red.part[4]);
+      if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, red.dpart[1]);
+      f = finish_row<TAIL>(a, row, in.weight, live, sums, shift,
+                           reduce_get<NT>(SumOf{}, red.dpart[0]), t == 0);
+    } else if (t == 0) {
+      a.loss[row] = 0.0f;
+    }
+    if (!f.live) {   /* zeros: terms of -inf */
+      shift.c = 1.0f;
+      shift.whole = f.factor = 0.0f;
+      single = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) x[i] = empty_vec<DT>();
+    }
+    char *g = static_cast<char *>(a.grad) + (uint64_t)row * a.gld * esz;
+    const bool more = next < a.rows;
+    const __amdgpu_buffer_rsrc_t to = bounded(g + in.shape.head * esz, in.shape.vecs * 16);
+    const __amdgpu_buffer_rsrc_t from = row_buffer<DT>(after);
+    if (more) slots_ahead(next, after, slot);
+    const uint32_t edge = edge_index<DT>(in.shape, t, true, true, a.vocab);
+    if (a.grad && edge < a.vocab) store1<DT>(g, edge, term(single, shift) * f.factor);
+    if (more) raw_single = fetch_edge<DT>(a, after);
+    if (!a.grad) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) x[i] = fetch_vec<DT>(from, after, i * (NT * 16));
+    } else {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      float e[ve];
+      asm volatile("" : "+v"(x[i]));   /* unpacked anew, not kept since the sum */
       unpack_vec<DT>(x[i], e);
 #pragma unroll
       for (uint32_t j = 0; j < ve; ++j) e[j] = term(e[j], shift) * f.factor;
-    } else {
-#pragma unroll
-      for (uint32_t j = 0; j < ve; ++j) e[j] = 0.0f;
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, pack_vec<DT>(e)), to,
+                                             (int)(t * 16 + i * (NT * 16)), 0, kNonTemporal);
+      x[i] = fetch_vec<DT>(from, after, i * (NT * 16));   /* past the last row: not used */
+      __builtin_amdgcn_sched_barrier(0);
     }
-    store_grad<DT>(a, g, sh.head, v, e);
+    }
+    if (more) logits_ahead(after, slot);
+    __syncthreads();
+    if (a.grad && f.live)
+      store_slots<DT, TAIL, NT>(a, g, lds, shift, f.total, sums.mass, f.coef, 0, a.vocab);
+    if (!more) return;
+    __syncthreads();   /* the slots in LDS are done with */
+    row = next;
+    in = after;
   }
-  __syncthreads();
-  if (f.live)
-    store_slots<DT, TAIL, NT>(a, g, lds, shift, f.total, sums.mass, f.coef, 0, a.vocab);
 }
 
 /* ------------------------------------------------------------------------
@@ -497,7 +711,7 @@ __global__ __launch_bounds__(NT) void distill_stats_kernel(DistillArgs a) {
   __syncthreads();
   sum = reduce_get<NT>(SumOf{}, dpart);
   if (threadIdx.x == 0) a.ws[blockIdx.x] = {sum, max, 0.0f};
-  if (part != 0) return;
+  if (part != 0 || !a.ws_z) return;
   for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = a.ids[row * a.slots + k];
     if (id >= 0 && (uint32_t)id < a.vocab) a.ws_z[row * a.slots + k] = load1<DT>(z, id);
@@ -517,7 +731,9 @@ __device__ __forceinline__ double part_factor(float max, const Shift &row, float
 template <int DT, bool TAIL, int NT>
 __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_t blocks) {
   constexpr uint32_t ve = kVecElems<DT>;
-  __shared__ SlotLds<NT> lds;
+  __shared__ ReduceLds<NT> red;
+  const SlotLds lds = slot_lds(a.slots);
+  pad_slots(a.slots, lds);
   const uint64_t row = blockIdx.x / blocks;   /* blocks: parts, or 1 without a gradient */
   const uint32_t part = blockIdx.x % blocks;
   constexpr uint64_t esz = DT == ZS_FP32 ? 4 : 2;
@@ -540,27 +756,27 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
     double sum = 0.0;
     for (uint32_t i = 0; i < a.parts; ++i)
       sum += w[i].sum * part_factor(w[i].max, shift, a.log2_scale);
-    const SlotTop top = slot_ids<DT, NT>(a, row, lds);
-    slot_logits<DT, NT>(a, row, z, a.ws_z, lds);
-    reduce_put(top.top, MaxOf{}, lds.part[1]);
-    reduce_put(top.any, MaxOf{}, lds.part[2]);
+    const SlotTop top = slot_ids<DT, NT>(a, row, 0, lds);
+    slot_logits<DT, NT>(a, row, z, a.ws_z, 0, lds);
+    reduce_put(top.top, MaxOf{}, red.part[1]);
+    reduce_put(top.any, MaxOf{}, red.part[2]);
     __syncthreads();
-    const float highest = reduce_get<NT>(MaxOf{}, lds.part[1]);
+    const float highest = reduce_get<NT>(MaxOf{}, red.part[1]);
     const float ref = TAIL ? a.lse[row] : highest;
-    const bool live = TAIL ? reduce_get<NT>(MaxOf{}, lds.part[2]) > 0.0f : highest > -INFINITY;
+    const bool live = TAIL ? reduce_get<NT>(MaxOf{}, red.part[2]) > 0.0f : highest > -INFINITY;
     sums = slot_weights<TAIL, NT>(a, ref, shift, lds, [&](uint32_t id, float zk) {
       uint32_t i = id < sh.head ? 0 : (id - sh.head) / ve / a.part_vecs;
       i = i < a.parts ? i : a.parts - 1;
       return (double)term(zk, shift_of(w[i].max, a.log2_scale)) *
              part_factor(w[i].max, shift, a.log2_scale);
     });
-    reduce_put(sums.mass, SumOf{}, lds.part[3]);
-    reduce_put(sums.cross, SumOf{}, lds.part[4]);
-    if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, lds.dpart[1]);
+    reduce_put(sums.mass, SumOf{}, red.part[3]);
+    reduce_put(sums.cross, SumOf{}, red.part[4]);
+    if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.dpart[1]);
     __syncthreads();
-    sums.mass = reduce_get<NT>(SumOf{}, lds.part[3]);
-    sums.cross = reduce_get<NT>(SumOf{}, lds.part[4]);
-    if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, lds.dpart[1]);
+    sums.mass = reduce_get<NT>(SumOf{}, red.part[3]);
+    sums.cross = reduce_get<NT>(SumOf{}, red.part[4]);
+    if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, red.dpart[1]);
     f = finish_row<TAIL>(a, row, weight, live, sums, shift, sum, first && threadIdx.x == 0);
   } else if (first && threadIdx.x == 0) {
     a.loss[row] = 0.0f;
@@ -579,7 +795,12 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
 #pragma unroll
       for (uint32_t j = 0; j < ve; ++j) x[j] = 0.0f;
     }
-    store_grad<DT>(a, g, sh.head, v, x);
+    if (a.vec_store) {
+      *reinterpret_cast<u32x4 *>(g + sh.head * esz + v * 16ull) = pack_vec<DT>(x);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < ve; ++j) store1<DT>(g, sh.head + (uint64_t)v * ve + j, x[j]);
+    }
   }
   __syncthreads();
   if (f.live)

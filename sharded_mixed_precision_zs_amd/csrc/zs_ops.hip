@@ -362,10 +362,12 @@ namespace {
 
 /* ------------------------------------------------------------------------
  * A row per block where its registers hold it (256 threads up to 4096
- * vectors of 16 bytes, 1024 up to 16384) and there are rows enough; else in
- * parts, so many that some 1024 blocks run.
+ * vectors of 16 bytes, 512 up to 16384; one at least, whatever its
+ * alignment) and there are rows enough; else in
+ * parts, so many that some 1024 blocks run. Gradient rows that are not
+ * aligned as the logits' go in parts too (one).
  * ---------------------------------------------------------------------- */
-constexpr int kDistillThreads = 256, kRowItems = 16;
+constexpr int kDistillThreads = 256, kRowItems = 32;
 constexpr uint64_t kDistillFewRows = 64, kDistillShortVecs = 4096;
 
 struct DistillSplit {
@@ -375,7 +377,7 @@ struct DistillSplit {
 
 DistillSplit distill_split(uint64_t rows, uint64_t vocab, int dtype) {
   const uint64_t vecs = vocab * esize(dtype) / 16;
-  if (vecs <= 1024 * kRowItems && (rows >= kDistillFewRows || vecs <= kDistillShortVecs))
+  if (vecs >= 2 && vecs <= 512 * kRowItems && (rows >= kDistillFewRows || vecs <= kDistillShortVecs))
     return {0, 0, (uint32_t)vecs};
   uint64_t parts = rows < 1024 ? 1024 / rows : 1;
   const uint64_t most = (vecs + kDistillThreads - 1) / kDistillThreads;
@@ -384,21 +386,40 @@ DistillSplit distill_split(uint64_t rows, uint64_t vocab, int dtype) {
   return {(uint32_t)parts, (uint32_t)((vecs + parts - 1) / parts), (uint32_t)vecs};
 }
 
+/* CUs of the current device (256 if unknown). */
+int cu_count() {
+  static thread_local int cached_dev = -1, cached = 256;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 256;
+  if (dev != cached_dev) {
+    int n = 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) n = 0;
+    cached = n > 0 ? n : 256;
+    cached_dev = dev;
+  }
+  return cached;
+}
+
+/* Blocks that walk the rows: as many as fit at the registers the kernel is
+ * held to (four waves per SIMD up to 16 vectors a thread, two beyond). */
 template <int DT, bool TAIL, int NT, int ITEMS>
 void launch_rows(const DistillArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL((distill_row_kernel<DT, TAIL, NT, ITEMS>), dim3((unsigned)a.rows), dim3(NT), 0,
+  const uint64_t fit = (uint64_t)cu_count() * (ITEMS <= 16 ? 16 : 8) / (NT / 64);
+  hipLaunchKernelGGL((distill_row_kernel<DT, TAIL, NT, ITEMS>),
+                     dim3((unsigned)(a.rows < fit ? a.rows : fit)), dim3(NT), slot_bytes(a.slots),
                      s, a);
 }
 
 template <int DT, bool TAIL>
 int launch_distill(const DistillArgs &a, const DistillSplit &sp, hipStream_t s) {
   if (!sp.parts) {
-    if (sp.vecs <= 256) launch_rows<DT, TAIL, 256, 1>(a, s);
-    else if (sp.vecs <= 1024) launch_rows<DT, TAIL, 256, 4>(a, s);
-    else if (sp.vecs <= 2048) launch_rows<DT, TAIL, 256, 8>(a, s);
+    if (sp.vecs <= 128) launch_rows<DT, TAIL, 64, 2>(a, s);
+    else if (sp.vecs <= 512) launch_rows<DT, TAIL, 64, 8>(a, s);
+    else if (sp.vecs <= 1024) launch_rows<DT, TAIL, 64, 16>(a, s);
+    else if (sp.vecs <= 2048) launch_rows<DT, TAIL, 128, 16>(a, s);
     else if (sp.vecs <= 4096) launch_rows<DT, TAIL, 256, 16>(a, s);
-    else if (sp.vecs <= 8192) launch_rows<DT, TAIL, 1024, 8>(a, s);
-    else launch_rows<DT, TAIL, 1024, kRowItems>(a, s);
+    else if (sp.vecs <= 8192) launch_rows<DT, TAIL, 512, 16>(a, s);
+    else launch_rows<DT, TAIL, 512, kRowItems>(a, s);
     return launch_result();
   }
   constexpr int NT = kDistillThreads;
@@ -407,7 +428,7 @@ int launch_distill(const DistillArgs &a, const DistillSplit &sp, hipStream_t s) 
                      0, s, a);
   if (int rc = launch_result()) return rc;
   hipLaunchKernelGGL((distill_grad_kernel<DT, TAIL, NT>), dim3((unsigned)(a.rows * blocks)),
-                     dim3(NT), 0, s, a, blocks);
+                     dim3(NT), slot_bytes(a.slots), s, a, blocks);
   return launch_result();
 }
 
@@ -418,7 +439,9 @@ extern "C" {
 uint64_t zs_distill_workspace(uint64_t rows, uint64_t vocab, uint32_t slots, int dtype) {
   if (rows == 0 || !valid_any(dtype) || matrix_too_big(rows, vocab)) return 0;
   const DistillSplit sp = distill_split(rows, vocab, dtype);
-  return sp.parts ? rows * (sp.parts * sizeof(DistillPart) + slots * 4ull) : 0;
+  /* one part where a row per block would do, for gradients that it cannot store */
+  return sp.parts ? rows * (sp.parts * sizeof(DistillPart) + slots * 4ull)
+                  : rows * sizeof(DistillPart);
 }
 
 int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
@@ -441,7 +464,7 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   if (!logits || !loss || (slots && (!ids || !teacher)))
     return fail(ZS_ERR_INVALID_ARG, "zs_distill: null pointer%s");
   const uint64_t esz = esize(dtype);
-  const DistillSplit sp = distill_split(rows, vocab, dtype);
+  DistillSplit sp = distill_split(rows, vocab, dtype);
   const uint64_t need = zs_distill_workspace(rows, vocab, slots, dtype);
   if (need && (!workspace || workspace_bytes < need))
     return fail(ZS_ERR_INVALID_ARG, "zs_distill: workspace too small%s");
@@ -477,20 +500,22 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   a.loss = loss;
   a.grad = grad;
   a.ws = static_cast<DistillPart *>(workspace);
-  a.ws_z = reinterpret_cast<float *>(a.ws + rows * sp.parts);
+  if (sp.parts) a.ws_z = reinterpret_cast<float *>(a.ws + rows * sp.parts);
   a.rows = rows;
   a.ld = ld;
   a.gld = grad_ld;
   a.vocab = (uint32_t)vocab;
   a.slots = slots;
-  a.parts = sp.parts;
-  a.part_vecs = sp.part_vecs;
   a.tau = temperature;
   a.inv_tau = 1.0f / temperature;
   a.log2_scale = (float)(1.4426950408889634 / temperature);
   a.scale = loss_scale;
   a.vec_store = grad && (((uintptr_t)grad ^ (uintptr_t)logits) & 15) == 0 &&
                 (grad_ld - ld) * esz % 16 == 0;
+  /* such a gradient is not the logits' own buffer: its slots' logits stay */
+  if (!sp.parts && grad && !a.vec_store) sp = {1, sp.vecs, sp.vecs};
+  a.parts = sp.parts;
+  a.part_vecs = sp.part_vecs;
   hipStream_t s = static_cast<hipStream_t>(stream);
   int rc = ZS_OK;
   with_any(dtype, [&](auto dt) {
