@@ -442,6 +442,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const void *p, uint32_
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
 }
 
+/* The gradient is stored non-temporally but in one-wave blocks: their short
+ * rows have a slot in many of their lines, and a line that has left the L2 by
+ * then is read back for it (65536 x 4096: 272 us plain, 326 non-temporal;
+ * 16384 x 32000: 469 and 441). */
 constexpr int kNonTemporal = 2;
 
 /* What a block knows of a row before it holds it. A row without weight is
@@ -653,7 +657,8 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
 #pragma unroll
       for (uint32_t j = 0; j < ve; ++j) e[j] = term(e[j], shift) * f.factor;
       __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, pack_vec<DT>(e)), to,
-                                             (int)(t * 16 + i * (NT * 16)), 0, kNonTemporal);
+                                             (int)(t * 16 + i * (NT * 16)), 0,
+                                             NT > 64 ? kNonTemporal : 0);
       x[i] = fetch_vec<DT>(from, after, i * (NT * 16));   /* past the last row: not used */
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -670,8 +675,8 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
 }
 
 /* ------------------------------------------------------------------------
- * Rows in parts, where there are few rows or a row is longer than a block's
- * registers: a block per part forms its statistics, then a block per part
+ * Rows in parts, where a row is longer than a block's registers (or its
+ * gradient is aligned another way): a block per part forms its statistics, then a block per part
  * joins all of its row's and writes its share of the gradient.
  * ---------------------------------------------------------------------- */
 template <int DT, int NT>

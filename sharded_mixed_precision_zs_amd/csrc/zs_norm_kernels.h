@@ -97,6 +97,43 @@ struct NormGradArgs {
   uint32_t cols, parts;
 };
 
+/* A row's share of one thread, as it lies in memory: the next row's is
+ * fetched while this one is summed. */
+template <int DT, bool AL, int ITEMS>
+struct GradRow {
+  Raw16<8> dy[ITEMS], h[ITEMS], dres[ITEMS];
+  float rstd;
+};
+
+template <int DT, bool AL>
+__device__ __forceinline__ Raw16<8> load8_raw(const void *row, uint32_t col, uint32_t cols) {
+  Raw16<8> r = {};
+  const uint16_t *p = static_cast<const uint16_t *>(row) + col;
+  if constexpr (AL) {
+    if (col < cols) r = ld16<8>(p);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < cols) r.w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+  }
+  return r;
+}
+
+template <int DT, bool AL, int G, int ITEMS>
+__device__ __forceinline__ void load_grad_row(const NormGradArgs &a, uint64_t row, uint32_t t,
+                                              GradRow<DT, AL, ITEMS> &r) {
+  const uint64_t at = row * a.cols;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t c = (i * G + t) * 8;
+    r.dy[i] = load8_raw<DT, AL>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols);
+    r.h[i] = load8_raw<DT, AL>(static_cast<const uint16_t *>(a.h) + at, c, a.cols);
+    if (a.dres)
+      r.dres[i] = load8_raw<DT, AL>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols);
+  }
+  r.rstd = a.rstd[row];
+}
+
 /* Each of `parts` groups of G threads walks rows p, p + parts, ... and keeps
  * its share of dg in registers; norm_gain_kernel adds the shares in order,
  * so the result does not depend on scheduling. */
@@ -107,50 +144,44 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_grad_kernel(NormGradAr
   const uint32_t t = threadIdx.x % G;
   const uint32_t p = blockIdx.x * kRows + threadIdx.x / G;
   if (p >= a.parts) return;
-  float dg[ITEMS][8];
+  float dg[ITEMS][8], g[ITEMS][8];
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i)
+  for (int i = 0; i < ITEMS; ++i) {
+    load8<DT, AL>(a.gain, (uint64_t)(i * G + t) * 8, a.cols, g[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
+  }
+  GradRow<DT, AL, ITEMS> r, next;
+  load_grad_row<DT, AL, G>(a, p, t, r);
   int turn = 0;
   for (uint64_t row = p; row < a.rows; row += a.parts, turn ^= 1) {
-    const uint16_t *dy = static_cast<const uint16_t *>(a.dy) + row * a.cols;
-    const uint16_t *hp = static_cast<const uint16_t *>(a.h) + row * a.cols;
-    const float rstd = a.rstd[row];
-    float h[ITEMS][8], d[ITEMS][8];
+    const bool more = row + a.parts < a.rows;
+    if (more) load_grad_row<DT, AL, G>(a, row + a.parts, t, next);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const uint64_t c = (uint64_t)(i * G + t) * 8;
-      load8<DT, AL>(dy, c, a.cols, d[i]);
-      load8<DT, AL>(hp, c, a.cols, h[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      float g[8];
-      load8<DT, AL>(a.gain, (uint64_t)(i * G + t) * 8, a.cols, g);
+      float h[8], d[8];
+      upcast<8, DT>(r.dy[i], d);
+      upcast<8, DT>(r.h[i], h);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dg[i][j] = fmaf(d[i][j], h[i][j] * rstd, dg[i][j]);
-        d[i][j] *= g[j];
-        dot = fmaf(d[i][j], h[i][j], dot);
+        dg[i][j] = fmaf(d[j], h[j] * r.rstd, dg[i][j]);
+        dot = fmaf(d[j] * g[i][j], h[j], dot);
       }
     }
-    const float s = group_sum<G>(dot, sums[turn]) / (float)a.cols * rstd * rstd;
+    const float s = group_sum<G>(dot, sums[turn]) / (float)a.cols * r.rstd * r.rstd;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const uint64_t c = (uint64_t)(i * G + t) * 8;
-      float o[8];
-      if (a.dres) {
-        load8<DT, AL>(static_cast<const uint16_t *>(a.dres) + row * a.cols, c, a.cols, o);
-      } else {
+      float h[8], d[8], o[8] = {};
+      upcast<8, DT>(r.dy[i], d);
+      upcast<8, DT>(r.h[i], h);
+      if (a.dres) upcast<8, DT>(r.dres[i], o);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = fmaf(rstd, fmaf(-h[i][j], s, d[i][j]), o[j]);
-      store8<DT, AL>(a.dx + row * a.cols, c, a.cols, o);
+      for (int j = 0; j < 8; ++j)
+        o[j] = fmaf(r.rstd, fmaf(-h[j], s, d[j] * g[i][j]), o[j]);
+      store8<DT, AL>(a.dx + row * a.cols, (uint64_t)(i * G + t) * 8, a.cols, o);
     }
+    if (more) r = next;
   }
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i)
@@ -161,25 +192,38 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_grad_kernel(NormGradAr
     }
 }
 
-/* dg[c] = sum of part[p][c] over p: 64 columns per block, 16 waves that
- * take every 16th share, joined in wave order. */
-constexpr int kGainWaves = 16;
+/* dg[c] = sum of part[p][c] over p: 32 columns per block, 32 half waves that
+ * take every 32nd share each (eight at a time, so that their latencies
+ * overlap), joined in order. */
+constexpr int kGainCols = 32, kGainRuns = 32;
 
-__global__ __launch_bounds__(64 * kGainWaves) void norm_gain_kernel(const float *part,
-                                                                    uint32_t parts, uint32_t cols,
-                                                                    float *dgain) {
-  __shared__ float sums[kGainWaves][64];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t c = blockIdx.x * 64 + lane;
+__global__ __launch_bounds__(kGainCols * kGainRuns) void norm_gain_kernel(const float *part,
+                                                                          uint32_t parts,
+                                                                          uint32_t cols,
+                                                                          float *dgain) {
+  __shared__ float sums[kGainRuns][kGainCols + 1];
+  const uint32_t lane = threadIdx.x % kGainCols, run = threadIdx.x / kGainCols;
+  const uint32_t c = blockIdx.x * kGainCols + lane;
   float s = 0.0f;
-  if (c < cols)
-    for (uint32_t p = wave; p < parts; p += kGainWaves) s += part[(uint64_t)p * cols + c];
-  sums[wave][lane] = s;
+  if (c < cols) {
+    const float *q = part + c;
+    for (uint32_t p = run; p < parts; p += 8 * kGainRuns) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t at = p + k * kGainRuns;
+        v[k] = at < parts ? q[(uint64_t)at * cols] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
+  }
+  sums[run][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < cols) {
+  if (run == 0 && c < cols) {
     s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kGainWaves; ++w) s += sums[w][lane];
+    for (int w = 0; w < kGainRuns; ++w) s += sums[w][lane];
     dgain[c] = s;
   }
 }

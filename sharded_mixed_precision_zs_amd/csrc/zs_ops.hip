@@ -95,9 +95,9 @@ void with_items(uint32_t need, F f) {
 }
 
 template <class F>
-void with_norm_shape(uint64_t rows, uint64_t padded, F f) {
+void with_norm_shape(uint64_t padded, F f) {
   const uint32_t vecs = (uint32_t)(padded / 8);
-  if (padded <= 512 || (padded <= 4096 && rows >= 1024))
+  if (padded <= 512)
     with_items((vecs + 63) / 64, [&](auto i) { f(Tag<64>{}, i); });
   else if (padded <= 16384)
     with_items((vecs + 255) / 256, [&](auto i) { f(Tag<256>{}, i); });
@@ -132,10 +132,13 @@ void launch_matmul(const MatmulArgs &a, hipStream_t s) {
   else launch_tile<AF, CDT, 128, 128>(a, s);
 }
 
-/* Groups that share the rows of a backward pass. */
-constexpr uint32_t kNormParts = 1024;
-
-uint32_t norm_parts(uint64_t rows) { return rows < kNormParts ? (uint32_t)rows : kNormParts; }
+/* Groups that share the rows of a backward pass: some four rows each, for
+ * their sums of dg cost as much again as a row or two; 256 at least, a block
+ * for every CU, and 1024 at most. */
+uint32_t norm_parts(uint64_t rows) {
+  const uint64_t want = rows / 4 < 256 ? 256 : rows / 4 > 1024 ? 1024 : rows / 4;
+  return (uint32_t)(rows < want ? rows : want);
+}
 
 }  // namespace
 
@@ -181,7 +184,7 @@ int zs_rmsnorm_forward(const void *x, const void *residual, const void *gain, in
   hipStream_t s = static_cast<hipStream_t>(stream);
   with16(dtype, [&](auto dt) {
     with_bool(al, [&](auto v) {
-      with_norm_shape(rows, padded, [&](auto g, auto items) {
+      with_norm_shape(padded, [&](auto g, auto items) {
         constexpr int G = decltype(g)::value, block = G < 256 ? 256 : G, per = block / G;
         hipLaunchKernelGGL((norm_kernel<decltype(dt)::value, decltype(v)::value, G,
                                         decltype(items)::value>),
@@ -238,7 +241,7 @@ int zs_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const 
   if (rows) {
     with16(dtype, [&](auto dt) {
       with_bool(al, [&](auto v) {
-        with_norm_shape(rows, padded_of(cols), [&](auto g, auto items) {
+        with_norm_shape(padded_of(cols), [&](auto g, auto items) {
           constexpr int G = decltype(g)::value, block = G < 256 ? 256 : G, per = block / G;
           hipLaunchKernelGGL((norm_grad_kernel<decltype(dt)::value, decltype(v)::value, G,
                                                decltype(items)::value>),
@@ -248,8 +251,8 @@ int zs_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const 
     });
     if (int rc = launch_result()) return rc;
   }
-  hipLaunchKernelGGL(norm_gain_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(64 * kGainWaves),
-                     0, s, a.part, parts, (uint32_t)cols, dgain);
+  hipLaunchKernelGGL(norm_gain_kernel, dim3((unsigned)((cols + kGainCols - 1) / kGainCols)),
+                     dim3(kGainCols * kGainRuns), 0, s, a.part, parts, (uint32_t)cols, dgain);
   return launch_result();
 }
 
@@ -361,14 +364,14 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
 namespace {
 
 /* ------------------------------------------------------------------------
- * A row per block where its registers hold it (256 threads up to 4096
- * vectors of 16 bytes, 512 up to 16384; one at least, whatever its
- * alignment) and there are rows enough; else in
- * parts, so many that some 1024 blocks run. Gradient rows that are not
- * aligned as the logits' go in parts too (one).
+ * A row per block where its registers hold it: blocks of 64 to 512 threads
+ * of at most 16 vectors of 16 bytes, so that several rows are in flight per
+ * CU; rows beyond 8192 vectors take 32 per thread and a CU to themselves.
+ * One launch beats the parts' two for a single row too (1 x 128000 bf16: 17 us
+ * against 23). In parts otherwise, so many that some 1024 blocks run;
+ * gradient rows that are not aligned as the logits' go there (one part).
  * ---------------------------------------------------------------------- */
 constexpr int kDistillThreads = 256, kRowItems = 32;
-constexpr uint64_t kDistillFewRows = 64, kDistillShortVecs = 4096;
 
 struct DistillSplit {
   uint32_t parts;      /* 0: a row per block */
@@ -377,8 +380,8 @@ struct DistillSplit {
 
 DistillSplit distill_split(uint64_t rows, uint64_t vocab, int dtype) {
   const uint64_t vecs = vocab * esize(dtype) / 16;
-  if (vecs >= 2 && vecs <= 512 * kRowItems && (rows >= kDistillFewRows || vecs <= kDistillShortVecs))
-    return {0, 0, (uint32_t)vecs};
+  /* two vectors' worth of elements hold one, whatever the row's alignment */
+  if (vecs >= 2 && vecs <= 512 * kRowItems) return {0, 0, (uint32_t)vecs};
   uint64_t parts = rows < 1024 ? 1024 / rows : 1;
   const uint64_t most = (vecs + kDistillThreads - 1) / kDistillThreads;
   if (parts > most) parts = most;
