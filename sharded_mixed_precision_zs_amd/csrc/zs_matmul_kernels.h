@@ -192,9 +192,9 @@ __device__ __forceinline__ void put_c4(uint8_t *lds, const float (&x)[4]) {
     *reinterpret_cast<u32x2 *>(lds) = u32x2{pack2<CDT>(x[0], x[1]), pack2<CDT>(x[2], x[3])};
 }
 
-template <bool V>
+template <int V>
 struct Const {
-  static constexpr bool value = V;
+  static constexpr int value = V;
 };
 
 template <int AF, int CDT, int BM, int BN>
@@ -453,10 +453,11 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
 
 /* ------------------------------------------------------------------------
  * Few rows of A (m <= 32 MF): bound by reading B once. A block owns 32 rows
- * of B; its eight waves share K in pieces of 256 elements (whole lines of
- * memory), operands straight to registers, and join in wave order.
+ * of B; its eight waves share K in pieces of 512 elements, operands straight
+ * to registers, all of a piece under way at once, and join in wave order.
  * ---------------------------------------------------------------------- */
 constexpr int kThinWaves = 8;
+constexpr uint32_t kThinGroups = 4;
 
 template <int AF, int CDT, int MF>
 __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs p, int vec) {
@@ -475,30 +476,46 @@ __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs
   f32x16 acc[MF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) acc[i] = f32x16{};
-  const uint32_t groups = p.padded / kMxGroup;
-  for (uint32_t gr = wave * 2; gr < groups; gr += kThinWaves * 2) {
+  /* COUNT groups from `first` on: all loads, then the products */
+  auto multiply = [&](uint32_t first, auto count) {
+    constexpr int COUNT = decltype(count)::value;
+    u32x4 fb[COUNT][2];
+    uint32_t wb[COUNT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (gr + h >= groups) break;
-      const uint32_t k = (gr + h) * kMxGroup;
-      const uint32_t wb = *reinterpret_cast<const uint32_t *>(bs + (gr + h) * 4) >> (8 * g);
+    for (int h = 0; h < COUNT; ++h) {
+      wb[h] = *reinterpret_cast<const uint32_t *>(bs + (first + h) * 4);
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        i32x8 fb{};
-        put4(fb, 0, *reinterpret_cast<const u32x4 *>(b + k / 2 + ks * 32 + g * 16));
+      for (int ks = 0; ks < 2; ++ks)
+        fb[h][ks] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4 *>(b + (first + h) * 64 + ks * 32 + g * 16));
+    }
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          const uint32_t wa = *reinterpret_cast<const uint32_t *>(as[i] + (gr + h) * 4) >> (8 * g);
-          i32x8 fa{};
+    for (int i = 0; i < MF; ++i) {
+#pragma unroll
+      for (int h = 0; h < COUNT; ++h) {
+        const uint64_t k = mx_bytes<AF>((uint64_t)(first + h) * kMxGroup);
+        const uint32_t wa = *reinterpret_cast<const uint32_t *>(as[i] + (first + h) * 4) >> (8 * g);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          i32x8 vb{}, va{};
+          put4(vb, 0, fb[h][ks]);
           if constexpr (AF == ZS_MX_E2M1) {
-            put4(fa, 0, *reinterpret_cast<const u32x4 *>(a[i] + k / 2 + ks * 32 + g * 16));
+            put4(va, 0, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 32 + g * 16));
           } else {
-            put4(fa, 0, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 64 + g * 16));
-            put4(fa, 4, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 64 + 32 + g * 16));
+            put4(va, 0, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 64 + g * 16));
+            put4(va, 4, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 64 + 32 + g * 16));
           }
-          acc[i] = mfma<AF>(fb, fa, acc[i], wb, wa, ks & 1);
+          acc[i] = mfma<AF>(vb, va, acc[i], wb[h] >> (8 * g), wa, ks & 1);
         }
       }
+    }
+  };
+  const uint32_t groups = p.padded / kMxGroup;
+  for (uint32_t gr = wave * kThinGroups; gr < groups; gr += kThinWaves * kThinGroups) {
+    if (gr + kThinGroups <= groups) {
+      multiply(gr, Const<(int)kThinGroups>{});
+    } else {
+      for (uint32_t h = gr; h < groups; ++h) multiply(h, Const<1>{});
     }
   }
 #pragma unroll

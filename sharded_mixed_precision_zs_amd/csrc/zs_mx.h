@@ -112,31 +112,51 @@ __device__ __forceinline__ void mx_decode(const uint32_t (&code)[2], uint32_t by
 }
 
 /* ------------------------------------------------------------------------
- * Eight elements of a row of `cols`, as float. AL: the row is 16-byte
- * aligned and cols is a multiple of 8, so the eight are all there or none;
- * otherwise element by element, zeros past the end.
+ * Eight elements of a row of `cols`. AL: the row is 16-byte aligned and cols
+ * is a multiple of 8, so the eight are all there or none. Otherwise the row
+ * may start at any element: eight that are there still move at once (the
+ * memory unit takes unaligned vectors), the last few one by one; zeros past
+ * the end.
  * ---------------------------------------------------------------------- */
+struct __attribute__((packed, aligned(2))) Loose16 { uint32_t w[4]; };   /* 8 16-bit elements */
+struct __attribute__((packed, aligned(4))) Loose32 { float x[8]; };
+
+template <bool AL>
+__device__ __forceinline__ Raw16<8> load8_raw(const void *row, uint64_t col, uint64_t cols) {
+  Raw16<8> r = {};
+  const uint16_t *p = static_cast<const uint16_t *>(row) + col;
+  if constexpr (AL) {
+    if (col < cols) r = ld16<8>(p);
+  } else if (col + 8 <= cols) {
+    const Loose16 v = *reinterpret_cast<const Loose16 *>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = v.w[j];
+  } else if (col < cols) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < cols) r.w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+  }
+  return r;
+}
+
 template <int DT, bool AL>
 __device__ __forceinline__ void load8(const void *row, uint64_t col, uint64_t cols, float (&x)[8]) {
-  if constexpr (AL) {
-    if (col >= cols) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-      return;
-    }
-    if constexpr (DT == ZS_FP32) {
-      ldf<8>(static_cast<const float *>(row) + col, x);
-    } else {
-      upcast<8, DT>(ld16<8>(static_cast<const uint16_t *>(row) + col), x);
-    }
+  if constexpr (DT != ZS_FP32) {
+    upcast<8, DT>(load8_raw<AL>(row, col, cols), x);
   } else {
+    const float *p = static_cast<const float *>(row) + col;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] = 0.0f;
-      if (col + j < cols) {
-        if constexpr (DT == ZS_FP32) x[j] = static_cast<const float *>(row)[col + j];
-        else x[j] = up_lo<DT>(static_cast<const uint16_t *>(row)[col + j]);
-      }
+    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+    if constexpr (AL) {
+      if (col < cols) ldf<8>(p, x);
+    } else if (col + 8 <= cols) {
+      const Loose32 v = *reinterpret_cast<const Loose32 *>(p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = v.x[j];
+    } else if (col < cols) {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (col + j < cols) x[j] = p[j];
     }
   }
 }
@@ -145,14 +165,16 @@ __device__ __forceinline__ void load8(const void *row, uint64_t col, uint64_t co
 template <int DT, bool AL>
 __device__ __forceinline__ void store8(uint16_t *row, uint64_t col, uint64_t cols,
                                        const float (&x)[8]) {
+  const u32x4 w = {pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
+                   pack2<DT>(x[6], x[7])};
   if constexpr (AL) {
-    if (col < cols)
-      *reinterpret_cast<u32x4 *>(row + col) = u32x4{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
-                                                    pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])};
-  } else {
+    if (col < cols) *reinterpret_cast<u32x4 *>(row + col) = w;
+  } else if (col + 8 <= cols) {
+    *reinterpret_cast<Loose16 *>(row + col) = Loose16{{w.x, w.y, w.z, w.w}};
+  } else if (col < cols) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + j < cols) row[col + j] = pack1<DT>(x[j]);
+    for (int j = 0; j < 7; ++j)
+      if (col + j < cols) row[col + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
   }
 }
 

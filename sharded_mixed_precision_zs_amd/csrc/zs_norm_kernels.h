@@ -105,20 +105,6 @@ struct GradRow {
   float rstd;
 };
 
-template <int DT, bool AL>
-__device__ __forceinline__ Raw16<8> load8_raw(const void *row, uint32_t col, uint32_t cols) {
-  Raw16<8> r = {};
-  const uint16_t *p = static_cast<const uint16_t *>(row) + col;
-  if constexpr (AL) {
-    if (col < cols) r = ld16<8>(p);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + j < cols) r.w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
-  }
-  return r;
-}
-
 template <int DT, bool AL, int G, int ITEMS>
 __device__ __forceinline__ void load_grad_row(const NormGradArgs &a, uint64_t row, uint32_t t,
                                               GradRow<DT, AL, ITEMS> &r) {
@@ -126,10 +112,10 @@ __device__ __forceinline__ void load_grad_row(const NormGradArgs &a, uint64_t ro
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const uint32_t c = (i * G + t) * 8;
-    r.dy[i] = load8_raw<DT, AL>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols);
-    r.h[i] = load8_raw<DT, AL>(static_cast<const uint16_t *>(a.h) + at, c, a.cols);
+    r.dy[i] = load8_raw<AL>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols);
+    r.h[i] = load8_raw<AL>(static_cast<const uint16_t *>(a.h) + at, c, a.cols);
     if (a.dres)
-      r.dres[i] = load8_raw<DT, AL>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols);
+      r.dres[i] = load8_raw<AL>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols);
   }
   r.rstd = a.rstd[row];
 }

@@ -48,14 +48,17 @@ __global__ __launch_bounds__(kBlock) void quant_rows_kernel(QuantArgs a) {
 }
 
 /* Along the columns: a block takes 128 rows (one group) of 64 columns
- * through LDS, as float; then each thread holds one column's block of 32.
- * The row stride of 65 floats keeps both ways of walking the tile off each
- * other's banks. */
-constexpr int kColTileR = 128, kColTileC = 64, kColStride = kColTileC + 1;
+ * through LDS, as float; then each thread holds one column's block of 32, the
+ * four blocks of a column in neighbouring lanes, which write whole lines
+ * together. A row stride of 65 floats and 16 more for every 32 rows keep both
+ * ways of walking the tile off each other's banks. */
+constexpr uint32_t kColTileR = 128, kColTileC = 64;
+
+__device__ __forceinline__ uint32_t col_row(uint32_t r) { return r * (kColTileC + 1) + r / 32 * 16; }
 
 template <int DT, bool AL, int FMT, int VDT>
 __global__ __launch_bounds__(kBlock) void quant_cols_kernel(QuantArgs a) {
-  __shared__ float tile[kColTileR * kColStride];
+  __shared__ float tile[kColTileR * (kColTileC + 1) + 48];
   constexpr uint64_t esz = DT == ZS_FP32 ? 4 : 2;
   const uint64_t r0 = (uint64_t)blockIdx.y * kColTileR, c0 = (uint64_t)blockIdx.x * kColTileC;
   const uint32_t t = threadIdx.x;
@@ -70,12 +73,13 @@ __global__ __launch_bounds__(kBlock) void quant_cols_kernel(QuantArgs a) {
       for (int j = 0; j < 8; ++j) x[j] = 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) tile[lr * kColStride + lc + j] = x[j];
+    for (int j = 0; j < 8; ++j) tile[col_row(lr) + lc + j] = x[j];
   }
   __syncthreads();
-  const uint32_t lc = t & 63, blk = t >> 6;   /* a column and its block of 32 rows */
+  const uint32_t lc = t / 4, blk = t % 4;   /* a column and its block of 32 rows */
   if (c0 + lc < a.cols) {
-    float *col = tile + blk * 32 * kColStride + lc;
+    constexpr uint32_t kColStride = kColTileC + 1;
+    float *col = tile + col_row(blk * 32) + lc;
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 32; ++j) top = umax(top, mag_bits(col[j * kColStride]));
@@ -115,7 +119,7 @@ __global__ __launch_bounds__(kBlock) void quant_cols_kernel(QuantArgs a) {
     if (r0 + lr >= a.rows) break;
     float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = tile[lr * kColStride + vc + j];
+    for (int j = 0; j < 8; ++j) x[j] = tile[col_row(lr) + vc + j];
     store8<VDT, AL>(a.values + (r0 + lr) * a.cols, c0 + vc, a.cols, x);
   }
 }
