@@ -537,10 +537,13 @@ int zs_mx_quantize(const void *src, int src_dtype, uint64_t rows, uint64_t cols,
  *       the result for quantised normal data), which 16-bit results do not
  *       show.
  *   workspace: NULL, or device memory (16-byte aligned) for partial sums.
- *       No variant needs it yet.
+ *       With zs_mx_matmul_workspace(m, n, k) bytes, a long product of few
+ *       rows and columns is split along k and joined in a fixed order; with
+ *       fewer, into fewer pieces or not at all. 0: this product is not split.
  * k == 0 gives zeros. Errors: ZS_ERR_INVALID_ARG (null pointers, dtype,
  * format, ldc < n), ZS_ERR_UNSUPPORTED (m or n above 2^30, k above 2^22,
  * alignment, fp32 with an 8-bit A). */
+uint64_t zs_mx_matmul_workspace(uint64_t m, uint64_t n, uint64_t k);
 int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
                  const uint8_t *b_codes, const uint8_t *b_scales, uint64_t m, uint64_t n,
                  uint64_t k, void *c, int c_dtype, uint64_t ldc, void *workspace,

@@ -25,6 +25,8 @@ struct MatmulArgs {
   void *c;
   uint64_t ldc;
   uint32_t m, n, padded;   /* padded: K rounded up to whole groups */
+  float *part;             /* tiles split along K: [splits][m][n] sums */
+  uint32_t split_groups;   /* groups of a split, a multiple of four; all: one split */
 };
 
 /* The matrix instruction's name for an element format. */
@@ -225,8 +227,12 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
   const uint32_t m0 = (band * kBand + in_band % high) * BM, n0 = (in_band / high) * BN;
 
   const uint64_t row_a = mx_bytes<AF>(p.padded), row_b = p.padded / 2;
-  const uint32_t groups = p.padded / kMxGroup, scale_row = p.padded / kMxBlock;
-  const uint8_t *ta = p.a + m0 * row_a, *tb = p.b + n0 * row_b;
+  const uint32_t scale_row = p.padded / kMxBlock;
+  const uint32_t group0 = blockIdx.y * p.split_groups;   /* this split's share of K */
+  const uint32_t left = p.padded / kMxGroup - group0;
+  const uint32_t groups = left < p.split_groups ? left : p.split_groups;
+  const uint8_t *ta = p.a + m0 * row_a + mx_bytes<AF>((uint64_t)group0 * kMxGroup);
+  const uint8_t *tb = p.b + n0 * row_b + (uint64_t)group0 * (kMxGroup / 2);
 
   /* Rows past the last are read as the last; their results are not stored. */
   const uint32_t last_a = p.m - 1 - m0, last_b = p.n - 1 - n0;
@@ -247,8 +253,9 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
 #pragma unroll
   for (int i = 0; i < kScaleRows; ++i) {
     const uint32_t t = threadIdx.x + i * 256, rb = t - BM;
-    scale_of[i] = t < BM ? p.as + (uint64_t)(m0 + (t < last_a ? t : last_a)) * scale_row
-                         : p.bs + (uint64_t)(n0 + (rb < last_b ? rb : last_b)) * scale_row;
+    scale_of[i] = (t < BM ? p.as + (uint64_t)(m0 + (t < last_a ? t : last_a)) * scale_row
+                          : p.bs + (uint64_t)(n0 + (rb < last_b ? rb : last_b)) * scale_row) +
+                  group0 * 4;
   }
 
   /* Bit i: the lane's piece of its i-th row lies in the upper half of a line. */
@@ -393,7 +400,13 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
   constexpr uint32_t kEsz = CDT == ZS_FP32 ? 4 : 2, kRow = FN * 32 * kEsz, kPieces = kRow / 16;
   static_assert(32 * kRow * 2 <= sizeof(sa0) && 32 * kRow * 2 <= sizeof(sb0), "strips fit");
   uint8_t *strip = (wave & 2 ? sb0 : sa0) + (wave & 1) * 32 * kRow;
-  const bool vec = ((uintptr_t)p.c & 15) == 0 && p.ldc * kEsz % 16 == 0;
+  uint8_t *c = static_cast<uint8_t *>(p.c);
+  uint64_t ldc = p.ldc;
+  if (p.part) {   /* CDT is fp32 then */
+    c = reinterpret_cast<uint8_t *>(p.part + (uint64_t)blockIdx.y * p.m * p.n);
+    ldc = p.n;
+  }
+  const bool vec = ((uintptr_t)c & 15) == 0 && ldc * kEsz % 16 == 0;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -411,16 +424,16 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
       constexpr uint32_t kRowsAtOnce = 64 / kPieces > 0 ? 64 / kPieces : 1;
 #pragma unroll
       for (uint32_t k = 0; k < 32 / kRowsAtOnce; ++k) {
-        const uint32_t lr = k * kRowsAtOnce + lane / kPieces, c = lane % kPieces;
-        const uint32_t row = m0 + tm + i * 32 + lr, col = col0 + c * (16 / kEsz);
+        const uint32_t lr = k * kRowsAtOnce + lane / kPieces, pc = lane % kPieces;
+        const uint32_t row = m0 + tm + i * 32 + lr, col = col0 + pc * (16 / kEsz);
         const u32x4 w = *reinterpret_cast<const u32x4 *>(strip + lr * kRow +
-                                                         ((c ^ (lr % kPieces)) * 16));
+                                                         ((pc ^ (lr % kPieces)) * 16));
         if (row >= p.m) continue;
-        uint8_t *out = static_cast<uint8_t *>(p.c) + ((uint64_t)row * p.ldc + col) * kEsz;
+        uint8_t *out = c + ((uint64_t)row * ldc + col) * kEsz;
         if (col + 16 / kEsz <= p.n) {
           *reinterpret_cast<u32x4 *>(out) = w;
         } else {
-          const uint8_t *b = strip + lr * kRow + ((c ^ (lr % kPieces)) * 16);
+          const uint8_t *b = strip + lr * kRow + ((pc ^ (lr % kPieces)) * 16);
           for (uint32_t e = 0; col + e < p.n; ++e) {
             if constexpr (kEsz == 4)
               reinterpret_cast<uint32_t *>(out)[e] = reinterpret_cast<const uint32_t *>(b)[e];
@@ -439,7 +452,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
           if (lc >= FN * 32 || col >= p.n) continue;
           const uint8_t *b = strip + lr * kRow + (((lc * kEsz / 16) ^ (lr % kPieces)) * 16) +
                              lc * kEsz % 16;
-          uint8_t *out = static_cast<uint8_t *>(p.c) + ((uint64_t)row * p.ldc + col) * kEsz;
+          uint8_t *out = c + ((uint64_t)row * ldc + col) * kEsz;
           if constexpr (kEsz == 4)
             *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(b);
           else
@@ -451,13 +464,25 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
   }
 }
 
+/* The splits' sums, added in order and rounded once. */
+template <int CDT>
+__global__ __launch_bounds__(kBlock) void matmul_join_kernel(MatmulArgs p, uint32_t splits) {
+  const uint64_t id = (uint64_t)blockIdx.x * kBlock + threadIdx.x, all = (uint64_t)p.m * p.n;
+  if (id >= all) return;
+  float s = 0.0f;
+  for (uint32_t k = 0; k < splits; ++k) s += p.part[k * all + id];
+  const uint32_t row = (uint32_t)(id / p.n), col = (uint32_t)(id % p.n);
+  if constexpr (CDT == ZS_FP32) static_cast<float *>(p.c)[row * p.ldc + col] = s;
+  else static_cast<uint16_t *>(p.c)[row * p.ldc + col] = pack1<CDT>(s);
+}
+
 /* ------------------------------------------------------------------------
  * Few rows of A (m <= 32 MF): bound by reading B once. A block owns 32 rows
  * of B; its eight waves share K in pieces of 512 elements, operands straight
  * to registers, all of a piece under way at once, and join in wave order.
  * ---------------------------------------------------------------------- */
 constexpr int kThinWaves = 8;
-constexpr uint32_t kThinGroups = 4;
+constexpr uint32_t kThinGroups = 2;
 
 template <int AF, int CDT, int MF>
 __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs p, int vec) {
@@ -486,8 +511,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs
       wb[h] = *reinterpret_cast<const uint32_t *>(bs + (first + h) * 4);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        fb[h][ks] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4 *>(b + (first + h) * 64 + ks * 32 + g * 16));
+        fb[h][ks] = *reinterpret_cast<const u32x4 *>(b + (first + h) * 64 + ks * 32 + g * 16);
     }
 #pragma unroll
     for (int i = 0; i < MF; ++i) {

@@ -100,29 +100,67 @@ void with_norm_shape(uint64_t padded, F f) {
 
 /* ------------------------------------------------------------------------
  * The product's variant: up to 64 rows of A, bound by B, the thin kernel;
- * the large tiles where they occupy every CU, else 128 x 128.
+ * the large tiles where they occupy every CU, else 128 x 128, and where even
+ * these leave three CUs of four idle and K is long, that split along K into
+ * pieces of 1024 elements or more, as far as the workspace holds their sums.
  * ---------------------------------------------------------------------- */
 template <int AF, int CDT, int BM, int BN>
-void launch_tile(const MatmulArgs &a, hipStream_t s) {
+void launch_tile(const MatmulArgs &a, uint32_t splits, hipStream_t s) {
   const uint64_t tiles = (uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN);
-  hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN>), dim3((unsigned)tiles), dim3(256), 0, s,
-                     a);
+  hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN>), dim3((unsigned)tiles, splits), dim3(256),
+                     0, s, a);
+}
+
+constexpr uint64_t kMaxMatmulK = 1ull << 22; /* byte offsets in a tile of 256 rows are 32 bits */
+constexpr uint64_t kFullChip = 256; /* blocks that give every CU one */
+
+struct MatmulSplit {
+  uint32_t splits, groups;   /* groups of 128 elements of K per split */
+};
+
+MatmulSplit matmul_split(uint64_t m, uint64_t n, uint64_t padded, uint64_t workspace_bytes) {
+  const uint64_t tiles = (m + 127) / 128 * ((n + 127) / 128), groups = padded / ZS_MX_GROUP;
+  uint64_t splits = kFullChip / tiles;
+  if (splits > groups / 8) splits = groups / 8;
+  if (splits > workspace_bytes / (m * n * 4)) splits = workspace_bytes / (m * n * 4);
+  /* four at least: two pieces cost more than they save (512 x 4096 x 4096
+   * 4-bit: 25 us against 16 in one), more pay (768 x 768 x 8192 8-bit A: 21
+   * against 34; 65 x 4096 x 4096: 13.5 against 17) */
+  if (m <= 64 || splits < 4) return {1, (uint32_t)groups};
+  const uint64_t each = (groups + splits - 1) / splits, four = (each + 3) / 4 * 4;
+  return {(uint32_t)((groups + four - 1) / four), (uint32_t)four};
 }
 
 template <int AF, int CDT>
-void launch_matmul(const MatmulArgs &a, hipStream_t s) {
+int launch_matmul(MatmulArgs a, float *workspace, uint64_t workspace_bytes, hipStream_t s) {
   constexpr uint64_t esz = CDT == ZS_FP32 ? 4 : 2;
+  a.split_groups = a.padded / ZS_MX_GROUP;
   if (a.m <= 64) {
     /* four results of a lane in one store */
     const int vec = aligned(a.c, 4 * esz) && a.ldc % 4 == 0;
     const dim3 grid((a.n + 31) / 32), block(64 * kThinWaves);
     if (a.m <= 32) hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, 1>), grid, block, 0, s, a, vec);
     else hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, 2>), grid, block, 0, s, a, vec);
-    return;
+    return launch_result();
   }
   constexpr int BM = AF == ZS_MX_E2M1 ? 256 : 128, BN = 256;
-  if ((uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN) >= 256) launch_tile<AF, CDT, BM, BN>(a, s);
-  else launch_tile<AF, CDT, 128, 128>(a, s);
+  if ((uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN) >= kFullChip) {
+    launch_tile<AF, CDT, BM, BN>(a, 1, s);
+    return launch_result();
+  }
+  const MatmulSplit sp = matmul_split(a.m, a.n, a.padded, workspace_bytes);
+  if (sp.splits < 2) {
+    launch_tile<AF, CDT, 128, 128>(a, 1, s);
+    return launch_result();
+  }
+  a.part = workspace;
+  a.split_groups = sp.groups;
+  launch_tile<AF, ZS_FP32, 128, 128>(a, sp.splits, s);
+  if (int rc = launch_result()) return rc;
+  const uint64_t all = (uint64_t)a.m * a.n;
+  hipLaunchKernelGGL((matmul_join_kernel<CDT>), dim3((unsigned)((all + kBlock - 1) / kBlock)),
+                     dim3(kBlock), 0, s, a, sp.splits);
+  return launch_result();
 }
 
 /* Groups that share the rows of a backward pass: some four rows each, for
@@ -311,6 +349,12 @@ int zs_mx_quantize(const void *src, int src_dtype, uint64_t rows, uint64_t cols,
   return launch_result();
 }
 
+uint64_t zs_mx_matmul_workspace(uint64_t m, uint64_t n, uint64_t k) {
+  if (!m || !n || too_big(m) || too_big(n) || matrix_too_big(m, n) || k > kMaxMatmulK) return 0;
+  const MatmulSplit sp = matmul_split(m, n, padded_of(k), ~0ull);
+  return sp.splits < 2 ? 0 : sp.splits * m * n * 4;
+}
+
 int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
                  const uint8_t *b_codes, const uint8_t *b_scales, uint64_t m, uint64_t n,
                  uint64_t k, void *c, int c_dtype, uint64_t ldc, void *workspace,
@@ -320,8 +364,7 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
   if (c_dtype == ZS_FP32 && a_format == ZS_MX_E4M3)
     return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: fp32 results need 4-bit operands%s");
   if (ldc < n) return fail(ZS_ERR_INVALID_ARG, "zs_mx_matmul: ldc below n%s");
-  /* within a tile of 256 rows, byte offsets are 32 bits */
-  constexpr uint64_t kMaxDim = 1ull << 30, kMaxMatmulK = 1ull << 22;
+  constexpr uint64_t kMaxDim = 1ull << 30;
   if (m > kMaxDim || n > kMaxDim || k > kMaxMatmulK || matrix_too_big(m, ldc) ||
       m / 128 * (n / 128) > kMaxGrid / 4)
     return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: m or n above 2^30, or k above 2^22%s");
@@ -341,15 +384,19 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
       return fail(ZS_ERR_ALIAS, "zs_mx_matmul: an output overlaps an input%s");
   if (overlaps(c, c_bytes, workspace, workspace_bytes))
     return fail(ZS_ERR_ALIAS, "zs_mx_matmul: the result overlaps the workspace%s");
-  MatmulArgs a{a_codes, a_scales, b_codes, b_scales, c, ldc,
-               (uint32_t)m, (uint32_t)n, (uint32_t)padded};
+  if (workspace && !aligned(workspace, 16))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: workspace not aligned%s");
+  const MatmulArgs a{a_codes, a_scales, b_codes, b_scales, c, ldc,
+                     (uint32_t)m, (uint32_t)n, (uint32_t)padded, nullptr, 0};
   hipStream_t s = static_cast<hipStream_t>(stream);
+  int rc = ZS_OK;
   with_format(a_format, [&](auto f) {
     with_any(c_dtype, [&](auto dt) {
-      launch_matmul<decltype(f)::value, decltype(dt)::value>(a, s);
+      rc = launch_matmul<decltype(f)::value, decltype(dt)::value>(
+          a, static_cast<float *>(workspace), workspace ? workspace_bytes : 0, s);
     });
   });
-  return launch_result();
+  return rc;
 }
 
 }  /* extern "C" */

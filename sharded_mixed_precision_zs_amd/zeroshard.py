@@ -107,6 +107,7 @@ def _load():
                                    C.POINTER(zs_device_scaler)], i32),
         "zs_step_device": ([C.POINTER(zs_step_args), vp, vp, vp, vp], i32),
         "zs_mx_quantize": ([vp, i32, u64, u64, u64, i32, i32, vp, vp, vp, i32, vp], i32),
+        "zs_mx_matmul_workspace": ([u64, u64, u64], u64),
         "zs_mx_matmul": ([vp, vp, i32, vp, vp, u64, u64, u64, vp, i32, u64, vp, u64, vp], i32),
         "zs_rmsnorm_forward": ([vp, vp, vp, i32, u64, u64, f32, vp, vp, vp, vp, vp, vp], i32),
         "zs_rmsnorm_backward_workspace": ([u64, u64], u64),
@@ -582,6 +583,11 @@ def zs_mx_quantize(src, fmt, codes, scales, columns=False, values=None, stream=N
     _check("zs_mx_quantize", _lib.zs_mx_quantize(
         p, _float_code(src, "src", fp32=True), r, c, ld, fmt, 1 if columns else 0, cp, sp, vp,
         vdt, _raw_stream(stream)))
+
+
+def zs_mx_matmul_workspace(m, n, k):
+    """Bytes of workspace with which zs_mx_matmul splits k as far as it would."""
+    return _lib.zs_mx_matmul_workspace(m, n, k)
 
 
 def zs_mx_matmul(a_codes, a_scales, a_format, b_codes, b_scales, out, k, workspace=None,

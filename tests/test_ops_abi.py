@@ -67,7 +67,7 @@ BAD = [
     ("matmul", dict(a=far(0, 8)), UNSUPPORTED), ("matmul", dict(b=far(2, 4)), UNSUPPORTED),
     ("matmul", dict(as_=far(1, 1)), UNSUPPORTED), ("matmul", dict(c=far(4, 1)), UNSUPPORTED),
     ("matmul", dict(c=far(0)), ALIAS), ("matmul", dict(c=far(3)), ALIAS),
-    ("matmul", dict(ws=far(4), wsb=64), ALIAS),
+    ("matmul", dict(ws=far(4), wsb=64), ALIAS), ("matmul", dict(ws=far(5, 8), wsb=64), UNSUPPORTED),
     ("forward", dict(x=None), INVALID), ("forward", dict(gain=None), INVALID),
     ("forward", dict(h=None), INVALID), ("forward", dict(codes=None), INVALID),
     ("forward", dict(scales=None), INVALID), ("forward", dict(codes=None, scales=None, y=None), INVALID),
@@ -119,6 +119,17 @@ def test_a_workspace_too_small_is_refused(zs):
     assert fn(*{**big, "ws": None, "wsb": 0}.values()) == zs.ZS_ERR_INVALID_ARG
     assert fn(*{**big, "ws": far(5, 8), "wsb": need}.values()) == zs.ZS_ERR_UNSUPPORTED
     assert fn(*{**big, "ws": far(4, 64), "wsb": need}.values()) == zs.ZS_ERR_ALIAS
+
+
+def test_workspaces_by_size(zs):
+    assert zs.zs_mx_matmul_workspace(1, 32000, 4096) == 0          # the thin kernel
+    assert zs.zs_mx_matmul_workspace(8192, 8192, 8192) == 0        # tiles enough
+    assert zs.zs_mx_matmul_workspace(768, 768, 512) == 0           # nothing to split
+    assert zs.zs_mx_matmul_workspace(768, 768, 8192) == 6 * 768 * 768 * 4   # 64 groups in pieces of 12
+    assert zs.zs_mx_matmul_workspace(0, 5, 8192) == 0
+    assert zs.zs_rmsnorm_backward_workspace(10, 100) == 10 * 100 * 4
+    assert zs.zs_rmsnorm_backward_workspace(1 << 30, 100) == 1024 * 100 * 4
+    assert zs.zs_distill_workspace(0, 100, 4, zs.ZS_BF16) == 0
 
 
 @pytest.mark.parametrize("name,change", [
