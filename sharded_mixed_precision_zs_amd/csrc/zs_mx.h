@@ -179,17 +179,17 @@ __device__ __forceinline__ void store8(uint16_t *row, uint64_t col, uint64_t col
 }
 
 /* Sum over the G threads of a row's group, on all of them; a fixed tree, so
- * the same inputs give the same bits. `part`: G / 64 floats of LDS; the
+ * the same inputs give the same bits. `part`: G / 64 values in LDS; the
  * caller uses another part of it, or waits, before the next call. */
-template <int G>
-__device__ __forceinline__ float group_sum(float v, float *part) {
+template <int G, class T>
+__device__ __forceinline__ T group_sum(T v, T *part) {
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
   if constexpr (G > 64) {
     const int wave = (int)(threadIdx.x >> 6);
     if ((threadIdx.x & 63) == 0) part[wave] = v;
     __syncthreads();
-    v = 0.0f;
+    v = 0;
 #pragma unroll
     for (int w = 0; w < G / 64; ++w) v += part[w];
   }

@@ -26,21 +26,44 @@ struct NormArgs {
   uint64_t rows;
   uint32_t cols, padded;     /* padded: cols rounded up to whole groups */
   float eps;
+  double inv_cols;
 };
 
+/* 1 / sqrt(ss * inv_cols + eps) as the sum of two floats: a float's root and
+ * quotient, corrected by one step of Newton's in binary64. */
+struct RowScale {
+  float hi, lo;
+};
+
+__device__ __forceinline__ RowScale row_scale(double ss, double inv_cols, float eps) {
+  const double m = ss * inv_cols + (double)eps;
+  const float r = 1.0f / sqrtf((float)m);
+  const double d = (double)r * (1.5 - 0.5 * m * (double)r * (double)r);
+  RowScale s;
+  s.hi = (float)d;
+  s.lo = (float)(d - (double)s.hi);
+  /* beyond float, or not a number: as the float says */
+  if (!(r <= 3.0e38f && r > 0.0f && s.hi <= 3.0e38f)) s = {r, 0.0f};
+  return s;
+}
+
 /* G threads per row (64: four rows per 256-thread block), ITEMS vectors of
- * eight elements per thread. */
+ * eight elements per thread. An element's square and its product with the
+ * gain are exact in fp32 (8 or 11 significant bits each), the squares' sum is
+ * kept in binary64 and the row's scale in two floats: y is off by little more
+ * than its one rounding, and the 8-bit code that it falls to hardly ever by
+ * that. */
 template <int DT, bool AL, int G, int ITEMS>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
   constexpr int kRows = G < 256 ? 256 / G : 1;
-  __shared__ float part[G / 64];
+  __shared__ double part[G / 64];
   const uint32_t t = threadIdx.x % G;
   const uint64_t row = (uint64_t)blockIdx.x * kRows + threadIdx.x / G;
   if (row >= a.rows) return;   /* a whole wave; blocks of one row never take it */
   const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.cols;
   const uint16_t *r = a.res ? static_cast<const uint16_t *>(a.res) + row * a.cols : nullptr;
   float h[ITEMS][8];
-  float ss = 0.0f;
+  double ss = 0.0;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) load8<DT, AL>(x, (uint64_t)(i * G + t) * 8, a.cols, h[i]);
   if (r) {
@@ -60,11 +83,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
   for (int i = 0; i < ITEMS; ++i) {
     if (a.h) store8<DT, AL>(a.h + row * a.cols, (uint64_t)(i * G + t) * 8, a.cols, h[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+    for (int j = 0; j < 8; ++j) ss += (double)(h[i][j] * h[i][j]);
   }
   ss = group_sum<G>(ss, part);
-  const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
-  if (a.rstd && t == 0) a.rstd[row] = rstd;
+  const RowScale rstd = row_scale(ss, a.inv_cols, a.eps);
+  if (a.rstd && t == 0) a.rstd[row] = rstd.hi;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const uint32_t v = i * G + t;
@@ -74,7 +97,8 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      y[j] = v * 8 + j < a.cols ? h[i][j] * rstd * g[j] : 0.0f;
+      const float hg = h[i][j] * g[j];
+      y[j] = v * 8 + j < a.cols ? fmaf(hg, rstd.hi, hg * rstd.lo) : 0.0f;
       top = umax(top, mag_bits(y[j]));
     }
     if (a.y) store8<DT, AL>(a.y + row * a.cols, (uint64_t)v * 8, a.cols, y);

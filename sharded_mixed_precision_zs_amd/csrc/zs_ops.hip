@@ -91,6 +91,7 @@ constexpr uint64_t kMaxNormCols = 65536;
 template <class F>
 void with_norm_shape(uint64_t padded, F f) {
   if (padded <= 512) f(Tag<64>{}, Tag<1>{});
+  else if (padded <= 1024) f(Tag<64>{}, Tag<2>{});
   else if (padded <= 2048) f(Tag<256>{}, Tag<1>{});
   else if (padded <= 4096) f(Tag<256>{}, Tag<2>{});
   else if (padded <= 8192) f(Tag<512>{}, Tag<2>{});
@@ -208,7 +209,7 @@ int zs_rmsnorm_forward(const void *x, const void *residual, const void *gain, in
         return fail(ZS_ERR_ALIAS, "zs_rmsnorm_forward: two outputs overlap%s");
   }
   NormArgs a{x, residual, gain, static_cast<uint16_t *>(h), static_cast<uint16_t *>(y), rstd,
-             codes, scales, rows, (uint32_t)cols, (uint32_t)padded, eps};
+             codes, scales, rows, (uint32_t)cols, (uint32_t)padded, eps, 1.0 / (double)cols};
   const bool al = cols % 8 == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(gain, 16) &&
                   aligned(h, 16) && aligned(y, 16);
   if (rows > kMaxGrid) return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: too many rows%s");
