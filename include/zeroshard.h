@@ -517,11 +517,11 @@ typedef enum { ZS_MX_E2M1 = 0, ZS_MX_E4M3 = 1 } zs_mx_format;
  *   columns: 0: codes and scales of `rows` rows of K = cols; otherwise of
  *            `cols` rows of K = rows (the transposed matrix).
  *   values : NULL, or values_dtype (bf16, fp16)[rows][cols], contiguous: the
- *            values that the codes stand for, laid out as src (what a layer
- *            without a 4-bit product multiplies by).
+ *            values that the codes stand for, rounded to nearest even, laid
+ *            out as src (what a layer without a 4-bit product multiplies by).
  * Errors: ZS_ERR_INVALID_ARG (null pointers, dtypes, format, ld < cols),
- * ZS_ERR_UNSUPPORTED (alignment of codes and scales, more than 2^48
- * elements, more than 8 388 480 rows along the columns). */
+ * ZS_ERR_UNSUPPORTED (alignment, more than 2^48 elements, more
+ * than 8 388 480 rows along the columns). */
 int zs_mx_quantize(const void *src, int src_dtype, uint64_t rows, uint64_t cols, uint64_t ld,
                    int format, int columns, uint8_t *codes, uint8_t *scales, void *values,
                    int values_dtype, void *stream);
@@ -562,7 +562,7 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
  *   codes, scales: y as ZS_MX_E4M3 rows (K = cols), or both NULL.
  *   y          : dtype[rows][cols] or NULL; codes or y must be given.
  * Errors: ZS_ERR_INVALID_ARG (null pointers, dtype, eps not finite or < 0),
- * ZS_ERR_UNSUPPORTED (cols > 65536, alignment of codes and scales). */
+ * ZS_ERR_UNSUPPORTED (cols > 65536, alignment). */
 int zs_rmsnorm_forward(const void *x, const void *residual, const void *gain, int dtype,
                        uint64_t rows, uint64_t cols, float eps, void *h, float *rstd,
                        uint8_t *codes, uint8_t *scales, void *y, void *stream);

@@ -55,8 +55,7 @@ __device__ __forceinline__ void store_c4(void *c, uint64_t at, uint32_t col, uin
 }
 
 /* ------------------------------------------------------------------------
- * Tiles of C through LDS. A block of four waves (two by two) computes
- * BM x BN, in stages of 256 elements of K that two LDS buffers hold in turn:
+ * Tiles of C through LDS. A block of NW waves, in two rows, computes BM x BN, in stages of 256 elements of K that two LDS buffers hold in turn:
  * while the matrix cores work on one, the loads of the next stage go
  * straight to the other, so a stage's arithmetic hides its loads.
  *
@@ -199,9 +198,11 @@ struct Const {
   static constexpr int value = V;
 };
 
-template <int AF, int CDT, int BM, int BN>
-__global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
-  constexpr int FM = BM / 64, FN = BN / 64;           /* 32 x 32 fragments per wave */
+template <int AF, int CDT, int BM, int BN, int NW>
+__global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs p) {
+  constexpr int kAcross = NW / 2, kThreads = 64 * NW;   /* two rows of NW / 2 waves */
+  constexpr int FM = BM / 64, FN = BN / (32 * kAcross); /* 32 x 32 fragments per wave */
+  constexpr int LA = BM / (8 * NW), LB = BN / (8 * NW); /* loads of 8 rows per wave */
   constexpr uint32_t kPlanes = AF == ZS_MX_E2M1 ? 1 : 2, kPlane = BM * 128;
   __shared__ __align__(16) uint8_t sa0[kPlanes * kPlane], sa1[kPlanes * kPlane];
   __shared__ __align__(16) uint8_t sb0[BN * 128], sb1[BN * 128];
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const uint32_t r = lane & 31, g = lane >> 5;
-  const uint32_t tm = (wave >> 1) * (BM / 2), tn = (wave & 1) * (BN / 2);   /* the wave's corner */
+  const uint32_t tm = wave / kAcross * (BM / 2), tn = wave % kAcross * (BN / kAcross);   /* its corner */
 
   /* Blocks go round the eight XCDs; each XCD takes a run of tiles, and runs
    * walk groups of eight tile rows, so that its L2 sees the same operands
@@ -236,23 +237,23 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
 
   /* Rows past the last are read as the last; their results are not stored. */
   const uint32_t last_a = p.m - 1 - m0, last_b = p.n - 1 - n0;
-  uint32_t off_a[BM / 32], off_b[BN / 32];
+  uint32_t off_a[LA], off_b[LB];
 #pragma unroll
-  for (int i = 0; i < BM / 32; ++i) {
-    const uint32_t row = (wave * (BM / 32) + i) * 8 + lane / 8;
+  for (int i = 0; i < LA; ++i) {
+    const uint32_t row = (wave * (LA) + i) * 8 + lane / 8;
     off_a[i] = (row < last_a ? row : last_a) * (uint32_t)row_a + ((lane & 7) ^ swizzle(row)) * 16;
   }
 #pragma unroll
-  for (int i = 0; i < BN / 32; ++i) {
-    const uint32_t row = (wave * (BN / 32) + i) * 8 + lane / 8;
+  for (int i = 0; i < LB; ++i) {
+    const uint32_t row = (wave * (LB) + i) * 8 + lane / 8;
     off_b[i] = (row < last_b ? row : last_b) * (uint32_t)row_b + ((lane & 7) ^ swizzle(row)) * 16;
   }
   /* this thread's rows of scales: A's, then B's */
-  constexpr int kScaleRows = (BM + BN + 255) / 256;
+  constexpr int kScaleRows = (BM + BN + kThreads - 1) / kThreads;
   const uint8_t *scale_of[kScaleRows];
 #pragma unroll
   for (int i = 0; i < kScaleRows; ++i) {
-    const uint32_t t = threadIdx.x + i * 256, rb = t - BM;
+    const uint32_t t = threadIdx.x + i * kThreads, rb = t - BM;
     scale_of[i] = (t < BM ? p.as + (uint64_t)(m0 + (t < last_a ? t : last_a)) * scale_row
                           : p.bs + (uint64_t)(n0 + (rb < last_b ? rb : last_b)) * scale_row) +
                   group0 * 4;
@@ -261,11 +262,11 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
   /* Bit i: the lane's piece of its i-th row lies in the upper half of a line. */
   uint32_t upper_a = 0, upper_b = 0;
 #pragma unroll
-  for (int i = 0; i < BM / 32; ++i)
-    upper_a |= ((((lane & 7) ^ swizzle((wave * (BM / 32) + i) * 8 + lane / 8)) >> 2) & 1) << i;
+  for (int i = 0; i < LA; ++i)
+    upper_a |= ((((lane & 7) ^ swizzle((wave * (LA) + i) * 8 + lane / 8)) >> 2) & 1) << i;
 #pragma unroll
-  for (int i = 0; i < BN / 32; ++i)
-    upper_b |= ((((lane & 7) ^ swizzle((wave * (BN / 32) + i) * 8 + lane / 8)) >> 2) & 1) << i;
+  for (int i = 0; i < LB; ++i)
+    upper_b |= ((((lane & 7) ^ swizzle((wave * (LB) + i) * 8 + lane / 8)) >> 2) & 1) << i;
 
   /* A stage of one group only (the last, where the groups are odd) loads the
    * half of each row that it has twice, rather than past the row's end. A
@@ -281,12 +282,12 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
 #pragma unroll
     for (uint32_t pl = 0; pl < kPlanes; ++pl)
 #pragma unroll
-      for (int i = 0; i < BM / 32; ++i)
+      for (int i = 0; i < LA; ++i)
         load_lds16((half ? qa : qa + pl * 128) + (off_a[i] - ((ua >> i) & 1) * 64),
-                   sa + pl * kPlane + (wave * (BM / 32) + i) * 1024);
+                   sa + pl * kPlane + (wave * (LA) + i) * 1024);
 #pragma unroll
-    for (int i = 0; i < BN / 32; ++i)
-      load_lds16(qb + (off_b[i] - ((ub >> i) & 1) * 64), sb + (wave * (BN / 32) + i) * 1024);
+    for (int i = 0; i < LB; ++i)
+      load_lds16(qb + (off_b[i] - ((ub >> i) & 1) * 64), sb + (wave * (LB) + i) * 1024);
   };
 
   f32x16 acc[FM][FN];
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
     const uint32_t at = group + 4 <= groups ? group : groups >= 4 ? groups - 4 : 0;
 #pragma unroll
     for (int i = 0; i < kScaleRows; ++i) {
-      if ((BM + BN) % 256 && threadIdx.x + i * 256 >= BM + BN) break;
+      if ((BM + BN) % kThreads && threadIdx.x + i * kThreads >= BM + BN) break;
       const W4 v = *reinterpret_cast<const W4 *>(scale_of[i] + at * 4);
 #pragma unroll
       for (int k = 0; k < 4; ++k) raw[i][k] = v.w[k];
@@ -312,11 +313,11 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
     const uint32_t late = group + 4 > groups && groups >= 4 ? group + 4 - groups : 0;   /* <= 3 */
 #pragma unroll
     for (int i = 0; i < kScaleRows; ++i) {
-      if ((BM + BN) % 256 && threadIdx.x + i * 256 >= BM + BN) break;
+      if ((BM + BN) % kThreads && threadIdx.x + i * kThreads >= BM + BN) break;
       u32x4 v = {raw[i][0], raw[i][1], raw[i][2], raw[i][3]};
       v = late & 1 ? u32x4{v.y, v.z, v.w, v.w} : v;
       v = late & 2 ? u32x4{v.z, v.w, v.w, v.w} : v;
-      *reinterpret_cast<u32x4 *>(scales + chunk + (threadIdx.x + i * 256) * 16) = v;
+      *reinterpret_cast<u32x4 *>(scales + chunk + (threadIdx.x + i * kThreads) * 16) = v;
     }
   };
 
@@ -365,7 +366,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
     } else {   /* shorter rows, of a single chunk, a word at a time */
 #pragma unroll
       for (int i = 0; i < kScaleRows; ++i) {
-        if ((BM + BN) % 256 && threadIdx.x + i * 256 >= BM + BN) break;
+        if ((BM + BN) % kThreads && threadIdx.x + i * kThreads >= BM + BN) break;
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k)
           raw[i][k] = *reinterpret_cast<const uint32_t *>(scale_of[i] +
@@ -398,8 +399,9 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
   /* Each wave turns strips of 32 rows round in its own part of LDS, so that
    * rows of C go out in runs: 16-byte pieces, swizzled as above. */
   constexpr uint32_t kEsz = CDT == ZS_FP32 ? 4 : 2, kRow = FN * 32 * kEsz, kPieces = kRow / 16;
-  static_assert(32 * kRow * 2 <= sizeof(sa0) && 32 * kRow * 2 <= sizeof(sb0), "strips fit");
-  uint8_t *strip = (wave & 2 ? sb0 : sa0) + (wave & 1) * 32 * kRow;
+  static_assert(32 * kRow * kAcross <= sizeof(sa0) && 32 * kRow * kAcross <= sizeof(sb0),
+                "strips fit");
+  uint8_t *strip = (wave / kAcross ? sb0 : sa0) + wave % kAcross * 32 * kRow;
   uint8_t *c = static_cast<uint8_t *>(p.c);
   uint64_t ldc = p.ldc;
   if (p.part) {   /* CDT is fp32 then */
@@ -420,43 +422,24 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs p) {
       }
     __builtin_amdgcn_wave_barrier();
     const uint32_t col0 = n0 + tn;
-    if (vec) {
-      constexpr uint32_t kRowsAtOnce = 64 / kPieces > 0 ? 64 / kPieces : 1;
+    constexpr uint32_t kRowsAtOnce = 64 / kPieces > 0 ? 64 / kPieces : 1;
 #pragma unroll
-      for (uint32_t k = 0; k < 32 / kRowsAtOnce; ++k) {
-        const uint32_t lr = k * kRowsAtOnce + lane / kPieces, pc = lane % kPieces;
-        const uint32_t row = m0 + tm + i * 32 + lr, col = col0 + pc * (16 / kEsz);
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(strip + lr * kRow +
-                                                         ((pc ^ (lr % kPieces)) * 16));
-        if (row >= p.m) continue;
-        uint8_t *out = c + ((uint64_t)row * ldc + col) * kEsz;
-        if (col + 16 / kEsz <= p.n) {
-          *reinterpret_cast<u32x4 *>(out) = w;
-        } else {
-          const uint8_t *b = strip + lr * kRow + ((pc ^ (lr % kPieces)) * 16);
-          for (uint32_t e = 0; col + e < p.n; ++e) {
-            if constexpr (kEsz == 4)
-              reinterpret_cast<uint32_t *>(out)[e] = reinterpret_cast<const uint32_t *>(b)[e];
-            else
-              reinterpret_cast<uint16_t *>(out)[e] = reinterpret_cast<const uint16_t *>(b)[e];
-          }
-        }
-      }
-    } else {
-      for (uint32_t lr = 0; lr < 32; ++lr) {
-        const uint32_t row = m0 + tm + i * 32 + lr;
-        if (row >= p.m) break;
-#pragma unroll
-        for (uint32_t h = 0; h < FN * 32 / 64 + (FN == 1); ++h) {
-          const uint32_t lc = h * 64 + lane, col = col0 + lc;
-          if (lc >= FN * 32 || col >= p.n) continue;
-          const uint8_t *b = strip + lr * kRow + (((lc * kEsz / 16) ^ (lr % kPieces)) * 16) +
-                             lc * kEsz % 16;
-          uint8_t *out = c + ((uint64_t)row * ldc + col) * kEsz;
+    for (uint32_t k = 0; k < 32 / kRowsAtOnce; ++k) {
+      const uint32_t lr = k * kRowsAtOnce + lane / kPieces, pc = lane % kPieces;
+      const uint32_t row = m0 + tm + i * 32 + lr, col = col0 + pc * (16 / kEsz);
+      const uint8_t *from = strip + lr * kRow + ((pc ^ (lr % kPieces)) * 16);
+      const u32x4 w = *reinterpret_cast<const u32x4 *>(from);
+      if (row >= p.m) continue;
+      uint8_t *out = c + ((uint64_t)row * ldc + col) * kEsz;
+      if (col + 16 / kEsz <= p.n) {
+        if (vec) *reinterpret_cast<u32x4 *>(out) = w;
+        else *reinterpret_cast<Loose16 *>(out) = Loose16{{w.x, w.y, w.z, w.w}};
+      } else {
+        for (uint32_t e = 0; col + e < p.n; ++e) {
           if constexpr (kEsz == 4)
-            *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(b);
+            reinterpret_cast<uint32_t *>(out)[e] = reinterpret_cast<const uint32_t *>(from)[e];
           else
-            *reinterpret_cast<uint16_t *>(out) = *reinterpret_cast<const uint16_t *>(b);
+            reinterpret_cast<uint16_t *>(out)[e] = reinterpret_cast<const uint16_t *>(from)[e];
         }
       }
     }
@@ -478,86 +461,132 @@ __global__ __launch_bounds__(kBlock) void matmul_join_kernel(MatmulArgs p, uint3
 
 /* ------------------------------------------------------------------------
  * Few rows of A (m <= 32 MF): bound by reading B once. A block owns 32 rows
- * of B; its eight waves share K in pieces of 512 elements, operands straight
- * to registers, all of a piece under way at once, and join in wave order.
+ * of B; its eight waves share K in pieces of 256 elements and join in wave
+ * order. B goes through LDS, a wave's piece in its own part, so that a load
+ * takes whole lines (eight lanes to a row's 128 bytes; straight to registers
+ * an instruction would touch 32 rows for 32 bytes each): two parts in turn,
+ * and no barrier but a wave's own wait for its loads. A comes from the caches.
  * ---------------------------------------------------------------------- */
 constexpr int kThinWaves = 8;
-constexpr uint32_t kThinGroups = 2;
+constexpr uint32_t kThinPart = 32 * 128;   /* a piece: 32 rows of 128 bytes */
 
 template <int AF, int CDT, int MF>
 __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs p, int vec) {
-  __shared__ float sums[kThinWaves][MF][16][64];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  /* staging, then the waves' sums in its place */
+  constexpr uint32_t kSums = kThinWaves * MF * 16 * 64 * 4, kStage = kThinWaves * kThinPart;
+  __shared__ __align__(16) uint8_t stage0[kSums > kStage ? kSums : kStage], stage1[kStage];
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const uint32_t r = lane & 31, g = lane >> 5, n0 = blockIdx.x * 32;
-  const uint64_t rb = n0 + r < p.n ? n0 + r : p.n - 1;
-  const uint8_t *b = p.b + rb * (p.padded / 2), *bs = p.bs + rb * (p.padded / kMxBlock);
+  const uint32_t last = p.n - 1 - n0;   /* rows past it are read as it */
+  const uint64_t row_b = p.padded / 2;
+  const uint32_t scale_row = p.padded / kMxBlock, groups = p.padded / kMxGroup;
+  const uint8_t *tb = p.b + n0 * row_b;
+  uint32_t off[4], upper = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t row = i * 8 + lane / 8, c = (lane & 7) ^ swizzle(row);
+    off[i] = (row < last ? row : last) * (uint32_t)row_b + c * 16;
+    upper |= (c >> 2) << i;
+  }
+  const uint8_t *bs = p.bs + (uint64_t)(n0 + (r < last ? r : last)) * scale_row;
   const uint8_t *a[MF], *as[MF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
     const uint64_t ra = i * 32 + r < p.m ? i * 32 + r : p.m - 1;
     a[i] = p.a + ra * mx_bytes<AF>(p.padded);
-    as[i] = p.as + ra * (p.padded / kMxBlock);
+    as[i] = p.as + ra * scale_row;
   }
   f32x16 acc[MF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) acc[i] = f32x16{};
-  /* COUNT groups from `first` on: all loads, then the products */
-  auto multiply = [&](uint32_t first, auto count) {
-    constexpr int COUNT = decltype(count)::value;
-    u32x4 fb[COUNT][2];
-    uint32_t wb[COUNT];
+  const uint32_t x = swizzle(r), stages = (groups + 1) / 2;
+  /* A piece's A and scales go to registers, its B to LDS. A last piece of one
+   * group loads what it has twice, and multiplies it once. */
+  struct Piece {
+    u32x4 a[MF][2][2][kHalves<AF>];
+    uint32_t wa[MF][2], wb[2];
+  };
+  auto load = [&](uint32_t stage, Piece &q, uint8_t *lds) {
 #pragma unroll
-    for (int h = 0; h < COUNT; ++h) {
-      wb[h] = *reinterpret_cast<const uint32_t *>(bs + (first + h) * 4);
+    for (uint32_t h = 0; h < 2; ++h) {
+      const uint32_t group = stage * 2 + h < groups ? stage * 2 + h : groups - 1;
+      const uint64_t k = mx_bytes<AF>((uint64_t)group * kMxGroup) + g * 16;
+      q.wb[h] = *reinterpret_cast<const uint32_t *>(bs + group * 4);
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        fb[h][ks] = *reinterpret_cast<const u32x4 *>(b + (first + h) * 64 + ks * 32 + g * 16);
+      for (int i = 0; i < MF; ++i) {
+        q.wa[i][h] = *reinterpret_cast<const uint32_t *>(as[i] + group * 4);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int v = 0; v < kHalves<AF>; ++v)
+            q.a[i][h][ks][v] =
+                *reinterpret_cast<const u32x4 *>(a[i] + k + (ks * kHalves<AF> + v) * 32);
+      }
     }
+    const uint32_t u = (stage + 1) * 2 > groups ? upper : 0;
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
+    for (int i = 0; i < 4; ++i)
+      load_lds16(tb + (uint64_t)stage * 128 + (off[i] - ((u >> i) & 1) * 64),
+                 lds + wave * kThinPart + i * 1024);
+  };
+  auto multiply = [&](uint32_t stage, const Piece &q, const uint8_t *lds) {
 #pragma unroll
-      for (int h = 0; h < COUNT; ++h) {
-        const uint64_t k = mx_bytes<AF>((uint64_t)(first + h) * kMxGroup);
-        const uint32_t wa = *reinterpret_cast<const uint32_t *>(as[i] + (first + h) * 4) >> (8 * g);
+    for (uint32_t h = 0; h < 2; ++h) {
+      if (stage * 2 + h >= groups) break;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          i32x8 vb{}, va{};
-          put4(vb, 0, fb[h][ks]);
-          if constexpr (AF == ZS_MX_E2M1) {
-            put4(va, 0, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 32 + g * 16));
-          } else {
-            put4(va, 0, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 64 + g * 16));
-            put4(va, 4, *reinterpret_cast<const u32x4 *>(a[i] + k + ks * 64 + 32 + g * 16));
-          }
-          acc[i] = mfma<AF>(vb, va, acc[i], wb[h] >> (8 * g), wa, ks & 1);
+      for (int ks = 0; ks < 2; ++ks) {
+        i32x8 vb{};
+        put4(vb, 0, piece(lds + wave * kThinPart, r, 4 * h + 2 * ks + g, x));
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          i32x8 va{};
+          put4(va, 0, q.a[i][h][ks][0]);
+          if constexpr (AF == ZS_MX_E4M3) put4(va, 4, q.a[i][h][ks][1]);
+          acc[i] = mfma<AF>(vb, va, acc[i], q.wb[h] >> (8 * g), q.wa[i][h] >> (8 * g), ks & 1);
         }
       }
     }
   };
-  const uint32_t groups = p.padded / kMxGroup;
-  for (uint32_t gr = wave * kThinGroups; gr < groups; gr += kThinWaves * kThinGroups) {
-    if (gr + kThinGroups <= groups) {
-      multiply(gr, Const<(int)kThinGroups>{});
-    } else {
-      for (uint32_t h = gr; h < groups; ++h) multiply(h, Const<1>{});
+  Piece q0, q1;
+  /* Both parts are asked for at once; each is filled again when it is read.
+   * The waits are written out: loads to LDS are counted with all others, in
+   * order; the last four asked for, the other part's, may be under way still
+   * (what the registers wait for, the compiler knows). */
+  if (wave < stages) load(wave, q0, stage0);
+  if (wave + kThinWaves < stages) load(wave + kThinWaves, q1, stage1);
+  for (uint32_t s = wave; s < stages; s += 2 * kThinWaves) {
+    if (s + kThinWaves < stages) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    multiply(s, q0, stage0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   /* read before it is filled again */
+    if (s + 2 * kThinWaves < stages) load(s + 2 * kThinWaves, q0, stage0);
+    if (s + kThinWaves < stages) {
+      if (s + 2 * kThinWaves < stages) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      multiply(s + kThinWaves, q1, stage1);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (s + 3 * kThinWaves < stages) load(s + 3 * kThinWaves, q1, stage1);
     }
   }
+  __syncthreads();
+  float *sums = reinterpret_cast<float *>(stage0);   /* [wave][MF][16][64] */
 #pragma unroll
   for (int i = 0; i < MF; ++i)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) sums[wave][i][e][lane] = acc[i][e];
+    for (int e = 0; e < 16; ++e) sums[((wave * MF + i) * 16 + e) * 64 + lane] = acc[i][e];
   __syncthreads();
   /* a thread takes four neighbouring results: fragment i, quarter q, lane l */
   for (uint32_t t = threadIdx.x; t < MF * 4 * 64; t += 64 * kThinWaves) {
     const uint32_t i = t / 256, q = (t / 64) & 3, l = t & 63;
-    float x[4] = {0, 0, 0, 0};
+    float v[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kThinWaves; ++w)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] += sums[w][i][q * 4 + e][l];
+      for (int e = 0; e < 4; ++e) v[e] += sums[((w * MF + i) * 16 + q * 4 + e) * 64 + l];
     const uint32_t row = i * 32 + (l & 31);
     if (row < p.m)
-      store_c4<CDT>(p.c, (uint64_t)row * p.ldc, n0 + q * 8 + (l >> 5) * 4, p.n, x, vec);
+      store_c4<CDT>(p.c, (uint64_t)row * p.ldc, n0 + q * 8 + (l >> 5) * 4, p.n, v, vec);
   }
 }
 

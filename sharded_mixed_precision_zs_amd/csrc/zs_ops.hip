@@ -105,11 +105,11 @@ void with_norm_shape(uint64_t padded, F f) {
  * these leave three CUs of four idle and K is long, that split along K into
  * pieces of 1024 elements or more, as far as the workspace holds their sums.
  * ---------------------------------------------------------------------- */
-template <int AF, int CDT, int BM, int BN>
+template <int AF, int CDT, int BM, int BN, int NW>
 void launch_tile(const MatmulArgs &a, uint32_t splits, hipStream_t s) {
   const uint64_t tiles = (uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN);
-  hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN>), dim3((unsigned)tiles, splits), dim3(256),
-                     0, s, a);
+  hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN, NW>), dim3((unsigned)tiles, splits),
+                     dim3(64 * NW), 0, s, a);
 }
 
 constexpr uint64_t kMaxMatmulK = 1ull << 22; /* byte offsets in a tile of 256 rows are 32 bits */
@@ -146,17 +146,17 @@ int launch_matmul(MatmulArgs a, float *workspace, uint64_t workspace_bytes, hipS
   }
   constexpr int BM = AF == ZS_MX_E2M1 ? 256 : 128, BN = 256;
   if ((uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN) >= kFullChip) {
-    launch_tile<AF, CDT, BM, BN>(a, 1, s);
+    launch_tile<AF, CDT, BM, BN, AF == ZS_MX_E2M1 ? 8 : 4>(a, 1, s);
     return launch_result();
   }
   const MatmulSplit sp = matmul_split(a.m, a.n, a.padded, workspace_bytes);
   if (sp.splits < 2) {
-    launch_tile<AF, CDT, 128, 128>(a, 1, s);
+    launch_tile<AF, CDT, 128, 128, 4>(a, 1, s);
     return launch_result();
   }
   a.part = workspace;
   a.split_groups = sp.groups;
-  launch_tile<AF, ZS_FP32, 128, 128>(a, sp.splits, s);
+  launch_tile<AF, ZS_FP32, 128, 128, 4>(a, sp.splits, s);
   if (int rc = launch_result()) return rc;
   const uint64_t all = (uint64_t)a.m * a.n;
   hipLaunchKernelGGL((matmul_join_kernel<CDT>), dim3((unsigned)((all + kBlock - 1) / kBlock)),
@@ -193,8 +193,10 @@ int zs_rmsnorm_forward(const void *x, const void *residual, const void *gain, in
     return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: rows of more than 65536 elements%s");
   if (rows == 0 || cols == 0) return ZS_OK;
   if (!x || !gain) return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_forward: null x or gain%s");
-  if (codes && (!aligned(codes, 16) || !aligned(scales, 4)))
-    return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: codes or scales not aligned%s");
+  if ((codes && (!aligned(codes, 16) || !aligned(scales, 4))) || !aligned(x, 2) ||
+      !aligned(residual, 2) || !aligned(gain, 2) || !aligned(h, 2) || !aligned(y, 2) ||
+      !aligned(rstd, 4))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: an operand is not aligned%s");
   const uint64_t padded = padded_of(cols), bytes = rows * cols * 2;
   const void *outs[] = {h, y, codes, scales, rstd};
   const uint64_t out_bytes[] = {bytes, bytes, rows * padded, rows * padded / ZS_MX_BLOCK, rows * 4};
@@ -247,8 +249,9 @@ int zs_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const 
       return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_backward: null pointer%s");
     if (!workspace || workspace_bytes < need)
       return fail(ZS_ERR_INVALID_ARG, "zs_rmsnorm_backward: workspace too small%s");
-    if (!aligned(workspace, 4))
-      return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_backward: workspace not aligned%s");
+    if (!aligned(workspace, 4) || !aligned(dy, 2) || !aligned(h, 2) || !aligned(gain, 2) ||
+        !aligned(dres, 2) || !aligned(dx, 2) || !aligned(rstd, 4) || !aligned(dgain, 4))
+      return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_backward: an operand is not aligned%s");
     const void *outs[] = {dx, dgain, workspace};
     const uint64_t out_bytes[] = {bytes, cols * 4, need};
     const void *ins[] = {dy, h, dres, rstd, gain};
@@ -300,8 +303,9 @@ int zs_mx_quantize(const void *src, int src_dtype, uint64_t rows, uint64_t cols,
   if (rows == 0 || cols == 0) return ZS_OK;
   if (!src || !codes || !scales)
     return fail(ZS_ERR_INVALID_ARG, "zs_mx_quantize: null pointer%s");
-  if (!aligned(codes, 16) || !aligned(scales, 4))
-    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: codes or scales not aligned%s");
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(src, esize(src_dtype)) ||
+      !aligned(values, 2))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: an operand is not aligned%s");
   const uint64_t orows = columns ? cols : rows, padded = padded_of(columns ? rows : cols);
   if (matrix_too_big(orows, padded))
     return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: more than 2^48 elements%s");
@@ -512,8 +516,9 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   const uint64_t need = zs_distill_workspace(rows, vocab, slots, dtype);
   if (need && (!workspace || workspace_bytes < need))
     return fail(ZS_ERR_INVALID_ARG, "zs_distill: workspace too small%s");
-  if (!aligned(logits, esz) || (grad && !aligned(grad, esz)) || !aligned(workspace, 16) ||
-      !aligned(dev, 8))
+  if (!aligned(logits, esz) || !aligned(grad, esz) || !aligned(workspace, 16) ||
+      !aligned(dev, 8) || !aligned(ids, 4) || !aligned(teacher, esz) || !aligned(loss, 4) ||
+      !aligned(teacher_lse, 4) || !aligned(row_weight, 4))
     return fail(ZS_ERR_UNSUPPORTED, "zs_distill: an operand is not aligned%s");
   const uint64_t z_bytes = extent(rows, vocab, ld, esz);
   const uint64_t g_bytes = grad ? extent(rows, vocab, grad_ld, esz) : 0;

@@ -57,6 +57,8 @@ BAD = [
     ("quantize", dict(codes=far(1, 8)), UNSUPPORTED), ("quantize", dict(scales=far(2, 2)), UNSUPPORTED),
     ("quantize", dict(rows=1 << 49), UNSUPPORTED), ("quantize", dict(rows=1 << 30, ld=1 << 30), UNSUPPORTED),
     ("quantize", dict(rows=1 << 24, columns=1, values=None), UNSUPPORTED),
+    ("quantize", dict(src=far(0, 1)), UNSUPPORTED), ("quantize", dict(values=far(3, 1)), UNSUPPORTED),
+    ("quantize", dict(src=far(0, 2), dtype=2), UNSUPPORTED),
     ("quantize", dict(codes=far(0, 512)), ALIAS), ("quantize", dict(values=far(0)), ALIAS),
     ("quantize", dict(values=far(1, 16)), ALIAS),
     ("matmul", dict(a=None), INVALID), ("matmul", dict(bs=None), INVALID),
@@ -75,6 +77,9 @@ BAD = [
     ("forward", dict(eps=math.nan), INVALID), ("forward", dict(eps=math.inf), INVALID),
     ("forward", dict(cols=65537), UNSUPPORTED), ("forward", dict(rows=1 << 49), UNSUPPORTED),
     ("forward", dict(codes=far(5, 8)), UNSUPPORTED),
+    ("forward", dict(x=far(0, 1)), UNSUPPORTED), ("forward", dict(res=far(1, 1)), UNSUPPORTED),
+    ("forward", dict(gain=far(2, 1)), UNSUPPORTED), ("forward", dict(h=far(3, 1)), UNSUPPORTED),
+    ("forward", dict(rstd=far(4, 2)), UNSUPPORTED), ("forward", dict(y=far(7, 1)), UNSUPPORTED),
     ("forward", dict(y=far(0)), ALIAS), ("forward", dict(h=far(0, 64)), ALIAS),
     ("forward", dict(rstd=far(2)), ALIAS), ("forward", dict(codes=far(7)), ALIAS),
     ("backward", dict(dy=None), INVALID), ("backward", dict(h=None), INVALID),
@@ -83,6 +88,8 @@ BAD = [
     ("backward", dict(ws=None), INVALID), ("backward", dict(wsb=8 * 64 * 4 - 1), INVALID),
     ("backward", dict(dtype=2), INVALID), ("backward", dict(cols=65537), UNSUPPORTED),
     ("backward", dict(ws=far(7, 2)), UNSUPPORTED),
+    ("backward", dict(dy=far(0, 1)), UNSUPPORTED), ("backward", dict(dres=far(4, 1)), UNSUPPORTED),
+    ("backward", dict(rstd=far(2, 2)), UNSUPPORTED), ("backward", dict(dgain=far(6, 2)), UNSUPPORTED),
     ("backward", dict(dx=far(0, 16)), ALIAS), ("backward", dict(dgain=far(5)), ALIAS),
     ("backward", dict(ws=far(1)), ALIAS), ("backward", dict(dgain=far(3)), ALIAS),
     ("distill", dict(z=None), INVALID), ("distill", dict(ids=None), INVALID),
@@ -95,6 +102,9 @@ BAD = [
     ("distill", dict(slots=1025), UNSUPPORTED), ("distill", dict(rows=1 << 49), UNSUPPORTED),
     ("distill", dict(z=far(0, 1)), UNSUPPORTED), ("distill", dict(grad=far(4, 1)), UNSUPPORTED),
     ("distill", dict(dev=far(6, 4)), UNSUPPORTED),
+    ("distill", dict(ids=far(1, 2)), UNSUPPORTED), ("distill", dict(teacher=far(2, 1)), UNSUPPORTED),
+    ("distill", dict(loss=far(3, 2)), UNSUPPORTED), ("distill", dict(lse=far(6, 2)), UNSUPPORTED),
+    ("distill", dict(weight=far(6, 2)), UNSUPPORTED),
     ("distill", dict(grad=far(0, 2)), ALIAS), ("distill", dict(grad=far(0), gld=101), ALIAS),
     ("distill", dict(loss=far(0)), ALIAS), ("distill", dict(grad=far(2)), ALIAS),
     ("distill", dict(loss=far(4)), ALIAS),
