@@ -460,7 +460,7 @@ __global__ __launch_bounds__(kBlock) void matmul_join_kernel(MatmulArgs p, uint3
 }
 
 /* ------------------------------------------------------------------------
- * Few rows of A (m <= 32 MF): bound by reading B once. A block owns 32 rows
+ * Few rows of A (m <= 32): bound by reading B once. A block owns 32 rows
  * of B; its eight waves share K in pieces of 256 elements and join in wave
  * order. B goes through LDS, a wave's piece in its own part, so that a load
  * takes whole lines (eight lanes to a row's 128 bytes; straight to registers
@@ -470,11 +470,12 @@ __global__ __launch_bounds__(kBlock) void matmul_join_kernel(MatmulArgs p, uint3
 constexpr int kThinWaves = 8;
 constexpr uint32_t kThinPart = 32 * 128;   /* a piece: 32 rows of 128 bytes */
 
-template <int AF, int CDT, int MF>
+template <int AF, int CDT>
 __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs p, int vec) {
   /* staging, then the waves' sums in its place */
-  constexpr uint32_t kSums = kThinWaves * MF * 16 * 64 * 4, kStage = kThinWaves * kThinPart;
-  __shared__ __align__(16) uint8_t stage0[kSums > kStage ? kSums : kStage], stage1[kStage];
+  constexpr uint32_t kSums = kThinWaves * 16 * 64 * 4, kStage = kThinWaves * kThinPart;
+  __shared__ __align__(16) uint8_t stage0[kStage], stage1[kStage];
+  static_assert(kSums <= kStage, "the sums fit");
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const uint32_t r = lane & 31, g = lane >> 5, n0 = blockIdx.x * 32;
@@ -490,22 +491,15 @@ __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs
     upper |= (c >> 2) << i;
   }
   const uint8_t *bs = p.bs + (uint64_t)(n0 + (r < last ? r : last)) * scale_row;
-  const uint8_t *a[MF], *as[MF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const uint64_t ra = i * 32 + r < p.m ? i * 32 + r : p.m - 1;
-    a[i] = p.a + ra * mx_bytes<AF>(p.padded);
-    as[i] = p.as + ra * scale_row;
-  }
-  f32x16 acc[MF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i) acc[i] = f32x16{};
+  const uint64_t ra = r < p.m ? r : p.m - 1;
+  const uint8_t *a = p.a + ra * mx_bytes<AF>(p.padded), *as = p.as + ra * scale_row;
+  f32x16 acc{};
   const uint32_t x = swizzle(r), stages = (groups + 1) / 2;
   /* A piece's A and scales go to registers, its B to LDS. A last piece of one
    * group loads what it has twice, and multiplies it once. */
   struct Piece {
-    u32x4 a[MF][2][2][kHalves<AF>];
-    uint32_t wa[MF][2], wb[2];
+    u32x4 a[2][2][kHalves<AF>];
+    uint32_t wa[2], wb[2];
   };
   auto load = [&](uint32_t stage, Piece &q, uint8_t *lds) {
 #pragma unroll
@@ -513,16 +507,12 @@ __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs
       const uint32_t group = stage * 2 + h < groups ? stage * 2 + h : groups - 1;
       const uint64_t k = mx_bytes<AF>((uint64_t)group * kMxGroup) + g * 16;
       q.wb[h] = *reinterpret_cast<const uint32_t *>(bs + group * 4);
+      q.wa[h] = *reinterpret_cast<const uint32_t *>(as + group * 4);
 #pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        q.wa[i][h] = *reinterpret_cast<const uint32_t *>(as[i] + group * 4);
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-          for (int v = 0; v < kHalves<AF>; ++v)
-            q.a[i][h][ks][v] =
-                *reinterpret_cast<const u32x4 *>(a[i] + k + (ks * kHalves<AF> + v) * 32);
-      }
+        for (int v = 0; v < kHalves<AF>; ++v)
+          q.a[h][ks][v] = *reinterpret_cast<const u32x4 *>(a + k + (ks * kHalves<AF> + v) * 32);
     }
     const uint32_t u = (stage + 1) * 2 > groups ? upper : 0;
 #pragma unroll
@@ -536,15 +526,11 @@ __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs
       if (stage * 2 + h >= groups) break;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        i32x8 vb{};
+        i32x8 vb{}, va{};
         put4(vb, 0, piece(lds + wave * kThinPart, r, 4 * h + 2 * ks + g, x));
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          i32x8 va{};
-          put4(va, 0, q.a[i][h][ks][0]);
-          if constexpr (AF == ZS_MX_E4M3) put4(va, 4, q.a[i][h][ks][1]);
-          acc[i] = mfma<AF>(vb, va, acc[i], q.wb[h] >> (8 * g), q.wa[i][h] >> (8 * g), ks & 1);
-        }
+        put4(va, 0, q.a[h][ks][0]);
+        if constexpr (AF == ZS_MX_E4M3) put4(va, 4, q.a[h][ks][1]);
+        acc = mfma<AF>(vb, va, acc, q.wb[h] >> (8 * g), q.wa[h] >> (8 * g), ks & 1);
       }
     }
   };
@@ -570,24 +556,19 @@ __global__ __launch_bounds__(64 * kThinWaves) void matmul_thin_kernel(MatmulArgs
     }
   }
   __syncthreads();
-  float *sums = reinterpret_cast<float *>(stage0);   /* [wave][MF][16][64] */
+  float *sums = reinterpret_cast<float *>(stage0);   /* [wave][16][64] */
 #pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sums[((wave * MF + i) * 16 + e) * 64 + lane] = acc[i][e];
+  for (int e = 0; e < 16; ++e) sums[(wave * 16 + e) * 64 + lane] = acc[e];
   __syncthreads();
-  /* a thread takes four neighbouring results: fragment i, quarter q, lane l */
-  for (uint32_t t = threadIdx.x; t < MF * 4 * 64; t += 64 * kThinWaves) {
-    const uint32_t i = t / 256, q = (t / 64) & 3, l = t & 63;
-    float v[4] = {0, 0, 0, 0};
+  /* a thread takes four neighbouring results: quarter q of lane l */
+  const uint32_t q = threadIdx.x / 64, l = threadIdx.x & 63;
+  if (q >= 4 || (l & 31) >= p.m) return;
+  float v[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < kThinWaves; ++w)
+  for (int w = 0; w < kThinWaves; ++w)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += sums[((w * MF + i) * 16 + q * 4 + e) * 64 + l];
-    const uint32_t row = i * 32 + (l & 31);
-    if (row < p.m)
-      store_c4<CDT>(p.c, (uint64_t)row * p.ldc, n0 + q * 8 + (l >> 5) * 4, p.n, v, vec);
-  }
+    for (int e = 0; e < 4; ++e) v[e] += sums[(w * 16 + q * 4 + e) * 64 + l];
+  store_c4<CDT>(p.c, (uint64_t)(l & 31) * p.ldc, n0 + q * 8 + (l >> 5) * 4, p.n, v, vec);
 }
 
 }  // namespace zs

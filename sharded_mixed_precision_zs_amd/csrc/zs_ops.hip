@@ -100,7 +100,7 @@ void with_norm_shape(uint64_t padded, F f) {
 }
 
 /* ------------------------------------------------------------------------
- * The product's variant: up to 64 rows of A, bound by B, the thin kernel;
+ * The product's variant: for few rows of A, bound by B, the thin kernel;
  * the large tiles where they occupy every CU, else 128 x 128, and where even
  * these leave three CUs of four idle and K is long, that split along K into
  * pieces of 1024 elements or more, as far as the workspace holds their sums.
@@ -115,6 +115,11 @@ void launch_tile(const MatmulArgs &a, uint32_t splits, hipStream_t s) {
 constexpr uint64_t kMaxMatmulK = 1ull << 22; /* byte offsets in a tile of 256 rows are 32 bits */
 constexpr uint64_t kFullChip = 256; /* blocks that give every CU one */
 
+/* Whether the thin kernel runs: every block reads all of A, which 32 rows of
+ * B to a block repay for a few rows of A, or where tiles would leave half of
+ * the CUs idle (8 x 32000 x 4096 8-bit A: 17 us, 32 rows 27, in tiles 22). */
+bool matmul_thin(uint64_t m, uint64_t n) { return m <= 16 || (m <= 32 && n <= 128 * 128); }
+
 struct MatmulSplit {
   uint32_t splits, groups;   /* groups of 128 elements of K per split */
 };
@@ -127,7 +132,7 @@ MatmulSplit matmul_split(uint64_t m, uint64_t n, uint64_t padded, uint64_t works
   /* four at least: two pieces cost more than they save (512 x 4096 x 4096
    * 4-bit: 25 us against 16 in one), more pay (768 x 768 x 8192 8-bit A: 21
    * against 34; 65 x 4096 x 4096: 13.5 against 17) */
-  if (m <= 64 || splits < 4) return {1, (uint32_t)groups};
+  if (matmul_thin(m, n) || splits < 4) return {1, (uint32_t)groups};
   const uint64_t each = (groups + splits - 1) / splits, four = (each + 3) / 4 * 4;
   return {(uint32_t)((groups + four - 1) / four), (uint32_t)four};
 }
@@ -136,12 +141,11 @@ template <int AF, int CDT>
 int launch_matmul(MatmulArgs a, float *workspace, uint64_t workspace_bytes, hipStream_t s) {
   constexpr uint64_t esz = CDT == ZS_FP32 ? 4 : 2;
   a.split_groups = a.padded / ZS_MX_GROUP;
-  if (a.m <= 64) {
+  if (matmul_thin(a.m, a.n)) {
     /* four results of a lane in one store */
     const int vec = aligned(a.c, 4 * esz) && a.ldc % 4 == 0;
-    const dim3 grid((a.n + 31) / 32), block(64 * kThinWaves);
-    if (a.m <= 32) hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, 1>), grid, block, 0, s, a, vec);
-    else hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, 2>), grid, block, 0, s, a, vec);
+    hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT>), dim3((a.n + 31) / 32), dim3(64 * kThinWaves), 0,
+                       s, a, vec);
     return launch_result();
   }
   constexpr int BM = AF == ZS_MX_E2M1 ? 256 : 128, BN = 256;
