@@ -454,6 +454,63 @@ def test_distill(zs, dt, tail):
 
 
 @pytest.mark.parametrize("dt", [BF16, FP32], ids=str)
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_more_slots_than_threads(zs, dt, tail):
+    """The shortest rows' blocks have 64 threads; the others of a row's slots come later."""
+    for r, v, k in ((3, 900, 300), (70, 1000, 65), (2, 5000, 1024)):
+        announce(f"distill {dt} tail={tail} {r}x{v} slots {k}")
+        z, ids, t, w, lse = distill_inputs(r, v, k, dt, tail, 1.0)
+        loss, grad, bound = ref.distill(z, ids, t, 1.0, lse, w, scale=64.0)
+        ol, og = torch.empty(r, device="cuda"), torch.empty(r, v, dtype=dt, device="cuda")
+        zs.zs_distill(z.cuda(), ids.cuda(), t.cuda(), 1.0, ol, grad=og, row_weight=w.cuda(),
+                      teacher_lse=None if lse is None else lse.cuda(), loss_scale=64.0,
+                      workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+        amp = 1.0
+        if tail:
+            amp = (grad.abs() / bound.clamp(min=1e-300)).amax(1, keepdim=True).clamp(min=1.0) * 4
+        close(og, grad, distill_tolerance(z, bound, grad, dt, 1.0, amp), "grad")
+        size = ((z.double().amax(1) - z.double().amin(1)) + 20) * w.double()
+        close(ol, loss, size * 2.0 ** -20, "loss")
+
+
+@pytest.mark.parametrize("dt,r,v,k,piece", [(BF16, 9000, 700, 5, 1000), (BF16, 2500, 16001, 130, 500),
+                                            (FP32, 1200, 13000, 3, 250), (BF16, 700, 70003, 20, 100)],
+                         ids=str)
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_more_rows_than_blocks(zs, dt, r, v, k, piece, tail):
+    """Blocks that go on to further rows give the bits of calls with a row to a block."""
+    announce(f"distill {dt} tail={tail} {r}x{v} slots {k}")
+    g = gen("rows", r, v, k)
+    z = torch.randn(r, v, device="cuda", generator=torch.Generator("cuda").manual_seed(7)).to(dt)
+    ids = torch.randint(-1, v, (r, k), generator=g, dtype=torch.int32).cuda()
+    t = randn(g, r, k).to(dt).cuda()
+    w = torch.randint(0, 4, (r,), generator=g).float().cuda()   # a quarter of the rows is skipped
+    lse = (torch.logsumexp(t.float(), 1) + 0.2) if tail else None
+    i = torch.int32 if dt == FP32 else torch.int16
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+
+    def run(z, ids, t, w, lse, grad):
+        loss = torch.empty(z.shape[0], device="cuda")
+        zs.zs_distill(z, ids, t, 1.0, loss, grad=grad, teacher_lse=lse, row_weight=w, workspace=ws)
+        return loss
+
+    grad = torch.full_like(z, 7.0)
+    loss = run(z, ids, t, w, lse, grad)
+    assert torch.equal(run(z, ids, t, w, lse, None), loss)
+    whole = torch.full_like(z, 7.0)   # a gradient aligned unlike its logits takes another kernel
+    for a in range(0, r, piece):
+        b = min(a + piece, r)
+        part = whole[a:b]
+        ol = run(z[a:b], ids[a:b], t[a:b], w[a:b], None if lse is None else lse[a:b], part)
+        assert torch.equal(ol, loss[a:b]), a
+        assert torch.equal(part.view(i), grad[a:b].view(i)), a
+    inplace = z.clone()
+    assert torch.equal(run(inplace, ids, t, w, lse, inplace), loss)
+    assert torch.equal(inplace.view(i), grad.view(i))
+    assert bool(torch.isfinite(loss).all()) and not bool(grad[w == 0].any())
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32], ids=str)
 def test_distill_strided_rows(zs, dt):
     """Logits and gradient in wider buffers, at offsets of their own."""
     for r, v, ld, off, gld, goff in ((3, 1000, 1008, 8, 1008, 8), (5, 999, 1003, 1, 1003, 1),
