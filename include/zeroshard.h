@@ -488,7 +488,8 @@ int zs_step_device(const zs_step_args *a, zs_device_scaler *dev, void *stream, v
  * device pointers, caller's buffers and workspaces, work enqueued on
  * `stream`, argument errors before anything is enqueued, no wait. All of
  * them can be captured into a HIP graph. Outputs that overlap an input or
- * each other are refused (ZS_ERR_ALIAS) except where stated. The same
+ * each other are refused (ZS_ERR_ALIAS) except where stated, and calls that
+ * would take a launch of 2^32 threads or more (ZS_ERR_UNSUPPORTED). The same
  * inputs give the same bits on every call.
  *
  * Microscaled rows. A matrix of `rows` x K elements is kept as codes and

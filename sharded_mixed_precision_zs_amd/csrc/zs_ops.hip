@@ -27,7 +27,10 @@ using zs_host::launch_result;
 using zs_host::overlaps;
 using zs_host::too_big;
 
-constexpr uint64_t kMaxGrid = 0x7fffffffull;
+constexpr uint64_t kMaxVocab = 0x7fffffffull;   /* token ids are 31 bits */
+
+/* Whether a launch may have so many blocks: its threads are counted in 32 bits. */
+bool fits(uint64_t blocks, uint64_t threads) { return blocks <= 0xffffffffull / threads; }
 
 bool valid16(int dt) { return dt == ZS_BF16 || dt == ZS_FP16; }
 bool valid_any(int dt) { return valid16(dt) || dt == ZS_FP32; }
@@ -105,11 +108,15 @@ void with_norm_shape(uint64_t padded, F f) {
  * these leave three CUs of four idle and K is long, that split along K into
  * pieces of 1024 elements or more, as far as the workspace holds their sums.
  * ---------------------------------------------------------------------- */
+int too_large() { return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: too large for one launch%s"); }
+
 template <int AF, int CDT, int BM, int BN, int NW>
-void launch_tile(const MatmulArgs &a, uint32_t splits, hipStream_t s) {
+int launch_tile(const MatmulArgs &a, uint32_t splits, hipStream_t s) {
   const uint64_t tiles = (uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN);
+  if (!fits(tiles, 64 * NW)) return too_large();
   hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN, NW>), dim3((unsigned)tiles, splits),
                      dim3(64 * NW), 0, s, a);
+  return launch_result();
 }
 
 constexpr uint64_t kMaxMatmulK = 1ull << 22; /* byte offsets in a tile of 256 rows are 32 bits */
@@ -144,24 +151,22 @@ int launch_matmul(MatmulArgs a, float *workspace, uint64_t workspace_bytes, hipS
   if (matmul_thin(a.m, a.n)) {
     /* four results of a lane in one store */
     const int vec = aligned(a.c, 4 * esz) && a.ldc % 4 == 0;
-    hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT>), dim3((a.n + 31) / 32), dim3(64 * kThinWaves), 0,
-                       s, a, vec);
+    const uint32_t blocks = (a.n + 31) / 32;
+    if (!fits(blocks, 64 * kThinWaves)) return too_large();
+    hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT>), dim3(blocks), dim3(64 * kThinWaves), 0, s, a,
+                       vec);
     return launch_result();
   }
   constexpr int BM = AF == ZS_MX_E2M1 ? 256 : 128, BN = 256;
-  if ((uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN) >= kFullChip) {
-    launch_tile<AF, CDT, BM, BN, AF == ZS_MX_E2M1 ? 8 : 4>(a, 1, s);
-    return launch_result();
-  }
+  if ((uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN) >= kFullChip)
+    return launch_tile<AF, CDT, BM, BN, AF == ZS_MX_E2M1 ? 8 : 4>(a, 1, s);
+
   const MatmulSplit sp = matmul_split(a.m, a.n, a.padded, workspace_bytes);
-  if (sp.splits < 2) {
-    launch_tile<AF, CDT, 128, 128, 4>(a, 1, s);
-    return launch_result();
-  }
+  if (sp.splits < 2) return launch_tile<AF, CDT, 128, 128, 4>(a, 1, s);
+
   a.part = workspace;
   a.split_groups = sp.groups;
-  launch_tile<AF, ZS_FP32, 128, 128, 4>(a, sp.splits, s);
-  if (int rc = launch_result()) return rc;
+  if (int rc = launch_tile<AF, ZS_FP32, 128, 128, 4>(a, sp.splits, s)) return rc;
   const uint64_t all = (uint64_t)a.m * a.n;
   hipLaunchKernelGGL((matmul_join_kernel<CDT>), dim3((unsigned)((all + kBlock - 1) / kBlock)),
                      dim3(kBlock), 0, s, a, sp.splits);
@@ -218,19 +223,25 @@ int zs_rmsnorm_forward(const void *x, const void *residual, const void *gain, in
              codes, scales, rows, (uint32_t)cols, (uint32_t)padded, eps, 1.0 / (double)cols};
   const bool al = cols % 8 == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(gain, 16) &&
                   aligned(h, 16) && aligned(y, 16);
-  if (rows > kMaxGrid) return fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: too many rows%s");
   hipStream_t s = static_cast<hipStream_t>(stream);
+  int rc = ZS_OK;
   with16(dtype, [&](auto dt) {
     with_bool(al, [&](auto v) {
       with_norm_shape(padded, [&](auto g, auto items) {
         constexpr int G = decltype(g)::value, block = G < 256 ? 256 : G, per = block / G;
+        const uint64_t blocks = (rows + per - 1) / per;
+        if (!fits(blocks, block)) {
+          rc = fail(ZS_ERR_UNSUPPORTED, "zs_rmsnorm_forward: too many rows for one launch%s");
+          return;
+        }
         hipLaunchKernelGGL((norm_kernel<decltype(dt)::value, decltype(v)::value, G,
                                         decltype(items)::value>),
-                           dim3((unsigned)((rows + per - 1) / per)), dim3(block), 0, s, a);
+                           dim3((unsigned)blocks), dim3(block), 0, s, a);
+        rc = launch_result();
       });
     });
   });
-  return launch_result();
+  return rc;
 }
 
 uint64_t zs_rmsnorm_backward_workspace(uint64_t rows, uint64_t cols) {
@@ -335,7 +346,7 @@ int zs_mx_quantize(const void *src, int src_dtype, uint64_t rows, uint64_t cols,
   } else {
     grid_x = (a.vecs + kBlock - 1) / kBlock;
   }
-  if (grid_x > kMaxGrid || grid_y > 65535)
+  if (!fits(grid_x, kBlock) || grid_y > 65535)
     return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: too large for one launch%s");
   const dim3 grid((unsigned)grid_x, (unsigned)grid_y);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -374,8 +385,7 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
     return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: fp32 results need 4-bit operands%s");
   if (ldc < n) return fail(ZS_ERR_INVALID_ARG, "zs_mx_matmul: ldc below n%s");
   constexpr uint64_t kMaxDim = 1ull << 30;
-  if (m > kMaxDim || n > kMaxDim || k > kMaxMatmulK || matrix_too_big(m, ldc) ||
-      m / 128 * (n / 128) > kMaxGrid / 4)
+  if (m > kMaxDim || n > kMaxDim || k > kMaxMatmulK || matrix_too_big(m, ldc))
     return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: m or n above 2^30, or k above 2^22%s");
   if (m == 0 || n == 0) return ZS_OK;
   if (!c || (k && (!a_codes || !a_scales || !b_codes || !b_scales)))
@@ -506,7 +516,7 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
     return fail(ZS_ERR_INVALID_ARG, "zs_distill: temperature must be finite and > 0%s");
   if (!dev && (!(loss_scale > 0.0f) || !isfinite(loss_scale)))
     return fail(ZS_ERR_INVALID_ARG, "zs_distill: loss_scale must be finite and > 0%s");
-  if (vocab == 0 || vocab > kMaxGrid || ld < vocab || (grad && grad_ld < vocab))
+  if (vocab == 0 || vocab > kMaxVocab || ld < vocab || (grad && grad_ld < vocab))
     return fail(ZS_ERR_INVALID_ARG,
                 "zs_distill: need 0 < vocab < 2^31 and rows at least vocab apart%s");
   if (slots > kMaxSlots) return fail(ZS_ERR_UNSUPPORTED, "zs_distill: more than 1024 slots%s");
@@ -541,8 +551,6 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
       if (overlaps(outs[i], out_bytes[i], outs[j], out_bytes[j]))
         return fail(ZS_ERR_ALIAS, "zs_distill: two outputs overlap%s");
   }
-  if (rows > kMaxGrid || rows * sp.parts > kMaxGrid)
-    return fail(ZS_ERR_UNSUPPORTED, "zs_distill: too many rows%s");
   DistillArgs a{};
   a.z = logits;
   a.ids = ids;
@@ -567,6 +575,9 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
                 (grad_ld - ld) * esz % 16 == 0;
   /* such a gradient is not the logits' own buffer: its slots' logits stay */
   if (!sp.parts && grad && !a.vec_store) sp = {1, sp.vecs, sp.vecs};
+  /* rows are counted in 32 bits, with room for a grid more */
+  if (rows >= 1ull << 31 || (sp.parts && !fits(rows * sp.parts, kDistillThreads)))
+    return fail(ZS_ERR_UNSUPPORTED, "zs_distill: too many rows%s");
   a.parts = sp.parts;
   a.part_vecs = sp.part_vecs;
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -23,11 +23,10 @@ struct QuantArgs {
 /* Along the rows: eight elements per thread, a block per quad of lanes. */
 template <int DT, bool AL, int FMT, int VDT>
 __global__ __launch_bounds__(kBlock) void quant_rows_kernel(QuantArgs a) {
-  const uint64_t id = (uint64_t)blockIdx.x * kBlock + threadIdx.x;
+  const uint32_t id = blockIdx.x * kBlock + threadIdx.x;   /* a launch has below 2^32 */
   if (id >= a.vecs) return;   /* whole quads: a row has a multiple of 16 vectors */
-  const uint64_t vpr = a.padded / 8;
-  const uint64_t row = a.vecs >> 32 ? id / vpr : (uint32_t)id / (uint32_t)vpr;
-  const uint64_t v = id - row * vpr;
+  const uint32_t vpr = (uint32_t)(a.padded / 8);
+  const uint64_t row = id / vpr, v = id % vpr;
   constexpr uint64_t esz = DT == ZS_FP32 ? 4 : 2;
   float x[8];
   load8<DT, AL>(static_cast<const char *>(a.src) + row * a.ld * esz, v * 8, a.cols, x);

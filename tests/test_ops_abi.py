@@ -120,6 +120,19 @@ def test_bad_arguments_are_refused(zs, name, change, status):
     assert zs.zs_last_error()
 
 
+@pytest.mark.parametrize("name,change", [
+    ("quantize", dict(rows=1 << 27, cols=1024, ld=1024, values=None)),
+    ("matmul", dict(m=1, n=1 << 29, ldc=1 << 29)),
+    ("matmul", dict(m=1 << 26, n=1 << 13, ldc=1 << 13)),
+    ("forward", dict(rows=1 << 27)),
+    ("distill", dict(rows=1 << 31, vocab=16, ld=16, gld=16, wsb=1 << 36)),
+    ("distill", dict(rows=1 << 26, vocab=5, ld=5, gld=5, wsb=1 << 36)),
+])
+def test_more_threads_than_a_launch_has_are_refused(zs, name, change):
+    fn, args = calls(zs)[name]
+    assert fn(*{**args, **change}.values()) == UNSUPPORTED
+
+
 def test_a_workspace_too_small_is_refused(zs):
     need = zs.zs_distill_workspace(8, 1 << 20, 4, zs.ZS_FP32)
     assert need > 0
