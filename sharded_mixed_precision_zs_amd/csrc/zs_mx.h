@@ -161,12 +161,10 @@ __device__ __forceinline__ void load8(const void *row, uint64_t col, uint64_t co
   }
 }
 
-/* Eight 16-bit elements of a row, rounded to nearest even. */
-template <int DT, bool AL>
-__device__ __forceinline__ void store8(uint16_t *row, uint64_t col, uint64_t cols,
-                                       const float (&x)[8]) {
-  const u32x4 w = {pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
-                   pack2<DT>(x[6], x[7])};
+/* Eight 16-bit elements of a row. */
+template <bool AL>
+__device__ __forceinline__ void store8_raw(uint16_t *row, uint64_t col, uint64_t cols,
+                                           const u32x4 &w) {
   if constexpr (AL) {
     if (col < cols) *reinterpret_cast<u32x4 *>(row + col) = w;
   } else if (col + 8 <= cols) {
@@ -176,6 +174,14 @@ __device__ __forceinline__ void store8(uint16_t *row, uint64_t col, uint64_t col
     for (int j = 0; j < 7; ++j)
       if (col + j < cols) row[col + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
   }
+}
+
+/* The same, rounded to nearest even. */
+template <int DT, bool AL>
+__device__ __forceinline__ void store8(uint16_t *row, uint64_t col, uint64_t cols,
+                                       const float (&x)[8]) {
+  store8_raw<AL>(row, col, cols, u32x4{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
+                                       pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
 }
 
 /* Sum over the G threads of a row's group, on all of them; a fixed tree, so

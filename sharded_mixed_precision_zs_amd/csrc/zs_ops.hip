@@ -341,7 +341,9 @@ int zs_mx_quantize(const void *src, int src_dtype, uint64_t rows, uint64_t cols,
                   aligned(values, 16);
   uint64_t grid_x, grid_y = 1;
   if (columns) {
-    grid_x = (cols + kColTileC - 1) / kColTileC;
+    const uint64_t across = kColTileW * (src_dtype == ZS_FP32 ? kColsPerWord<ZS_FP32>
+                                                              : kColsPerWord<ZS_BF16>);
+    grid_x = (cols + across - 1) / across;
     grid_y = padded / kColTileR;
   } else {
     grid_x = (a.vecs + kBlock - 1) / kBlock;

@@ -46,80 +46,130 @@ __global__ __launch_bounds__(kBlock) void quant_rows_kernel(QuantArgs a) {
   }
 }
 
-/* Along the columns: a block takes 128 rows (one group) of 64 columns
- * through LDS, as float; then each thread holds one column's block of 32, the
- * four blocks of a column in neighbouring lanes, which write whole lines
- * together. A row stride of 65 floats and 16 more for every 32 rows keep both
- * ways of walking the tile off each other's banks. */
-constexpr uint32_t kColTileR = 128, kColTileC = 64;
+/* Along the columns: a block takes 128 rows (one group) of 64 words, one
+ * column of fp32 or two of 16 bits each, through LDS; then each thread holds
+ * a word's column or columns of 32 rows, the four blocks of a column in
+ * neighbouring lanes, which write whole lines together. A row stride of 65
+ * words and 16 more for every 32 rows keep both ways of walking the tile off
+ * each other's banks. */
+constexpr uint32_t kColTileR = 128, kColTileW = 64;
 
-__device__ __forceinline__ uint32_t col_row(uint32_t r) { return r * (kColTileC + 1) + r / 32 * 16; }
+template <int DT>
+constexpr uint32_t kColsPerWord = DT == ZS_FP32 ? 1 : 2;
+
+__device__ __forceinline__ uint32_t col_row(uint32_t r) { return r * (kColTileW + 1) + r / 32 * 16; }
 
 template <int DT, bool AL, int FMT, int VDT>
 __global__ __launch_bounds__(kBlock) void quant_cols_kernel(QuantArgs a) {
-  __shared__ float tile[kColTileR * (kColTileC + 1) + 48];
+  __shared__ uint32_t tile[kColTileR * (kColTileW + 1) + 48];
   constexpr uint64_t esz = DT == ZS_FP32 ? 4 : 2;
-  const uint64_t r0 = (uint64_t)blockIdx.y * kColTileR, c0 = (uint64_t)blockIdx.x * kColTileC;
-  const uint32_t t = threadIdx.x;
+  /* P columns per word; W words to a thread's eight columns, kAcross threads
+   * to a row and kDown rows at a time */
+  constexpr uint32_t P = kColsPerWord<DT>, W = 8 / P, kAcross = kColTileW / W;
+  constexpr uint32_t kDown = kBlock / kAcross, kPasses = kColTileR / kDown;
+  const uint64_t r0 = (uint64_t)blockIdx.y * kColTileR;
+  const uint64_t c0 = (uint64_t)blockIdx.x * kColTileW * P;
+  const uint32_t t = threadIdx.x, tr = t / kAcross, tw = t % kAcross * W;
+  uint32_t raw[kPasses][W];   /* all of a thread's loads are under way together */
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lr = i * 32 + t / 8, lc = (t % 8) * 8;
-    float x[8];
-    if (r0 + lr < a.rows) {
-      load8<DT, AL>(static_cast<const char *>(a.src) + (r0 + lr) * a.ld * esz, c0 + lc, a.cols, x);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) tile[col_row(lr) + lc + j] = x[j];
-  }
-  __syncthreads();
-  const uint32_t lc = t / 4, blk = t % 4;   /* a column and its block of 32 rows */
-  if (c0 + lc < a.cols) {
-    constexpr uint32_t kColStride = kColTileC + 1;
-    float *col = tile + col_row(blk * 32) + lc;
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) top = umax(top, mag_bits(col[j * kColStride]));
-    const uint32_t byte = mx_scale_byte<FMT>(top);
-    uint32_t words[8];
-#pragma unroll
-    for (int o = 0; o < 4; ++o) {
+  for (uint32_t i = 0; i < kPasses; ++i) {
+    const uint64_t row = r0 + i * kDown + tr;
+    const char *src = static_cast<const char *>(a.src) + row * a.ld * esz;
+    const uint64_t cols = row < a.rows ? a.cols : 0;   /* past the last row: zeros */
+    if constexpr (P == 1) {
       float x[8];
-      uint32_t code[2];
+      load8<DT, AL>(src, c0 + tw, cols, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = col[(o * 8 + j) * kColStride];
-      mx_encode<FMT>(x, byte, code);
-      if constexpr (FMT == ZS_MX_E2M1) {
-        words[o] = code[0];
-      } else {
-        words[2 * o] = code[0];
-        words[2 * o + 1] = code[1];
+      for (uint32_t j = 0; j < W; ++j) raw[i][j] = __float_as_uint(x[j]);
+    } else {
+      const Raw16<8> x = load8_raw<AL>(src, c0 + tw * P, cols);
+#pragma unroll
+      for (uint32_t j = 0; j < W; ++j) raw[i][j] = x.w[j];
+    }
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < kPasses; ++i)
+#pragma unroll
+    for (uint32_t j = 0; j < W; ++j) tile[col_row(i * kDown + tr) + tw + j] = raw[i][j];
+  __syncthreads();
+  const uint32_t lw = t / 4, blk = t % 4;   /* a word and its block of 32 rows */
+  constexpr uint32_t kStride = kColTileW + 1, kWords = FMT == ZS_MX_E2M1 ? 4 : 8;
+  uint32_t *col = tile + col_row(blk * 32) + lw;
+  if (c0 + lw * P < a.cols) {
+    uint32_t w[32], code[P][kWords], byte[P];
+#pragma unroll
+    for (uint32_t j = 0; j < 32; ++j) w[j] = col[j * kStride];
+    auto value = [&](uint32_t j, uint32_t p) {
+      if constexpr (P == 1) return __uint_as_float(w[j]);
+      else return p ? up_hi<DT>(w[j]) : up_lo<DT>(w[j]);
+    };
+#pragma unroll
+    for (uint32_t p = 0; p < P; ++p) {
+      uint32_t top = 0;
+#pragma unroll
+      for (uint32_t j = 0; j < 32; ++j) top = umax(top, mag_bits(value(j, p)));
+      byte[p] = mx_scale_byte<FMT>(top);
+#pragma unroll
+      for (uint32_t o = 0; o < 4; ++o) {
+        float x[8];
+        uint32_t c[2];
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) x[j] = value(o * 8 + j, p);
+        mx_encode<FMT>(x, byte[p], c);
+        if constexpr (FMT == ZS_MX_E2M1) {
+          code[p][o] = c[0];
+        } else {
+          code[p][2 * o] = c[0];
+          code[p][2 * o + 1] = c[1];
+        }
       }
-      if (a.values) {
-        mx_decode<FMT>(code, byte, x);
+      const uint64_t orow = c0 + lw * P + p, k = r0 + blk * 32;
+      if (orow < a.cols) {
+        u32x4 *out = reinterpret_cast<u32x4 *>(a.codes + orow * mx_bytes<FMT>(a.padded) +
+                                               mx_bytes<FMT>(k));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) col[(o * 8 + j) * kColStride] = x[j];
+        for (uint32_t q = 0; q < kWords / 4; ++q)
+          out[q] = u32x4{code[p][4 * q], code[p][4 * q + 1], code[p][4 * q + 2],
+                         code[p][4 * q + 3]};
+        a.scales[orow * (a.padded / kMxBlock) + k / kMxBlock] = (uint8_t)byte[p];
       }
     }
-    const uint64_t orow = c0 + lc, k = r0 + blk * 32;
-    u32x4 *out = reinterpret_cast<u32x4 *>(a.codes + orow * mx_bytes<FMT>(a.padded) +
-                                           mx_bytes<FMT>(k));
-    out[0] = u32x4{words[0], words[1], words[2], words[3]};
-    if constexpr (FMT == ZS_MX_E4M3) out[1] = u32x4{words[4], words[5], words[6], words[7]};
-    a.scales[orow * (a.padded / kMxBlock) + k / kMxBlock] = (uint8_t)byte;
+    if (a.values) {   /* they take the source's place in the tile */
+#pragma unroll
+      for (uint32_t o = 0; o < 4; ++o) {
+        float x[P][8];
+#pragma unroll
+        for (uint32_t p = 0; p < P; ++p) {
+          uint32_t c[2] = {code[p][FMT == ZS_MX_E2M1 ? o : 2 * o], 0};
+          if constexpr (FMT == ZS_MX_E4M3) c[1] = code[p][2 * o + 1];
+          mx_decode<FMT>(c, byte[p], x[p]);
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+          uint32_t v;
+          if constexpr (P == 1) v = __float_as_uint(x[0][j]);
+          else v = pack2<VDT>(x[0][j], x[1][j]);
+          col[(o * 8 + j) * kStride] = v;
+        }
+      }
+    }
   }
   if (!a.values) return;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lr = i * 32 + t / 8, vc = (t % 8) * 8;
-    if (r0 + lr >= a.rows) break;
-    float x[8];
+  for (uint32_t i = 0; i < kPasses; ++i) {
+    const uint64_t row = r0 + i * kDown + tr;
+    if (row >= a.rows) break;
+    const uint32_t *from = tile + col_row(i * kDown + tr) + tw;
+    uint16_t *to = a.values + row * a.cols;
+    if constexpr (P == 1) {
+      float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = tile[col_row(lr) + vc + j];
-    store8<VDT, AL>(a.values + (r0 + lr) * a.cols, c0 + vc, a.cols, x);
+      for (uint32_t j = 0; j < 8; ++j) x[j] = __uint_as_float(from[j]);
+      store8<VDT, AL>(to, c0 + tw, a.cols, x);
+    } else {
+      store8_raw<AL>(to, c0 + tw * P, a.cols, u32x4{from[0], from[1], from[2], from[3]});
+    }
   }
 }
 
