@@ -336,21 +336,23 @@ int zs_mx_quantize(const void *src, int src_dtype, uint64_t rows, uint64_t cols,
         return fail(ZS_ERR_ALIAS, "zs_mx_quantize: two outputs overlap%s");
   }
   QuantArgs a{src, rows, cols, ld, codes, scales, static_cast<uint16_t *>(values), padded,
-              rows * (padded / 8)};
+              rows * (padded / 8), 0, 0};
   const bool al = cols % 8 == 0 && aligned(src, 16) && ld * esize(src_dtype) % 16 == 0 &&
                   aligned(values, 16);
-  uint64_t grid_x, grid_y = 1;
+  uint64_t blocks = (a.vecs + kBlock - 1) / kBlock;
   if (columns) {
     const uint64_t across = kColTileW * (src_dtype == ZS_FP32 ? kColsPerWord<ZS_FP32>
                                                               : kColsPerWord<ZS_BF16>);
-    grid_x = (cols + across - 1) / across;
-    grid_y = padded / kColTileR;
-  } else {
-    grid_x = (a.vecs + kBlock - 1) / kBlock;
+    const uint64_t tiles_c = (cols + across - 1) / across, tiles_r = padded / kColTileR;
+    if (tiles_r > 65535)
+      return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: too many rows along the columns%s");
+    blocks = tiles_c * tiles_r;
+    a.tiles_r = (uint32_t)tiles_r;
+    a.tiles_c = (uint32_t)tiles_c;
   }
-  if (!fits(grid_x, kBlock) || grid_y > 65535)
+  if (!fits(blocks, kBlock))
     return fail(ZS_ERR_UNSUPPORTED, "zs_mx_quantize: too large for one launch%s");
-  const dim3 grid((unsigned)grid_x, (unsigned)grid_y);
+  const dim3 grid((unsigned)blocks);
   hipStream_t s = static_cast<hipStream_t>(stream);
   with_any(src_dtype, [&](auto dt) {
     with16(values ? values_dtype : ZS_BF16, [&](auto vdt) {

@@ -17,6 +17,7 @@ struct QuantArgs {
   uint16_t *values;      /* [rows][cols], optional */
   uint64_t padded;       /* the blocked dimension rounded up to whole groups */
   uint64_t vecs;         /* rows variant: vectors of eight in all */
+  uint32_t tiles_r, tiles_c;   /* columns variant: tiles down and across */
 };
 
 
@@ -52,7 +53,7 @@ __global__ __launch_bounds__(kBlock) void quant_rows_kernel(QuantArgs a) {
  * neighbouring lanes, which write whole lines together. A row stride of 65
  * words and 16 more for every 32 rows keep both ways of walking the tile off
  * each other's banks. */
-constexpr uint32_t kColTileR = 128, kColTileW = 64;
+constexpr uint32_t kColTileR = 128, kColTileW = 64, kColBand = 4;
 
 template <int DT>
 constexpr uint32_t kColsPerWord = DT == ZS_FP32 ? 1 : 2;
@@ -67,8 +68,16 @@ __global__ __launch_bounds__(kBlock) void quant_cols_kernel(QuantArgs a) {
    * to a row and kDown rows at a time */
   constexpr uint32_t P = kColsPerWord<DT>, W = 8 / P, kAcross = kColTileW / W;
   constexpr uint32_t kDown = kBlock / kAcross, kPasses = kColTileR / kDown;
-  const uint64_t r0 = (uint64_t)blockIdx.y * kColTileR;
-  const uint64_t c0 = (uint64_t)blockIdx.x * kColTileW * P;
+  /* Blocks go round the eight XCDs; each XCD takes a run of tiles, and runs
+   * walk down bands of kColBand tiles across: what the groups of a column
+   * write next to each other, its scales above all, then meets in one L2. */
+  const uint32_t total = a.tiles_r * a.tiles_c, per = total / 8, extra = total % 8;
+  const uint32_t xcd = blockIdx.x % 8;
+  const uint32_t id = xcd * per + (xcd < extra ? xcd : extra) + blockIdx.x / 8;
+  const uint32_t band = id / (kColBand * a.tiles_r), in_band = id % (kColBand * a.tiles_r);
+  const uint32_t rest = a.tiles_c - band * kColBand, wide = rest < kColBand ? rest : kColBand;
+  const uint64_t r0 = (uint64_t)(in_band / wide) * kColTileR;
+  const uint64_t c0 = (uint64_t)(band * kColBand + in_band % wide) * kColTileW * P;
   const uint32_t t = threadIdx.x, tr = t / kAcross, tw = t % kAcross * W;
   uint32_t raw[kPasses][W];   /* all of a thread's loads are under way together */
 #pragma unroll
