@@ -121,12 +121,12 @@ __device__ __forceinline__ void mx_decode(const uint32_t (&code)[2], uint32_t by
 struct __attribute__((packed, aligned(2))) Loose16 { uint32_t w[4]; };   /* 8 16-bit elements */
 struct __attribute__((packed, aligned(4))) Loose32 { float x[8]; };
 
-template <bool AL>
+template <bool AL, bool ONCE = false>
 __device__ __forceinline__ Raw16<8> load8_raw(const void *row, uint64_t col, uint64_t cols) {
   Raw16<8> r = {};
   const uint16_t *p = static_cast<const uint16_t *>(row) + col;
   if constexpr (AL) {
-    if (col < cols) r = ld16<8>(p);
+    if (col < cols) r = ld16<8, ONCE>(p);
   } else if (col + 8 <= cols) {
     const Loose16 v = *reinterpret_cast<const Loose16 *>(p);
 #pragma unroll
@@ -139,16 +139,16 @@ __device__ __forceinline__ Raw16<8> load8_raw(const void *row, uint64_t col, uin
   return r;
 }
 
-template <int DT, bool AL>
+template <int DT, bool AL, bool ONCE = false>
 __device__ __forceinline__ void load8(const void *row, uint64_t col, uint64_t cols, float (&x)[8]) {
   if constexpr (DT != ZS_FP32) {
-    upcast<8, DT>(load8_raw<AL>(row, col, cols), x);
+    upcast<8, DT>(load8_raw<AL, ONCE>(row, col, cols), x);
   } else {
     const float *p = static_cast<const float *>(row) + col;
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = 0.0f;
     if constexpr (AL) {
-      if (col < cols) ldf<8>(p, x);
+      if (col < cols) ldf_p<8, ONCE>(p, x);
     } else if (col + 8 <= cols) {
       const Loose32 v = *reinterpret_cast<const Loose32 *>(p);
 #pragma unroll

@@ -65,12 +65,12 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
   float h[ITEMS][8];
   double ss = 0.0;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) load8<DT, AL>(x, (uint64_t)(i * G + t) * 8, a.cols, h[i]);
+  for (int i = 0; i < ITEMS; ++i) load8<DT, AL, true>(x, (uint64_t)(i * G + t) * 8, a.cols, h[i]);
   if (r) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       float b[8];
-      load8<DT, AL>(r, (uint64_t)(i * G + t) * 8, a.cols, b);
+      load8<DT, AL, true>(r, (uint64_t)(i * G + t) * 8, a.cols, b);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const uint32_t w = pack2<DT>(h[i][j] + b[j], h[i][j + 1] + b[j + 1]);
@@ -136,10 +136,10 @@ __device__ __forceinline__ void load_grad_row(const NormGradArgs &a, uint64_t ro
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const uint32_t c = (i * G + t) * 8;
-    r.dy[i] = load8_raw<AL>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols);
-    r.h[i] = load8_raw<AL>(static_cast<const uint16_t *>(a.h) + at, c, a.cols);
+    r.dy[i] = load8_raw<AL, true>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols);
+    r.h[i] = load8_raw<AL, true>(static_cast<const uint16_t *>(a.h) + at, c, a.cols);
     if (a.dres)
-      r.dres[i] = load8_raw<AL>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols);
+      r.dres[i] = load8_raw<AL, true>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols);
   }
   r.rstd = a.rstd[row];
 }

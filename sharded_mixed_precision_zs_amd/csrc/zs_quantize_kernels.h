@@ -30,7 +30,7 @@ __global__ __launch_bounds__(kBlock) void quant_rows_kernel(QuantArgs a) {
   const uint64_t row = id / vpr, v = id % vpr;
   constexpr uint64_t esz = DT == ZS_FP32 ? 4 : 2;
   float x[8];
-  load8<DT, AL>(static_cast<const char *>(a.src) + row * a.ld * esz, v * 8, a.cols, x);
+  load8<DT, AL, true>(static_cast<const char *>(a.src) + row * a.ld * esz, v * 8, a.cols, x);
   uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = umax(top, mag_bits(x[j]));
@@ -87,11 +87,11 @@ __global__ __launch_bounds__(kBlock) void quant_cols_kernel(QuantArgs a) {
     const uint64_t cols = row < a.rows ? a.cols : 0;   /* past the last row: zeros */
     if constexpr (P == 1) {
       float x[8];
-      load8<DT, AL>(src, c0 + tw, cols, x);
+      load8<DT, AL, true>(src, c0 + tw, cols, x);
 #pragma unroll
       for (uint32_t j = 0; j < W; ++j) raw[i][j] = __float_as_uint(x[j]);
     } else {
-      const Raw16<8> x = load8_raw<AL>(src, c0 + tw * P, cols);
+      const Raw16<8> x = load8_raw<AL, true>(src, c0 + tw * P, cols);
 #pragma unroll
       for (uint32_t j = 0; j < W; ++j) raw[i][j] = x.w[j];
     }
