@@ -1,7 +1,10 @@
 /*
  * zs_quantize_kernels.h -- microscaled copies of a matrix, along its rows or
  * along its columns (gfx950). Bound by HBM: 4 or 2 bytes in, 17/32 or 33/32
- * out per element, and 2 more where the rounded values are asked for.
+ * out per element, and 2 more where the rounded values are asked for. The
+ * codes stay in the caches for the product; the values, which go into a
+ * buffer of a later time, are stored non-temporally (bf16 8191 x 4096 along
+ * the columns: 33.3 us plain, 32.2).
  */
 #ifndef ZS_QUANTIZE_KERNELS_H
 #define ZS_QUANTIZE_KERNELS_H
@@ -20,8 +23,9 @@ struct QuantArgs {
   uint32_t tiles_r, tiles_c;   /* columns variant: tiles down and across */
 };
 
-
-/* Along the rows: eight elements per thread, a block per quad of lanes. */
+/* Along the rows: eight elements per thread, a block of 32 per quad of lanes,
+ * whose maximum two lane moves join: no LDS and one pass. fp32 50257 x 768 to
+ * E2M1: 26 us (6.8 TB/s), with values 43 (5.8 TB/s). */
 template <int DT, bool AL, int FMT, int VDT>
 __global__ __launch_bounds__(kBlock) void quant_rows_kernel(QuantArgs a) {
   const uint32_t id = blockIdx.x * kBlock + threadIdx.x;   /* a launch has below 2^32 */
@@ -43,7 +47,7 @@ __global__ __launch_bounds__(kBlock) void quant_rows_kernel(QuantArgs a) {
   if ((v & 3) == 0) a.scales[row * (a.padded / kMxBlock) + v / 4] = (uint8_t)byte;
   if (a.values) {
     mx_decode<FMT>(code, byte, x);
-    store8<VDT, AL>(a.values + row * a.cols, v * 8, a.cols, x);
+    store8<VDT, AL, true>(a.values + row * a.cols, v * 8, a.cols, x);
   }
 }
 
@@ -52,7 +56,10 @@ __global__ __launch_bounds__(kBlock) void quant_rows_kernel(QuantArgs a) {
  * a word's column or columns of 32 rows, the four blocks of a column in
  * neighbouring lanes, which write whole lines together. A row stride of 65
  * words and 16 more for every 32 rows keep both ways of walking the tile off
- * each other's banks. */
+ * each other's banks. bf16 8191 x 4096 to E4M3 with values: 32 us, 5.2 TB/s
+ * (one 16-bit column to a word, blocks in the grid's order and plain loads:
+ * 40 us). Bound by HBM, where a tile's 256-byte rows come and its columns'
+ * 128 bytes go; finding the maxima in half the instructions changed nothing. */
 constexpr uint32_t kColTileR = 128, kColTileW = 64, kColBand = 4;
 
 template <int DT>
@@ -175,9 +182,9 @@ __global__ __launch_bounds__(kBlock) void quant_cols_kernel(QuantArgs a) {
       float x[8];
 #pragma unroll
       for (uint32_t j = 0; j < 8; ++j) x[j] = __uint_as_float(from[j]);
-      store8<VDT, AL>(to, c0 + tw, a.cols, x);
+      store8<VDT, AL, true>(to, c0 + tw, a.cols, x);
     } else {
-      store8_raw<AL>(to, c0 + tw * P, a.cols, u32x4{from[0], from[1], from[2], from[3]});
+      store8_raw<AL, true>(to, c0 + tw * P, a.cols, u32x4{from[0], from[1], from[2], from[3]});
     }
   }
 }
