@@ -105,9 +105,12 @@ void with_norm_shape(uint64_t padded, F f) {
 
 /* ------------------------------------------------------------------------
  * The product's variant: for few rows of A, bound by B, the thin kernel;
- * the large tiles where they occupy every CU, else 128 x 128, and where even
- * these leave three CUs of four idle and K is long, that split along K into
- * pieces of 1024 elements or more, as far as the workspace holds their sums.
+ * the large tiles where they occupy every CU (4096^3 of 4 x 4 bits 42 us,
+ * 53 in tiles of 128 x 128; 8 x 4 bits 72 and 82), else 128 x 128 (2048 x
+ * 4096 x 4096 of 4 x 4 bits, whose large tiles fill half of the CUs: 29 us,
+ * large 36), and where even these leave three CUs of four idle and K is long,
+ * that split along K into pieces of 1024 elements or more, as far as the
+ * workspace holds their sums.
  * ---------------------------------------------------------------------- */
 int too_large() { return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: too large for one launch%s"); }
 
@@ -431,8 +434,8 @@ namespace {
  * A row per block where its registers hold it: blocks of 64 to 512 threads
  * of at most 16 vectors of 16 bytes, so that several rows are in flight per
  * CU; rows beyond 8192 vectors take 32 per thread and a CU to themselves.
- * One launch beats the parts' two for a single row too (1 x 128000 bf16: 17 us
- * against 23). In parts otherwise, so many that some 1024 blocks run;
+ * One launch beats the parts' two for a few rows too (13 x 50257: 10 us
+ * against 15; 1 x 128000: 17 against 23). In parts otherwise, so many that some 1024 blocks run;
  * gradient rows that are not aligned as the logits' go there (one part).
  * ---------------------------------------------------------------------- */
 constexpr int kDistillThreads = 256, kRowItems = 32;
