@@ -120,6 +120,37 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
   }
 }
 
+/* Eight elements for the backward pass, which fetches a row ahead: the last
+ * few of a row that is not whole vectors come with what is before them, and
+ * are shifted down when they are used, so that no load waits for another
+ * (8192 x 2047 bf16: 40 us; one by one where they are asked for, 61). */
+template <bool AL>
+__device__ __forceinline__ Raw16<8> load8_ahead(const void *row, uint32_t col, uint32_t cols) {
+  if (AL || cols < 8) return load8_raw<AL, true>(row, col, cols);
+  Raw16<8> r = {};
+  if (col < cols) {
+    const uint32_t at = col + 8 <= cols ? col : cols - 8;
+    const Loose16 v =
+        *reinterpret_cast<const Loose16 *>(static_cast<const uint16_t *>(row) + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = v.w[j];
+  }
+  return r;
+}
+
+template <bool AL>
+__device__ __forceinline__ void settle8(Raw16<8> &r, uint32_t col, uint32_t cols) {
+  if (AL || cols < 8 || col >= cols || col + 8 <= cols) return;
+  const uint32_t k = col + 8 - cols;   /* 1 .. 7 elements too early */
+  if (k & 4) r.w[0] = r.w[2], r.w[1] = r.w[3], r.w[2] = r.w[3] = 0;
+  if (k & 2) r.w[0] = r.w[1], r.w[1] = r.w[2], r.w[2] = r.w[3], r.w[3] = 0;
+  if (k & 1) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) r.w[j] = r.w[j] >> 16 | r.w[j + 1] << 16;
+    r.w[3] >>= 16;
+  }
+}
+
 struct NormGradArgs {
   const void *dy, *h, *gain, *dres;   /* dres optional */
   const float *rstd;
@@ -144,10 +175,10 @@ __device__ __forceinline__ void load_grad_row(const NormGradArgs &a, uint64_t ro
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const uint32_t c = (i * G + t) * 8;
-    r.dy[i] = load8_raw<AL, true>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols);
-    r.h[i] = load8_raw<AL, true>(static_cast<const uint16_t *>(a.h) + at, c, a.cols);
+    r.dy[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols);
+    r.h[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.h) + at, c, a.cols);
     if (a.dres)
-      r.dres[i] = load8_raw<AL, true>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols);
+      r.dres[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols);
   }
   r.rstd = a.rstd[row];
 }
@@ -156,7 +187,7 @@ __device__ __forceinline__ void load_grad_row(const NormGradArgs &a, uint64_t ro
  * its share of dg in registers; norm_gain_kernel adds the shares in order,
  * so the result does not depend on scheduling (no atomics). One barrier a
  * row: the dot product's parts lie in two places in turn. 16384 x 4096 bf16
- * with dres: 105 us and 5 for the shares of dg, 5.1 TB/s of the 537 MB of
+ * with dres: 102 us and 5 for the shares of dg, 5.3 TB/s of the 537 MB of
  * the rows; bound by HBM and, by 4 %, the second launch. */
 template <int DT, bool AL, int G, int ITEMS>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_grad_kernel(NormGradArgs a) {
@@ -182,6 +213,9 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_grad_kernel(NormGradAr
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       float h[8], d[8];
+      settle8<AL>(r.dy[i], (i * G + t) * 8, a.cols);
+      settle8<AL>(r.h[i], (i * G + t) * 8, a.cols);
+      if (a.dres) settle8<AL>(r.dres[i], (i * G + t) * 8, a.cols);
       upcast<8, DT>(r.dy[i], d);
       upcast<8, DT>(r.h[i], h);
 #pragma unroll
