@@ -47,6 +47,37 @@ __device__ __forceinline__ RowScale row_scale(double ss, double inv_cols, float 
   return s;
 }
 
+/* Eight elements of a row, asked for ahead: the last few of a row that is not
+ * whole vectors come with what is before them, and are shifted down when they
+ * are used, so that no load waits for another (8192 x 2047 bf16 backward: 42
+ * us; one by one where they are asked for, 61). */
+template <bool AL>
+__device__ __forceinline__ Raw16<8> load8_ahead(const void *row, uint32_t col, uint32_t cols) {
+  if (AL || cols < 8) return load8_raw<AL, true>(row, col, cols);
+  Raw16<8> r = {};
+  if (col < cols) {
+    const uint32_t at = col + 8 <= cols ? col : cols - 8;
+    const Loose16 v =
+        *reinterpret_cast<const Loose16 *>(static_cast<const uint16_t *>(row) + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = v.w[j];
+  }
+  return r;
+}
+
+template <bool AL>
+__device__ __forceinline__ void settle8(Raw16<8> &r, uint32_t col, uint32_t cols) {
+  if (AL || cols < 8 || col >= cols || col + 8 <= cols) return;
+  const uint32_t k = col + 8 - cols;   /* 1 .. 7 elements too early */
+  if (k & 4) r.w[0] = r.w[2], r.w[1] = r.w[3], r.w[2] = r.w[3] = 0;
+  if (k & 2) r.w[0] = r.w[1], r.w[1] = r.w[2], r.w[2] = r.w[3], r.w[3] = 0;
+  if (k & 1) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) r.w[j] = r.w[j] >> 16 | r.w[j + 1] << 16;
+    r.w[3] >>= 16;
+  }
+}
+
 /* One row per group of G threads (64: four rows per 256-thread block), ITEMS
  * vectors of eight elements per thread: x and the residual are asked for
  * whole before anything waits, and stay in registers until y. 16384 x 4096
@@ -70,15 +101,26 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
   if (row >= a.rows) return;   /* a whole wave; blocks of one row never take it */
   const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.cols;
   const uint16_t *r = a.res ? static_cast<const uint16_t *>(a.res) + row * a.cols : nullptr;
+  Raw16<8> xr[ITEMS], rr[ITEMS];
   float h[ITEMS][8];
   double ss = 0.0;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) load8<DT, AL, true>(x, (uint64_t)(i * G + t) * 8, a.cols, h[i]);
+  for (int i = 0; i < ITEMS; ++i) xr[i] = load8_ahead<AL>(x, (i * G + t) * 8, a.cols);
+  if (r) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) rr[i] = load8_ahead<AL>(r, (i * G + t) * 8, a.cols);
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    settle8<AL>(xr[i], (i * G + t) * 8, a.cols);
+    upcast<8, DT>(xr[i], h[i]);
+  }
   if (r) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       float b[8];
-      load8<DT, AL, true>(r, (uint64_t)(i * G + t) * 8, a.cols, b);
+      settle8<AL>(rr[i], (i * G + t) * 8, a.cols);
+      upcast<8, DT>(rr[i], b);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const uint32_t w = pack2<DT>(h[i][j] + b[j], h[i][j + 1] + b[j + 1]);
@@ -117,37 +159,6 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
       *reinterpret_cast<u32x2 *>(a.codes + row * a.padded + v * 8) = u32x2{code[0], code[1]};
       if ((v & 3) == 0) a.scales[row * (a.padded / kMxBlock) + v / 4] = (uint8_t)byte;
     }
-  }
-}
-
-/* Eight elements for the backward pass, which fetches a row ahead: the last
- * few of a row that is not whole vectors come with what is before them, and
- * are shifted down when they are used, so that no load waits for another
- * (8192 x 2047 bf16: 40 us; one by one where they are asked for, 61). */
-template <bool AL>
-__device__ __forceinline__ Raw16<8> load8_ahead(const void *row, uint32_t col, uint32_t cols) {
-  if (AL || cols < 8) return load8_raw<AL, true>(row, col, cols);
-  Raw16<8> r = {};
-  if (col < cols) {
-    const uint32_t at = col + 8 <= cols ? col : cols - 8;
-    const Loose16 v =
-        *reinterpret_cast<const Loose16 *>(static_cast<const uint16_t *>(row) + at);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = v.w[j];
-  }
-  return r;
-}
-
-template <bool AL>
-__device__ __forceinline__ void settle8(Raw16<8> &r, uint32_t col, uint32_t cols) {
-  if (AL || cols < 8 || col >= cols || col + 8 <= cols) return;
-  const uint32_t k = col + 8 - cols;   /* 1 .. 7 elements too early */
-  if (k & 4) r.w[0] = r.w[2], r.w[1] = r.w[3], r.w[2] = r.w[3] = 0;
-  if (k & 2) r.w[0] = r.w[1], r.w[1] = r.w[2], r.w[2] = r.w[3], r.w[3] = 0;
-  if (k & 1) {
-#pragma unroll
-    for (int j = 0; j < 3; ++j) r.w[j] = r.w[j] >> 16 | r.w[j + 1] << 16;
-    r.w[3] >>= 16;
   }
 }
 
