@@ -106,7 +106,7 @@ void with_norm_shape(uint64_t padded, F f) {
 /* ------------------------------------------------------------------------
  * The product's variant: for few rows of A, bound by B, the thin kernel;
  * the large tiles where they occupy every CU (4096^3 of 4 x 4 bits 42 us,
- * 53 in tiles of 128 x 128; 8 x 4 bits 72 and 82), else 128 x 128 (2048 x
+ * 53 in tiles of 128 x 128; 8 x 4 bits 106 and 120), else 128 x 128 (2048 x
  * 4096 x 4096 of 4 x 4 bits, whose large tiles fill half of the CUs: 29 us,
  * large 36), and where even these leave three CUs of four idle and K is long,
  * that split along K into pieces of 1024 elements or more, as far as the
@@ -128,8 +128,12 @@ constexpr uint64_t kFullChip = 256; /* blocks that give every CU one */
 
 /* Whether the thin kernel runs: every block reads all of A, which 32 rows of
  * B to a block repay for a few rows of A, or where tiles would leave half of
- * the CUs idle (8 x 32000 x 4096 8-bit A: 17 us, 32 rows 27, in tiles 22). */
-bool matmul_thin(uint64_t m, uint64_t n) { return m <= 16 || (m <= 32 && n <= 128 * 128); }
+ * the CUs idle, or spend most of the two passes over an 8-bit A on rows that
+ * are not there (32 x 32000 x 4096: 8-bit A 29 us, in tiles 31; 17 rows 23 and
+ * 31; 4-bit A 20 us, in tiles 16). */
+bool matmul_thin(uint64_t m, uint64_t n, bool wide_a) {
+  return m <= 16 || (m <= 32 && (wide_a || n <= 128 * 128));
+}
 
 struct MatmulSplit {
   uint32_t splits, groups;   /* groups of 128 elements of K per split */
@@ -141,9 +145,9 @@ MatmulSplit matmul_split(uint64_t m, uint64_t n, uint64_t padded, uint64_t works
   if (splits > groups / 8) splits = groups / 8;
   if (splits > workspace_bytes / (m * n * 4)) splits = workspace_bytes / (m * n * 4);
   /* four at least: two pieces cost more than they save (512 x 4096 x 4096
-   * 4-bit: 25 us against 16 in one), more pay (768 x 768 x 8192 8-bit A: 21
-   * against 34; 65 x 4096 x 4096: 13.5 against 17) */
-  if (matmul_thin(m, n) || splits < 4) return {1, (uint32_t)groups};
+   * 4-bit: 25 us against 16 in one), more pay (768 x 768 x 8192 8-bit A: 24
+   * against 53; 65 x 4096 x 4096: 16 against 29) */
+  if (matmul_thin(m, n, false) || splits < 4) return {1, (uint32_t)groups};
   const uint64_t each = (groups + splits - 1) / splits, four = (each + 3) / 4 * 4;
   return {(uint32_t)((groups + four - 1) / four), (uint32_t)four};
 }
@@ -152,13 +156,19 @@ template <int AF, int CDT>
 int launch_matmul(MatmulArgs a, float *workspace, uint64_t workspace_bytes, hipStream_t s) {
   constexpr uint64_t esz = CDT == ZS_FP32 ? 4 : 2;
   a.split_groups = a.padded / ZS_MX_GROUP;
-  if (matmul_thin(a.m, a.n)) {
+  if (matmul_thin(a.m, a.n, AF == ZS_MX_E4M3)) {
     /* four results of a lane in one store */
     const int vec = aligned(a.c, 4 * esz) && a.ldc % 4 == 0;
     const uint32_t blocks = (a.n + 31) / 32;
     if (!fits(blocks, 64 * kThinWaves)) return too_large();
-    hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT>), dim3(blocks), dim3(64 * kThinWaves), 0, s, a,
-                       vec);
+    /* both halves of an 8-bit A in one instruction: 1 x 32000 x 4096 15.6 us,
+     * in two 18.9; 4 rows 18.0 and 19.3; 16 rows 26.6 and 22.5 */
+    if (AF == ZS_MX_E4M3 && a.m <= 4)
+      hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, AF == ZS_MX_E4M3>), dim3(blocks),
+                         dim3(64 * kThinWaves), 0, s, a, vec);
+    else
+      hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, false>), dim3(blocks), dim3(64 * kThinWaves),
+                         0, s, a, vec);
     return launch_result();
   }
   constexpr int BM = AF == ZS_MX_E2M1 ? 256 : 128, BN = 256;
