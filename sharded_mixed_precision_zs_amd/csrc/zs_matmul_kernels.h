@@ -106,6 +106,13 @@ __device__ __forceinline__ void load_lds16(const uint8_t *src, uint8_t *dst) {
   __builtin_amdgcn_global_load_lds((global_void *)src, (lds_void *)dst, 16, 0, 0);
 }
 
+/* A barrier behind which every wave's loads to LDS are there. The barrier
+ * itself does not promise that: it orders what a wave has waited for. */
+__device__ __forceinline__ void loads_barrier() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
 template <int AF>
 __device__ __forceinline__ f32x16 mfma(const i32x8 &b, const i32x8 &a, f32x16 acc, uint32_t sb,
                                        uint32_t sa, bool high) {
@@ -397,7 +404,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs
     read_step<AF, FM, FN>(qa, qb, 3, kPlane, r, g, x, f1);
     multiply_step<AF, FM, FN>(f0, 2, w, acc);
     interleave<AF, FM, FN>();
-    __syncthreads();
+    loads_barrier();
     __builtin_amdgcn_sched_barrier(0);
     /* past the last stage, what is loaded and read here is not used */
     read_step<AF, FM, FN>(next_sa + tm * 128, next_sb + tn * 128, 0, kPlane, r, g, x, f0);
@@ -424,7 +431,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs
       }
     }
     put_scales(0, 0);
-    __syncthreads();
+    loads_barrier();
     load(1, sa1, sb1);
     read_scales<FM, FN>(scales + srow_a, scales + srow_b, r, g, w0);
     read_step<AF, FM, FN>(sa0 + tm * 128, sb0 + tn * 128, 0, kPlane, r, g, x, f0);
@@ -443,7 +450,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs
     multiply_step<AF, FM, FN>(f0, 0, w0, acc);
     multiply_step<AF, FM, FN>(f1, 1, w0, acc);
   }
-  __syncthreads();
+  loads_barrier();   /* the strips below take the place of what was loaded last */
 
   /* Each wave turns strips of 32 rows round in its own part of LDS, so that
    * rows of C go out in runs: 16-byte pieces, swizzled as above. */
