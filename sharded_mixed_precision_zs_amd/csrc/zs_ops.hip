@@ -463,7 +463,12 @@ DistillSplit distill_split(uint64_t rows, uint64_t vocab, int dtype) {
   const uint64_t most = (vecs + kDistillThreads - 1) / kDistillThreads;
   if (parts > most) parts = most;
   if (parts < 1) parts = 1;
-  return {(uint32_t)parts, (uint32_t)((vecs + parts - 1) / parts), (uint32_t)vecs};
+  const uint64_t each = vecs ? (vecs + parts - 1) / parts : 1;
+  /* as many as have vectors: the last part starts at the row's last vector at
+   * the latest (a row that is not aligned has one fewer), and has what comes
+   * after them, so the parts' shares of the vocabulary leave nothing out */
+  parts = vecs ? (vecs + each - 1) / each : 1;
+  return {(uint32_t)parts, (uint32_t)each, (uint32_t)vecs};
 }
 
 /* CUs of the current device (256 if unknown). */

@@ -66,3 +66,41 @@ def test_product_of_8_bits_adds_up_in_32(zs, kind):
                         workspace=ws)
         acc = (2 * k / 64 + 10) * 2.0 ** -24 * mag
         close(out, want, U[BF16] * (want.abs() + acc) + acc + TINY[BF16], f"{m}x{n}x{k}")
+
+
+# ---- distillation --------------------------------------------------------------
+
+def distill(zs, z, ids, t, tau=1.0, lse=None, w=None, scale=1.0, grad=None):
+    """(loss, gradient) of the kernels, on the CPU."""
+    r, v = z.shape
+    loss = torch.empty(r, device="cuda")
+    grad = torch.empty(r, v, dtype=z.dtype, device="cuda") if grad is None else grad
+    need = zs.zs_distill_workspace(r, v, ids.shape[1], zs._float_code(z, "z", True))
+    gpu = [None if x is None else x.cuda() for x in (z, ids, t, lse, w)]
+    zs.zs_distill(*gpu[:3], tau, loss, grad=grad, teacher_lse=gpu[3], row_weight=gpu[4],
+                  loss_scale=scale,
+                  workspace=torch.empty(max(need, 16), dtype=torch.uint8, device="cuda"))
+    return loss.cpu(), grad.cpu()
+
+
+@pytest.mark.parametrize("rows,vocab,dt", [(3, 349189, FP32), (1, 1048585, FP32),
+                                           (2, 1048585, BF16), (1, 2097165, FP16)], ids=str)
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_slots_at_the_end_of_a_long_row(zs, rows, vocab, dt, tail):
+    """Every slot's gradient holds its p, wherever its token lies. Tolerance: U of the
+    type, and 2^-19 of q + p for exponents, sums and products in fp32."""
+    announce(f"distill {dt} tail={tail} {rows}x{vocab}")
+    g = gen("end", rows, vocab)
+    z = torch.randn(rows, vocab, generator=g).to(dt)
+    ids = (vocab - 1 - torch.arange(40)).expand(rows, 40).contiguous().int()
+    ids[:, 30:] = torch.randint(0, vocab // 2, (rows, 10), generator=g, dtype=torch.int32)
+    t = torch.randn(rows, 40, generator=g).to(dt)
+    lse = (torch.logsumexp(t.double(), 1) + 0.3).float() if tail else None
+    loss, grad = distill(zs, z, ids, t, lse=lse, scale=64.0)
+    want, wgrad, bound = ref.distill(z, ids, t, 1.0, lse, None, 64.0)
+    at = ids.long()
+    acc = 2.0 ** -19 * bound.gather(1, at)
+    close(grad.gather(1, at), wgrad.gather(1, at),
+          U[dt] * (wgrad.gather(1, at).abs() + acc) + acc + TINY[dt], "slots' gradients")
+    # terms of the size of the logits' spread (below 20), each to 2^-20
+    close(loss, want, 20 * 2.0 ** -20 + want.abs() * 2.0 ** -20, "loss")
