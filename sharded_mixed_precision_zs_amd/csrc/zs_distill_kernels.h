@@ -13,9 +13,13 @@
  *
  * With the teacher's logsumexp over its whole vocabulary, the mass that it
  * has off the slots, pr, meets the student's, qr, as one more outcome; off
- * the slots the gradient is then q * (1 - pr / qr). qr = (S - sum of the
- * slots' terms) / S: both sums are kept in binary64 over the same fp32 terms,
- * so what cancels cancels exactly, however little is left.
+ * the slots the gradient is then q * (1 - pr / qr). However little qr is, its
+ * sum leaves the slots' terms out as they come (taking them off the whole sum
+ * would leave rounding): a bit for each element in LDS says whether it is a
+ * slot's. Where the sum is below 2^-40, the terms off the slots are formed
+ * 2^96 larger, and so reach down to 2^-222 of the row's largest; what is
+ * smaller counts as none. Gradients off the slots come from terms that are
+ * scaled by their sum's power of two: neither 1 / qr nor pr / qr overflows.
  *
  * Bound by HBM: logits in, gradient out, once each where a block's registers
  * hold the row (distill_row_kernel), the logits twice or three times in parts.
@@ -29,11 +33,12 @@ namespace zs {
 
 constexpr uint32_t kMaxSlots = ZS_DISTILL_MAX_SLOTS;
 
-/* Statistics of one part of a row: maximum and sum of terms. */
+/* Statistics of one part of a row: maximum, and sum of terms 2^lift too large
+ * (the terms off the slots, with a teacher's tail). */
 struct DistillPart {
   double sum;
   float max;
-  float pad;
+  float lift;
 };
 
 struct DistillArgs {
@@ -223,6 +228,19 @@ __device__ __forceinline__ float term(float z, const Shift &s) {
   return exp2_fast(fmaf(z, s.c, -s.whole));
 }
 
+/* The shift that makes terms 2^96 larger, where a sum of those off the slots
+ * below 2^-40 asks for it; false if it does not or cannot be (beyond 2^24 whole
+ * numbers are apart by more). Not for every row: a term near the largest would
+ * have an exponent near 96, and six bits less. */
+constexpr float kLift = 96.0f, kLittle = 9.09494702e-13f;   /* 2^-40 */
+
+__device__ __forceinline__ bool lift(Shift &s, double sum) {
+  const float low = s.whole - kLift;
+  if (!(sum < (double)kLittle) || s.whole - low != kLift) return false;
+  s.whole = low;
+  return true;
+}
+
 /* ------------------------------------------------------------------------
  * The slots of one row, by a whole block of NT threads: the teacher's
  * probabilities and what the loss sums over them.
@@ -257,8 +275,7 @@ __device__ __forceinline__ void pad_slots(uint32_t slots, const SlotLds &s) {
 /* What the reductions over a block pass between its waves. */
 template <int NT>
 struct ReduceLds {
-  float part[5][NT / 64];
-  double dpart[2][NT / 64];
+  float part[8][NT / 64];
 };
 
 /* Sum of the weights of token id's slots. */
@@ -322,16 +339,15 @@ __device__ __forceinline__ void slot_logits(const DistillArgs &a, uint64_t row, 
 struct SlotSums {
   float mass;     /* sum of w */
   float cross;    /* sum of w * ((t - ref) - (u - max u)) */
-  double terms;   /* sum of the distinct slots' terms */
+  float terms;    /* sum of the distinct slots' terms */
 };
 
 /* This thread's share; weights w = exp(t - ref) take the logits' place.
- * All ids are in LDS before this. `term_of(token, logit)`: the token's term
- * with the very bits that it has in the row's sum. */
-template <bool TAIL, int NT, class F>
+ * All ids are in LDS before this. */
+template <bool TAIL, int NT>
 __device__ __forceinline__ SlotSums slot_weights(const DistillArgs &a, float ref, const Shift &sh,
-                                                 const SlotLds &s, F term_of) {
-  SlotSums r{0.0f, 0.0f, 0.0};
+                                                 const SlotLds &s) {
+  SlotSums r{0.0f, 0.0f, 0.0f};
   for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = s.id[k];
     float w = 0.0f;
@@ -341,7 +357,7 @@ __device__ __forceinline__ SlotSums slot_weights(const DistillArgs &a, float ref
       r.mass += w;
       if (!(w == 0.0f)) r.cross += w * ((t - ref) - (zk - sh.max) * a.inv_tau);
       if constexpr (TAIL) {
-        if (!slot_seen(s, k, id)) r.terms += term_of((uint32_t)id, zk);
+        if (!slot_seen(s, k, id)) r.terms += term(zk, sh);
       }
     }
     s.w[k] = w;
@@ -354,28 +370,37 @@ __device__ __forceinline__ SlotSums slot_weights(const DistillArgs &a, float ref
  * rounding's remainder would make the loss infinite. */
 constexpr float kTailFloor = 9.5367431640625e-7f;
 
-/* Loss of a row (without its weight and tau^2) and the factor of the
- * logits off the slots. */
+/* Loss of a row (without its weight and tau^2), the sum of all terms, and
+ * what makes gradients of the terms off the slots: term * up * share * coef. */
 struct RowResult {
-  float loss, off;
+  float loss, total, up, share;
 };
 
+/* sum: of the terms off the slots with TAIL (2^96 too large if `lifted`), of
+ * all terms without. */
 template <bool TAIL>
-__device__ __forceinline__ RowResult row_result(const SlotSums &s, const Shift &sh, double sum) {
+__device__ __forceinline__ RowResult row_result(const SlotSums &s, const Shift &sh, float sum,
+                                                bool lifted) {
   RowResult r;
-  const float log_total = logf((float)sum) - sh.rest;   /* of the terms by the maximum */
+  const float down = lifted ? 1.26217745e-29f : 1.0f;   /* 2^-96 */
+  r.total = TAIL ? sum * down + s.terms : sum;
+  r.up = 1.0f;
+  r.share = 1.0f / r.total;
+  const float log_sum = logf(r.total), log_total = log_sum - sh.rest;   /* by the maximum */
   if constexpr (TAIL) {
     r.loss = s.cross + s.mass * log_total;
     float pr = 1.0f - s.mass;
     pr = pr >= kTailFloor ? pr : 0.0f;   /* NaN mass: the loss is NaN already */
-    const double rest = sum - s.terms;
-    const float qr = rest > 0.0 ? (float)(rest / sum) : 0.0f;
-    if (pr > 0.0f) r.loss += pr * (logf(pr) - logf(qr));
+    const float log_rest = logf(sum) - (lifted ? kLift * 0.69314718f : 0.0f);
+    if (pr > 0.0f) r.loss += pr * (logf(pr) - (log_rest - log_sum));
     /* nothing off the slots: every such term is 0 whatever its factor */
-    r.off = qr > 0.0f ? 1.0f - pr / qr : 1.0f;
+    if (sum > 0.0f) {
+      const uint32_t e = __float_as_uint(sum) >> 23;   /* of 2^(e - 127), at most 2^31 */
+      r.up = __uint_as_float((254 - e) << 23);
+      r.share = __uint_as_float(e << 23) * down / r.total - pr / (sum * r.up);
+    }
   } else {
     r.loss = s.cross / s.mass - logf(s.mass) + log_total;
-    r.off = 1.0f;
   }
   return r;
 }
@@ -397,31 +422,50 @@ __device__ __forceinline__ void store_slots(const DistillArgs &a, void *g, const
 
 /* What a row's sweep multiplies by. */
 struct RowFactors {
-  float total, coef, factor;
+  float total, coef, up, factor;
   bool live;
 };
+
+/* The gradient of a logit off the slots, from its term. */
+template <bool TAIL>
+__device__ __forceinline__ float off_slots(float term, const RowFactors &f) {
+  return (TAIL ? term * f.up : term) * f.factor;
+}
 
 /* From the joined sums: the row's loss (stored by the thread that `says`)
  * and its factors. */
 template <bool TAIL>
 __device__ __forceinline__ RowFactors finish_row(const DistillArgs &a, uint64_t row, float weight,
                                                  bool live, const SlotSums &s, const Shift &sh,
-                                                 double sum, bool says) {
-  const RowResult r = row_result<TAIL>(s, sh, sum);
+                                                 float sum, bool lifted, bool says) {
+  const RowResult r = row_result<TAIL>(s, sh, sum, lifted);
   RowFactors f;
   f.live = live;
-  f.total = (float)sum;
+  f.total = r.total;
   f.coef = (a.dev ? a.dev->scale : a.scale) * a.tau * weight;
-  f.factor = f.coef * r.off / f.total;
+  f.up = r.up;
+  f.factor = TAIL ? f.coef * r.share : f.coef / f.total;
   if (says) a.loss[row] = live ? weight * a.tau * a.tau * r.loss : 0.0f;
   return f;
 }
 
-/* A thread's sum of terms: binary64 where slots' terms are taken out of it. */
-template <bool TAIL>
-struct Sum { typedef float type; };
-template <>
-struct Sum<true> { typedef double type; };
+/* The elements of a row that are slots': a bit for each of a vector's, a byte
+ * for each vector, and a word for the single elements, by the threads that
+ * hold them. */
+template <int DT>
+__device__ __forceinline__ void mark_slot(uint32_t *bits, uint32_t edges, const RowShape &s,
+                                          int32_t id, bool on) {
+  constexpr uint32_t ve = kVecElems<DT>;
+  const uint32_t at = (uint32_t)id - s.head;   /* wraps for the head's */
+  const bool inside = at < s.vecs * ve;
+  const uint32_t v = at / ve;
+  const uint32_t word = inside ? v / 4 : edges;
+  const uint32_t bit = inside                 ? v % 4 * 8 + at % ve
+                       : (uint32_t)id < s.head ? (uint32_t)id
+                                               : 8 + (at - s.vecs * ve);
+  if (on) atomicOr(bits + word, 1u << bit);
+  else bits[word] = 0;
+}
 
 /* ------------------------------------------------------------------------
  * A row per block, held in registers between its statistics and its
@@ -549,9 +593,15 @@ template <int DT, bool TAIL, int NT, int ITEMS>
 __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(DistillArgs a) {
   constexpr uint32_t ve = kVecElems<DT>, esz = DT == ZS_FP32 ? 4 : 2;
   __shared__ ReduceLds<NT> red;
+  constexpr uint32_t kMarks = NT * ITEMS / 4;   /* words; one more for the edges */
+  __shared__ uint32_t marks[TAIL ? kMarks + 1 : 1];
   const SlotLds lds = slot_lds(a.slots);
   pad_slots(a.slots, lds);
   const uint32_t t = threadIdx.x;
+  if constexpr (TAIL) {   /* a row clears its own marks afterwards */
+    for (uint32_t i = t; i <= kMarks; i += NT) marks[i] = 0;
+    __syncthreads();
+  }
   uint32_t row = blockIdx.x;
   RowIn in = open_row<DT, TAIL>(a, row);
   auto slots_ahead = [&](uint32_t r, const RowIn &q, SlotAhead &s) {
@@ -582,9 +632,9 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
     asm volatile("" : "+s"(row));
     const uint32_t next = row + gridDim.x;
     const RowIn after = open_row<DT, TAIL>(a, next < a.rows ? next : row);
-    RowFactors f{1.0f, 0.0f, 0.0f, false};
+    RowFactors f{1.0f, 0.0f, 1.0f, 0.0f, false};
     SlotSums sums{};
-    Shift shift{};
+    Shift shift{}, off{};   /* off: of the terms off the slots */
     float single = -INFINITY;
     if (in.weight != 0.0f) {   /* uniform over the block */
       VecMax<DT> max;
@@ -605,6 +655,10 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
         slot_logits<DT, NT>(a, row, in.z, nullptr, NT, lds);
         top = {fmaxf(top.top, more.top), fmaxf(top.any, more.any)};
       }
+      if constexpr (TAIL) {
+        for (uint32_t k = t; k < a.slots; k += NT)
+          if (lds.id[k] >= 0) mark_slot<DT>(marks, kMarks, in.shape, lds.id[k], true);
+      }
       reduce_put(fmaxf(max.get(), single), MaxOf{}, red.part[0]);
       reduce_put(top.top, MaxOf{}, red.part[1]);
       reduce_put(top.any, MaxOf{}, red.part[2]);
@@ -613,36 +667,64 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
       const float highest = reduce_get<NT>(MaxOf{}, red.part[1]);
       const float ref = TAIL ? in.lse : highest;
       const bool live = TAIL ? reduce_get<NT>(MaxOf{}, red.part[2]) > 0.0f : highest > -INFINITY;
-      typename Sum<TAIL>::type sum = in.edge < a.vocab ? term(single, shift) : 0.0f;
+      off = shift;
+      auto sum_terms = [&] {
+        float sum = in.edge < a.vocab ? term(single, off) : 0.0f;
+        if constexpr (TAIL) {
+          if (in.edge < a.vocab && marks[kMarks] >> t & 1) sum = 0.0f;
+        }
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        float e[ve];
-        unpack_vec<DT>(x[i], e);
-        typename Sum<TAIL>::type some = 0;
+        for (int i = 0; i < ITEMS; ++i) {
+          float e[ve];
+          if constexpr (TAIL) asm volatile("" : "+v"(x[i]));   /* unpacked anew each time */
+          unpack_vec<DT>(x[i], e);
+          float some = 0.0f;
+          if constexpr (TAIL) {
+            const uint32_t m = reinterpret_cast<const uint8_t *>(marks)[i * NT + t];
+            if (m) {
 #pragma unroll
-        for (uint32_t j = 0; j < ve; ++j) some += term(e[j], shift);
-        sum += (int)t < (int)in.shape.vecs - i * NT ? some : 0;
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      sums = slot_weights<TAIL, NT>(a, ref, shift, lds, [&](uint32_t, float zk) {
-        return (double)term(zk, shift);
-      });
+              for (uint32_t j = 0; j < ve; ++j) e[j] = m >> j & 1 ? -INFINITY : e[j];
+            }
+          }
+#pragma unroll
+          for (uint32_t j = 0; j < ve; ++j) some += term(e[j], off);
+          sum += (int)t < (int)in.shape.vecs - i * NT ? some : 0;
+          if constexpr (TAIL) asm volatile("" : "+v"(sum));   /* now, not behind the next branch */
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        return sum;
+      };
+      reduce_put(sum_terms(), SumOf{}, red.part[5]);
+      sums = slot_weights<TAIL, NT>(a, ref, shift, lds);
       reduce_put(sums.mass, SumOf{}, red.part[3]);
       reduce_put(sums.cross, SumOf{}, red.part[4]);
-      reduce_put((double)sum, SumOf{}, red.dpart[0]);
-      if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.dpart[1]);
+      if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.part[6]);
       __syncthreads();
+      float sum = reduce_get<NT>(SumOf{}, red.part[5]);
+      bool lifted = false;
+      if constexpr (TAIL) {
+        lifted = lift(off, sum);   /* uniform over the block */
+        if (lifted) {
+          reduce_put(sum_terms(), SumOf{}, red.part[7]);
+          __syncthreads();
+          sum = reduce_get<NT>(SumOf{}, red.part[7]);
+        }
+      }
       sums.mass = reduce_get<NT>(SumOf{}, red.part[3]);
       sums.cross = reduce_get<NT>(SumOf{}, red.part[4]);
-      if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, red.dpart[1]);
-      f = finish_row<TAIL>(a, row, in.weight, live, sums, shift,
-                           reduce_get<NT>(SumOf{}, red.dpart[0]), t == 0);
+      if constexpr (TAIL) {
+        sums.terms = reduce_get<NT>(SumOf{}, red.part[6]);
+        for (uint32_t k = t; k < a.slots; k += NT)
+          if (lds.id[k] >= 0) mark_slot<DT>(marks, kMarks, in.shape, lds.id[k], false);
+      }
+      f = finish_row<TAIL>(a, row, in.weight, live, sums, shift, sum, lifted, t == 0);
     } else if (t == 0) {
       a.loss[row] = 0.0f;
     }
     if (!f.live) {   /* zeros: terms of -inf */
-      shift.c = 1.0f;
-      shift.whole = f.factor = 0.0f;
+      off.c = 1.0f;
+      off.whole = f.factor = 0.0f;
+      f.up = 1.0f;
       single = -INFINITY;
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) x[i] = empty_vec<DT>();
@@ -653,7 +735,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
     const __amdgpu_buffer_rsrc_t from = row_buffer<DT>(after);
     if (more) slots_ahead(next, after, slot);
     const uint32_t edge = edge_index<DT>(in.shape, t, true, true, a.vocab);
-    if (a.grad && edge < a.vocab) store1<DT>(g, edge, term(single, shift) * f.factor);
+    if (a.grad && edge < a.vocab) store1<DT>(g, edge, off_slots<TAIL>(term(single, off), f));
     if (more) raw_single = fetch_edge<DT>(a, after);
     if (!a.grad) {
 #pragma unroll
@@ -665,7 +747,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
         asm volatile("" : "+v"(x[i]));   /* unpacked anew, not kept since the sum */
         unpack_vec<DT>(x[i], e);
 #pragma unroll
-        for (uint32_t j = 0; j < ve; ++j) e[j] = term(e[j], shift) * f.factor;
+        for (uint32_t j = 0; j < ve; ++j) e[j] = off_slots<TAIL>(term(e[j], off), f);
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, pack_vec<DT>(e)), to,
                                                (int)(t * 16 + i * (NT * 16)), 0,
                                                NT > 64 ? kNonTemporal : 0);
@@ -690,12 +772,36 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
  * then a block per part joins all of its row's and writes its share of the
  * gradient. Two launches and no wait between blocks; a part, read up to three
  * times, is short enough for the caches where few rows make many parts.
+ *
+ * A part's sum leaves the slots out with TAIL: a bit of LDS for every vector,
+ * its number counted modulo the bits there are, says which to look at closely.
  * ---------------------------------------------------------------------- */
-template <int DT, int NT>
+constexpr uint32_t kFilterWords = 1024;
+
+/* -inf in the place of the slots' among N elements from token `first` on. */
+template <uint32_t N>
+__device__ __forceinline__ void leave_slots_out(const SlotLds &s, uint32_t slots, uint32_t first,
+                                                float (&x)[N]) {
+  for (uint32_t k = 0; k < slots; k += 4) {
+    const int4 o = *reinterpret_cast<const int4 *>(s.id + k);
+    const uint32_t at[4] = {(uint32_t)o.x - first, (uint32_t)o.y - first, (uint32_t)o.z - first,
+                            (uint32_t)o.w - first};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (at[i] >= N) continue;
+#pragma unroll
+      for (uint32_t j = 0; j < N; ++j) x[j] = at[i] == j ? -INFINITY : x[j];
+    }
+  }
+}
+
+template <int DT, bool TAIL, int NT>
 __global__ __launch_bounds__(NT) void distill_stats_kernel(DistillArgs a) {
   constexpr uint32_t ve = kVecElems<DT>;
   __shared__ float fpart[NT / 64];
-  __shared__ double dpart[NT / 64];
+  __shared__ double dpart[2][NT / 64];
+  __shared__ uint32_t filter[TAIL ? kFilterWords : 1];
+  const SlotLds lds = slot_lds(a.slots);   /* ids, with TAIL */
   const uint64_t row = blockIdx.x / a.parts;
   const uint32_t part = blockIdx.x % a.parts;
   if (a.weight && a.weight[row] == 0.0f) return;
@@ -706,6 +812,17 @@ __global__ __launch_bounds__(NT) void distill_stats_kernel(DistillArgs a) {
   const uint32_t v0 = part * a.part_vecs;
   const uint32_t v1 = v0 + a.part_vecs < sh.vecs ? v0 + a.part_vecs : sh.vecs;
   const uint32_t edge = edge_index<DT>(sh, threadIdx.x, part == 0, part == a.parts - 1, a.vocab);
+  if constexpr (TAIL) {
+    pad_slots(a.slots, lds);
+    for (uint32_t i = threadIdx.x; i < kFilterWords; i += NT) filter[i] = 0;
+    __syncthreads();
+    for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
+      const int32_t id = a.ids[row * a.slots + k];
+      lds.id[k] = id;
+      const uint32_t v = ((uint32_t)id - sh.head) / ve;   /* ids elsewhere only set a bit more */
+      atomicOr(filter + v / 32 % kFilterWords, 1u << v % 32);
+    }
+  }
   float max = edge < a.vocab ? load1<DT>(z, edge) : -INFINITY;
   for (uint32_t v = v0 + threadIdx.x; v < v1; v += NT) {
     float x[ve];
@@ -716,18 +833,33 @@ __global__ __launch_bounds__(NT) void distill_stats_kernel(DistillArgs a) {
   reduce_put(max, MaxOf{}, fpart);
   __syncthreads();
   max = reduce_get<NT>(MaxOf{}, fpart);
-  const Shift shift = shift_of(max, a.log2_scale);
-  double sum = edge < a.vocab ? (double)term(load1<DT>(z, edge), shift) : 0.0;
-  for (uint32_t v = v0 + threadIdx.x; v < v1; v += NT) {
-    float x[ve];
-    unpack_vec<DT>(zv[v], x);
-#pragma unroll
-    for (uint32_t j = 0; j < ve; ++j) sum += (double)term(x[j], shift);
+  float single[1] = {edge < a.vocab ? load1<DT>(z, edge) : -INFINITY};
+  if constexpr (TAIL) {
+    if (edge < a.vocab) leave_slots_out(lds, a.slots, edge, single);
   }
-  reduce_put(sum, SumOf{}, dpart);
-  __syncthreads();
-  sum = reduce_get<NT>(SumOf{}, dpart);
-  if (threadIdx.x == 0) a.ws[blockIdx.x] = {sum, max, 0.0f};
+  Shift off = shift_of(max, a.log2_scale);
+  double sum;
+  bool lifted = false;
+  for (;;) {
+    sum = edge < a.vocab ? (double)term(single[0], off) : 0.0;
+    for (uint32_t v = v0 + threadIdx.x; v < v1; v += NT) {
+      float x[ve];
+      unpack_vec<DT>(zv[v], x);
+      if constexpr (TAIL) {
+        if (filter[v / 32 % kFilterWords] >> v % 32 & 1)
+          leave_slots_out(lds, a.slots, sh.head + v * ve, x);
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < ve; ++j) sum += (double)term(x[j], off);
+    }
+    reduce_put(sum, SumOf{}, dpart[lifted]);
+    __syncthreads();
+    sum = reduce_get<NT>(SumOf{}, dpart[lifted]);
+    if (!TAIL || lifted) break;
+    lifted = lift(off, sum);   /* uniform over the block */
+    if (!lifted) break;
+  }
+  if (threadIdx.x == 0) a.ws[blockIdx.x] = {sum, max, lifted ? kLift : 0.0f};
   if (part != 0 || !a.ws_z) return;
   for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = a.ids[row * a.slots + k];
@@ -738,11 +870,12 @@ __global__ __launch_bounds__(NT) void distill_stats_kernel(DistillArgs a) {
 /* What turns a part's terms into the row's. They are by its own whole
  * number, so the factor is a power of two and exact; where the two scale
  * differently (beyond 2^60) the part has no terms worth the name. A part of
- * nothing but -inf has the sum 0. */
-__device__ __forceinline__ double part_factor(float max, const Shift &row, float c) {
-  if (max == -INFINITY) return 1.0;
-  const Shift own = shift_of(max, c);
-  return (double)exp2_fast(own.c == row.c ? own.whole - row.whole : -INFINITY);
+ * nothing but -inf has the sum 0, one with a NaN or +inf off the slots a NaN. */
+__device__ __forceinline__ double part_factor(const DistillPart &w, const Shift &row, float c) {
+  const Shift own = shift_of(w.max, c);
+  const float by = own.whole - row.whole;
+  const bool some = w.max != -INFINITY && own.c == row.c && by > -800.0f;
+  return __hiloint2double(some ? (1023 + (int)(by - w.lift)) << 20 : 0, 0);
 }
 
 template <int DT, bool TAIL, int NT>
@@ -762,8 +895,8 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
   const uint32_t v1 = v0 + a.part_vecs < sh.vecs ? v0 + a.part_vecs : sh.vecs;
   const bool first = part == 0, last = part == a.parts - 1;
   const uint32_t edge = edge_index<DT>(sh, threadIdx.x, first, last, a.vocab);
-  RowFactors f{1.0f, 0.0f, 0.0f, false};
-  Shift shift{};
+  RowFactors f{1.0f, 0.0f, 1.0f, 0.0f, false};
+  Shift shift{}, off{};
   SlotSums sums{};
   if (weight != 0.0f) {
     const DistillPart *w = a.ws + row * a.parts;
@@ -772,7 +905,13 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
     shift = shift_of(max, a.log2_scale);
     double sum = 0.0;
     for (uint32_t i = 0; i < a.parts; ++i)
-      sum += w[i].sum * part_factor(w[i].max, shift, a.log2_scale);
+      sum += w[i].sum * part_factor(w[i], shift, a.log2_scale);
+    off = shift;
+    bool lifted = false;
+    if constexpr (TAIL) {
+      lifted = lift(off, sum);
+      if (lifted) sum *= 7.9228162514264338e28;   /* 2^96 */
+    }
     const SlotTop top = slot_ids<DT, NT>(a, row, 0, lds);
     slot_logits<DT, NT>(a, row, z, a.ws_z, 0, lds);
     reduce_put(top.top, MaxOf{}, red.part[1]);
@@ -781,33 +920,29 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
     const float highest = reduce_get<NT>(MaxOf{}, red.part[1]);
     const float ref = TAIL ? a.lse[row] : highest;
     const bool live = TAIL ? reduce_get<NT>(MaxOf{}, red.part[2]) > 0.0f : highest > -INFINITY;
-    sums = slot_weights<TAIL, NT>(a, ref, shift, lds, [&](uint32_t id, float zk) {
-      uint32_t i = id < sh.head ? 0 : (id - sh.head) / ve / a.part_vecs;
-      i = i < a.parts ? i : a.parts - 1;
-      return (double)term(zk, shift_of(w[i].max, a.log2_scale)) *
-             part_factor(w[i].max, shift, a.log2_scale);
-    });
+    sums = slot_weights<TAIL, NT>(a, ref, shift, lds);
     reduce_put(sums.mass, SumOf{}, red.part[3]);
     reduce_put(sums.cross, SumOf{}, red.part[4]);
-    if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.dpart[1]);
+    if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.part[6]);
     __syncthreads();
     sums.mass = reduce_get<NT>(SumOf{}, red.part[3]);
     sums.cross = reduce_get<NT>(SumOf{}, red.part[4]);
-    if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, red.dpart[1]);
-    f = finish_row<TAIL>(a, row, weight, live, sums, shift, sum, first && threadIdx.x == 0);
+    if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, red.part[6]);
+    f = finish_row<TAIL>(a, row, weight, live, sums, shift, (float)sum, lifted,
+                         first && threadIdx.x == 0);
   } else if (first && threadIdx.x == 0) {
     a.loss[row] = 0.0f;
   }
   if (!g) return;
   const u32x4 *zv = reinterpret_cast<const u32x4 *>(z + sh.head * esz);
   if (edge < a.vocab)
-    store1<DT>(g, edge, f.live ? term(load1<DT>(z, edge), shift) * f.factor : 0.0f);
+    store1<DT>(g, edge, f.live ? off_slots<TAIL>(term(load1<DT>(z, edge), off), f) : 0.0f);
   for (uint32_t v = v0 + threadIdx.x; v < v1; v += NT) {
     float x[ve];
     if (f.live) {
       unpack_vec<DT>(zv[v], x);
 #pragma unroll
-      for (uint32_t j = 0; j < ve; ++j) x[j] = term(x[j], shift) * f.factor;
+      for (uint32_t j = 0; j < ve; ++j) x[j] = off_slots<TAIL>(term(x[j], off), f);
     } else {
 #pragma unroll
       for (uint32_t j = 0; j < ve; ++j) x[j] = 0.0f;

@@ -509,8 +509,8 @@ int launch_distill(const DistillArgs &a, const DistillSplit &sp, hipStream_t s) 
   }
   constexpr int NT = kDistillThreads;
   const uint32_t blocks = a.grad ? sp.parts : 1;
-  hipLaunchKernelGGL((distill_stats_kernel<DT, NT>), dim3((unsigned)(a.rows * sp.parts)), dim3(NT),
-                     0, s, a);
+  hipLaunchKernelGGL((distill_stats_kernel<DT, TAIL, NT>), dim3((unsigned)(a.rows * sp.parts)),
+                     dim3(NT), slot_bytes(a.slots), s, a);
   if (int rc = launch_result()) return rc;
   hipLaunchKernelGGL((distill_grad_kernel<DT, TAIL, NT>), dim3((unsigned)(a.rows * blocks)),
                      dim3(NT), slot_bytes(a.slots), s, a, blocks);

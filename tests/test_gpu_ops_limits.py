@@ -104,3 +104,66 @@ def test_distill_slots_at_the_end_of_a_long_row(zs, rows, vocab, dt, tail):
           U[dt] * (wgrad.gather(1, at).abs() + acc) + acc + TINY[dt], "slots' gradients")
     # terms of the size of the logits' spread (below 20), each to 2^-20
     close(loss, want, 20 * 2.0 ** -20 + want.abs() * 2.0 ** -20, "loss")
+
+
+def distill_close(z, got, want, tau, dt):
+    """A term's exponent carries two roundings of 2^-24 of its size, and the exp, the sums
+    and the products some 2^-19: of q + p on the slots, of q + pr q / qr off them."""
+    (loss, grad), (wloss, wgrad, bound) = got, want
+    arg = ((z.double().amax(1, keepdim=True) - z.double()) / tau).clamp(max=90)
+    acc = (wgrad.abs() + 2 * bound) * (arg * 2.0 ** -22 + 2.0 ** -19)
+    close(grad, wgrad, U[dt] * (wgrad.abs() + acc) + acc + TINY[dt], "gradient")
+    # the loss: terms of the size of the logits' spread, weighted by p and pr
+    close(loss, wloss, (arg.amax(1) + 20) * 2.0 ** -20 * tau * tau, "loss")
+
+
+@pytest.mark.parametrize("vocab", [1003, 40000, 140001])   # short and long rows, and in parts
+@pytest.mark.parametrize("dt,tau,gap", [(FP32, 1.0, 20), (FP32, 1.0, 35), (FP32, 1.0, 45),
+                                        (FP32, 1.0, 60), (FP32, 1.0, 80), (BF16, 0.5, 22),
+                                        (FP16, 0.5, 30), (BF16, 1.0, 60)], ids=str)
+def test_distill_with_little_mass_off_the_slots(zs, vocab, dt, tau, gap):
+    """A student that is sure of its slots, the teacher less so: what the student has off
+    them counts however little it is."""
+    announce(f"gap {gap} {dt} tau {tau} vocabulary {vocab}")
+    g = gen("gap", vocab, gap)
+    z = torch.randn(3, vocab, generator=g) * 0.5
+    ids = torch.stack([torch.randperm(vocab, generator=g)[:32] for _ in range(3)]).int()
+    ids[0, :4] = torch.tensor([0, 1, vocab - 1, vocab - 2])    # the ends
+    ids[0, 4:] = torch.arange(16, 44)
+    ids[1, 5], ids[1, 6] = ids[1, 4], -1                       # one twice, one empty
+    z.scatter_add_(1, ids.clamp(min=0).long(), torch.full((3, 32), float(gap)))
+    z[1, int(ids[1, 4])] = float(gap)
+    z = z.to(dt)
+    t = torch.randn(3, 32, generator=g).to(dt)
+    kept = torch.where(ids >= 0, t.double() / tau, -math.inf)
+    lse = (torch.logsumexp(kept, 1) + 0.1).float()
+    want = ref.distill(z, ids, t, tau, lse, None, 64.0)
+    assert torch.isfinite(want[0]).all()
+    distill_close(z, distill(zs, z, ids, t, tau, lse, None, 64.0), want, tau, dt)
+    if dt == FP32:   # in place, and a gradient whose rows are aligned otherwise
+        place = z.cuda()
+        loss, grad = distill(zs, place, ids, t, tau, lse, None, 64.0, grad=place)
+        distill_close(z, (loss, grad), want, tau, dt)
+        wide = torch.empty(3, vocab + 3, device="cuda")
+        distill_close(z, distill(zs, z, ids, t, tau, lse, None, 64.0, grad=wide[:, 1:vocab + 1]), want,
+                      tau, dt)
+
+
+@pytest.mark.parametrize("vocab", [5000, 140001])
+@pytest.mark.parametrize("gap", [30, 95, 140])
+def test_distill_down_to_the_smallest_mass(zs, vocab, gap):
+    """Terms reach down to 2^-222 of a row's largest, e^-153."""
+    announce(f"gap {gap} vocabulary {vocab}")
+    g = gen("least", vocab, gap)
+    z = torch.randn(2, vocab, generator=g) * 0.5
+    ids = torch.stack([torch.randperm(vocab, generator=g)[:20] for _ in range(2)]).int()
+    z.scatter_add_(1, ids.long(), torch.full((2, 20), float(gap)))
+    t = torch.randn(2, 20, generator=g)
+    lse = (torch.logsumexp(t.double(), 1) + 0.2).float()
+    want = ref.distill(z, ids, t, 1.0, lse)
+    got = distill(zs, z, ids, t, 1.0, lse)
+    # exponents of up to 150, beyond distill_close's 90
+    (loss, grad), (wloss, wgrad, bound) = got, want
+    acc = (wgrad.abs() + 2 * bound) * ((gap + 10) * 2.0 ** -22 + 2.0 ** -19)
+    close(grad, wgrad, U[FP32] * (wgrad.abs() + acc) + acc + TINY[FP32], "gradient")
+    close(loss, wloss, (gap + 30) * 2.0 ** -20, "loss")
