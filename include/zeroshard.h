@@ -592,11 +592,12 @@ int zs_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const 
  *   without teacher_lse: p = softmax of t / temperature over the row's slots,
  *     loss = w * temperature^2 * sum p * (log p - log q[id]);
  *   with it: p = exp(t / temperature - teacher_lse), and the teacher's mass
- *     off the slots, pr = 1 - sum p (0 if that is below 2^-20, where fp32
- *     says nothing any more), is one more outcome against the student's,
- *     qr: loss += w * temperature^2 * pr * (log pr - log qr). qr counts down
- *     to tokens of 2^-222 of the row's most likely one; with less than that
- *     off the slots, as with nothing but -inf, the loss is +inf.
+ *     off the slots, pr = 1 - sum p (0 if that is below 2^-20 or below
+ *     2^-22 |teacher_lse|, where an fp32 logsumexp says nothing any more), is
+ *     one more outcome against the student's, qr:
+ *     loss += w * temperature^2 * pr * (log pr - log qr). qr counts down to
+ *     tokens of 2^-222 of the row's most likely one; with less than that off
+ *     the slots, as with nothing but -inf, the loss is +inf.
  *   grad = S * d loss / d logits: S * w * temperature * (q - p) on the slots,
  *     and off them S * w * temperature * q, times (1 - pr / qr) with
  *     teacher_lse. S = dev->scale, or loss_scale without dev: the factor that

@@ -54,6 +54,7 @@ struct DistillArgs {
   uint64_t rows, ld, gld;
   uint32_t vocab, slots, parts, part_vecs;
   float tau, inv_tau, log2_scale, scale;   /* log2_scale = log2(e) / tau */
+  double inv_tau64;
   int vec_store;                   /* gradient rows are aligned as the logits' */
 };
 
@@ -275,7 +276,8 @@ __device__ __forceinline__ void pad_slots(uint32_t slots, const SlotLds &s) {
 /* What the reductions over a block pass between its waves. */
 template <int NT>
 struct ReduceLds {
-  float part[8][NT / 64];
+  float part[7][NT / 64];
+  double mass[NT / 64];
 };
 
 /* Sum of the weights of token id's slots. */
@@ -303,8 +305,8 @@ __device__ __forceinline__ bool slot_seen(const SlotLds &s, uint32_t k, int32_t 
   return seen;
 }
 
-/* From slot `first` on: ids and the teacher's logits over the temperature;
- * returns their maximum (+inf for a NaN) and whether a slot is filled. */
+/* From slot `first` on: ids and the teacher's logits; returns the logits'
+ * maximum over the temperature (+inf for a NaN) and whether a slot is filled. */
 struct SlotTop {
   float top, any;
 };
@@ -316,11 +318,11 @@ __device__ __forceinline__ SlotTop slot_ids(const DistillArgs &a, uint64_t row, 
   for (uint32_t k = first + threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = a.ids[row * a.slots + k];
     const bool ok = id >= 0 && (uint32_t)id < a.vocab;
-    const float t = ok ? load1<DT>(a.teacher, row * a.slots + k) * a.inv_tau : -INFINITY;
+    const float t = ok ? load1<DT>(a.teacher, row * a.slots + k) : -INFINITY;
     s.id[k] = ok ? id : -1;
     s.w[k] = t;
     if (ok) r.any = 1.0f;
-    r.top = fmaxf(r.top, t != t ? INFINITY : t);
+    r.top = fmaxf(r.top, t != t ? INFINITY : t * a.inv_tau);
   }
   return r;
 }
@@ -337,25 +339,34 @@ __device__ __forceinline__ void slot_logits(const DistillArgs &a, uint64_t row, 
 }
 
 struct SlotSums {
-  float mass;     /* sum of w */
+  double mass;    /* sum of w */
   float cross;    /* sum of w * ((t - ref) - (u - max u)) */
   float terms;    /* sum of the distinct slots' terms */
 };
 
-/* This thread's share; weights w = exp(t - ref) take the logits' place.
- * All ids are in LDS before this. */
+/* This thread's share; weights w = exp(t / tau - ref) take the logits' place.
+ * All ids are in LDS before this. With a tail the exponent is formed in
+ * binary64: what it is off by goes into 1 - mass whole. */
 template <bool TAIL, int NT>
 __device__ __forceinline__ SlotSums slot_weights(const DistillArgs &a, float ref, const Shift &sh,
                                                  const SlotLds &s) {
-  SlotSums r{0.0f, 0.0f, 0.0f};
+  SlotSums r{0.0, 0.0f, 0.0f};
   for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = s.id[k];
     float w = 0.0f;
     if (id >= 0) {
       const float t = s.w[k], zk = s.z[k];
-      w = exp2_fast((t - ref) * 1.44269504f);
-      r.mass += w;
-      if (!(w == 0.0f)) r.cross += w * ((t - ref) - (zk - sh.max) * a.inv_tau);
+      float u;
+      if constexpr (TAIL) {
+        const double d = fma((double)t, a.inv_tau64, -(double)ref);
+        u = (float)d;
+        w = exp2_fast((float)(d * 1.4426950408889634));
+      } else {
+        u = t * a.inv_tau - ref;
+        w = exp2_fast(u * 1.44269504f);
+      }
+      r.mass += (double)w;
+      if (!(w == 0.0f)) r.cross += w * (u - (zk - sh.max) * a.inv_tau);
       if constexpr (TAIL) {
         if (!slot_seen(s, k, id)) r.terms += term(zk, sh);
       }
@@ -365,10 +376,15 @@ __device__ __forceinline__ SlotSums slot_weights(const DistillArgs &a, float ref
   return r;
 }
 
-/* The teacher's mass off its slots counts as none below 2^-20: its fp32
- * logsumexp does not say more, and against a student without such mass the
- * rounding's remainder would make the loss infinite. */
-constexpr float kTailFloor = 9.5367431640625e-7f;
+/* The teacher's mass off its slots counts as none below 2^-20 or 2^-22 of
+ * |lse|, whichever is more: its fp32 logsumexp does not say more, and against
+ * a student without such mass the rounding's remainder would make the loss
+ * infinite. A logsumexp that is off by half a step, 2^-24 |lse|, changes the
+ * mass by as much; one of fp32 logits by three times that; the terms' exp and
+ * the rounding of its exponent add 2^-22 at most. */
+__device__ __forceinline__ float tail_floor(float lse) {
+  return fmaxf(9.53674316e-7f, 2.38418579e-7f * fabsf(lse));
+}
 
 /* Loss of a row (without its weight and tau^2), the sum of all terms, and
  * what makes gradients of the terms off the slots: term * up * share * coef. */
@@ -379,18 +395,19 @@ struct RowResult {
 /* sum: of the terms off the slots with TAIL (2^96 too large if `lifted`), of
  * all terms without. */
 template <bool TAIL>
-__device__ __forceinline__ RowResult row_result(const SlotSums &s, const Shift &sh, float sum,
-                                                bool lifted) {
+__device__ __forceinline__ RowResult row_result(const SlotSums &s, const Shift &sh, float lse,
+                                                float sum, bool lifted) {
   RowResult r;
+  const float mass = (float)s.mass;
   const float down = lifted ? 1.26217745e-29f : 1.0f;   /* 2^-96 */
   r.total = TAIL ? sum * down + s.terms : sum;
   r.up = 1.0f;
   r.share = 1.0f / r.total;
   const float log_sum = logf(r.total), log_total = log_sum - sh.rest;   /* by the maximum */
   if constexpr (TAIL) {
-    r.loss = s.cross + s.mass * log_total;
-    float pr = 1.0f - s.mass;
-    pr = pr >= kTailFloor ? pr : 0.0f;   /* NaN mass: the loss is NaN already */
+    r.loss = s.cross + mass * log_total;
+    float pr = (float)(1.0 - s.mass);
+    pr = pr >= tail_floor(lse) ? pr : 0.0f;   /* NaN mass: the loss is NaN already */
     const float log_rest = logf(sum) - (lifted ? kLift * 0.69314718f : 0.0f);
     if (pr > 0.0f) r.loss += pr * (logf(pr) - (log_rest - log_sum));
     /* nothing off the slots: every such term is 0 whatever its factor */
@@ -400,7 +417,7 @@ __device__ __forceinline__ RowResult row_result(const SlotSums &s, const Shift &
       r.share = __uint_as_float(e << 23) * down / r.total - pr / (sum * r.up);
     }
   } else {
-    r.loss = s.cross / s.mass - logf(s.mass) + log_total;
+    r.loss = s.cross / mass - logf(mass) + log_total;
   }
   return r;
 }
@@ -436,9 +453,10 @@ __device__ __forceinline__ float off_slots(float term, const RowFactors &f) {
  * and its factors. */
 template <bool TAIL>
 __device__ __forceinline__ RowFactors finish_row(const DistillArgs &a, uint64_t row, float weight,
-                                                 bool live, const SlotSums &s, const Shift &sh,
-                                                 float sum, bool lifted, bool says) {
-  const RowResult r = row_result<TAIL>(s, sh, sum, lifted);
+                                                 float lse, bool live, const SlotSums &s,
+                                                 const Shift &sh, float sum, bool lifted,
+                                                 bool says) {
+  const RowResult r = row_result<TAIL>(s, sh, lse, sum, lifted);
   RowFactors f;
   f.live = live;
   f.total = r.total;
@@ -644,11 +662,11 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
       SlotTop top{-INFINITY, 0.0f};
       if (t < a.slots) {
         const bool ok = (uint32_t)slot.id < a.vocab;
-        const float v = ok ? raw_value<DT>(slot.t) * a.inv_tau : -INFINITY;
+        const float v = ok ? raw_value<DT>(slot.t) : -INFINITY;
         lds.id[t] = ok ? slot.id : -1;
         lds.w[t] = v;
         lds.z[t] = raw_value<DT>(slot.z);
-        if (ok) top = {v != v ? INFINITY : v, 1.0f};
+        if (ok) top = {v != v ? INFINITY : v * a.inv_tau, 1.0f};
       }
       if (a.slots > NT) {   /* the others */
         const SlotTop more = slot_ids<DT, NT>(a, row, NT, lds);
@@ -694,30 +712,30 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
         }
         return sum;
       };
-      reduce_put(sum_terms(), SumOf{}, red.part[5]);
+      reduce_put(sum_terms(), SumOf{}, red.part[4]);
       sums = slot_weights<TAIL, NT>(a, ref, shift, lds);
-      reduce_put(sums.mass, SumOf{}, red.part[3]);
-      reduce_put(sums.cross, SumOf{}, red.part[4]);
-      if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.part[6]);
+      reduce_put(sums.mass, SumOf{}, red.mass);
+      reduce_put(sums.cross, SumOf{}, red.part[3]);
+      if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.part[5]);
       __syncthreads();
-      float sum = reduce_get<NT>(SumOf{}, red.part[5]);
+      float sum = reduce_get<NT>(SumOf{}, red.part[4]);
       bool lifted = false;
       if constexpr (TAIL) {
         lifted = lift(off, sum);   /* uniform over the block */
         if (lifted) {
-          reduce_put(sum_terms(), SumOf{}, red.part[7]);
+          reduce_put(sum_terms(), SumOf{}, red.part[6]);
           __syncthreads();
-          sum = reduce_get<NT>(SumOf{}, red.part[7]);
+          sum = reduce_get<NT>(SumOf{}, red.part[6]);
         }
       }
-      sums.mass = reduce_get<NT>(SumOf{}, red.part[3]);
-      sums.cross = reduce_get<NT>(SumOf{}, red.part[4]);
+      sums.mass = reduce_get<NT>(SumOf{}, red.mass);
+      sums.cross = reduce_get<NT>(SumOf{}, red.part[3]);
       if constexpr (TAIL) {
-        sums.terms = reduce_get<NT>(SumOf{}, red.part[6]);
+        sums.terms = reduce_get<NT>(SumOf{}, red.part[5]);
         for (uint32_t k = t; k < a.slots; k += NT)
           if (lds.id[k] >= 0) mark_slot<DT>(marks, kMarks, in.shape, lds.id[k], false);
       }
-      f = finish_row<TAIL>(a, row, in.weight, live, sums, shift, sum, lifted, t == 0);
+      f = finish_row<TAIL>(a, row, in.weight, in.lse, live, sums, shift, sum, lifted, t == 0);
     } else if (t == 0) {
       a.loss[row] = 0.0f;
     }
@@ -758,7 +776,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
     if (more) logits_ahead(after, slot);
     __syncthreads();
     if (a.grad && f.live)
-      store_slots<DT, TAIL, NT>(a, g, lds, shift, f.total, sums.mass, f.coef, 0, a.vocab);
+      store_slots<DT, TAIL, NT>(a, g, lds, shift, f.total, (float)sums.mass, f.coef, 0, a.vocab);
     if (!more) return;
     __syncthreads();   /* the slots in LDS are done with */
     row = next;
@@ -921,14 +939,14 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
     const float ref = TAIL ? a.lse[row] : highest;
     const bool live = TAIL ? reduce_get<NT>(MaxOf{}, red.part[2]) > 0.0f : highest > -INFINITY;
     sums = slot_weights<TAIL, NT>(a, ref, shift, lds);
-    reduce_put(sums.mass, SumOf{}, red.part[3]);
-    reduce_put(sums.cross, SumOf{}, red.part[4]);
-    if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.part[6]);
+    reduce_put(sums.mass, SumOf{}, red.mass);
+    reduce_put(sums.cross, SumOf{}, red.part[3]);
+    if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.part[5]);
     __syncthreads();
-    sums.mass = reduce_get<NT>(SumOf{}, red.part[3]);
-    sums.cross = reduce_get<NT>(SumOf{}, red.part[4]);
-    if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, red.part[6]);
-    f = finish_row<TAIL>(a, row, weight, live, sums, shift, (float)sum, lifted,
+    sums.mass = reduce_get<NT>(SumOf{}, red.mass);
+    sums.cross = reduce_get<NT>(SumOf{}, red.part[3]);
+    if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, red.part[5]);
+    f = finish_row<TAIL>(a, row, weight, ref, live, sums, shift, (float)sum, lifted,
                          first && threadIdx.x == 0);
   } else if (first && threadIdx.x == 0) {
     a.loss[row] = 0.0f;
@@ -956,7 +974,7 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
   }
   __syncthreads();
   if (f.live)
-    store_slots<DT, TAIL, NT>(a, g, lds, shift, f.total, sums.mass, f.coef,
+    store_slots<DT, TAIL, NT>(a, g, lds, shift, f.total, (float)sums.mass, f.coef,
                               first ? 0 : sh.head + v0 * ve,
                               last ? a.vocab : sh.head + v1 * ve);
 }

@@ -592,6 +592,7 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   a.slots = slots;
   a.tau = temperature;
   a.inv_tau = 1.0f / temperature;
+  a.inv_tau64 = 1.0 / temperature;
   a.log2_scale = (float)(1.4426950408889634 / temperature);
   a.scale = loss_scale;
   a.vec_store = grad && (((uintptr_t)grad ^ (uintptr_t)logits) & 15) == 0 &&

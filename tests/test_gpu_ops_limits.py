@@ -167,3 +167,28 @@ def test_distill_down_to_the_smallest_mass(zs, vocab, gap):
     acc = (wgrad.abs() + 2 * bound) * ((gap + 10) * 2.0 ** -22 + 2.0 ** -19)
     close(grad, wgrad, U[FP32] * (wgrad.abs() + acc) + acc + TINY[FP32], "gradient")
     close(loss, wloss, (gap + 30) * 2.0 ** -20, "loss")
+
+
+@pytest.mark.parametrize("vocab", [2000, 140001])
+@pytest.mark.parametrize("level,tau", [(1, 1.0), (20, 1.0), (40, 1.0), (-200, 1.0), (200, 1.0),
+                                       (20, 0.7), (6, 0.1)])
+@pytest.mark.parametrize("dt", [BF16, FP32], ids=str)
+def test_distill_of_a_teacher_with_all_its_mass_on_the_slots(zs, vocab, level, tau, dt):
+    """What rounding leaves of the teacher's mass is none: a student that has none off
+    the slots either gets a finite loss. The teacher's probabilities are off by the
+    rounding of its logsumexp, 2^-24 of its size, and 2^-19; the loss by that of terms
+    of the size of the spread, below 20."""
+    rows, k = 200 if vocab == 2000 else 20, 16
+    announce(f"level {level} tau {tau} {dt} {rows}x{vocab}")
+    g = gen("full", vocab, level, tau)
+    t = (torch.randn(rows, k, generator=g) * tau + level).to(dt)
+    ids = (torch.arange(k) * 3).expand(rows, k).contiguous().int()
+    z = torch.full((rows, vocab), -math.inf)
+    z.scatter_(1, ids.long(), torch.randn(rows, k, generator=g) * tau)
+    z = z.to(dt)
+    lse = torch.logsumexp(t.double() / tau, 1)
+    want, wgrad, bound = ref.distill(z, ids, t, tau, lse, None, 8.0)   # the exact one
+    loss, grad = distill(zs, z, ids, t, tau, lse.float(), None, 8.0)
+    off = float(lse.abs().max()) * 2.0 ** -24 + 2.0 ** -19
+    close(loss, want, 20 * off * tau * tau, "loss")
+    close(grad, wgrad, U[dt] * wgrad.abs() + 2 * bound * off + TINY[dt], "gradient")
