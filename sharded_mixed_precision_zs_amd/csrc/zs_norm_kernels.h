@@ -7,9 +7,9 @@
  *   dg = sum over rows of dy * h * rstd
  *
  * Both are bound by HBM: every element is read once, kept in registers
- * between the row's sum and its use, and written once. Sums are fp32. The
- * statistics are those of the rounded h, which is what the backward pass
- * reads, so both passes see the same row.
+ * between the row's sum and its use, and written once. Sums are binary64
+ * forward and fp32 backward. The statistics are those of the rounded h, which
+ * is what the backward pass reads, so both passes see the same row.
  */
 #ifndef ZS_NORM_KERNELS_H
 #define ZS_NORM_KERNELS_H
@@ -29,21 +29,22 @@ struct NormArgs {
   double inv_cols;
 };
 
-/* 1 / sqrt(ss * inv_cols + eps) as the sum of two floats: a float's root and
- * quotient, corrected by one step of Newton's in binary64. */
+/* 1 / sqrt(ss * inv_cols + eps) as the sum of two floats: the binary64
+ * instruction's estimate, good to more than a float, corrected by one step of
+ * Newton's. Binary64 throughout, for a bf16 row's squares leave fp32's range. */
 struct RowScale {
   float hi, lo;
 };
 
 __device__ __forceinline__ RowScale row_scale(double ss, double inv_cols, float eps) {
   const double m = ss * inv_cols + (double)eps;
-  const float r = 1.0f / sqrtf((float)m);
-  const double d = (double)r * (1.5 - 0.5 * m * (double)r * (double)r);
+  const double r = __builtin_amdgcn_rsq(m);
+  const double d = fma(0.5 * r, fma(-m * r, r, 1.0), r);
   RowScale s;
   s.hi = (float)d;
   s.lo = (float)(d - (double)s.hi);
-  /* beyond float, or not a number: as the float says */
-  if (!(r <= 3.0e38f && r > 0.0f && s.hi <= 3.0e38f)) s = {r, 0.0f};
+  /* beyond float, or not a number: as the estimate says */
+  if (!(r > 0.0 && s.hi <= 3.0e38f)) s = {(float)r, 0.0f};
   return s;
 }
 
@@ -88,10 +89,10 @@ __device__ __forceinline__ void settle8(Raw16<8> &r, uint32_t col, uint32_t cols
  * by 4096 x 4096: 5.11 ms plain, 5.00 so, equal up to 2048 rows). What the
  * next kernel reads, codes and y, stays in the caches.
  *
- * Precision: an element's square and its product with the gain are exact in
- * fp32 (8 or 11 significant bits each), the squares' sum is kept in binary64
- * and the row's scale in two floats: y is off by little more than its one
- * rounding, and the 8-bit code that it falls to hardly ever by that. */
+ * Precision: an element's product with the gain is exact in fp32 (8 or 11
+ * significant bits each), the squares and their sum are binary64 and the row's
+ * scale two floats: y is off by little more than its one rounding, and the
+ * 8-bit code that it falls to hardly ever by that. */
 template <int DT, bool AL, int G, int ITEMS>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
   constexpr int kRows = G < 256 ? 256 / G : 1;
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
   for (int i = 0; i < ITEMS; ++i) {
     if (a.h) store8<DT, AL, true>(a.h + row * a.cols, (uint64_t)(i * G + t) * 8, a.cols, h[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss += (double)(h[i][j] * h[i][j]);
+    for (int j = 0; j < 8; ++j) ss = fma((double)h[i][j], (double)h[i][j], ss);
   }
   ss = group_sum<G>(ss, part);
   const RowScale rstd = row_scale(ss, a.inv_cols, a.eps);

@@ -192,3 +192,36 @@ def test_distill_of_a_teacher_with_all_its_mass_on_the_slots(zs, vocab, level, t
     off = float(lse.abs().max()) * 2.0 ** -24 + 2.0 ** -19
     close(loss, want, 20 * off * tau * tau, "loss")
     close(grad, wgrad, U[dt] * wgrad.abs() + 2 * bound * off + TINY[dt], "gradient")
+
+
+# ---- norm ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("size", [1e30, 1e25, 1e19, 1e-19, 1e-25, 1e-30])
+@pytest.mark.parametrize("cols", [256, 1000, 5000])
+def test_norm_of_rows_whose_squares_leave_32_bits(zs, size, cols):
+    """Tolerances as for other rows: y's one rounding and a few of fp32; backward a
+    chain of 64 + 6 + 16 additions and a handful of products."""
+    announce(f"norm of size {size:g} x {cols}")
+    g = gen("size", size, cols)
+    h = (randn(g, 4, cols) * size).to(BF16)
+    gain, dy = (1 + 0.2 * randn(g, cols)).to(BF16), (randn(g, 4, cols) * 0.1).to(BF16)
+    want, wr = ref.rmsnorm(h.double(), gain.double(), 0.0)
+    y, rstd = torch.empty(4, cols, dtype=BF16, device="cuda"), torch.empty(4, device="cuda")
+    codes, scales = zs.mx_empty(4, cols, zs.ZS_MX_E4M3)
+    zs.zs_rmsnorm_forward(h.cuda(), gain.cuda(), 0.0, y=y, rstd=rstd, codes=codes, scales=scales)
+    few = 4 * 2.0 ** -24
+    close(rstd, wr, few * wr, "rstd")
+    close(y, want, (U[BF16] * (1 + few) + few) * want.abs() + TINY[BF16], "y")
+    got, byte = ref.mx_values(codes.cpu(), scales.cpu(), "e4m3", cols), scales.cpu()
+    s = ref.pow2(byte.long() - 127).repeat_interleave(32, 1)[:, :cols]
+    tol = torch.maximum(want.abs() * 2.0 ** -4, s * 2.0 ** -10)
+    close(got, want, torch.where(want.abs() > 448 * s, want.abs() - 448 * s + tol, tol)
+          + few * want.abs(), "8-bit y")
+    dx, dgain = torch.empty_like(y), torch.empty(cols, device="cuda")
+    ws = torch.empty(zs.zs_rmsnorm_backward_workspace(4, cols), dtype=torch.uint8, device="cuda")
+    zs.zs_rmsnorm_backward(dy.cuda(), h.cuda(), rstd, gain.cuda(), dx, dgain, ws)
+    wdx, wdg, mag, gmag = ref.rmsnorm_grad(dy.double(), h.double(), rstd.cpu().double(),
+                                           gain.double(), None)
+    acc = (64 + 6 + 16 + 8) * 2.0 ** -24 * mag
+    close(dx, wdx, U[BF16] * (wdx.abs() + acc) + acc + TINY[BF16], "dx")
+    close(dgain, wdg, 36 * 2.0 ** -24 * gmag + 1e-37, "dgain")
