@@ -617,10 +617,10 @@ int zs_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const 
  *            16-byte aligned.
  * Logits of -inf are tokens that cannot be chosen (q = 0); a NaN, +inf or a
  * row of -inf gives a NaN row.
- * Errors: ZS_ERR_INVALID_ARG (null pointers, dtype, temperature or
- * loss_scale not finite and > 0, vocab 0 or above 2^31 - 1, rows closer
- * than vocab, workspace too small), ZS_ERR_UNSUPPORTED (slots > 1024,
- * alignment). */
+ * Errors: ZS_ERR_INVALID_ARG (null pointers, dtype, temperature not finite
+ * or below 2^-126, loss_scale not finite and > 0, vocab 0 or above 2^31 - 1,
+ * rows closer than vocab, workspace too small), ZS_ERR_UNSUPPORTED (slots >
+ * 1024, alignment). */
 #define ZS_DISTILL_MAX_SLOTS 1024
 uint64_t zs_distill_workspace(uint64_t rows, uint64_t vocab, uint32_t slots, int dtype);
 int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,

@@ -535,8 +535,9 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
                const zs_device_scaler *dev, float *loss, void *grad, uint64_t grad_ld,
                void *workspace, uint64_t workspace_bytes, void *stream) {
   if (!valid_any(dtype)) return fail(ZS_ERR_INVALID_ARG, "zs_distill: bad dtype%s");
-  if (!(temperature > 0.0f) || !isfinite(temperature))
-    return fail(ZS_ERR_INVALID_ARG, "zs_distill: temperature must be finite and > 0%s");
+  /* the reciprocal of anything smaller is no fp32 number */
+  if (!(temperature >= 0x1p-126f) || !isfinite(temperature))
+    return fail(ZS_ERR_INVALID_ARG, "zs_distill: temperature must be finite and at least 2^-126%s");
   if (!dev && (!(loss_scale > 0.0f) || !isfinite(loss_scale)))
     return fail(ZS_ERR_INVALID_ARG, "zs_distill: loss_scale must be finite and > 0%s");
   if (vocab == 0 || vocab > kMaxVocab || ld < vocab || (grad && grad_ld < vocab))

@@ -29,3 +29,10 @@ def test_parts_of_a_long_row_leave_nothing_out(zs, dtype):
             for head in range(ve):
                 have = (vocab - head) // ve          # whole vectors after `head` elements
                 assert (parts - 1) * each <= have <= parts * each
+
+
+@pytest.mark.parametrize("tau,status", [(2.0 ** -127, 1), (1e-42, 1), (0.0, 1), (2.0 ** -126, 0)])
+def test_a_temperature_without_a_reciprocal_is_refused(zs, tau, status):
+    """rows = 0 enqueues nothing."""
+    assert zs._lib.zs_distill(None, 0, 0, 100, 100, None, None, 4, tau, None, None, 1.0, None, None,
+                              None, 0, None, 0, None) == status
