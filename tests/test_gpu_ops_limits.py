@@ -225,3 +225,29 @@ def test_norm_of_rows_whose_squares_leave_32_bits(zs, size, cols):
     acc = (64 + 6 + 16 + 8) * 2.0 ** -24 * mag
     close(dx, wdx, U[BF16] * (wdx.abs() + acc) + acc + TINY[BF16], "dx")
     close(dgain, wdg, 36 * 2.0 ** -24 * gmag + 1e-37, "dgain")
+
+
+# ---- the head's backward products ----------------------------------------------
+
+def test_head_backward_products_against_64_bits(zs):
+    """Logits' gradients have a few large entries in a row: both products of them against
+    64 bits, at the tolerance of test_product_of_8_bits_adds_up_in_32."""
+    from sharded_mixed_precision_zs_amd.head import DistillHead
+    rows, width, vocab, slots = 300, 256, 5000, 8
+    announce("head backward products")
+    g = gen("head")
+    params = torch.cat([torch.ones(width), 0.05 * randn(g, vocab * width)]).to(BF16)
+    ids = torch.randint(0, vocab, (rows, slots), generator=g, dtype=torch.int32)
+    head = DistillHead(rows, width, vocab, slots)
+    head.step(params.cuda(), randn(g, rows, width).to(BF16).cuda(),
+              randn(g, rows, width).to(BF16).cuda(), ids.cuda(),
+              (3 * randn(g, rows, slots)).to(BF16).cuda(), loss_scale=1024.0)
+    torch.cuda.synchronize()
+    grad, y = head.logits.cpu().double(), head.y.cpu().double()
+    weight = head.split(params)[1].double()
+    for out, a, b, k in ((head.dy, grad, weight.t().contiguous(), vocab),
+                         (head.split(head.grads)[1], grad.t().contiguous(), y.t().contiguous(), rows)):
+        a, b = ref.mx_quantize(a, "e4m3")[2], ref.mx_quantize(b, "e2m1")[2]
+        want, mag = a @ b.t(), a.abs() @ b.abs().t()
+        acc = (2 * zs.mx_padded(k) / 64 + 10) * 2.0 ** -24 * mag
+        close(out, want, U[BF16] * (want.abs() + acc) + acc + TINY[BF16], f"k {k}")
