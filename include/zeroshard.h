@@ -617,6 +617,9 @@ int zs_rmsnorm_backward(const void *dy, const void *h, const float *rstd, const 
  *            16-byte aligned.
  * Logits of -inf are tokens that cannot be chosen (q = 0); a NaN, +inf or a
  * row of -inf gives a NaN row.
+ * Each logit is read once up to 131072 logits of 16 bits or 65536 of 32. Longer
+ * rows, and a gradient whose rows lie otherwise to 16 bytes than the logits',
+ * are read two or three times (twice the time and more).
  * Errors: ZS_ERR_INVALID_ARG (null pointers, dtype, temperature not finite
  * or below 2^-126, loss_scale not finite and > 0, vocab 0 or above 2^31 - 1,
  * rows closer than vocab, workspace too small), ZS_ERR_UNSUPPORTED (slots >

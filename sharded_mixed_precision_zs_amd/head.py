@@ -8,6 +8,10 @@ gives out and the loss-scaled 16-bit gradients that it takes in.
     dy = dlogits8 W4 ; dW = dlogits8^T y4             8 x 4 bits
     dx, dgain = rmsnorm backward                      16 bits, fp32
 
+The product's right side is always 4 bits. For dW that is y, quantised anew from
+its 16 bits along the rows: the weights' gradient sees it coarser than the
+forward pass, which has it in 8 bits.
+
 Everything is queued on one stream through the library's own kernels; with the
 shard's device scaler nothing waits for the host, and a gradient that
 overflows is skipped by the step that reads it.
