@@ -552,8 +552,9 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
 /* Root-mean-square norm with the residual's addition and an 8-bit output:
  *   h = R16(x + residual);  rstd = 1 / sqrt(mean(h^2) + eps);
  *   y = h * rstd * gain
- * per row, fp32 between the roundings; the statistics are those of the
- * rounded h, which zs_rmsnorm_backward reads.
+ * per row; the statistics are those of the rounded h, which
+ * zs_rmsnorm_backward reads, and y's 16 bits, codes and scales are rounded
+ * once, from more than fp32.
  *   x, residual: dtype (bf16, fp16)[rows][cols]; residual may be NULL.
  *   gain       : dtype[cols].
  *   h          : dtype[rows][cols], the new residual stream; may be x's or

@@ -48,6 +48,22 @@ __device__ __forceinline__ RowScale row_scale(double ss, double inv_cols, float 
   return s;
 }
 
+/* hg (hi + lo), rounded to odd: where it is no float, to the neighbour whose
+ * last bit is set. Rounded again to 16 or 8 bits this gives what the exact
+ * value gives, for it is neither a tie nor a power of two that the exact value
+ * is not. (Rounded to nearest first, one code in some millions fell to the
+ * other side of a tie, and a block's scale with it at a power of two; it costs
+ * 1.5 us of 16384 x 4096's 76.) */
+__device__ __forceinline__ float times_odd(float hg, const RowScale &s) {
+  const float small = hg * s.lo, y = fmaf(hg, s.hi, small);
+  const float rest = fmaf(hg, s.hi, -y) + small;
+  const int b = __float_as_int(y);
+  /* towards 0, if the rest points there, and the last bit set */
+  const int odd = (b + ((b ^ __float_as_int(rest)) >> 31)) | 1;
+  constexpr int kFiniteNotZero = 0x198;   /* normal and subnormal, of either sign */
+  return __int_as_float(__builtin_amdgcn_classf(rest, kFiniteNotZero) ? odd : b);
+}
+
 /* Eight elements of a row, asked for ahead: the last few of a row that is not
  * whole vectors come with what is before them, and are shifted down when they
  * are used, so that no load waits for another (8192 x 2047 bf16 backward: 42
@@ -82,7 +98,7 @@ __device__ __forceinline__ void settle8(Raw16<8> &r, uint32_t col, uint32_t cols
 /* One row per group of G threads (64: four rows per 256-thread block), ITEMS
  * vectors of eight elements per thread: x and the residual are asked for
  * whole before anything waits, and stay in registers until y. 16384 x 4096
- * bf16 with residual, h and codes: 75 us, 6.3 TB/s of the 472 MB that it has
+ * bf16 with residual, h and codes: 76 us, 6.2 TB/s of the 472 MB that it has
  * to move, what a plain copy reaches; one row of 768 is a launch (2.9 us).
  * h is stored non-temporally: the next norm reads it, after a layer's
  * products (16384 x 4096: 82 us plain; eight norms each before two products
@@ -90,9 +106,9 @@ __device__ __forceinline__ void settle8(Raw16<8> &r, uint32_t col, uint32_t cols
  * next kernel reads, codes and y, stays in the caches.
  *
  * Precision: an element's product with the gain is exact in fp32 (8 or 11
- * significant bits each), the squares and their sum are binary64 and the row's
- * scale two floats: y is off by little more than its one rounding, and the
- * 8-bit code that it falls to hardly ever by that. */
+ * significant bits each), the squares and their sum are binary64, the row's
+ * scale two floats, and y keeps what its 16 or 8 bits are rounded by: both are
+ * the 64-bit result's own but within some 2^-45 of a tie. */
 template <int DT, bool AL, int G, int ITEMS>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
   constexpr int kRows = G < 256 ? 256 / G : 1;
@@ -146,10 +162,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void norm_kernel(NormArgs a) {
     float g[8], y[8];
     load8<DT, AL>(a.gain, (uint64_t)v * 8, a.cols, g);
     uint32_t top = 0;
+    /* zeros past the row's end: h and the gain are 0 there, but 0 * inf is not */
+    const RowScale s = v * 8 < a.cols ? rstd : RowScale{0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float hg = h[i][j] * g[j];
-      y[j] = v * 8 + j < a.cols ? fmaf(hg, rstd.hi, hg * rstd.lo) : 0.0f;
+      y[j] = times_odd(h[i][j] * g[j], s);
       top = umax(top, mag_bits(y[j]));
     }
     if (a.y) store8<DT, AL>(a.y + row * a.cols, (uint64_t)v * 8, a.cols, y);

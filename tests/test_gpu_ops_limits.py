@@ -251,3 +251,29 @@ def test_head_backward_products_against_64_bits(zs):
         want, mag = a @ b.t(), a.abs() @ b.abs().t()
         acc = (2 * zs.mx_padded(k) / 64 + 10) * 2.0 ** -24 * mag
         close(out, want, U[BF16] * (want.abs() + acc) + acc + TINY[BF16], f"k {k}")
+
+
+@pytest.mark.parametrize("dt,rows,cols", [(BF16, 2048, 4096), (FP16, 4096, 2048), (BF16, 5000, 1001)],
+                         ids=str)
+def test_norm_rounds_once(zs, dt, rows, cols):
+    """Every code, scale and 16-bit y of millions is the 64-bit result's: rounding to fp32
+    in between would put several on the other side of a tie or a power of two."""
+    announce(f"norm rounds once {dt} {rows}x{cols}")
+    g = torch.Generator("cuda").manual_seed(cols)
+    h = torch.randn(rows, cols, generator=g, device="cuda").to(dt)
+    gain = (1 + 0.1 * torch.randn(cols, generator=g, device="cuda")).to(dt)
+    y = torch.empty(rows, cols, dtype=dt, device="cuda")
+    codes, scales = zs.mx_empty(rows, cols, zs.ZS_MX_E4M3)
+    eps = 2.0 ** -17                                           # the same in 32 and 64 bits
+    zs.zs_rmsnorm_forward(h, gain, eps, y=y, codes=codes, scales=scales)
+    want = ref.rmsnorm(h.double(), gain.double(), eps)[0].cpu()
+    wrong = 0
+    for first in range(0, rows, 512):
+        part = slice(first, first + 512)
+        c, s, _ = ref.mx_quantize(want[part], "e4m3")
+        wrong += int((codes[part].cpu() != c).sum()) + int((scales[part].cpu() != s).sum())
+    # torch rounds binary64 to 16 bits by way of fp32: y within half a step of the 64 bits
+    step = torch.where(want == 0, 0.0, torch.ldexp(torch.ones_like(want), torch.frexp(want).exponent - 1))
+    step = (step * torch.finfo(dt).eps).clamp(min=2 * TINY[dt])
+    over = (y.cpu().double() - want).abs() > step / 2 * (1 + 2.0 ** -40)
+    assert wrong == 0 and not bool(over.any()), (wrong, int(over.sum()))
