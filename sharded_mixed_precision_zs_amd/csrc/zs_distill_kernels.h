@@ -273,12 +273,30 @@ __device__ __forceinline__ void pad_slots(uint32_t slots, const SlotLds &s) {
   }
 }
 
-/* What the reductions over a block pass between its waves. */
+/* What the reductions over a block pass between its waves. A row's terms are
+ * added in fp32 by each thread and joined in binary64. */
 template <int NT>
 struct ReduceLds {
-  float part[7][NT / 64];
-  double mass[NT / 64];
+  float part[5][NT / 64];
+  double dpart[4][NT / 64];
 };
+
+template <int NT>
+__device__ __forceinline__ void put_mass(float v, ReduceLds<NT> &l) {
+  reduce_put(v, SumOf{}, l.part[4]);
+}
+template <int NT>
+__device__ __forceinline__ void put_mass(double v, ReduceLds<NT> &l) {
+  reduce_put(v, SumOf{}, l.dpart[0]);
+}
+template <int NT>
+__device__ __forceinline__ void get_mass(float &v, const ReduceLds<NT> &l) {
+  v = reduce_get<NT>(SumOf{}, l.part[4]);
+}
+template <int NT>
+__device__ __forceinline__ void get_mass(double &v, const ReduceLds<NT> &l) {
+  v = reduce_get<NT>(SumOf{}, l.dpart[0]);
+}
 
 /* Sum of the weights of token id's slots. */
 __device__ __forceinline__ float slot_weight(const SlotLds &s, uint32_t slots, int32_t id) {
@@ -338,19 +356,26 @@ __device__ __forceinline__ void slot_logits(const DistillArgs &a, uint64_t row, 
   }
 }
 
+/* The teacher's mass: binary64 where the rest of 1 counts. */
+template <bool TAIL>
+struct Exact { typedef float type; };
+template <>
+struct Exact<true> { typedef double type; };
+
+template <bool TAIL>
 struct SlotSums {
-  double mass;    /* sum of w */
+  typename Exact<TAIL>::type mass;   /* sum of w */
   float cross;    /* sum of w * ((t - ref) - (u - max u)) */
-  float terms;    /* sum of the distinct slots' terms */
+  double terms;   /* sum of the distinct slots' terms */
 };
 
 /* This thread's share; weights w = exp(t / tau - ref) take the logits' place.
  * All ids are in LDS before this. With a tail the exponent is formed in
  * binary64: what it is off by goes into 1 - mass whole. */
 template <bool TAIL, int NT>
-__device__ __forceinline__ SlotSums slot_weights(const DistillArgs &a, float ref, const Shift &sh,
-                                                 const SlotLds &s) {
-  SlotSums r{0.0, 0.0f, 0.0f};
+__device__ __forceinline__ SlotSums<TAIL> slot_weights(const DistillArgs &a, float ref,
+                                                       const Shift &sh, const SlotLds &s) {
+  SlotSums<TAIL> r{0, 0.0f, 0.0};
   for (uint32_t k = threadIdx.x; k < a.slots; k += NT) {
     const int32_t id = s.id[k];
     float w = 0.0f;
@@ -365,10 +390,10 @@ __device__ __forceinline__ SlotSums slot_weights(const DistillArgs &a, float ref
         u = t * a.inv_tau - ref;
         w = exp2_fast(u * 1.44269504f);
       }
-      r.mass += (double)w;
+      r.mass += w;
       if (!(w == 0.0f)) r.cross += w * (u - (zk - sh.max) * a.inv_tau);
       if constexpr (TAIL) {
-        if (!slot_seen(s, k, id)) r.terms += term(zk, sh);
+        if (!slot_seen(s, k, id)) r.terms += (double)term(zk, sh);
       }
     }
     s.w[k] = w;
@@ -395,18 +420,18 @@ struct RowResult {
 /* sum: of the terms off the slots with TAIL (2^96 too large if `lifted`), of
  * all terms without. */
 template <bool TAIL>
-__device__ __forceinline__ RowResult row_result(const SlotSums &s, const Shift &sh, float lse,
-                                                float sum, bool lifted) {
+__device__ __forceinline__ RowResult row_result(const SlotSums<TAIL> &s, const Shift &sh, float lse,
+                                                double sum64, bool lifted) {
   RowResult r;
-  const float mass = (float)s.mass;
+  const float mass = (float)s.mass, sum = (float)sum64;
   const float down = lifted ? 1.26217745e-29f : 1.0f;   /* 2^-96 */
-  r.total = TAIL ? sum * down + s.terms : sum;
+  r.total = TAIL ? (float)(sum64 * (double)down + s.terms) : sum;
   r.up = 1.0f;
   r.share = 1.0f / r.total;
   const float log_sum = logf(r.total), log_total = log_sum - sh.rest;   /* by the maximum */
   if constexpr (TAIL) {
     r.loss = s.cross + mass * log_total;
-    float pr = (float)(1.0 - s.mass);
+    float pr = (float)(1.0 - (double)s.mass);
     pr = pr >= tail_floor(lse) ? pr : 0.0f;   /* NaN mass: the loss is NaN already */
     const float log_rest = logf(sum) - (lifted ? kLift * 0.69314718f : 0.0f);
     if (pr > 0.0f) r.loss += pr * (logf(pr) - (log_rest - log_sum));
@@ -453,8 +478,8 @@ __device__ __forceinline__ float off_slots(float term, const RowFactors &f) {
  * and its factors. */
 template <bool TAIL>
 __device__ __forceinline__ RowFactors finish_row(const DistillArgs &a, uint64_t row, float weight,
-                                                 float lse, bool live, const SlotSums &s,
-                                                 const Shift &sh, float sum, bool lifted,
+                                                 float lse, bool live, const SlotSums<TAIL> &s,
+                                                 const Shift &sh, double sum, bool lifted,
                                                  bool says) {
   const RowResult r = row_result<TAIL>(s, sh, lse, sum, lifted);
   RowFactors f;
@@ -651,7 +676,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
     const uint32_t next = row + gridDim.x;
     const RowIn after = open_row<DT, TAIL>(a, next < a.rows ? next : row);
     RowFactors f{1.0f, 0.0f, 1.0f, 0.0f, false};
-    SlotSums sums{};
+    SlotSums<TAIL> sums{};
     Shift shift{}, off{};   /* off: of the terms off the slots */
     float single = -INFINITY;
     if (in.weight != 0.0f) {   /* uniform over the block */
@@ -712,26 +737,26 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
         }
         return sum;
       };
-      reduce_put(sum_terms(), SumOf{}, red.part[4]);
+      reduce_put((double)sum_terms(), SumOf{}, red.dpart[1]);
       sums = slot_weights<TAIL, NT>(a, ref, shift, lds);
-      reduce_put(sums.mass, SumOf{}, red.mass);
+      put_mass<NT>(sums.mass, red);
       reduce_put(sums.cross, SumOf{}, red.part[3]);
-      if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.part[5]);
+      if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.dpart[2]);
       __syncthreads();
-      float sum = reduce_get<NT>(SumOf{}, red.part[4]);
+      double sum = reduce_get<NT>(SumOf{}, red.dpart[1]);
       bool lifted = false;
       if constexpr (TAIL) {
         lifted = lift(off, sum);   /* uniform over the block */
         if (lifted) {
-          reduce_put(sum_terms(), SumOf{}, red.part[6]);
+          reduce_put((double)sum_terms(), SumOf{}, red.dpart[3]);
           __syncthreads();
-          sum = reduce_get<NT>(SumOf{}, red.part[6]);
+          sum = reduce_get<NT>(SumOf{}, red.dpart[3]);
         }
       }
-      sums.mass = reduce_get<NT>(SumOf{}, red.mass);
+      get_mass<NT>(sums.mass, red);
       sums.cross = reduce_get<NT>(SumOf{}, red.part[3]);
       if constexpr (TAIL) {
-        sums.terms = reduce_get<NT>(SumOf{}, red.part[5]);
+        sums.terms = reduce_get<NT>(SumOf{}, red.dpart[2]);
         for (uint32_t k = t; k < a.slots; k += NT)
           if (lds.id[k] >= 0) mark_slot<DT>(marks, kMarks, in.shape, lds.id[k], false);
       }
@@ -915,7 +940,7 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
   const uint32_t edge = edge_index<DT>(sh, threadIdx.x, first, last, a.vocab);
   RowFactors f{1.0f, 0.0f, 1.0f, 0.0f, false};
   Shift shift{}, off{};
-  SlotSums sums{};
+  SlotSums<TAIL> sums{};
   if (weight != 0.0f) {
     const DistillPart *w = a.ws + row * a.parts;
     float max = -INFINITY;
@@ -939,14 +964,14 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
     const float ref = TAIL ? a.lse[row] : highest;
     const bool live = TAIL ? reduce_get<NT>(MaxOf{}, red.part[2]) > 0.0f : highest > -INFINITY;
     sums = slot_weights<TAIL, NT>(a, ref, shift, lds);
-    reduce_put(sums.mass, SumOf{}, red.mass);
+    put_mass<NT>(sums.mass, red);
     reduce_put(sums.cross, SumOf{}, red.part[3]);
-    if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.part[5]);
+    if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.dpart[2]);
     __syncthreads();
-    sums.mass = reduce_get<NT>(SumOf{}, red.mass);
+    get_mass<NT>(sums.mass, red);
     sums.cross = reduce_get<NT>(SumOf{}, red.part[3]);
-    if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, red.part[5]);
-    f = finish_row<TAIL>(a, row, weight, ref, live, sums, shift, (float)sum, lifted,
+    if constexpr (TAIL) sums.terms = reduce_get<NT>(SumOf{}, red.dpart[2]);
+    f = finish_row<TAIL>(a, row, weight, ref, live, sums, shift, sum, lifted,
                          first && threadIdx.x == 0);
   } else if (first && threadIdx.x == 0) {
     a.loss[row] = 0.0f;
