@@ -513,8 +513,8 @@ __device__ __forceinline__ void mark_slot(uint32_t *bits, uint32_t edges, const 
 /* ------------------------------------------------------------------------
  * A row per block, held in registers between its statistics and its
  * gradient: ITEMS 16-byte vectors per thread and, in a few threads, one
- * single element. So each logit is read once: 8192 x 128000 bf16 in 876 us,
- * 4.8 TB/s (read twice, in parts, 1490), with a teacher's tail 960, the loss
+ * single element. So each logit is read once: 8192 x 128000 bf16 in 879 us,
+ * 4.8 TB/s (read twice, in parts, 1490), with a teacher's tail 970, the loss
  * alone 490; 8192 x 50257 375 us, 16384 x 32000 441 us, 13 x 50257 10 us.
  *
  * Rows of up to 16 vectors a thread leave room for two waves or more of other

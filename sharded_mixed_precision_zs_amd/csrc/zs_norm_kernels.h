@@ -53,7 +53,7 @@ __device__ __forceinline__ RowScale row_scale(double ss, double inv_cols, float 
  * value gives, for it is neither a tie nor a power of two that the exact value
  * is not. (Rounded to nearest first, one code in some millions fell to the
  * other side of a tie, and a block's scale with it at a power of two; it costs
- * 1.5 us of 16384 x 4096's 76.) */
+ * 1.5 us of 16384 x 4096's 75.) */
 __device__ __forceinline__ float times_odd(float hg, const RowScale &s) {
   const float small = hg * s.lo, y = fmaf(hg, s.hi, small);
   const float rest = fmaf(hg, s.hi, -y) + small;
@@ -98,7 +98,7 @@ __device__ __forceinline__ void settle8(Raw16<8> &r, uint32_t col, uint32_t cols
 /* One row per group of G threads (64: four rows per 256-thread block), ITEMS
  * vectors of eight elements per thread: x and the residual are asked for
  * whole before anything waits, and stay in registers until y. 16384 x 4096
- * bf16 with residual, h and codes: 76 us, 6.2 TB/s of the 472 MB that it has
+ * bf16 with residual, h and codes: 75 us, 6.3 TB/s of the 472 MB that it has
  * to move, what a plain copy reaches; one row of 768 is a launch (2.9 us).
  * h is stored non-temporally: the next norm reads it, after a layer's
  * products (16384 x 4096: 82 us plain; eight norms each before two products
