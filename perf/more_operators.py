@@ -372,6 +372,16 @@ def _kept(s):
     return halves >= drop, 65536 / (65536 - drop)
 
 
+def _rounded(v, dt):
+    """A float64 tensor rounded once to 16 bits: through float32 rounded to odd, not to nearest,
+    which would make ties of values that are none."""
+    y = v.float()
+    rest = v - y.double()
+    bits = y.view(torch.int32)
+    odd = (bits - ((rest < 0) != (y < 0)).int()) | 1
+    return torch.where(rest != 0, odd, bits).view(torch.float32).to(dt)
+
+
 def _plain_dropout(s):
     kept, factor = _kept(s)
     out = torch.where(kept, s["x"].float() * factor, 0.0)
@@ -393,7 +403,7 @@ def _plain_block(s):
     if s["gate"] is not None:
         n = n * s["gate"].double()
     n = torch.where(kept, n * factor, 0.0)
-    h = (s["res"].double() * s["residual_scale"] + n * s["branch_scale"]).to(s["x"].dtype)
+    h = _rounded(s["res"].double() * s["residual_scale"] + n * s["branch_scale"], s["x"].dtype)
     v = h.double()
     rstd = (v.square().mean(1) + EPS).rsqrt()
     y = (v * rstd.unsqueeze(1) * s["gain"].double()).float()
@@ -783,7 +793,10 @@ def exact(case, seed):
             x = x / rms.unsqueeze(1) * post
         h = (s["res"].to(F64) * s["residual_scale"] + x * gate * factor)
         out["h"] = h
-        h = h.to(s["x"].dtype).to(F64)
+        # to the nearest of 8 or 11 significant bits, ties to even
+        step = _power((torch.frexp(h).exponent - (8 if case["dtype"] == "bf16" else 11)).clamp(
+            min=-133 if case["dtype"] == "bf16" else -24))
+        h = torch.round(h / step) * step
         rms = torch.sqrt(torch.mean(h * h, 1) + EPS)
         out["rstd"] = 1 / rms
         y = h / rms.unsqueeze(1) * gain
