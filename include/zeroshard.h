@@ -633,6 +633,94 @@ int zs_distill(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
                const zs_device_scaler *dev, float *loss, void *grad, uint64_t grad_ld,
                void *workspace, uint64_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of the student's last block, in front of the output end and by
+ * its conventions.
+ *
+ * Dropout without a stored mask. Element (row, col) of a matrix is dropped if
+ * its 16 random bits, as a number, are below round(p * 65536): p counts in
+ * steps of 2^-16. The others are multiplied by 65536 / (65536 - that number);
+ * a p that rounds to 1 drops everything. The bits are those of Philox4x32 with
+ * seven rounds (Salmon, Moraes, Dror and Shaw, 2011): key = seed (low word
+ * first), counter = {col / 8, row, low and high word of offset + *dev_offset},
+ * word (col % 8) / 2 of the result, its low half for an even col. So the mask
+ * follows from seed, offset and place alone: the backward pass forms it again,
+ * a part of the rows from row 0 on has the same one, and every layer and step
+ * takes an offset of its own. dev_offset: NULL, or a device uint64 that is
+ * added (modulo 2^64) as the kernel runs, so that a captured graph's replays
+ * draw anew. */
+typedef struct {
+  float p;                    /* in [0, 1] */
+  uint64_t seed, offset;
+  const uint64_t *dev_offset; /* 8-byte aligned */
+} zs_dropout_rule;
+
+/* out = R(residual + (kept ? x / (1 - p) : 0)), and R(...) of the second term
+ * alone without a residual. The gradient of x is the same call on out's
+ * gradient without the residual; the residual's is out's.
+ *   x, residual, out: dtype (bf16, fp16, fp32)[rows][cols], contiguous;
+ *                     residual may be NULL; out may be x's or residual's buffer.
+ * A dropped element is replaced, not multiplied: NaN and infinities in its
+ * place are gone. Errors: ZS_ERR_INVALID_ARG (null pointers, dtype, p outside
+ * [0, 1]), ZS_ERR_UNSUPPORTED (alignment, 2^32 rows or more, more than 2^32
+ * groups of eight elements of a row). */
+int zs_dropout(const void *x, const void *residual, int dtype, uint64_t rows, uint64_t cols,
+               const zs_dropout_rule *rule, void *out, void *stream);
+
+/* A block's end: norm of its output, gate, dropout, residual with both
+ * scales, and the next block's norm with its 8-bit output, in one pass:
+ *   n = x * post_rstd * post_gain,  post_rstd = 1 / sqrt(mean(x^2) + eps)
+ *   h = R16(residual_scale * residual + branch_scale * k * gate * n)
+ *   y = h * rstd * gain,            rstd = 1 / sqrt(mean(h^2) + eps)
+ * per row, k as in zs_dropout. h is rounded once, from more than fp32; what y
+ * and its 8 bits are made of is the rounded h, as in zs_rmsnorm_forward.
+ *   x, residual: dtype (bf16, fp16)[rows][cols], both needed.
+ *   post_gain  : dtype[cols], or NULL: no first norm (n = x).
+ *   gate       : dtype[cols], one for all rows, or NULL (1).
+ *   gain       : dtype[cols].
+ *   dropout    : NULL: none.
+ *   h          : dtype[rows][cols]; may be x's or residual's own buffer (x is
+ *                needed again by the backward pass with a post_gain or gate).
+ *   post_rstd, rstd: fp32[rows], or NULL; post_rstd with a post_gain only.
+ *   codes, scales, y: as in zs_rmsnorm_forward; codes or y must be given.
+ * Errors: ZS_ERR_INVALID_ARG (null pointers, dtype, eps not finite or < 0,
+ * scales not finite, p outside [0, 1]), ZS_ERR_UNSUPPORTED (cols > 65536,
+ * alignment). */
+int zs_block_norm_forward(const void *x, const void *residual, const void *post_gain,
+                          const void *gate, const void *gain, int dtype, uint64_t rows,
+                          uint64_t cols, float eps, float residual_scale, float branch_scale,
+                          const zs_dropout_rule *dropout, void *h, float *post_rstd, float *rstd,
+                          uint8_t *codes, uint8_t *scales, void *y, void *stream);
+
+/* Gradients of zs_block_norm_forward (the 8-bit rounding passes it through):
+ *   dh = dres + rstd * (gain*dy - h * rstd^2 * mean(gain*dy*h))
+ *   dresidual = R16(residual_scale * dh)
+ *   t = branch_scale * k * dh,  q = t * gate * post_gain
+ *   dx = R16(post_rstd * (q - x * post_rstd^2 * mean(q*x)))   (R16(q) without
+ *        a post_gain)
+ *   dgain = sum over rows of dy * h * rstd
+ *   dpost_gain = gate * u, dgate = post_gain * u,
+ *        u = sum over rows of t * x * post_rstd
+ *   dy, h, rstd, gain, x, post_rstd, post_gain, gate, dropout and the scales:
+ *          as in the forward call; x may be NULL without post_gain and gate.
+ *   dres : dtype[rows][cols], what h receives from elsewhere, or NULL.
+ *   dx, dresidual: dtype[rows][cols]; each may be dy's, h's, dres's or x's own
+ *          buffer.
+ *   dgain, dpost_gain, dgate: fp32[cols], the last two where there is a
+ *          post_gain or gate, NULL otherwise; zeros when rows == 0.
+ *   workspace: zs_block_norm_backward_workspace(rows, cols) bytes, 4-byte
+ *          aligned.
+ * Errors: as zs_block_norm_forward; a workspace too small is
+ * ZS_ERR_INVALID_ARG, 2^32 rows or more ZS_ERR_UNSUPPORTED. */
+uint64_t zs_block_norm_backward_workspace(uint64_t rows, uint64_t cols);
+int zs_block_norm_backward(const void *dy, const void *h, const float *rstd, const void *gain,
+                           const void *dres, const void *x, const float *post_rstd,
+                           const void *post_gain, const void *gate, int dtype, uint64_t rows,
+                           uint64_t cols, float residual_scale, float branch_scale,
+                           const zs_dropout_rule *dropout, void *dx, void *dresidual,
+                           float *dgain, float *dpost_gain, float *dgate, void *workspace,
+                           uint64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -2,6 +2,7 @@
 
   libzeroshard.so        the shard-step library (HIP, gfx950)  <- csrc/zeroshard.hip
                          + the operators of the model's output end <- csrc/zs_ops.hip
+                         + of its last block <- csrc/zs_block.hip
                          + its host-side offload update (gcc) <- csrc/offload_cpu.cpp
   synth/libzssynth_dev.so   device twin of the input generator (HIP, gfx950)
   synth/libzssynth_host.so  host twin of the input generator (gcc)
@@ -89,12 +90,27 @@ def _run(cmd, verbose):
     subprocess.run(cmd, check=True)
 
 
+def _run_all(cmds, verbose):
+    """Commands that do not depend on each other, side by side."""
+    if verbose:
+        for cmd in cmds:
+            print(" ".join(cmd), flush=True)
+    running = [(cmd, subprocess.Popen(cmd)) for cmd in cmds]
+    failed = [subprocess.CalledProcessError(p.returncode, cmd)
+              for cmd, p in running if p.wait() != 0]
+    if failed:
+        raise failed[0]
+
+
 def _hip_lib(src, out, verbose, extra=()):
     tmp = out + ".tmp"
     _run([HIPCC, *HIP_FLAGS, "-I", INCLUDE, *extra, src, *hip_runtime_link_flags(verbose),
           "-o", tmp], verbose)
     os.replace(tmp, out)
 
+
+# The operators' sources, each an object of its own.
+OPERATOR_SOURCES = ["zs_ops.hip", "zs_block.hip"]
 
 # Host half of the library (the ZeRO-Offload update): gcc, no contraction so
 # vector mul/add stay separate IEEE operations; F16C for the fp16 convert.
@@ -106,13 +122,14 @@ def build_zeroshard(verbose=False):
     obj = os.path.join(PKG, "csrc", "offload_cpu.o")
     _run(["g++", *CPU_FLAGS, "-I", INCLUDE, "-c", os.path.join(PKG, "csrc", "offload_cpu.cpp"),
           "-o", obj], verbose)
-    ops = os.path.join(PKG, "csrc", "zs_ops.o")
-    _run([HIPCC, *HIP_FLAGS, "-I", INCLUDE, "-c", os.path.join(PKG, "csrc", "zs_ops.hip"),
-          "-o", ops], verbose)
+    ops = [os.path.join(PKG, "csrc", name) for name in OPERATOR_SOURCES]
+    _run_all([[HIPCC, *HIP_FLAGS, "-I", INCLUDE, "-c", src, "-o", src[:-4] + ".o"]
+              for src in ops], verbose)
+    objects = [obj] + [src[:-4] + ".o" for src in ops]
     _hip_lib(os.path.join(PKG, "csrc", "zeroshard.hip"), LIB, verbose,
-             extra=[obj, ops, "-pthread"])
-    os.remove(obj)
-    os.remove(ops)
+             extra=[*objects, "-pthread"])
+    for o in objects:
+        os.remove(o)
     return LIB
 
 

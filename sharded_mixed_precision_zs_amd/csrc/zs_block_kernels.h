@@ -1,0 +1,355 @@
+/*
+ * zs_block_kernels.h -- a block's end (gfx950): its output normed, gated,
+ * dropped out, scaled and added to the scaled residual stream, and the next
+ * block's norm of the sum; forward and backward.
+ *
+ *   n = x r1 g1 gate,  r1 = 1 / sqrt(mean(x^2) + eps)
+ *   h = R16(l res + a k n)       k: 0, or 1 / (1 - p)
+ *   y = h r2 g2,       r2 = 1 / sqrt(mean(h^2) + eps)
+ *
+ *   dh = dres + r2 (g2 dy - h r2^2 mean(g2 dy h))
+ *   t = a k dh;  u = sum over rows of t x r1;  dgate = g1 u;  dg1 = gate u
+ *   dx = r1 (q - x r1^2 mean(q x)),  q = t g1 gate
+ *   dres' = l dh;  dg2 = sum over rows of dy h r2
+ *
+ * The gate is one vector for all rows, so that its gradient and that of the
+ * first gain are one sum u, times the other. Without the first norm r1 and g1
+ * are 1 and dx = q.
+ *
+ * Bound by HBM, the forward pass nearly as much by its instructions: every
+ * element is read once, stays in registers over both sums of its row, and is
+ * written once.
+ */
+#ifndef ZS_BLOCK_KERNELS_H
+#define ZS_BLOCK_KERNELS_H
+
+#include "zs_norm_rows.h"
+#include "zs_philox.h"
+
+namespace zs {
+
+struct BlockArgs {
+  const void *x, *res, *post_gain, *gate, *gain;   /* post_gain, gate optional */
+  uint16_t *h, *y;                                 /* y optional */
+  float *post_rstd, *rstd;                         /* optional */
+  uint8_t *codes, *scales;                         /* both or neither */
+  uint64_t rows;
+  uint32_t cols, padded;
+  float eps;
+  double inv_cols, residual_scale, branch_scale;
+  DropArgs drop;
+};
+
+/* v rounded to odd in fp32: where it is no float, to the neighbour whose last
+ * bit is set. Rounded again to 16 bits this gives what v gives. */
+__device__ __forceinline__ float odd_float(double v) {
+  const float y = (float)v;
+  const float rest = (float)(v - (double)y);
+  const int b = __float_as_int(y);
+  const int odd = (b + ((b ^ __float_as_int(rest)) >> 31)) | 1;
+  constexpr int kFiniteNotZero = 0x198;   /* normal and subnormal, of either sign */
+  return __int_as_float(__builtin_amdgcn_classf(rest, kFiniteNotZero) ? odd : b);
+}
+
+/* As norm_kernel: a row per group of G threads, ITEMS vectors of eight each.
+ * The sum that becomes h is binary64 and rounded once, so that h is the 64-bit
+ * result's own, and with it what the second norm and its codes see. */
+template <int DT, bool AL, int G, int ITEMS>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void block_kernel(BlockArgs a) {
+  constexpr int kRows = G < 256 ? 256 / G : 1;
+  __shared__ double part[2][G / 64];
+  const uint32_t t = threadIdx.x % G;
+  const uint64_t row = (uint64_t)blockIdx.x * kRows + threadIdx.x / G;
+  if (row >= a.rows) return;   /* a whole wave; blocks of one row never take it */
+  const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.cols;
+  const uint16_t *res = static_cast<const uint16_t *>(a.res) + row * a.cols;
+  Raw16<8> xr[ITEMS], rr[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) xr[i] = load8_ahead<AL>(x, (i * G + t) * 8, a.cols);
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) rr[i] = load8_ahead<AL>(res, (i * G + t) * 8, a.cols);
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    settle8<AL>(xr[i], (i * G + t) * 8, a.cols);
+    settle8<AL>(rr[i], (i * G + t) * 8, a.cols);
+  }
+  double scale = a.branch_scale;
+  if (a.post_gain) {
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      float e[8];
+      upcast<8, DT>(xr[i], e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fma((double)e[j], (double)e[j], ss);
+    }
+    const double r1 = row_scale64(group_sum<G>(ss, part[0]), a.inv_cols, a.eps);
+    if (a.post_rstd && t == 0) a.post_rstd[row] = (float)r1;
+    scale *= r1;
+  }
+  const uint64_t offset = a.drop.threshold ? drop_offset(a.drop) : 0;
+  if (a.drop.threshold) scale *= a.drop.factor64;
+  float h[ITEMS][8];
+  double ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t v = i * G + t;
+    float e[8], r[8];
+    upcast<8, DT>(xr[i], e);
+    upcast<8, DT>(rr[i], r);
+    float g1[8], gate[8];
+    if (a.post_gain) {
+      load8<DT, AL>(a.post_gain, (uint64_t)v * 8, a.cols, g1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] *= g1[j];   /* exact: 22 bits at most */
+    }
+    double d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = e[j];
+    if (a.gate) {
+      load8<DT, AL>(a.gate, (uint64_t)v * 8, a.cols, gate);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] *= (double)gate[j];   /* exact: 33 bits at most */
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double l = a.residual_scale * (double)r[j];   /* exact: 35 bits */
+      d[j] = fma(scale, d[j], l);
+    }
+    if (a.drop.threshold) {
+      const RandomWords w = random_words(a.drop, offset, v, (uint32_t)row);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        d[j] = kept(w, j, a.drop.threshold) ? d[j] : a.residual_scale * (double)r[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const uint32_t w = pack2<DT>(odd_float(d[j]), odd_float(d[j + 1]));
+      h[i][j] = up_lo<DT>(w);
+      h[i][j + 1] = up_hi<DT>(w);
+    }
+    /* past the row's end x and res are 0, and so is h, but 0 * inf is not */
+    if (v * 8 + 8 > a.cols) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = v * 8 + j < a.cols ? h[i][j] : 0.0f;
+    }
+    store8<DT, AL, true>(a.h + row * a.cols, (uint64_t)v * 8, a.cols, h[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fma((double)h[i][j], (double)h[i][j], ss);
+  }
+  ss = group_sum<G>(ss, part[1]);
+  const RowScale rstd = row_scale(ss, a.inv_cols, a.eps);
+  if (a.rstd && t == 0) a.rstd[row] = rstd.hi;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t v = i * G + t;
+    if (v * 8 >= a.padded) break;   /* whole quads: padded is a multiple of 128 */
+    float g[8], y[8];
+    load8<DT, AL>(a.gain, (uint64_t)v * 8, a.cols, g);
+    uint32_t top = 0;
+    const RowScale s = v * 8 < a.cols ? rstd : RowScale{0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      y[j] = times_odd(h[i][j] * g[j], s);
+      top = umax(top, mag_bits(y[j]));
+    }
+    if (a.y) store8<DT, AL>(a.y + row * a.cols, (uint64_t)v * 8, a.cols, y);
+    if (a.codes) {
+      const uint32_t byte = mx_scale_byte<ZS_MX_E4M3>(quad_max(top));
+      uint32_t code[2];
+      mx_encode<ZS_MX_E4M3>(y, byte, code);
+      *reinterpret_cast<u32x2 *>(a.codes + row * a.padded + v * 8) = u32x2{code[0], code[1]};
+      if ((v & 3) == 0) a.scales[row * (a.padded / kMxBlock) + v / 4] = (uint8_t)byte;
+    }
+  }
+}
+
+struct BlockGradArgs {
+  const void *dy, *h, *gain, *dres, *x, *post_gain, *gate;   /* dres, x, post_gain, gate optional */
+  const float *rstd, *post_rstd;
+  uint16_t *dx, *dresidual;
+  float *part;                   /* [parts][2][cols]: shares of dg2, and of u */
+  uint64_t rows;
+  uint32_t cols, parts;
+  float residual_scale, branch_scale;
+  DropArgs drop;
+};
+
+template <int ITEMS>
+struct BlockGradRow {
+  Raw16<8> dy[ITEMS], h[ITEMS], dres[ITEMS], x[ITEMS];
+  float rstd, post_rstd;
+};
+
+template <bool AL, int G, int ITEMS>
+__device__ __forceinline__ void load_block_row(const BlockGradArgs &a, uint64_t row, uint32_t t,
+                                               BlockGradRow<ITEMS> &r) {
+  const uint64_t at = row * a.cols;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t c = (i * G + t) * 8;
+    r.dy[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols);
+    r.h[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.h) + at, c, a.cols);
+    if (a.dres)
+      r.dres[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols);
+    if (a.x) r.x[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.x) + at, c, a.cols);
+  }
+  r.rstd = a.rstd[row];
+  r.post_rstd = a.post_rstd ? a.post_rstd[row] : 1.0f;
+}
+
+/* As norm_grad_kernel: `parts` groups walk the rows and keep their shares of
+ * both sums over rows in registers; block_gain_kernel adds the shares in
+ * order. Two barriers a row, one for each of its two dot products. */
+template <int DT, bool AL, int G, int ITEMS>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void block_grad_kernel(BlockGradArgs a) {
+  constexpr int kRows = G < 256 ? 256 / G : 1;
+  __shared__ float sums[2][2][G / 64];
+  const uint32_t t = threadIdx.x % G;
+  const uint32_t p = blockIdx.x * kRows + threadIdx.x / G;
+  if (p >= a.parts) return;
+  float dg[ITEMS][8], du[ITEMS][8], g[ITEMS][8], q[ITEMS][8];   /* q: g1 gate, exact */
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    load8<DT, AL>(a.gain, (uint64_t)(i * G + t) * 8, a.cols, g[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = du[i][j] = 0.0f, q[i][j] = 1.0f;
+    if (a.post_gain) load8<DT, AL>(a.post_gain, (uint64_t)(i * G + t) * 8, a.cols, q[i]);
+    if (a.gate) {
+      float gate[8];
+      load8<DT, AL>(a.gate, (uint64_t)(i * G + t) * 8, a.cols, gate);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[i][j] *= gate[j];
+    }
+  }
+  const uint64_t offset = a.drop.threshold ? drop_offset(a.drop) : 0;
+  const float scale = a.drop.threshold ? a.branch_scale * a.drop.factor : a.branch_scale;
+  const float inv_cols = 1.0f / (float)a.cols;
+  BlockGradRow<ITEMS> r, next;
+  load_block_row<AL, G>(a, p, t, r);
+  int turn = 0;
+  for (uint64_t row = p; row < a.rows; row += a.parts, turn ^= 1) {
+    const bool more = row + a.parts < a.rows;
+    if (more) load_block_row<AL, G>(a, row + a.parts, t, next);
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      float h[8], d[8];
+      settle8<AL>(r.dy[i], (i * G + t) * 8, a.cols);
+      settle8<AL>(r.h[i], (i * G + t) * 8, a.cols);
+      if (a.dres) settle8<AL>(r.dres[i], (i * G + t) * 8, a.cols);
+      if (a.x) settle8<AL>(r.x[i], (i * G + t) * 8, a.cols);
+      upcast<8, DT>(r.dy[i], d);
+      upcast<8, DT>(r.h[i], h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dg[i][j] = fmaf(d[j], h[j] * r.rstd, dg[i][j]);
+        dot = fmaf(d[j] * g[i][j], h[j], dot);
+      }
+    }
+    const float s = group_sum<G>(dot, sums[turn][0]) * inv_cols * r.rstd * r.rstd;
+    float dn[ITEMS][8];
+    dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      float h[8], d[8], o[8] = {}, x[8] = {};
+      upcast<8, DT>(r.dy[i], d);
+      upcast<8, DT>(r.h[i], h);
+      if (a.dres) upcast<8, DT>(r.dres[i], o);
+      if (a.x) upcast<8, DT>(r.x[i], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[j] = fmaf(r.rstd, fmaf(-h[j], s, d[j] * g[i][j]), o[j]);   /* dh */
+        d[j] = o[j] * a.residual_scale;
+        o[j] *= scale;
+      }
+      store8<DT, AL, true>(a.dresidual + row * a.cols, (uint64_t)(i * G + t) * 8, a.cols, d);
+      if (a.drop.threshold) {
+        const RandomWords w = random_words(a.drop, offset, i * G + t, (uint32_t)row);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = kept(w, j, a.drop.threshold) ? o[j] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        du[i][j] = fmaf(o[j], x[j] * r.post_rstd, du[i][j]);
+        dn[i][j] = o[j] * q[i][j];
+        dot = fmaf(dn[i][j], x[j], dot);
+      }
+    }
+    float s1 = 0.0f;
+    if (a.post_gain)
+      s1 = group_sum<G>(dot, sums[turn][1]) * inv_cols * r.post_rstd * r.post_rstd;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (a.post_gain) {
+        float x[8];
+        upcast<8, DT>(r.x[i], x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dn[i][j] = r.post_rstd * fmaf(-x[j], s1, dn[i][j]);
+      }
+      store8<DT, AL, true>(a.dx + row * a.cols, (uint64_t)(i * G + t) * 8, a.cols, dn[i]);
+    }
+    if (more) r = next;
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t c = (i * G + t) * 8 + j;
+      if (c < a.cols) {
+        a.part[(uint64_t)p * 2 * a.cols + c] = dg[i][j];
+        if (a.x) a.part[((uint64_t)p * 2 + 1) * a.cols + c] = du[i][j];
+      }
+    }
+}
+
+/* The shares joined in order, as norm_gain_kernel does: blockIdx.y 0 for dg2,
+ * 1 for u, which the other vector makes dg1 and dgate. */
+constexpr int kBlockGainCols = 32, kBlockGainRuns = 32;
+
+struct BlockGainArgs {
+  const float *part;
+  const void *post_gain, *gate;
+  float *dgain, *dpost_gain, *dgate;
+  uint32_t parts, cols;
+};
+
+template <int DT>
+__global__ __launch_bounds__(kBlockGainCols * kBlockGainRuns) void block_gain_kernel(
+    BlockGainArgs a) {
+  __shared__ float sums[kBlockGainRuns][kBlockGainCols + 1];
+  const uint32_t lane = threadIdx.x % kBlockGainCols, run = threadIdx.x / kBlockGainCols;
+  const uint32_t c = blockIdx.x * kBlockGainCols + lane;
+  float s = 0.0f;
+  if (c < a.cols) {
+    const float *q = a.part + (uint64_t)blockIdx.y * a.cols + c;
+    for (uint32_t p = run; p < a.parts; p += 8 * kBlockGainRuns) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t at = p + k * kBlockGainRuns;
+        v[k] = at < a.parts ? q[(uint64_t)at * 2 * a.cols] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
+  }
+  sums[run][lane] = s;
+  __syncthreads();
+  if (run != 0 || c >= a.cols) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kBlockGainRuns; ++w) s += sums[w][lane];
+  if (blockIdx.y == 0) {
+    a.dgain[c] = s;
+    return;
+  }
+  const auto at = [&](const void *v) {
+    return v ? up_lo<DT>(static_cast<const uint16_t *>(v)[c]) : 1.0f;
+  };
+  if (a.dpost_gain) a.dpost_gain[c] = s * at(a.gate);
+  if (a.dgate) a.dgate[c] = s * at(a.post_gain);
+}
+
+}  // namespace zs
+#endif  // ZS_BLOCK_KERNELS_H

@@ -27,7 +27,7 @@
 #ifndef ZS_DISTILL_KERNELS_H
 #define ZS_DISTILL_KERNELS_H
 
-#include "zs_mx.h"
+#include "zs_logits.h"
 
 namespace zs {
 
@@ -57,177 +57,6 @@ struct DistillArgs {
   double inv_tau64;
   int vec_store;                   /* gradient rows are aligned as the logits' */
 };
-
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-template <int DT>
-__device__ __forceinline__ float load1(const void *p, uint64_t i) {
-  if constexpr (DT == ZS_FP32) return static_cast<const float *>(p)[i];
-  else return up_lo<DT>(static_cast<const uint16_t *>(p)[i]);
-}
-
-/* An element as it lies in memory, and its value: apart, so that nothing
- * waits for the element before its value is used. */
-template <int DT>
-__device__ __forceinline__ uint32_t load_raw(const void *p, uint64_t i) {
-  if constexpr (DT == ZS_FP32) return static_cast<const uint32_t *>(p)[i];
-  else return static_cast<const uint16_t *>(p)[i];
-}
-
-template <int DT>
-__device__ __forceinline__ float raw_value(uint32_t w) {
-  if constexpr (DT == ZS_FP32) return __uint_as_float(w);
-  else return up_lo<DT>(w);
-}
-
-/* A value that nothing writes while the kernel runs, by the scalar unit:
- * vector loads return in order, and this one must not wait for a row. */
-__device__ __forceinline__ float load_scalar(const float *p, uint32_t i) {
-  return reinterpret_cast<const __attribute__((address_space(4))) float *>(
-      reinterpret_cast<uintptr_t>(p))[i];
-}
-
-template <int DT>
-__device__ __forceinline__ void store1(void *p, uint64_t i, float x) {
-  if constexpr (DT == ZS_FP32) static_cast<float *>(p)[i] = x;
-  else static_cast<uint16_t *>(p)[i] = pack1<DT>(x);
-}
-
-/* Elements per 16-byte vector. */
-template <int DT>
-constexpr uint32_t kVecElems = DT == ZS_FP32 ? 4 : 8;
-
-template <int DT>
-__device__ __forceinline__ void unpack_vec(const u32x4 &w, float (&x)[kVecElems<DT>]) {
-  if constexpr (DT == ZS_FP32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(w[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = up_lo<DT>(w[j]);
-      x[2 * j + 1] = up_hi<DT>(w[j]);
-    }
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ u32x4 pack_vec(const float (&x)[kVecElems<DT>]) {
-  u32x4 w;
-  if constexpr (DT == ZS_FP32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(x[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pack2<DT>(x[2 * j], x[2 * j + 1]);
-  }
-  return w;
-}
-
-/* A row as whole 16-byte vectors between a few single elements at either
- * end, whatever the row's alignment. */
-struct RowShape {
-  uint32_t head, vecs, tail;   /* elements, vectors, elements */
-};
-
-template <int DT>
-__device__ __forceinline__ RowShape row_shape(const void *row, uint32_t n) {
-  constexpr uint32_t esz = DT == ZS_FP32 ? 4 : 2, ve = kVecElems<DT>;
-  RowShape s;
-  s.head = (uint32_t)((16 - ((uintptr_t)row & 15)) & 15) / esz;
-  if (s.head > n) s.head = n;
-  s.vecs = (n - s.head) / ve;
-  s.tail = n - s.head - s.vecs * ve;
-  return s;
-}
-
-/* The single element that thread t has besides its vectors: the head's in
- * threads 0 .. 7, the tail's in threads 8 .. 15; vocab if none. */
-template <int DT>
-__device__ __forceinline__ uint32_t edge_index(const RowShape &s, uint32_t t, bool first,
-                                               bool last, uint32_t vocab) {
-  if (first && t < s.head) return t;
-  if (last && t >= 8 && t - 8 < s.tail) return s.head + s.vecs * kVecElems<DT> + t - 8;
-  return vocab;
-}
-
-/* ------------------------------------------------------------------------
- * Reductions over a block: within each wave, then over the waves' results by
- * every wave alike; a fixed tree, on all threads. `part`: NT / 64 values that
- * nothing else uses before the next barrier.
- * ---------------------------------------------------------------------- */
-struct MaxOf {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
-struct SumOf {
-  template <class T>
-  __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
-};
-
-/* A value of another lane of the same 16, by the lane pattern CTRL. */
-template <int CTRL>
-__device__ __forceinline__ float lane_move(float v) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
-}
-template <int CTRL>
-__device__ __forceinline__ double lane_move(double v) {
-  const uint64_t b = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xf, 0xf, true);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf,
-                                                         true);
-  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
-}
-
-/* Within groups of `width` lanes: neighbours, pairs, then the mirrored half
- * of 8 and of 16 lanes (equal within each half by then), then across. */
-template <class T, class Op>
-__device__ __forceinline__ T wave_reduce(T v, Op op, int width) {
-  v = op(v, lane_move<0xB1>(v));
-  v = op(v, lane_move<0x4E>(v));
-  if (width > 4) v = op(v, lane_move<0x141>(v));
-  if (width > 8) v = op(v, lane_move<0x140>(v));
-  if (width > 16) v = op(v, __shfl_xor(v, 16, 64));
-  if (width > 32) v = op(v, __shfl_xor(v, 32, 64));
-  return v;
-}
-
-/* Before the barrier: the wave's result; after it: the block's. */
-template <class T, class Op>
-__device__ __forceinline__ void reduce_put(T v, Op op, T *part) {
-  v = wave_reduce(v, op, 64);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-}
-
-template <int NT, class T, class Op>
-__device__ __forceinline__ T reduce_get(Op op, const T *part) {
-  if constexpr (NT == 64) return part[0];
-  if constexpr (NT == 128) return op(part[0], part[1]);
-  return wave_reduce(part[threadIdx.x & (NT / 64 - 1)], op, NT / 64);
-}
-
-/* ------------------------------------------------------------------------
- * Terms. A maximum of -inf (nothing but -inf) counts as 0, so that such
- * terms are 0 and a NaN stays one. Beyond 2^60 in exponent units, where
- * z c could overflow, neighbouring values lie so far apart that any c gives
- * terms of 1 and 0: 2^-4 does.
- * ---------------------------------------------------------------------- */
-struct Shift {
-  float max, c, whole;
-  float rest;   /* ln 2 * (max c - whole) */
-};
-
-__device__ __forceinline__ Shift shift_of(float max, float c) {
-  Shift s;
-  s.max = max == -INFINITY ? 0.0f : max;
-  s.c = fabsf(s.max * c) < 1.15292150e18f ? c : 0.0625f;
-  s.whole = rintf(s.max * s.c);
-  s.rest = fmaf(s.max, s.c, -s.whole) * 0.69314718f;
-  return s;
-}
-
-__device__ __forceinline__ float term(float z, const Shift &s) {
-  return exp2_fast(fmaf(z, s.c, -s.whole));
-}
 
 /* The shift that makes terms 2^96 larger, where a sum of those off the slots
  * below 2^-40 asks for it; false if it does not or cannot be (beyond 2^24 whole
@@ -525,20 +354,6 @@ __device__ __forceinline__ void mark_slot(uint32_t *bits, uint32_t edges, const 
  * the vectors arrive, twice the threads with half of the vectors, or blocks
  * that start apart in time gained nothing or little.
  * ---------------------------------------------------------------------- */
-template <int DT>
-__device__ __forceinline__ u32x4 empty_vec() {   /* -inf */
-  const uint32_t w = DT == ZS_FP32 ? 0xff800000u : DT == ZS_BF16 ? 0xff80ff80u : 0xfc00fc00u;
-  return u32x4{w, w, w, w};
-}
-
-/* A buffer that hardware checks the bounds of: reads past `bytes` give 0 and
- * writes there are dropped, without a branch in the code. Only the vector
- * offset is checked, so all of an offset goes there. The description is that
- * of plain 32-bit data. */
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const void *p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
-}
-
 /* The gradient is stored non-temporally but in one-wave blocks: their short
  * rows have a slot in many of their lines, and a line that has left the L2 by
  * then is read back for it (65536 x 4096: 272 us plain, 326 non-temporal;
@@ -580,39 +395,6 @@ __device__ __forceinline__ u32x4 fetch_vec(__amdgpu_buffer_rsrc_t row, const Row
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                        row, (int)(mine < last ? mine : last), 0, 0));
 }
-
-/* Running maximum of whole vectors. Written in instructions for two reasons:
- * the compiler would quiet every operand first, and it would carry the
- * values unpacked here to the sums, at twice the registers. What a NaN does
- * to the row, its sum does anyway. */
-template <int DT>
-struct VecMax {
-  uint32_t m = DT == ZS_FP16 ? 0xfc00fc00u : 0xff800000u;   /* -inf, two of them in fp16 */
-
-  __device__ __forceinline__ void add(const u32x4 &x) {
-    if constexpr (DT == ZS_FP16) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) asm("v_pk_max_f16 %0, %0, %1" : "+v"(m) : "v"(x[j]));
-    } else if constexpr (DT == ZS_FP32) {
-#pragma unroll
-      for (int j = 0; j < 4; j += 2)
-        asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[j]), "v"(x[j + 1]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t lo, hi;
-        asm("v_lshlrev_b32 %0, 16, %1" : "=v"(lo) : "v"(x[j]));
-        asm("v_and_b32 %0, 0xffff0000, %1" : "=v"(hi) : "v"(x[j]));
-        asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(lo), "v"(hi));
-      }
-    }
-  }
-
-  __device__ __forceinline__ float get() const {
-    if constexpr (DT == ZS_FP16) return fmaxf(up_lo<DT>(m), up_hi<DT>(m));
-    else return __uint_as_float(m);
-  }
-};
 
 template <int DT>
 __device__ __forceinline__ uint32_t fetch_edge(const DistillArgs &a, const RowIn &r) {

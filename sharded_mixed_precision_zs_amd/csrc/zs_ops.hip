@@ -14,188 +14,16 @@
 #include "zeroshard.h"
 
 #include "zs_distill_kernels.h"
-#include "zs_host_common.h"
-#include "zs_matmul_kernels.h"
+#include "zs_matmul_launch.h"
 #include "zs_norm_kernels.h"
+#include "zs_norm_launch.h"
+#include "zs_ops_common.h"
 #include "zs_quantize_kernels.h"
 
 namespace {
 
 using namespace zs;
-using zs_host::fail;
-using zs_host::launch_result;
-using zs_host::overlaps;
-using zs_host::too_big;
-
-constexpr uint64_t kMaxVocab = 0x7fffffffull;   /* token ids are 31 bits */
-
-/* Whether a launch may have so many blocks: its threads are counted in 32 bits. */
-bool fits(uint64_t blocks, uint64_t threads) { return blocks <= 0xffffffffull / threads; }
-
-bool valid16(int dt) { return dt == ZS_BF16 || dt == ZS_FP16; }
-bool valid_any(int dt) { return valid16(dt) || dt == ZS_FP32; }
-bool valid_format(int f) { return f == ZS_MX_E2M1 || f == ZS_MX_E4M3; }
-
-uint64_t esize(int dt) { return dt == ZS_FP32 ? 4 : 2; }
-uint64_t padded_of(uint64_t k) { return (k + ZS_MX_GROUP - 1) / ZS_MX_GROUP * ZS_MX_GROUP; }
-uint64_t code_bytes(int format, uint64_t padded) { return format == ZS_MX_E2M1 ? padded / 2 : padded; }
-
-bool aligned(const void *p, uint64_t bytes) { return (uintptr_t)p % bytes == 0; }
-
-/* Bytes from the first to the last element of `rows` rows of `cols`, `ld` apart. */
-uint64_t extent(uint64_t rows, uint64_t cols, uint64_t ld, uint64_t esz) {
-  return rows ? ((rows - 1) * ld + cols) * esz : 0;
-}
-
-/* A matrix whose element counts stay below 2^48. */
-bool matrix_too_big(uint64_t rows, uint64_t cols) {
-  return too_big(rows) || too_big(cols) || (cols && rows > zs_host::kMaxElems / cols);
-}
-
-/* Calls f with std::integral_constant-like tags chosen at run time. */
-template <int V>
-struct Tag {
-  static constexpr int value = V;
-};
-
-template <class F>
-void with16(int dt, F f) {
-  if (dt == ZS_BF16) f(Tag<ZS_BF16>{});
-  else f(Tag<ZS_FP16>{});
-}
-
-template <class F>
-void with_any(int dt, F f) {
-  if (dt == ZS_FP32) f(Tag<ZS_FP32>{});
-  else with16(dt, f);
-}
-
-template <class F>
-void with_format(int fmt, F f) {
-  if (fmt == ZS_MX_E2M1) f(Tag<ZS_MX_E2M1>{});
-  else f(Tag<ZS_MX_E4M3>{});
-}
-
-template <class F>
-void with_bool(bool b, F f) {
-  if (b) f(Tag<1>{});
-  else f(Tag<0>{});
-}
-
-/* ------------------------------------------------------------------------
- * The norm's threads per row and vectors of eight per thread: a wave for
- * short rows, then a block that grows with the row, so that a thread has two
- * vectors and the backward pass's sums and next row fit its registers
- * (16384 x 4096 backward: 110 us with 256 threads of two vectors, 285 with
- * one wave of eight; up to 1024 elements one wave saves the barrier: 65536 x
- * 1024 forward in 87 us). That ends at 8192 elements: the backward pass of
- * 1024 threads, of 128 registers each, keeps 72 to 284 bytes a thread in
- * scratch memory up to 16384 and 1.5 to 2.1 KB above.
- * ---------------------------------------------------------------------- */
-constexpr uint64_t kMaxNormCols = 65536;
-
-template <class F>
-void with_norm_shape(uint64_t padded, F f) {
-  if (padded <= 512) f(Tag<64>{}, Tag<1>{});
-  else if (padded <= 1024) f(Tag<64>{}, Tag<2>{});
-  else if (padded <= 2048) f(Tag<256>{}, Tag<1>{});
-  else if (padded <= 4096) f(Tag<256>{}, Tag<2>{});
-  else if (padded <= 8192) f(Tag<512>{}, Tag<2>{});
-  else if (padded <= 16384) f(Tag<1024>{}, Tag<2>{});
-  else f(Tag<1024>{}, Tag<8>{});
-}
-
-/* ------------------------------------------------------------------------
- * The product's variant: for few rows of A, bound by B, the thin kernel;
- * the large tiles where they occupy every CU (4096^3 of 4 x 4 bits 42 us,
- * 53 in tiles of 128 x 128; 8 x 4 bits 106 and 120), else 128 x 128 (2048 x
- * 4096 x 4096 of 4 x 4 bits, whose large tiles fill half of the CUs: 29 us,
- * large 36), and where even these leave three CUs of four idle and K is long,
- * that split along K into pieces of 1024 elements or more, as far as the
- * workspace holds their sums.
- * ---------------------------------------------------------------------- */
-int too_large() { return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: too large for one launch%s"); }
-
-template <int AF, int CDT, int BM, int BN, int NW>
-int launch_tile(const MatmulArgs &a, uint32_t splits, hipStream_t s) {
-  const uint64_t tiles = (uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN);
-  if (!fits(tiles, 64 * NW)) return too_large();
-  hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN, NW>), dim3((unsigned)tiles, splits),
-                     dim3(64 * NW), 0, s, a);
-  return launch_result();
-}
-
-constexpr uint64_t kMaxMatmulK = 1ull << 22; /* byte offsets in a tile of 256 rows are 32 bits */
-constexpr uint64_t kFullChip = 256; /* blocks that give every CU one */
-
-/* Whether the thin kernel runs: every block reads all of A, which 32 rows of
- * B to a block repay for a few rows of A, or where tiles would leave half of
- * the CUs idle, or spend most of the two passes over an 8-bit A on rows that
- * are not there (32 x 32000 x 4096: 8-bit A 29 us, in tiles 31; 17 rows 23 and
- * 31; 4-bit A 20 us, in tiles 16). */
-bool matmul_thin(uint64_t m, uint64_t n, bool wide_a) {
-  return m <= 16 || (m <= 32 && (wide_a || n <= 128 * 128));
-}
-
-struct MatmulSplit {
-  uint32_t splits, groups;   /* groups of 128 elements of K per split */
-};
-
-MatmulSplit matmul_split(uint64_t m, uint64_t n, uint64_t padded, uint64_t workspace_bytes) {
-  const uint64_t tiles = (m + 127) / 128 * ((n + 127) / 128), groups = padded / ZS_MX_GROUP;
-  uint64_t splits = kFullChip / tiles;
-  if (splits > groups / 8) splits = groups / 8;
-  if (splits > workspace_bytes / (m * n * 4)) splits = workspace_bytes / (m * n * 4);
-  /* four at least: two pieces cost more than they save (512 x 4096 x 4096
-   * 4-bit: 25 us against 16 in one), more pay (768 x 768 x 8192 8-bit A: 24
-   * against 53; 65 x 4096 x 4096: 16 against 29) */
-  if (matmul_thin(m, n, false) || splits < 4) return {1, (uint32_t)groups};
-  const uint64_t each = (groups + splits - 1) / splits, four = (each + 3) / 4 * 4;
-  return {(uint32_t)((groups + four - 1) / four), (uint32_t)four};
-}
-
-template <int AF, int CDT>
-int launch_matmul(MatmulArgs a, float *workspace, uint64_t workspace_bytes, hipStream_t s) {
-  constexpr uint64_t esz = CDT == ZS_FP32 ? 4 : 2;
-  a.split_groups = a.padded / ZS_MX_GROUP;
-  if (matmul_thin(a.m, a.n, AF == ZS_MX_E4M3)) {
-    /* four results of a lane in one store */
-    const int vec = aligned(a.c, 4 * esz) && a.ldc % 4 == 0;
-    const uint32_t blocks = (a.n + 31) / 32;
-    if (!fits(blocks, 64 * kThinWaves)) return too_large();
-    /* both halves of an 8-bit A in one instruction: 1 x 32000 x 4096 15.6 us,
-     * in two 18.9; 4 rows 18.0 and 19.3; 16 rows 26.6 and 22.5 */
-    if (AF == ZS_MX_E4M3 && a.m <= 4)
-      hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, AF == ZS_MX_E4M3>), dim3(blocks),
-                         dim3(64 * kThinWaves), 0, s, a, vec);
-    else
-      hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, false>), dim3(blocks), dim3(64 * kThinWaves),
-                         0, s, a, vec);
-    return launch_result();
-  }
-  constexpr int BM = AF == ZS_MX_E2M1 ? 256 : 128, BN = 256;
-  if ((uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN) >= kFullChip)
-    return launch_tile<AF, CDT, BM, BN, AF == ZS_MX_E2M1 ? 8 : 4>(a, 1, s);
-
-  const MatmulSplit sp = matmul_split(a.m, a.n, a.padded, workspace_bytes);
-  if (sp.splits < 2) return launch_tile<AF, CDT, 128, 128, 4>(a, 1, s);
-
-  a.part = workspace;
-  a.split_groups = sp.groups;
-  if (int rc = launch_tile<AF, ZS_FP32, 128, 128, 4>(a, sp.splits, s)) return rc;
-  const uint64_t all = (uint64_t)a.m * a.n;
-  hipLaunchKernelGGL((matmul_join_kernel<CDT>), dim3((unsigned)((all + kBlock - 1) / kBlock)),
-                     dim3(kBlock), 0, s, a, sp.splits);
-  return launch_result();
-}
-
-/* Groups that share the rows of a backward pass: some four rows each, for
- * their sums of dg cost as much again as a row or two; 256 at least, a block
- * for every CU, and 1024 at most. */
-uint32_t norm_parts(uint64_t rows) {
-  const uint64_t want = rows / 4 < 256 ? 256 : rows / 4 > 1024 ? 1024 : rows / 4;
-  return (uint32_t)(rows < want ? rows : want);
-}
+using namespace zs_ops;
 
 }  // namespace
 
@@ -474,20 +302,6 @@ DistillSplit distill_split(uint64_t rows, uint64_t vocab, int dtype) {
    * after them, so the parts' shares of the vocabulary leave nothing out */
   parts = vecs ? (vecs + each - 1) / each : 1;
   return {(uint32_t)parts, (uint32_t)each, (uint32_t)vecs};
-}
-
-/* CUs of the current device (256 if unknown). */
-int cu_count() {
-  static thread_local int cached_dev = -1, cached = 256;
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return 256;
-  if (dev != cached_dev) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) n = 0;
-    cached = n > 0 ? n : 256;
-    cached_dev = dev;
-  }
-  return cached;
 }
 
 /* Blocks that walk the rows: as many as fit at the registers the kernel is

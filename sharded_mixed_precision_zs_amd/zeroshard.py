@@ -75,6 +75,11 @@ class zs_device_scaler(C.Structure):
                 ("last_alpha", C.c_float), ("last_bc2", C.c_float)]
 
 
+class zs_dropout_rule(C.Structure):
+    _fields_ = [("p", C.c_float), ("seed", C.c_uint64), ("offset", C.c_uint64),
+                ("dev_offset", C.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libzeroshard is not built ({LIB_PATH}); "
@@ -83,6 +88,7 @@ def _load():
     # build.py), so it shares torch's streams and allocations
     lib = C.CDLL(LIB_PATH)
     vp, u32, u64, f32, i32 = C.c_void_p, C.c_uint32, C.c_uint64, C.c_float, C.c_int
+    rule = C.POINTER(zs_dropout_rule)
     sig = {
         "zs_abi_version": ([], i32),
         "zs_status_string": ([i32], C.c_char_p),
@@ -115,6 +121,12 @@ def _load():
         "zs_distill_workspace": ([u64, u64, u32, i32], u64),
         "zs_distill": ([vp, i32, u64, u64, u64, vp, vp, u32, f32, vp, vp, f32, vp, vp, vp, u64,
                         vp, u64, vp], i32),
+        "zs_dropout": ([vp, vp, i32, u64, u64, rule, vp, vp], i32),
+        "zs_block_norm_forward": ([vp, vp, vp, vp, vp, i32, u64, u64, f32, f32, f32, rule, vp, vp,
+                                   vp, vp, vp, vp, vp], i32),
+        "zs_block_norm_backward_workspace": ([u64, u64], u64),
+        "zs_block_norm_backward": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, u64, u64, f32, f32,
+                                    rule, vp, vp, vp, vp, vp, vp, u64, vp], i32),
         "zs_offload_step": ([vp, vp, vp, vp, vp, vp, vp, u64, C.POINTER(zs_adamw_hparams), i32,
                              vp, vp, i32, i32, vp, C.POINTER(C.c_int)], i32),
     }
@@ -668,3 +680,80 @@ def zs_distill(logits, ids, teacher, temperature, loss, grad=None, teacher_lse=N
         _dense(row_weight, (rows,), f32, "row_weight"), loss_scale,
         None if dev_scaler is None else _dev_scaler_ptr(dev_scaler),
         _dense(loss, (rows,), f32, "loss"), gp, gld, wp, wb, _raw_stream(stream)))
+
+
+# ---- operators of the student's last block ------------------------------------
+
+def _rule(dropout):
+    """A zs_dropout_rule from (p, seed, offset) or (p, seed, offset, dev_offset), the last a
+    CUDA int64 tensor of one element; None stays None."""
+    if dropout is None or isinstance(dropout, zs_dropout_rule):
+        return dropout
+    p, seed, offset, *more = dropout
+    dev = more[0] if more else None
+    if dev is not None and (not dev.is_cuda or dev.element_size() != 8 or dev.numel() != 1):
+        raise ValueError("dev_offset: CUDA tensor of one 64-bit element expected")
+    mask = (1 << 64) - 1
+    return zs_dropout_rule(p, seed & mask, offset & mask, None if dev is None else dev.data_ptr())
+
+
+def zs_dropout(x, out, rule, residual=None, stream=None):
+    """out = residual + dropout(x) of a 2-D tensor; rule: (p, seed, offset[, dev_offset]).
+    out may be x or residual."""
+    if x.dim() != 2:
+        raise ValueError("x: 2-D tensor expected")
+    shape, dt = x.shape, x.dtype
+    _check("zs_dropout", _lib.zs_dropout(
+        _dense(x, shape, dt, "x"), _dense(residual, shape, dt, "residual"),
+        _float_code(x, "x", fp32=True), *shape, _rule(rule), _dense(out, shape, dt, "out"),
+        _raw_stream(stream)))
+
+
+def zs_block_norm_forward(x, residual, gain, eps, h, rstd=None, post_gain=None, post_rstd=None,
+                          gate=None, residual_scale=1.0, branch_scale=1.0, dropout=None,
+                          codes=None, scales=None, y=None, stream=None):
+    """h = residual_scale * residual + branch_scale * dropout(gate * norm(x)), then h's norm
+    into 8-bit microscaled rows (codes, scales) and / or a 16-bit y. Without post_gain x is
+    taken as it is, without gate the gate is 1; dropout: (p, seed, offset[, dev_offset])."""
+    if x.dim() != 2:
+        raise ValueError("x: 2-D tensor expected")
+    shape, dt, f32 = x.shape, x.dtype, _t().f32
+    cp = sp = None
+    if codes is not None or scales is not None:
+        if codes is None or scales is None:
+            raise ValueError("codes and scales go together")
+        cp, sp = _mx_ptrs(codes, scales, *shape, ZS_MX_E4M3, "y")
+    _check("zs_block_norm_forward", _lib.zs_block_norm_forward(
+        _dense(x, shape, dt, "x"), _dense(residual, shape, dt, "residual"),
+        _dense(post_gain, shape[1:], dt, "post_gain"), _dense(gate, shape[1:], dt, "gate"),
+        _dense(gain, shape[1:], dt, "gain"), _float_code(x, "x"), *shape, eps, residual_scale,
+        branch_scale, _rule(dropout), _dense(h, shape, dt, "h"),
+        _dense(post_rstd, shape[:1], f32, "post_rstd"), _dense(rstd, shape[:1], f32, "rstd"),
+        cp, sp, _dense(y, shape, dt, "y"), _raw_stream(stream)))
+
+
+def zs_block_norm_backward_workspace(rows, cols):
+    """Bytes of workspace that zs_block_norm_backward needs."""
+    return _lib.zs_block_norm_backward_workspace(rows, cols)
+
+
+def zs_block_norm_backward(dy, h, rstd, gain, dx, dresidual, dgain, workspace, x=None,
+                           post_gain=None, post_rstd=None, gate=None, dpost_gain=None, dgate=None,
+                           dres=None, residual_scale=1.0, branch_scale=1.0, dropout=None,
+                           stream=None):
+    """Gradients of zs_block_norm_forward: dx and dresidual (16 bits) and the fp32 dgain,
+    dpost_gain and dgate. dres: what h receives from elsewhere."""
+    if dy.dim() != 2:
+        raise ValueError("dy: 2-D tensor expected")
+    shape, dt, f32 = dy.shape, dy.dtype, _t().f32
+    wp, wb = _workspace(workspace)
+    _check("zs_block_norm_backward", _lib.zs_block_norm_backward(
+        _dense(dy, shape, dt, "dy"), _dense(h, shape, dt, "h"),
+        _dense(rstd, shape[:1], f32, "rstd"), _dense(gain, shape[1:], dt, "gain"),
+        _dense(dres, shape, dt, "dres"), _dense(x, shape, dt, "x"),
+        _dense(post_rstd, shape[:1], f32, "post_rstd"),
+        _dense(post_gain, shape[1:], dt, "post_gain"), _dense(gate, shape[1:], dt, "gate"),
+        _float_code(dy, "dy"), *shape, residual_scale, branch_scale, _rule(dropout),
+        _dense(dx, shape, dt, "dx"), _dense(dresidual, shape, dt, "dresidual"),
+        _dense(dgain, shape[1:], f32, "dgain"), _dense(dpost_gain, shape[1:], f32, "dpost_gain"),
+        _dense(dgate, shape[1:], f32, "dgate"), wp, wb, _raw_stream(stream)))
