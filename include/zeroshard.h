@@ -721,6 +721,93 @@ int zs_block_norm_backward(const void *dy, const void *h, const float *rstd, con
                            float *dgain, float *dpost_gain, float *dgate, void *workspace,
                            uint64_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Losses on the log-probabilities of given tokens: what a student is trained
+ * on after distillation, at the place of zs_distill and by its conventions.
+ * Per row, with u = logits / temperature and the row's token a,
+ *   logp = u[a] - logsumexp(u),
+ * and with g the loss's slope in logp,
+ *   grad = S * g / temperature * (1[j = a] - softmax(u)[j]),
+ * S = dev->scale, or loss_scale without dev. 1 - softmax(u)[a] is the sum of
+ * the others, and small values of it and of logp keep their precision.
+ *   logits : dtype (bf16, fp16, fp32)[rows][vocab], rows `ld` apart.
+ *   ids    : int32[rows]; an id outside [0, vocab) is no token (a prompt's,
+ *            or padding): its logits are not read, its gradient is zero.
+ *   grad   : NULL (loss only), or dtype[rows][vocab], rows `grad_ld` apart;
+ *            may be the logits' own buffer.
+ *   workspace: the entry point's _workspace(rows, vocab, dtype) bytes, 16-byte
+ *            aligned.
+ * Logits of -inf are tokens that cannot be chosen; a NaN, +inf or a row of
+ * -inf gives a NaN row. A row's result depends on the row, on how it is aligned
+ * to 16 bytes and, in a sum's last bits, on the number of rows. Errors of all three:
+ * ZS_ERR_INVALID_ARG (null pointers, dtype, temperature not finite or below
+ * 2^-126, loss_scale not finite and > 0, vocab 0 or above 2^31 - 1, rows
+ * closer than vocab, workspace too small), ZS_ERR_UNSUPPORTED (2^31 rows or
+ * more, alignment).
+ *
+ * The log-probabilities alone (of the sampler, or of a reference model):
+ *   logp   : fp32[rows]; 0 for rows without a token. */
+uint64_t zs_logprob_workspace(uint64_t rows, uint64_t vocab, int dtype);
+int zs_logprob(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
+               const int32_t *ids, float temperature, float *logp, void *workspace,
+               uint64_t workspace_bytes, void *stream);
+
+/* Clipped policy loss with a KL term, per row:
+ *   r = exp(logp - old_logp),  d = ref_logp - logp
+ *   loss = w * (-min(r * A, clip(r, 1 - clip_low, 1 + clip_high) * A)
+ *               + kl_weight * (exp(d) - 1 - d))
+ * and its slope in logp, which has no part of the first term where that is
+ * clipped (A > 0 and r > 1 + clip_high, or A < 0 and r < 1 - clip_low).
+ *   advantage: fp32[rows], A.
+ *   old_logp : fp32[rows], the sampler's; NULL: r is 1 (its slope is A's).
+ *   ref_logp : fp32[rows], the reference model's; NULL: no KL term.
+ *   row_weight: NULL (all 1), or fp32[rows]. A row of weight 0 gives logp and
+ *              loss 0 and a zero gradient, whatever its logits.
+ *   logp     : NULL, or fp32[rows]; loss: fp32[rows]; 0 for rows without a
+ *              token.
+ * Further errors: ZS_ERR_INVALID_ARG (clip_low outside [0, 1], clip_high not
+ * finite and >= 0, kl_weight not finite). */
+uint64_t zs_policy_workspace(uint64_t rows, uint64_t vocab, int dtype);
+int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
+              const int32_t *ids, float temperature, const float *advantage,
+              const float *old_logp, const float *ref_logp, float clip_low, float clip_high,
+              float kl_weight, const float *row_weight, float loss_scale,
+              const zs_device_scaler *dev, float *logp, float *loss, void *grad, uint64_t grad_ld,
+              void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* Preference loss of pairs of sequences. Sequence s is rows starts[s] ..
+ * starts[s + 1] - 1; pair p prefers sequence 2p to sequence 2p + 1. With L
+ * a sequence's sum of logp over its tokens (with `mean`, their mean; 0 without
+ * tokens) and D = (L - ref)[2p] - (L - ref)[2p + 1], per pair:
+ *   ZS_PREFERENCE_SIGMOID: w * ((1 - smoothing) * softplus(-beta * D)
+ *                               + smoothing * softplus(beta * D))
+ *   ZS_PREFERENCE_HINGE  : w * max(0, 1 - beta * D)
+ *   ZS_PREFERENCE_SQUARE : w * (D - 1 / (2 * beta))^2
+ * Sums are binary64, in a fixed order.
+ *   starts : int32[2 * pairs + 1] on the device, ascending; values are taken
+ *            to lie in [0, rows]. Rows before the first and from the last on
+ *            are not read, and their gradient's rows are left as they were.
+ *   ref_logp: NULL (zeros), or fp32[2 * pairs], the reference model's L.
+ *   pair_weight: NULL (all 1), or fp32[pairs]; with weight 0 loss and gradient
+ *            are zero, whatever the logits.
+ *   seq_logp: NULL, or fp32[2 * pairs], L; loss: fp32[pairs].
+ * The logits are read twice: a row's gradient needs its whole pair's loss.
+ * Further errors: ZS_ERR_INVALID_ARG (kind, beta not finite and > 0, smoothing
+ * outside [0, 1] or with another kind than the sigmoid), ZS_ERR_UNSUPPORTED
+ * (2^24 pairs or more). */
+typedef enum {
+  ZS_PREFERENCE_SIGMOID = 0,
+  ZS_PREFERENCE_HINGE = 1,
+  ZS_PREFERENCE_SQUARE = 2
+} zs_preference_kind;
+uint64_t zs_preference_workspace(uint64_t rows, uint64_t vocab, int dtype);
+int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
+                  const int32_t *ids, const int32_t *starts, uint64_t pairs, float temperature,
+                  const float *ref_logp, int kind, float beta, float smoothing, int mean,
+                  const float *pair_weight, float loss_scale, const zs_device_scaler *dev,
+                  float *seq_logp, float *loss, void *grad, uint64_t grad_ld, void *workspace,
+                  uint64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,7 @@ ZS_STATE_GROUP = 1024
 ZS_MX_E2M1, ZS_MX_E4M3 = 0, 1
 ZS_MX_BLOCK, ZS_MX_GROUP = 32, 128
 ZS_DISTILL_MAX_SLOTS = 1024
+ZS_PREFERENCE_SIGMOID, ZS_PREFERENCE_HINGE, ZS_PREFERENCE_SQUARE = 0, 1, 2
 ZS_OK, ZS_ERR_INVALID_ARG, ZS_ERR_UNSUPPORTED, ZS_ERR_ALIAS, ZS_ERR_HIP = range(5)
 
 LIB_PATH = _build.LIB
@@ -127,6 +128,14 @@ def _load():
         "zs_block_norm_backward_workspace": ([u64, u64], u64),
         "zs_block_norm_backward": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, u64, u64, f32, f32,
                                     rule, vp, vp, vp, vp, vp, vp, u64, vp], i32),
+        "zs_logprob_workspace": ([u64, u64, i32], u64),
+        "zs_logprob": ([vp, i32, u64, u64, u64, vp, f32, vp, vp, u64, vp], i32),
+        "zs_policy_workspace": ([u64, u64, i32], u64),
+        "zs_policy": ([vp, i32, u64, u64, u64, vp, f32, vp, vp, vp, f32, f32, f32, vp, f32, vp, vp,
+                       vp, vp, u64, vp, u64, vp], i32),
+        "zs_preference_workspace": ([u64, u64, i32], u64),
+        "zs_preference": ([vp, i32, u64, u64, u64, vp, vp, u64, f32, vp, i32, f32, f32, i32, vp,
+                           f32, vp, vp, vp, vp, u64, vp, u64, vp], i32),
         "zs_offload_step": ([vp, vp, vp, vp, vp, vp, vp, u64, C.POINTER(zs_adamw_hparams), i32,
                              vp, vp, i32, i32, vp, C.POINTER(C.c_int)], i32),
     }
@@ -757,3 +766,82 @@ def zs_block_norm_backward(dy, h, rstd, gain, dx, dresidual, dgain, workspace, x
         _dense(dx, shape, dt, "dx"), _dense(dresidual, shape, dt, "dresidual"),
         _dense(dgain, shape[1:], f32, "dgain"), _dense(dpost_gain, shape[1:], f32, "dpost_gain"),
         _dense(dgate, shape[1:], f32, "dgate"), wp, wb, _raw_stream(stream)))
+
+
+# ---- losses on the log-probabilities of given tokens ---------------------------
+
+def _grad_rows(grad, logits, rows, vocab):
+    """(address, row stride) of a gradient of the logits' shape and type; (None, 0) without."""
+    if grad is None:
+        return None, 0
+    if grad.dtype != logits.dtype:
+        raise ValueError("grad: the logits' dtype expected")
+    gp, _, _, gld = _rows(grad, "grad", (rows, vocab))
+    return gp, gld
+
+
+def zs_logprob_workspace(rows, vocab, dtype):
+    """Bytes of workspace that zs_logprob needs; dtype: the logits' zs_dtype."""
+    return _lib.zs_logprob_workspace(rows, vocab, dtype)
+
+
+def zs_logprob(logits, ids, logp, temperature=1.0, workspace=None, stream=None):
+    """Log-probability of each row's token ids[row] (0 where that is no token)."""
+    p, rows, vocab, ld = _rows(logits, "logits")
+    wp, wb = _workspace(workspace)
+    _check("zs_logprob", _lib.zs_logprob(
+        p, _float_code(logits, "logits", fp32=True), rows, vocab, ld,
+        _dense(ids, (rows,), _t().i32, "ids"), temperature, _dense(logp, (rows,), _t().f32, "logp"),
+        wp, wb, _raw_stream(stream)))
+
+
+def zs_policy_workspace(rows, vocab, dtype):
+    """Bytes of workspace that zs_policy needs; dtype: the logits' zs_dtype."""
+    return _lib.zs_policy_workspace(rows, vocab, dtype)
+
+
+def zs_policy(logits, ids, advantage, loss, temperature=1.0, old_logp=None, ref_logp=None,
+              clip_low=0.2, clip_high=0.2, kl_weight=0.0, row_weight=None, loss_scale=1.0,
+              dev_scaler=None, logp=None, grad=None, workspace=None, stream=None):
+    """Clipped policy loss per row and, with grad, the logits' gradient times the loss scale
+    (loss_scale, or dev_scaler's). grad may be logits itself."""
+    p, rows, vocab, ld = _rows(logits, "logits")
+    f32 = _t().f32
+    gp, gld = _grad_rows(grad, logits, rows, vocab)
+    wp, wb = _workspace(workspace)
+    per_row = {name: _dense(t, (rows,), f32, name) for name, t in
+               (("advantage", advantage), ("old_logp", old_logp), ("ref_logp", ref_logp),
+                ("row_weight", row_weight), ("logp", logp), ("loss", loss))}
+    _check("zs_policy", _lib.zs_policy(
+        p, _float_code(logits, "logits", fp32=True), rows, vocab, ld,
+        _dense(ids, (rows,), _t().i32, "ids"), temperature, per_row["advantage"],
+        per_row["old_logp"], per_row["ref_logp"], clip_low, clip_high, kl_weight,
+        per_row["row_weight"], loss_scale,
+        None if dev_scaler is None else _dev_scaler_ptr(dev_scaler), per_row["logp"],
+        per_row["loss"], gp, gld, wp, wb, _raw_stream(stream)))
+
+
+def zs_preference_workspace(rows, vocab, dtype):
+    """Bytes of workspace that zs_preference needs; dtype: the logits' zs_dtype."""
+    return _lib.zs_preference_workspace(rows, vocab, dtype)
+
+
+def zs_preference(logits, ids, starts, beta, loss, kind=ZS_PREFERENCE_SIGMOID, smoothing=0.0,
+                  mean=False, temperature=1.0, ref_logp=None, pair_weight=None, loss_scale=1.0,
+                  dev_scaler=None, seq_logp=None, grad=None, workspace=None, stream=None):
+    """Preference loss per pair of sequences (rows starts[s] to starts[s + 1] of logits and ids;
+    pair p prefers sequence 2p) and, with grad, the logits' gradient times the loss scale. grad
+    may be logits itself; its rows outside all sequences are left as they were."""
+    p, rows, vocab, ld = _rows(logits, "logits")
+    f32, i32 = _t().f32, _t().i32
+    pairs = loss.shape[0] if loss.dim() == 1 else -1
+    gp, gld = _grad_rows(grad, logits, rows, vocab)
+    wp, wb = _workspace(workspace)
+    _check("zs_preference", _lib.zs_preference(
+        p, _float_code(logits, "logits", fp32=True), rows, vocab, ld,
+        _dense(ids, (rows,), i32, "ids"), _dense(starts, (2 * pairs + 1,), i32, "starts"), pairs,
+        temperature, _dense(ref_logp, (2 * pairs,), f32, "ref_logp"), kind, beta, smoothing,
+        1 if mean else 0, _dense(pair_weight, (pairs,), f32, "pair_weight"), loss_scale,
+        None if dev_scaler is None else _dev_scaler_ptr(dev_scaler),
+        _dense(seq_logp, (2 * pairs,), f32, "seq_logp"), _dense(loss, (pairs,), f32, "loss"), gp,
+        gld, wp, wb, _raw_stream(stream)))

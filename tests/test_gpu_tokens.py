@@ -1,0 +1,416 @@
+"""The losses on given tokens' log-probabilities on the GPU against their 64-bit
+plain forms.
+
+Tolerances, fixed before the first run. U: half a step of a type, relative. A
+term 2^(z c - I) has the rounding of its exponent, of c (relative to the row's
+largest) and of the instruction: with D the row's spread of z / tau, relative
+(2 D + 6) 2^-24. A thread adds at most 32 terms in fp32, everything beyond in
+binary64. So a sum is off by delta = (2 D + 38) 2^-24 of itself, a
+log-probability by 2 delta, or by that much of itself where it is small.
+"""
+import math
+import zlib
+
+import pytest
+import torch
+
+import token_reference as ref
+from gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+BF16, FP16, FP32, F64 = torch.bfloat16, torch.float16, torch.float32, torch.float64
+U = {t: torch.finfo(t).eps / 2 for t in (BF16, FP16, FP32)}
+TINY = {BF16: 2.0 ** -134, FP16: 2.0 ** -25, FP32: 2.0 ** -126}
+SHAPES = [(1, 1), (2, 3), (3, 9), (5, 15), (4, 100), (6, 1000), (7, 4099), (3, 50257), (2, 66000),
+          (2, 140001), (1100, 520), (1030, 2001)]
+
+
+@pytest.fixture(scope="module")
+def zs(hip_built):
+    from sharded_mixed_precision_zs_amd import zeroshard
+    return zeroshard
+
+
+def gen(*key):
+    return torch.Generator().manual_seed(zlib.crc32(repr(key).encode()))
+
+
+def code(zs, dtype):
+    return {BF16: zs.ZS_BF16, FP16: zs.ZS_FP16, FP32: zs.ZS_FP32}[dtype]
+
+
+def f32(t):
+    return None if t is None else t.float()
+
+
+def cu(t):
+    return None if t is None else t.cuda()
+
+
+def problem(rows, vocab, dtype):
+    """Logits; tokens, some of which are none, one of which is nearly certain, one unlikely."""
+    g = gen("z", rows, vocab)
+    z = 2 * torch.randn(rows, vocab, generator=g)
+    ids = torch.randint(0, vocab, (rows,), generator=g)
+    z[torch.arange(rows), ids] += 3
+    z[0, ids[0]] += 25
+    if rows > 3:
+        z[1, ids[1]] -= 30
+        ids[2], ids[3] = -1, vocab
+    return z.to(dtype), ids.int(), g
+
+
+def spread(z, tau):
+    zz = z.double() / tau
+    return zz.amax(1) - zz.masked_fill(torch.isinf(zz), 0).amin(1)
+
+
+def errors(z, tau, logp):
+    delta = (2 * spread(z, tau) + 38) * 2.0 ** -24
+    return delta, 2 * delta * (2 * logp.abs()).clamp(max=1) + 2.0 ** -23 * logp.abs()
+
+
+def check(got, want, tol, what):
+    got, want, tol = got.double().cpu(), want.double(), torch.as_tensor(tol).double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), f"{what}: NaN positions differ"
+    inf = torch.isinf(want)
+    assert torch.equal(got[inf], want[inf]), f"{what}: infinities differ"
+    ok = ~inf & ~torch.isnan(want)
+    err, tol = (got - want).abs()[ok], tol.expand(want.shape)[ok]
+    assert bool((err <= tol).all()), (
+        f"{what}: {int((err > tol).sum())} of {err.numel()} off; worst "
+        f"{float((err / tol.clamp(min=1e-300)).max()):.3g} times the tolerance")
+
+
+def check_grad(got, want, z, ids, tau, delta, dslope, dtype, what):
+    """dslope: error of the slope times scale / tau, per row."""
+    q = torch.softmax(z.double() / tau, 1)
+    live = (ids >= 0) & (ids < z.shape[1])
+    at = torch.arange(z.shape[0])[live]
+    share = q.clone()
+    others = q.clone()
+    others[at, ids[live].long()] = 0
+    share[at, ids[live].long()] = others[live].sum(1)
+    inner = want.abs() * (3 * delta.unsqueeze(1) + 2.0 ** -22) + share * dslope.unsqueeze(1)
+    check(got, want, U[dtype] * (want.abs() + inner) + inner + TINY[dtype], what)
+
+
+def guarded_like(z, ld=None):
+    """An output of z's shape in a buffer of a known value, rows `ld` apart, and a check that
+    nothing else was written."""
+    rows, vocab = z.shape
+    ld = ld or vocab
+    raw = torch.full((rows * ld + 32,), 7.0, dtype=z.dtype, device="cuda")
+    out = raw[16:16 + rows * ld].view(rows, ld)[:, :vocab]
+
+    def whole():
+        mask = torch.ones_like(raw, dtype=torch.bool)
+        mask[16:16 + rows * ld].view(rows, ld)[:, :vocab] = False
+        return bool((raw[mask] == 7.0).all())
+
+    return out, whole
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+@pytest.mark.parametrize("tau", [1.0, 0.7])
+def test_logprob_against_64_bits(zs, dtype, tau):
+    for rows, vocab in SHAPES:
+        announce(f"logprob {dtype} {tau} {rows}x{vocab}")
+        z, ids, _ = problem(rows, vocab, dtype)
+        want, _, _ = ref.logprob(z.double(), ids, float(torch.tensor(tau)))
+        out = torch.full((rows,), 9.0, device="cuda")
+        ws = torch.empty(zs.zs_logprob_workspace(rows, vocab, code(zs, dtype)), dtype=torch.uint8,
+                         device="cuda")
+        zs.zs_logprob(z.cuda(), ids.cuda(), out, temperature=tau, workspace=ws)
+        check(out, want, errors(z, tau, want)[1] + 1e-45, "logp")
+
+
+def run_policy(zs, z, ids, tau, adv, old, refs, weight, scale, grad, kl=0.05, **more):
+    rows, vocab = z.shape
+    logp, loss = torch.full((rows,), 9.0, device="cuda"), torch.full((rows,), 9.0, device="cuda")
+    need = zs.zs_policy_workspace(rows, vocab, code(zs, z.dtype))
+    zs.zs_policy(z, cu(ids), cu(adv), loss, temperature=tau, old_logp=cu(old), ref_logp=cu(refs),
+                 clip_low=0.2, clip_high=0.28, kl_weight=kl, row_weight=cu(weight),
+                 loss_scale=scale, logp=logp, grad=grad,
+                 workspace=torch.empty(need, dtype=torch.uint8, device="cuda"), **more)
+    return logp, loss
+
+
+def policy_inputs(z, ids, g, tau, old, refs, weighted):
+    rows = z.shape[0]
+    logp = ref.logprob(z.double(), ids, tau)[0]
+    adv = torch.randn(rows, generator=g)
+    # clipped on either side, or not; never within 1e-3 of an end
+    drift = torch.tensor([0.05, 0.4, -0.4, 0.1, -0.1, 0.3, -0.3])[torch.arange(rows) % 7]
+    o = (logp - drift.double()).float() if old else None
+    r = (logp + 0.3 * torch.randn(rows, generator=g)).float() if refs else None
+    w = torch.rand(rows, generator=g) if weighted else None
+    if weighted:
+        w[rows // 2] = 0
+    return adv, o, r, w
+
+
+def check_policy(z, ids, tau, adv, o, r, w, scale, logp, loss, grad, what):
+    tau = float(torch.tensor(tau))
+    dbl = lambda t: None if t is None else t.double()
+    low, high, kl = (float(torch.tensor(v)) for v in (0.2, 0.28, 0.05))
+    lp, want, g, mag = ref.policy(z.double(), ids, tau, adv.double(), dbl(o), dbl(r), low, high, kl,
+                                  dbl(w), scale)
+    delta, dlogp = errors(z, tau, lp)
+    check(logp, lp, dlogp + 1e-45, what + " logp")
+    # ratio and KL follow the log-probability; exp, products and sums beside it
+    check(loss, want, (mag * tau / scale + want.abs()) * (2 * dlogp + 2.0 ** -20) + 1e-45,
+          what + " loss")
+    if grad is not None:
+        check_grad(grad, g, z, ids, tau, delta, mag * (2 * dlogp + 2.0 ** -20), z.dtype, what)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+@pytest.mark.parametrize("old,refs,weighted", [(True, True, True), (False, True, False),
+                                               (True, False, False)])
+def test_policy_against_64_bits(zs, dtype, old, refs, weighted):
+    for rows, vocab in SHAPES:
+        announce(f"policy {dtype} {old} {refs} {rows}x{vocab}")
+        tau = 1.0 if old else 2.0
+        z, ids, g = problem(rows, vocab, dtype)
+        adv, o, r, w = policy_inputs(z, ids, g, tau, old, refs, weighted)
+        grad, whole = guarded_like(z)
+        logp, loss = run_policy(zs, z.cuda(), ids, tau, adv, o, r, w, 256.0, grad)
+        check_policy(z, ids, tau, adv, o, r, w, 256.0, logp, loss, grad, f"{rows}x{vocab}")
+        assert whole()
+        # without a gradient, and in the logits' place
+        l2, s2 = run_policy(zs, z.cuda(), ids, tau, adv, o, r, w, 256.0, None)
+        inplace = z.cuda()
+        l3, s3 = run_policy(zs, inplace, ids, tau, adv, o, r, w, 256.0, inplace)
+        assert torch.equal(l3, logp) and torch.equal(s3, loss) and torch.equal(inplace, grad)
+        check_policy(z, ids, tau, adv, o, r, w, 256.0, l2, s2, None, "loss alone")
+
+
+def test_policy_strided_and_unaligned(zs):
+    for dtype, off, vocab, ld, gld in ((BF16, 3, 1001, 1016, 1001), (FP16, 1, 9000, 9003, 9010),
+                                       (FP32, 1, 501, 777, 501), (BF16, 0, 20000, 20008, 20016)):
+        announce(f"policy strided {dtype} {vocab}")
+        z, ids, g = problem(6, vocab, dtype)
+        base = torch.zeros(6 * ld + 16, dtype=dtype, device="cuda")
+        view = base[off:off + 6 * ld].view(6, ld)[:, :vocab]
+        view.copy_(z)
+        adv, o, r, w = policy_inputs(z, ids, g, 1.0, True, True, False)
+        grad, whole = guarded_like(z, gld)
+        logp, loss = run_policy(zs, view, ids, 1.0, adv, o, r, w, 64.0, grad)
+        check_policy(z, ids, 1.0, adv, o, r, w, 64.0, logp, loss, grad, f"{vocab}")
+        assert whole()
+
+
+def test_policy_rows_that_are_not_finite(zs):
+    """-inf logits cannot be chosen; NaN, +inf and rows of -inf spoil their own row alone; rows
+    without a token or weight are not looked at."""
+    for dtype in (BF16, FP32):
+        z, ids, g = problem(12, 1000, dtype)
+        adv, o, r, w = policy_inputs(z, ids, g, 1.0, True, True, True)
+        ids[4:] = torch.arange(4, 12)
+        lp = ref.logprob(z.double(), ids, 1.0)[0]
+        o, r = (lp - 0.1).float(), (lp + 0.1).float()
+        z[4, 100:900] = -math.inf
+        z[5, 7] = math.nan
+        z[7, 8] = math.inf
+        z[8] = -math.inf
+        z[2] = math.nan                 # no token
+        z[6] = math.nan                 # no weight
+        w[6] = 0
+        z[9, 9] = -math.inf             # the token itself cannot be chosen
+        r[9] = -5
+        grad = torch.full_like(z, 3.0).cuda()
+        logp, loss = run_policy(zs, z.cuda(), ids, 1.0, adv, o, r, w, 16.0, grad)
+        bad = [5, 7, 8]
+        assert torch.isnan(logp[bad]).all() and torch.isnan(grad[bad].float()).all(1).all()
+        for row in (2, 3, 6):
+            assert logp[row] == 0 and loss[row] == 0 and not grad[row].any()
+        assert logp[9] == -math.inf and loss[9] == math.inf
+        keep = [0, 1, 4, 10, 11]
+        check_policy(z[keep], ids[keep], 1.0, adv[keep], o[keep], r[keep], w[keep], 16.0,
+                     logp[keep], loss[keep], grad[keep], "the others")
+
+
+def test_policy_sure_and_far_apart(zs):
+    """A token that has all but 2^-40 of the mass keeps its gradient and log-probability; logits
+    beyond the exponents' range do not overflow."""
+    z = torch.full((4, 300), -28.0)
+    z[0, 5] = 0.0
+    z[1] = torch.linspace(-3e4, 3e4, 300)
+    z[2] = torch.linspace(-3e38, 3e38, 300, dtype=F64).float()
+    z[3, :10] = 3e38
+    ids, adv = torch.tensor([5, 298, 299, 3], dtype=torch.int32), torch.ones(4)
+    grad = torch.empty(4, 300, device="cuda")
+    logp, loss = run_policy(zs, z.cuda(), ids, 1.0, adv, None, None, None, 1.0, grad, kl=0.0)
+    lp, q, _ = ref.logprob(z.double(), ids, 1.0)
+    g = ref.logit_grad(q, ids, torch.full((4,), -1.0, dtype=F64))
+    assert abs(float(logp[0]) / float(lp[0]) - 1) < 1e-5
+    assert abs(float(grad[0, 5]) / float(g[0, 5]) - 1) < 1e-5
+    assert torch.isfinite(grad).all()
+    # row 1: neighbours 200 apart; the token one below the top has none of the mass
+    assert abs(float(logp[1]) - float(lp[1])) < 1e-3 * 200 and logp[2] == 0 and not grad[2].any()
+    assert abs(float(logp[3]) + math.log(10)) < 1e-5
+
+
+def test_policy_scale_from_the_device(zs):
+    z, ids, g = problem(9, 777, BF16)
+    adv, o, r, w = policy_inputs(z, ids, g, 1.0, True, True, True)
+    scaler = zs.zs_loss_scaler(scale=512.0, clean_steps=0, growth_interval=0, dynamic=0, step_t=0,
+                               skipped=0)
+    dev = zs.device_scaler_upload(zs.zs_device_scaler_make(scaler, 0.9, 0.999))
+    a, b = torch.empty_like(z).cuda(), torch.empty_like(z).cuda()
+    run_policy(zs, z.cuda(), ids, 1.0, adv, o, r, w, 512.0, a)
+    run_policy(zs, z.cuda(), ids, 1.0, adv, o, r, w, 1.0, b, dev_scaler=dev)
+    assert torch.equal(a, b)
+
+
+# ---- pairs ---------------------------------------------------------------------
+
+def run_preference(zs, z, ids, starts, grad, refs=None, weight=None, **how):
+    pairs = (len(starts) - 1) // 2
+    loss, seq = torch.full((pairs,), 9.0, device="cuda"), torch.full((2 * pairs,), 9.0, device="cuda")
+    need = zs.zs_preference_workspace(*z.shape, code(zs, z.dtype))
+    zs.zs_preference(z, cu(ids), torch.tensor(starts, dtype=torch.int32).cuda(), how.pop("beta"),
+                     loss, ref_logp=cu(refs), pair_weight=cu(weight), seq_logp=seq, grad=grad,
+                     workspace=torch.empty(max(16, need), dtype=torch.uint8, device="cuda"), **how)
+    return loss, seq
+
+
+PAIRS = [((1, 1), [0, 1, 1]), ((2, 9), [0, 1, 2]), ((9, 100), [0, 2, 5, 7, 9]),
+         ((14, 1000), [2, 5, 9, 9, 12]), ((11, 4099), [0, 4, 11]), ((5, 50257), [0, 3, 5]),
+         ((3, 140001), [0, 1, 3]), ((1100, 520), [0, 300, 600, 700, 1100]),
+         ((1040, 2001), [3, 500, 501, 800, 1039])]
+KINDS = [("sigmoid", 0.0, False), ("sigmoid", 0.2, True), ("hinge", 0.0, False), ("square", 0.0, True)]
+
+
+def kind_of(zs, kind):
+    return {"sigmoid": zs.ZS_PREFERENCE_SIGMOID, "hinge": zs.ZS_PREFERENCE_HINGE,
+            "square": zs.ZS_PREFERENCE_SQUARE}[kind]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+@pytest.mark.parametrize("kind,smoothing,mean", KINDS)
+def test_preference_against_64_bits(zs, dtype, kind, smoothing, mean):
+    beta = 0.25
+    for (rows, vocab), starts in PAIRS:
+        announce(f"preference {dtype} {kind} {rows}x{vocab}")
+        z, ids, g = problem(rows, vocab, dtype)
+        pairs = (len(starts) - 1) // 2
+        own = ref.preference(z.double(), ids, starts, 1.0, None, kind, beta, smoothing, mean, None,
+                             1.0)[1]
+        refs = (own + torch.randn(2 * pairs, generator=g)).float()
+        weight = 0.5 + torch.rand(pairs, generator=g)
+        grad, whole = guarded_like(z)
+        loss, seq = run_preference(zs, z.cuda(), ids, starts, grad, refs, weight, beta=beta,
+                                   kind=kind_of(zs, kind), smoothing=smoothing, mean=mean,
+                                   loss_scale=64.0)
+        wl, ws, wg, slope, inside = ref.preference(z.double(), ids, starts, 1.0, refs.double(), kind,
+                                                   beta, float(torch.tensor(smoothing)), mean,
+                                                   weight.double(), 64.0)
+        lp = ref.logprob(z.double(), ids, 1.0)[0]
+        delta, dlogp = errors(z, 1.0, lp)
+        count = torch.ones(2 * pairs, dtype=F64)
+        dl = torch.zeros(2 * pairs, dtype=F64)
+        drow = torch.zeros(rows, dtype=F64)
+        for s in range(2 * pairs):
+            live = (ids[starts[s]:starts[s + 1]] >= 0) & (ids[starts[s]:starts[s + 1]] < vocab)
+            count[s] = max(1, int(live.sum())) if mean else 1
+            dl[s] = dlogp[starts[s]:starts[s + 1]].sum() / count[s]
+        check(seq, ws, dl + 2.0 ** -24 * ws.abs() + 1e-45, "seq_logp")
+        dd = dl[0::2] + dl[1::2]
+        bend = 2.0 if kind == "square" else beta * beta
+        steep = torch.stack([torch.as_tensor(ref.pair_loss(float(x), kind, beta, smoothing)[1])
+                             for x in (ws - refs.double())[0::2] - (ws - refs.double())[1::2]]).double()
+        check(loss, wl, weight.double() * (steep.abs() * dd + bend * dd * dd) + 2.0 ** -22 * wl + 1e-45,
+              "loss")
+        for s in range(2 * pairs):
+            drow[starts[s]:starts[s + 1]] = 64 * weight[s // 2] * bend * dd[s // 2] / count[s]
+        drow = drow + 2.0 ** -22 * slope
+        check_grad(grad[inside.cuda()], wg[inside], z[inside], ids[inside], 1.0, delta[inside],
+                   drow[inside], dtype, "grad")
+        assert bool((grad[~inside.cuda()] == 7.0).all()) and whole()
+        inplace = z.cuda()
+        l2, s2 = run_preference(zs, inplace, ids, starts, inplace, refs, weight, beta=beta,
+                                kind=kind_of(zs, kind), smoothing=smoothing, mean=mean,
+                                loss_scale=64.0)
+        assert torch.equal(l2, loss) and torch.equal(s2, seq)
+        assert torch.equal(inplace[inside.cuda()], grad[inside.cuda()])
+        assert torch.equal(inplace[~inside.cuda()].cpu(), z[~inside])
+        l3, s3 = run_preference(zs, z.cuda(), ids, starts, None, refs, weight, beta=beta,
+                                kind=kind_of(zs, kind), smoothing=smoothing, mean=mean)
+        assert torch.equal(l3, loss) and torch.equal(s3, seq)
+
+
+def test_preference_masks_weights_and_nan(zs):
+    """A pair without weight, sequences without a token, a NaN in one pair: the others stay."""
+    z, ids, _ = problem(40, 600, BF16)
+    ids = (torch.arange(40, dtype=torch.int32) * 13) % 600
+    starts = [0, 5, 10, 15, 20, 25, 30, 35, 40]
+    ids[10:15] = -1                          # pair 1 prefers an answer without tokens
+    clean = torch.empty_like(z).cuda()
+    w = torch.tensor([1.0, 1.0, 0.0, 2.0])
+    l0, s0 = run_preference(zs, z.cuda(), ids, starts, clean, None, w, beta=0.1)
+    bad = z.clone()
+    bad[21, 5] = math.nan                    # pair 2 has no weight
+    bad[12] = math.nan                       # not a token's row
+    g1 = torch.empty_like(z).cuda()
+    l1, s1 = run_preference(zs, bad.cuda(), ids, starts, g1, None, w, beta=0.1)
+    assert torch.equal(l1, l0) and torch.equal(g1, clean)
+    assert not g1[10:15].any() and not g1[20:30].any() and l1[2] == 0
+    assert float(s1[2]) == 0 and torch.isnan(s1[4])
+    bad[36, 7] = math.nan
+    for kind in ("sigmoid", "hinge", "square"):
+        l2, _ = run_preference(zs, bad.cuda(), ids, starts, g1, None, w, beta=0.1,
+                               kind=kind_of(zs, kind))
+        assert torch.isnan(l2[3]) and torch.isfinite(l2[:3]).all()
+        assert torch.isnan(g1[30:].float()).any(1).all() and torch.isfinite(g1[:30].float()).all()
+
+
+def test_preference_starts_out_of_range_stay_inside(zs):
+    """Starts below 0 and past the rows are taken as the ends; nothing else is written."""
+    z, ids, _ = problem(20, 300, FP16)
+    ids = ids.clamp(0, 299)
+    grad, whole = guarded_like(z)
+    loss, seq = run_preference(zs, z.cuda(), ids, [-5, 8, 1 << 30], grad, beta=0.1)
+    l2, s2 = run_preference(zs, z.cuda(), ids, [0, 8, 20], torch.empty_like(z).cuda(), beta=0.1)
+    assert torch.equal(loss, l2) and torch.equal(seq, s2) and whole()
+
+
+def test_preference_without_rows(zs):
+    z = torch.empty(0, 50, device="cuda")
+    loss, seq = run_preference(zs, z, torch.empty(0, dtype=torch.int32), [0, 0, 0], z, beta=0.1)
+    assert abs(float(loss) - math.log(2)) < 1e-6 and not seq.any()
+
+
+def test_token_losses_captured_and_replayed(zs):
+    """Replays with new logits in the same buffers, eager work between them."""
+    for rows, vocab in ((40, 3000), (1100, 700)):
+        z, ids, g = problem(rows, vocab, BF16)
+        adv, o, r, w = (cu(t) for t in policy_inputs(z, ids, g, 1.0, True, True, True))
+        dz, di = z.cuda(), ids.cuda()
+        starts = torch.tensor([0, rows // 4, rows // 2, rows], dtype=torch.int32).cuda()
+        starts = torch.cat([starts, starts[-1:]])       # an empty last sequence
+        ws = torch.empty(zs.zs_policy_workspace(rows, vocab, zs.ZS_BF16), dtype=torch.uint8,
+                         device="cuda")
+        outs = [torch.empty_like(dz), torch.empty_like(dz), torch.empty(rows, device="cuda"),
+                torch.empty(rows, device="cuda"), torch.empty(2, device="cuda")]
+
+        def both(outs):
+            zs.zs_policy(dz, di, adv, outs[2], old_logp=o, ref_logp=r, kl_weight=0.1, row_weight=w,
+                         logp=outs[3], grad=outs[0], workspace=ws)
+            zs.zs_preference(dz, di, starts, 0.1, outs[4], grad=outs[1], workspace=ws)
+
+        both(outs)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            both(outs)
+        for i in range(3):
+            dz.copy_(torch.randn(rows, vocab, generator=g).to(BF16))
+            graph.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in outs]
+            both(outs)
+            torch.cuda.synchronize()
+            for a, b in zip(got, outs):
+                assert torch.equal(a, b)
