@@ -721,6 +721,47 @@ int zs_block_norm_backward(const void *dy, const void *h, const float *rstd, con
                            float *dgain, float *dpost_gain, float *dgate, void *workspace,
                            uint64_t workspace_bytes, void *stream);
 
+/* C = R16(residual + act(A B^T + bias)): zs_mx_matmul with an epilogue, its
+ * sums in fp32 up to the one rounding. A, B, m, n, k, ldc and the workspace
+ * (zs_mx_matmul_workspace(m, n, k) bytes) as there.
+ *   bias    : c_dtype[n], or NULL.
+ *   activation: ZS_ACT_NONE; ZS_ACT_RELU: max(x, 0); ZS_ACT_GELU: 0.5 x (1 +
+ *             tanh(sqrt(2 / pi) (x + 0.044715 x^3))); ZS_ACT_SILU: x / (1 +
+ *             exp(-x)).
+ *   residual: c_dtype[m][n], rows `ldr` apart, or NULL.
+ *   pre     : NULL, or c_dtype[m][n], contiguous: R16(A B^T + bias), which
+ *             zs_activation_backward reads. The activation itself sees the sum
+ *             before it is rounded.
+ *   c       : c_dtype (bf16, fp16)[m][n], rows `ldc` apart; may be the
+ *             residual's own buffer.
+ * k == 0 gives residual + act(bias). Errors: as zs_mx_matmul, and
+ * ZS_ERR_INVALID_ARG (activation, ldr < n). */
+typedef enum { ZS_ACT_NONE = 0, ZS_ACT_RELU = 1, ZS_ACT_GELU = 2, ZS_ACT_SILU = 3 } zs_activation;
+int zs_mx_linear(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
+                 const uint8_t *b_codes, const uint8_t *b_scales, uint64_t m, uint64_t n,
+                 uint64_t k, const void *bias, int activation, const void *residual, uint64_t ldr,
+                 void *pre, void *c, int c_dtype, uint64_t ldc, void *workspace,
+                 uint64_t workspace_bytes, void *stream);
+
+/* Gradient of zs_mx_linear's epilogue: dpre = R16(dc * act'(pre)), and
+ * dbias = sum over rows of dc * act'(pre), unrounded (the residual's gradient
+ * is dc; the products' come from dpre by zs_mx_quantize and zs_mx_matmul).
+ *   dc   : dtype (bf16, fp16)[rows][cols], contiguous.
+ *   pre  : dtype[rows][cols], as zs_mx_linear stored it; NULL with
+ *          ZS_ACT_NONE.
+ *   dpre : dtype[rows][cols], may be dc's or pre's own buffer, or NULL.
+ *   dbias: fp32[cols], or NULL; one of the two must be given. Zeros when
+ *          rows == 0.
+ *   workspace: zs_activation_backward_workspace(rows, cols) bytes, 4-byte
+ *          aligned; not needed without dbias.
+ * act' of the ReLU at 0 is 0. Errors: ZS_ERR_INVALID_ARG (null pointers, dtype,
+ * activation, no output, workspace too small), ZS_ERR_UNSUPPORTED (2^31
+ * columns or more, alignment). */
+uint64_t zs_activation_backward_workspace(uint64_t rows, uint64_t cols);
+int zs_activation_backward(const void *dc, const void *pre, int activation, int dtype,
+                           uint64_t rows, uint64_t cols, void *dpre, float *dbias,
+                           void *workspace, uint64_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------------
  * Losses on the log-probabilities of given tokens: what a student is trained
  * on after distillation, at the place of zs_distill and by its conventions.

@@ -2,7 +2,7 @@
 
   libzeroshard.so        the shard-step library (HIP, gfx950)  <- csrc/zeroshard.hip
                          + the operators of the model's output end <- csrc/zs_ops.hip
-                         + of its last block <- csrc/zs_block.hip
+                         + of its last block <- csrc/zs_block.hip, csrc/zs_linear.hip
                          + of its preference and policy losses <- csrc/zs_tokens.hip
                          + its host-side offload update (gcc) <- csrc/offload_cpu.cpp
   synth/libzssynth_dev.so   device twin of the input generator (HIP, gfx950)
@@ -111,7 +111,8 @@ def _hip_lib(src, out, verbose, extra=()):
 
 
 # The operators' sources, each an object of its own.
-OPERATOR_SOURCES = ["zs_ops.hip", "zs_block.hip", "zs_tokens.hip"]
+OPERATOR_SOURCES = ["zs_ops.hip", "zs_block.hip", "zs_linear.hip",
+                    "zs_tokens.hip"]
 
 # Host half of the library (the ZeRO-Offload update): gcc, no contraction so
 # vector mul/add stay separate IEEE operations; F16C for the fp16 convert.

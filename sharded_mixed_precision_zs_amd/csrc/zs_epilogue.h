@@ -1,0 +1,169 @@
+/*
+ * zs_epilogue.h -- what a product does with its fp32 sums before they are
+ * stored, and activations (gfx950):
+ *   pre = sum + bias;  c = R16(residual + act(pre))
+ * pre is rounded only where it is stored; the activation sees its fp32.
+ *
+ * gelu, the form with the hyperbolic tangent, 0.5 x (1 + tanh u), and silu are
+ * both x times the logistic function of w: 2 u = 2 sqrt(2 / pi) (x + 0.044715
+ * x^3), and x. So neither 1 + tanh nor a sum near it loses the small values.
+ */
+#ifndef ZS_EPILOGUE_H
+#define ZS_EPILOGUE_H
+
+#include "zs_mx.h"
+
+namespace zs {
+
+constexpr float kGeluCube = 0.044715f;
+constexpr float kGeluLog2 = 2.30220819f;   /* 2 sqrt(2 / pi) log2(e) */
+constexpr float kGelu = 1.59576912f;       /* 2 sqrt(2 / pi) */
+constexpr float kLog2e = 1.44269504f;
+
+/* The instruction's reciprocal is off by a unit in the last place, of 24 bits
+ * where the result has 8 or 11. */
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if constexpr (ACT == ZS_ACT_RELU) return x > 0.0f ? x : x == x ? 0.0f : x;
+  if constexpr (ACT == ZS_ACT_GELU || ACT == ZS_ACT_SILU) {
+    const float w = ACT == ZS_ACT_GELU ? kGeluLog2 * x * fmaf(kGeluCube * x, x, 1.0f) : kLog2e * x;
+    return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-w));
+  }
+  return x;
+}
+
+/* d act / d x. With p the logistic function of w and q = 1 - p, formed without
+ * the difference: p (1 + x q w'). Beyond 30 the slope is 0 or 1 in any type
+ * here, and w' of such x would leave fp32. */
+template <int ACT>
+__device__ __forceinline__ float slope_of(float x) {
+  if constexpr (ACT == ZS_ACT_RELU) return x > 0.0f ? 1.0f : x == x ? 0.0f : x;
+  if constexpr (ACT == ZS_ACT_GELU || ACT == ZS_ACT_SILU) {
+    constexpr float top = ACT == ZS_ACT_GELU ? 30.0f : 110.0f;
+    const float c = __builtin_amdgcn_fmed3f(x, -top, top);
+    float w = kLog2e * c, dw = 1.0f;
+    if constexpr (ACT == ZS_ACT_GELU) {
+      const float s = c * c;
+      w = kGeluLog2 * c * fmaf(kGeluCube, s, 1.0f);
+      dw = kGelu * fmaf(3.0f * kGeluCube, s, 1.0f);
+    }
+    const float t = __builtin_amdgcn_exp2f(-fabsf(w));
+    const float big = __builtin_amdgcn_rcpf(1.0f + t), small = t * big;
+    const float p = w >= 0.0f ? big : small, q = w >= 0.0f ? small : big;
+    return x == x ? p * fmaf(c * q, dw, 1.0f) : x;
+  }
+  return 1.0f;
+}
+
+struct NoEpilogue {
+  static constexpr bool kOn = false;
+};
+
+/* The activation is one of a launch's few: told apart at run time, once for
+ * the values of a thread. */
+struct Epilogue {
+  static constexpr bool kOn = true;
+  const void *bias, *res;   /* optional */
+  uint16_t *pre;            /* optional, [m][n] */
+  uint64_t ldr;
+  int act;
+
+  template <int N>
+  __device__ __forceinline__ void apply(float (&x)[N]) const {
+    if (act == ZS_ACT_GELU) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = activate<ZS_ACT_GELU>(x[j]);
+    } else if (act == ZS_ACT_SILU) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = activate<ZS_ACT_SILU>(x[j]);
+    } else if (act == ZS_ACT_RELU) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = activate<ZS_ACT_RELU>(x[j]);
+    }
+  }
+
+  /* Eight neighbouring sums of a row, their bias given, to memory. */
+  template <int CDT>
+  __device__ __forceinline__ void store(uint64_t row, uint32_t col, uint32_t n, float (&x)[8],
+                                        const float (&b)[8], uint16_t *c, uint64_t ldc) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] += b[j];
+    if (pre) store8<CDT, false>(pre + row * n, col, n, x);
+    apply(x);
+    if (res) {
+      float r[8];
+      load8<CDT, false>(static_cast<const uint16_t *>(res) + row * ldr, col, n, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] += r[j];
+    }
+    store8<CDT, false>(c + row * ldc, col, n, x);
+  }
+
+  /* One sum. */
+  template <int CDT>
+  __device__ __forceinline__ void store1(uint64_t row, uint32_t col, uint32_t n, float x,
+                                         uint16_t *c, uint64_t ldc) const {
+    if (col >= n) return;
+    float v[1] = {x};
+    if (bias) v[0] += up_lo<CDT>(static_cast<const uint16_t *>(bias)[col]);
+    if (pre) pre[row * n + col] = pack1<CDT>(v[0]);
+    apply(v);
+    if (res) v[0] += up_lo<CDT>(static_cast<const uint16_t *>(res)[row * ldr + col]);
+    c[row * ldc + col] = pack1<CDT>(v[0]);
+  }
+};
+
+/* ------------------------------------------------------------------------
+ * The gradient of bias and activation: dpre = dc act'(pre), and dpre's sum
+ * over the rows. A block is kAcross vectors of eight columns by kDown rows at
+ * a time, and walks a share of the rows; a thread keeps its columns' sums,
+ * unrounded, in registers, and the shares are joined in order. Bound by HBM.
+ * ---------------------------------------------------------------------- */
+struct ActGradArgs {
+  const void *dc, *pre;   /* pre optional: no activation */
+  uint16_t *dpre;         /* optional */
+  float *part;            /* [parts][cols], optional */
+  uint64_t rows;
+  uint32_t cols, parts;
+};
+
+template <int DT, bool AL, int ACT, int ACROSS>
+__global__ __launch_bounds__(kBlock) void act_grad_kernel(ActGradArgs a) {
+  constexpr uint32_t kDown = kBlock / ACROSS;
+  const uint32_t v = blockIdx.x * ACROSS + threadIdx.x % ACROSS;
+  const uint32_t p = blockIdx.y * kDown + threadIdx.x / ACROSS;
+  const uint64_t col = (uint64_t)v * 8;
+  if (p >= a.parts || col >= a.cols) return;
+  const uint16_t *dc = static_cast<const uint16_t *>(a.dc);
+  const uint16_t *pre = static_cast<const uint16_t *>(a.pre);
+  float sum[8] = {};
+  Raw16<8> d = load8_raw<AL, true>(dc + (uint64_t)p * a.cols, col, a.cols), s = {};
+  if constexpr (ACT != ZS_ACT_NONE) s = load8_raw<AL, true>(pre + (uint64_t)p * a.cols, col, a.cols);
+  for (uint64_t row = p; row < a.rows; row += a.parts) {
+    const uint64_t next = row + a.parts;
+    Raw16<8> d1 = {}, s1 = {};
+    if (next < a.rows) {
+      d1 = load8_raw<AL, true>(dc + next * a.cols, col, a.cols);
+      if constexpr (ACT != ZS_ACT_NONE) s1 = load8_raw<AL, true>(pre + next * a.cols, col, a.cols);
+    }
+    float x[8], y[8];
+    upcast<8, DT>(d, x);
+    if constexpr (ACT != ZS_ACT_NONE) {
+      upcast<8, DT>(s, y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= slope_of<ACT>(y[j]);
+    }
+    if (a.dpre) store8<DT, AL>(a.dpre + row * a.cols, col, a.cols, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += x[j];
+    d = d1;
+    s = s1;
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (col + j < a.cols) a.part[(uint64_t)p * a.cols + col + j] = sum[j];
+}
+
+}  // namespace zs
+#endif  // ZS_EPILOGUE_H

@@ -24,7 +24,7 @@
 #ifndef ZS_MATMUL_KERNELS_H
 #define ZS_MATMUL_KERNELS_H
 
-#include "zs_mx.h"
+#include "zs_epilogue.h"
 
 namespace zs {
 
@@ -253,8 +253,8 @@ struct Const {
   static constexpr int value = V;
 };
 
-template <int AF, int CDT, int BM, int BN, int NW>
-__global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs p) {
+template <int AF, int CDT, int BM, int BN, int NW, class E>
+__global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs p, E epilogue) {
   constexpr int kAcross = NW / 2, kThreads = 64 * NW;   /* two rows of NW / 2 waves */
   constexpr int FM = BM / 64, FN = BN / (32 * kAcross); /* 32 x 32 fragments per wave */
   constexpr int LA = BM / (8 * NW), LB = BN / (8 * NW); /* loads of 8 rows per wave */
@@ -453,8 +453,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs
   loads_barrier();   /* the strips below take the place of what was loaded last */
 
   /* Each wave turns strips of 32 rows round in its own part of LDS, so that
-   * rows of C go out in runs: 16-byte pieces, swizzled as above. */
-  constexpr uint32_t kEsz = CDT == ZS_FP32 ? 4 : 2, kRow = FN * 32 * kEsz, kPieces = kRow / 16;
+   * rows of C go out in runs: 16-byte pieces, swizzled as above. With an
+   * epilogue the strips are fp32, and a lane finishes eight results. */
+  constexpr int SDT = E::kOn ? ZS_FP32 : CDT;   /* the strips' type */
+  constexpr uint32_t kEsz = SDT == ZS_FP32 ? 4 : 2, kRow = FN * 32 * kEsz, kPieces = kRow / 16;
   static_assert(32 * kRow * kAcross <= sizeof(sa0) && 32 * kRow * kAcross <= sizeof(sb0),
                 "strips fit");
   uint8_t *strip = (wave / kAcross ? sb0 : sa0) + wave % kAcross * 32 * kRow;
@@ -474,10 +476,34 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs
         const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                             acc[i][j][4 * q + 3]};
         const uint32_t byte = (j * 32 + q * 8 + g * 4) * kEsz;
-        put_c4<CDT>(strip + r * kRow + (((byte / 16) ^ (r % kPieces)) * 16) + byte % 16, v);
+        put_c4<SDT>(strip + r * kRow + (((byte / 16) ^ (r % kPieces)) * 16) + byte % 16, v);
       }
     __builtin_amdgcn_wave_barrier();
     const uint32_t col0 = n0 + tn;
+    if constexpr (E::kOn) {
+      constexpr uint32_t kAhead = FN * 4, kRows = 64 / kAhead;   /* lanes to a row, rows at once */
+      const uint32_t pc = lane % kAhead, col = col0 + pc * 8;
+      float bias[8] = {};
+      if (epilogue.bias) load8<CDT, false>(epilogue.bias, col, p.n, bias);
+#pragma unroll
+      for (uint32_t k = 0; k < 32 / kRows; ++k) {
+        const uint32_t lr = k * kRows + lane / kAhead, row = m0 + tm + i * 32 + lr;
+        float v[8];
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+          const float4 w = *reinterpret_cast<const float4 *>(
+              strip + lr * kRow + (((2 * pc + h) ^ (lr % kPieces)) * 16));
+          v[4 * h] = w.x;
+          v[4 * h + 1] = w.y;
+          v[4 * h + 2] = w.z;
+          v[4 * h + 3] = w.w;
+        }
+        if (row < p.m)
+          epilogue.template store<CDT>(row, col, p.n, v, bias, static_cast<uint16_t *>(p.c), p.ldc);
+      }
+      __builtin_amdgcn_wave_barrier();
+      continue;
+    }
     constexpr uint32_t kRowsAtOnce = 64 / kPieces > 0 ? 64 / kPieces : 1;
 #pragma unroll
     for (uint32_t k = 0; k < 32 / kRowsAtOnce; ++k) {
@@ -506,14 +532,17 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs
 /* The splits' sums, added in order and rounded once: a thread per result, its
  * sums still in the caches (768 x 768 x 8192 of 8 x 4 bits in six pieces: 24
  * us both launches, one piece 53). */
-template <int CDT>
-__global__ __launch_bounds__(kBlock) void matmul_join_kernel(MatmulArgs p, uint32_t splits) {
+template <int CDT, class E>
+__global__ __launch_bounds__(kBlock) void matmul_join_kernel(MatmulArgs p, uint32_t splits,
+                                                             E epilogue) {
   const uint64_t id = (uint64_t)blockIdx.x * kBlock + threadIdx.x, all = (uint64_t)p.m * p.n;
   if (id >= all) return;
   float s = 0.0f;
   for (uint32_t k = 0; k < splits; ++k) s += p.part[k * all + id];
   const uint32_t row = (uint32_t)(id / p.n), col = (uint32_t)(id % p.n);
-  if constexpr (CDT == ZS_FP32) static_cast<float *>(p.c)[row * p.ldc + col] = s;
+  if constexpr (E::kOn)
+    epilogue.template store1<CDT>(row, col, p.n, s, static_cast<uint16_t *>(p.c), p.ldc);
+  else if constexpr (CDT == ZS_FP32) static_cast<float *>(p.c)[row * p.ldc + col] = s;
   else static_cast<uint16_t *>(p.c)[row * p.ldc + col] = pack1<CDT>(s);
 }
 
@@ -533,8 +562,9 @@ __global__ __launch_bounds__(kBlock) void matmul_join_kernel(MatmulArgs p, uint3
 constexpr int kThinWaves = 8;
 constexpr uint32_t kThinPart = 32 * 128;   /* a piece: 32 rows of 128 bytes */
 
-template <int AF, int CDT, bool PAIR>
-__global__ __launch_bounds__(64 * kThinWaves, 4) void matmul_thin_kernel(MatmulArgs p, int vec) {
+template <int AF, int CDT, bool PAIR, class E>
+__global__ __launch_bounds__(64 * kThinWaves, 4) void matmul_thin_kernel(MatmulArgs p, int vec,
+                                                                         E epilogue) {
   /* staging, then the waves' sums in its place */
   constexpr uint32_t kSums = kThinWaves * 16 * 64 * 4, kStage = kThinWaves * kThinPart;
   __shared__ __align__(16) uint8_t stage0[kStage], stage1[kStage];
@@ -647,7 +677,15 @@ __global__ __launch_bounds__(64 * kThinWaves, 4) void matmul_thin_kernel(MatmulA
       v[e] += sums[(w * 16 + q * 4 + e) * 64 + l];
       if constexpr (PAIR) v[e] += sums[(w * 16 + q * 4 + e) * 64 + l + 16];   /* l & 31 < 16 */
     }
-  store_c4<CDT>(p.c, (uint64_t)(l & 31) * p.ldc, n0 + q * 8 + (l >> 5) * 4, p.n, v, vec);
+  const uint32_t col = n0 + q * 8 + (l >> 5) * 4;
+  if constexpr (E::kOn) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      epilogue.template store1<CDT>(l & 31, col + e, p.n, v[e], static_cast<uint16_t *>(p.c),
+                                    p.ldc);
+  } else {
+    store_c4<CDT>(p.c, (uint64_t)(l & 31) * p.ldc, col, p.n, v, vec);
+  }
 }
 
 }  // namespace zs

@@ -23,12 +23,12 @@ using namespace zs;
  * ---------------------------------------------------------------------- */
 inline int too_large() { return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: too large for one launch%s"); }
 
-template <int AF, int CDT, int BM, int BN, int NW>
-int launch_tile(const MatmulArgs &a, uint32_t splits, hipStream_t s) {
+template <int AF, int CDT, int BM, int BN, int NW, class E>
+int launch_tile(const MatmulArgs &a, uint32_t splits, const E &e, hipStream_t s) {
   const uint64_t tiles = (uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN);
   if (!fits(tiles, 64 * NW)) return too_large();
-  hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN, NW>), dim3((unsigned)tiles, splits),
-                     dim3(64 * NW), 0, s, a);
+  hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN, NW, E>), dim3((unsigned)tiles, splits),
+                     dim3(64 * NW), 0, s, a, e);
   return launch_result();
 }
 
@@ -61,8 +61,14 @@ inline MatmulSplit matmul_split(uint64_t m, uint64_t n, uint64_t padded, uint64_
   return {(uint32_t)((groups + four - 1) / four), (uint32_t)four};
 }
 
-template <int AF, int CDT>
-int launch_matmul(MatmulArgs a, float *workspace, uint64_t workspace_bytes, hipStream_t s) {
+/* What a split product's first launch has for an epilogue: none, by a name of
+ * its own in each of the sources that launch one. */
+template <class E>
+struct SplitEpilogue : NoEpilogue {};
+
+template <int AF, int CDT, class E>
+int launch_matmul(MatmulArgs a, const E &e, float *workspace, uint64_t workspace_bytes,
+                  hipStream_t s) {
   constexpr uint64_t esz = CDT == ZS_FP32 ? 4 : 2;
   a.split_groups = a.padded / ZS_MX_GROUP;
   if (matmul_thin(a.m, a.n, AF == ZS_MX_E4M3)) {
@@ -73,26 +79,26 @@ int launch_matmul(MatmulArgs a, float *workspace, uint64_t workspace_bytes, hipS
     /* both halves of an 8-bit A in one instruction: 1 x 32000 x 4096 15.6 us,
      * in two 18.9; 4 rows 18.0 and 19.3; 16 rows 26.6 and 22.5 */
     if (AF == ZS_MX_E4M3 && a.m <= 4)
-      hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, AF == ZS_MX_E4M3>), dim3(blocks),
-                         dim3(64 * kThinWaves), 0, s, a, vec);
+      hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, AF == ZS_MX_E4M3, E>), dim3(blocks),
+                         dim3(64 * kThinWaves), 0, s, a, vec, e);
     else
-      hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, false>), dim3(blocks), dim3(64 * kThinWaves),
-                         0, s, a, vec);
+      hipLaunchKernelGGL((matmul_thin_kernel<AF, CDT, false, E>), dim3(blocks), dim3(64 * kThinWaves),
+                         0, s, a, vec, e);
     return launch_result();
   }
   constexpr int BM = AF == ZS_MX_E2M1 ? 256 : 128, BN = 256;
   if ((uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN) >= kFullChip)
-    return launch_tile<AF, CDT, BM, BN, AF == ZS_MX_E2M1 ? 8 : 4>(a, 1, s);
+    return launch_tile<AF, CDT, BM, BN, AF == ZS_MX_E2M1 ? 8 : 4>(a, 1, e, s);
 
   const MatmulSplit sp = matmul_split(a.m, a.n, a.padded, workspace_bytes);
-  if (sp.splits < 2) return launch_tile<AF, CDT, 128, 128, 4>(a, 1, s);
+  if (sp.splits < 2) return launch_tile<AF, CDT, 128, 128, 4>(a, 1, e, s);
 
   a.part = workspace;
   a.split_groups = sp.groups;
-  if (int rc = launch_tile<AF, ZS_FP32, 128, 128, 4>(a, sp.splits, s)) return rc;
+  if (int rc = launch_tile<AF, ZS_FP32, 128, 128, 4>(a, sp.splits, SplitEpilogue<E>{}, s)) return rc;
   const uint64_t all = (uint64_t)a.m * a.n;
-  hipLaunchKernelGGL((matmul_join_kernel<CDT>), dim3((unsigned)((all + kBlock - 1) / kBlock)),
-                     dim3(kBlock), 0, s, a, sp.splits);
+  hipLaunchKernelGGL((matmul_join_kernel<CDT, E>), dim3((unsigned)((all + kBlock - 1) / kBlock)),
+                     dim3(kBlock), 0, s, a, sp.splits, e);
   return launch_result();
 }
 

@@ -260,7 +260,7 @@ int zs_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
   with_format(a_format, [&](auto f) {
     with_any(c_dtype, [&](auto dt) {
       rc = launch_matmul<decltype(f)::value, decltype(dt)::value>(
-          a, static_cast<float *>(workspace), workspace ? workspace_bytes : 0, s);
+          a, NoEpilogue{}, static_cast<float *>(workspace), workspace ? workspace_bytes : 0, s);
     });
   });
   return rc;

@@ -24,6 +24,7 @@ ZS_STATE_GROUP = 1024
 ZS_MX_E2M1, ZS_MX_E4M3 = 0, 1
 ZS_MX_BLOCK, ZS_MX_GROUP = 32, 128
 ZS_DISTILL_MAX_SLOTS = 1024
+ZS_ACT_NONE, ZS_ACT_RELU, ZS_ACT_GELU, ZS_ACT_SILU = 0, 1, 2, 3
 ZS_PREFERENCE_SIGMOID, ZS_PREFERENCE_HINGE, ZS_PREFERENCE_SQUARE = 0, 1, 2
 ZS_OK, ZS_ERR_INVALID_ARG, ZS_ERR_UNSUPPORTED, ZS_ERR_ALIAS, ZS_ERR_HIP = range(5)
 
@@ -128,6 +129,10 @@ def _load():
         "zs_block_norm_backward_workspace": ([u64, u64], u64),
         "zs_block_norm_backward": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, u64, u64, f32, f32,
                                     rule, vp, vp, vp, vp, vp, vp, u64, vp], i32),
+        "zs_mx_linear": ([vp, vp, i32, vp, vp, u64, u64, u64, vp, i32, vp, u64, vp, vp, i32, u64, vp,
+                          u64, vp], i32),
+        "zs_activation_backward_workspace": ([u64, u64], u64),
+        "zs_activation_backward": ([vp, vp, i32, i32, u64, u64, vp, vp, vp, u64, vp], i32),
         "zs_logprob_workspace": ([u64, u64, i32], u64),
         "zs_logprob": ([vp, i32, u64, u64, u64, vp, f32, vp, vp, u64, vp], i32),
         "zs_policy_workspace": ([u64, u64, i32], u64),
@@ -766,6 +771,45 @@ def zs_block_norm_backward(dy, h, rstd, gain, dx, dresidual, dgain, workspace, x
         _dense(dx, shape, dt, "dx"), _dense(dresidual, shape, dt, "dresidual"),
         _dense(dgain, shape[1:], f32, "dgain"), _dense(dpost_gain, shape[1:], f32, "dpost_gain"),
         _dense(dgate, shape[1:], f32, "dgate"), wp, wb, _raw_stream(stream)))
+
+
+def zs_mx_linear(a_codes, a_scales, a_format, b_codes, b_scales, out, k, bias=None,
+                 activation=ZS_ACT_NONE, residual=None, pre=None, workspace=None, stream=None):
+    """out[m][n] = residual + act(A B^T + bias): A m microscaled rows of k elements in a_format,
+    B n in ZS_MX_E2M1. pre: what the activation is applied to, 16 bits. out may be residual."""
+    p, m, n, ld = _rows(out, "out")
+    dt = out.dtype
+    ac, asc = _mx_ptrs(a_codes, a_scales, m, k, a_format, "A")
+    bc, bsc = _mx_ptrs(b_codes, b_scales, n, k, ZS_MX_E2M1, "B")
+    rp, rld = None, 0
+    if residual is not None:
+        if residual.dtype != dt:
+            raise ValueError("residual: out's dtype expected")
+        rp, _, _, rld = _rows(residual, "residual", (m, n))
+    wp, wb = _workspace(workspace)
+    _check("zs_mx_linear", _lib.zs_mx_linear(
+        ac, asc, a_format, bc, bsc, m, n, k, _dense(bias, (n,), dt, "bias"), activation, rp, rld,
+        _dense(pre, (m, n), dt, "pre"), p, _float_code(out, "out"), ld, wp, wb,
+        _raw_stream(stream)))
+
+
+def zs_activation_backward_workspace(rows, cols):
+    """Bytes of workspace that zs_activation_backward needs for dbias."""
+    return _lib.zs_activation_backward_workspace(rows, cols)
+
+
+def zs_activation_backward(dout, pre, activation, dpre=None, dbias=None, workspace=None,
+                           stream=None):
+    """dpre = dout * act'(pre) and its sum over the rows, the fp32 dbias; pre: zs_mx_linear's
+    (None without an activation). dpre may be dout or pre."""
+    if dout.dim() != 2:
+        raise ValueError("dout: 2-D tensor expected")
+    shape, dt = dout.shape, dout.dtype
+    wp, wb = _workspace(workspace)
+    _check("zs_activation_backward", _lib.zs_activation_backward(
+        _dense(dout, shape, dt, "dout"), _dense(pre, shape, dt, "pre"), activation,
+        _float_code(dout, "dout"), *shape, _dense(dpre, shape, dt, "dpre"),
+        _dense(dbias, shape[1:], _t().f32, "dbias"), wp, wb, _raw_stream(stream)))
 
 
 # ---- losses on the log-probabilities of given tokens ---------------------------
