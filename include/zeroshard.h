@@ -827,7 +827,9 @@ int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint
  * Sums are binary64, in a fixed order.
  *   starts : int32[2 * pairs + 1] on the device, ascending; values are taken
  *            to lie in [0, rows]. Rows before the first and from the last on
- *            are not read, and their gradient's rows are left as they were.
+ *            are not read.
+ *   clear  : 0: the gradient's rows outside all sequences are left as they
+ *            were; otherwise they are filled with zeros.
  *   ref_logp: NULL (zeros), or fp32[2 * pairs], the reference model's L.
  *   pair_weight: NULL (all 1), or fp32[pairs]; with weight 0 loss and gradient
  *            are zero, whatever the logits.
@@ -846,8 +848,8 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
                   const int32_t *ids, const int32_t *starts, uint64_t pairs, float temperature,
                   const float *ref_logp, int kind, float beta, float smoothing, int mean,
                   const float *pair_weight, float loss_scale, const zs_device_scaler *dev,
-                  float *seq_logp, float *loss, void *grad, uint64_t grad_ld, void *workspace,
-                  uint64_t workspace_bytes, void *stream);
+                  float *seq_logp, float *loss, void *grad, uint64_t grad_ld, int clear,
+                  void *workspace, uint64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

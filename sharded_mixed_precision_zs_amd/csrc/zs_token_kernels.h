@@ -49,7 +49,7 @@ struct TokenArgs {
   float *seq_logp;                 /* optional */
   float beta, smoothing;
   uint32_t pairs;
-  int kind, mean;
+  int kind, mean, clear;           /* clear: zeros in gradient rows outside all sequences */
 
   void *grad;                      /* optional */
   TokenPart *ws;                   /* [rows][parts] */
@@ -364,8 +364,9 @@ __global__ __launch_bounds__(NT) void token_grad_kernel(TokenArgs a) {
   constexpr int U = kTokenAhead;
   const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x;
   const TokenSpan span = token_span(a);
-  if (row < span.first || row >= span.last) return;
-  const TokenPlan p = a.plan[row];
+  const bool inside = row >= span.first && row < span.last;
+  if (!inside && !a.clear) return;
+  const TokenPlan p = inside ? a.plan[row] : TokenPlan{0.0f, 0.0f, 0.0f, -1};
   const char *z = static_cast<const char *>(a.z) + (uint64_t)row * a.ld * esz;
   char *g = static_cast<char *>(a.grad) + (uint64_t)row * a.gld * esz;
   const RowShape sh = row_shape<DT>(z, a.vocab);

@@ -237,7 +237,7 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
                   const int32_t *ids, const int32_t *starts, uint64_t pairs, float temperature,
                   const float *ref_logp, int kind, float beta, float smoothing, int mean,
                   const float *pair_weight, float loss_scale, const zs_device_scaler *dev,
-                  float *seq_logp, float *loss, void *grad, uint64_t grad_ld, void *workspace,
+                  float *seq_logp, float *loss, void *grad, uint64_t grad_ld, int clear, void *workspace,
                   uint64_t workspace_bytes, void *stream) {
   ZS_TOKEN_CHECKS("zs_preference");
   if (kind != ZS_PREFERENCE_SIGMOID && kind != ZS_PREFERENCE_HINGE && kind != ZS_PREFERENCE_SQUARE)
@@ -251,8 +251,8 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
   if (!dev && (!(loss_scale > 0.0f) || !isfinite(loss_scale)))
     return fail(ZS_ERR_INVALID_ARG, "zs_preference: loss_scale must be finite and > 0%s");
   if (pairs >> 24) return fail(ZS_ERR_UNSUPPORTED, "zs_preference: 2^24 pairs or more%s");
-  if (pairs == 0) return ZS_OK;
-  if (!starts || !loss || (rows && (!logits || !ids)))
+  if (pairs == 0 && !(clear && grad && rows)) return ZS_OK;
+  if (!starts || (pairs && !loss) || (rows && (!logits || !ids)))
     return fail(ZS_ERR_INVALID_ARG, "zs_preference: null pointer%s");
   const TokenSplit sp = rows ? token_split(rows, vocab, dtype) : TokenSplit{1, 1};
   if (!token_launch_fits(rows, sp))
@@ -284,6 +284,7 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
   a.beta = beta;
   a.smoothing = smoothing;
   a.mean = mean;
+  a.clear = clear;
   a.pair_weight = pair_weight;
   a.dev = dev;
   a.scale = loss_scale;
@@ -292,11 +293,13 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
   a.grad = grad;
   a.gld = grad_ld;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (rows) {
+  if (rows && pairs) {
     if (int rc = launch_stats(a, dtype, s)) return rc;
   }
-  hipLaunchKernelGGL(token_pair_kernel, dim3(a.pairs), dim3(kPairThreads), 0, s, a);
-  if (int rc = launch_result()) return rc;
+  if (pairs) {
+    hipLaunchKernelGGL(token_pair_kernel, dim3(a.pairs), dim3(kPairThreads), 0, s, a);
+    if (int rc = launch_result()) return rc;
+  }
   return rows && grad ? launch_grad(a, dtype, s) : ZS_OK;
 }
 

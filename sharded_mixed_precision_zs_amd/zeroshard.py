@@ -140,7 +140,7 @@ def _load():
                        vp, vp, u64, vp, u64, vp], i32),
         "zs_preference_workspace": ([u64, u64, i32], u64),
         "zs_preference": ([vp, i32, u64, u64, u64, vp, vp, u64, f32, vp, i32, f32, f32, i32, vp,
-                           f32, vp, vp, vp, vp, u64, vp, u64, vp], i32),
+                           f32, vp, vp, vp, vp, u64, i32, vp, u64, vp], i32),
         "zs_offload_step": ([vp, vp, vp, vp, vp, vp, vp, u64, C.POINTER(zs_adamw_hparams), i32,
                              vp, vp, i32, i32, vp, C.POINTER(C.c_int)], i32),
     }
@@ -872,10 +872,12 @@ def zs_preference_workspace(rows, vocab, dtype):
 
 def zs_preference(logits, ids, starts, beta, loss, kind=ZS_PREFERENCE_SIGMOID, smoothing=0.0,
                   mean=False, temperature=1.0, ref_logp=None, pair_weight=None, loss_scale=1.0,
-                  dev_scaler=None, seq_logp=None, grad=None, workspace=None, stream=None):
+                  dev_scaler=None, seq_logp=None, grad=None, clear=False, workspace=None,
+                  stream=None):
     """Preference loss per pair of sequences (rows starts[s] to starts[s + 1] of logits and ids;
     pair p prefers sequence 2p) and, with grad, the logits' gradient times the loss scale. grad
-    may be logits itself; its rows outside all sequences are left as they were."""
+    may be logits itself; its rows outside all sequences are left as they were, or with clear
+    filled with zeros."""
     p, rows, vocab, ld = _rows(logits, "logits")
     f32, i32 = _t().f32, _t().i32
     pairs = loss.shape[0] if loss.dim() == 1 else -1
@@ -888,4 +890,4 @@ def zs_preference(logits, ids, starts, beta, loss, kind=ZS_PREFERENCE_SIGMOID, s
         1 if mean else 0, _dense(pair_weight, (pairs,), f32, "pair_weight"), loss_scale,
         None if dev_scaler is None else _dev_scaler_ptr(dev_scaler),
         _dense(seq_logp, (2 * pairs,), f32, "seq_logp"), _dense(loss, (pairs,), f32, "loss"), gp,
-        gld, wp, wb, _raw_stream(stream)))
+        gld, 1 if clear else 0, wp, wb, _raw_stream(stream)))

@@ -336,6 +336,12 @@ def test_preference_against_64_bits(zs, dtype, kind, smoothing, mean):
         assert torch.equal(l2, loss) and torch.equal(s2, seq)
         assert torch.equal(inplace[inside.cuda()], grad[inside.cuda()])
         assert torch.equal(inplace[~inside.cuda()].cpu(), z[~inside])
+        cleared = torch.full_like(inplace, 7.0)
+        run_preference(zs, z.cuda(), ids, starts, cleared, refs, weight, beta=beta,
+                       kind=kind_of(zs, kind), smoothing=smoothing, mean=mean, loss_scale=64.0,
+                       clear=True)
+        assert torch.equal(cleared[inside.cuda()], grad[inside.cuda()])
+        assert not cleared[~inside.cuda()].any()
         l3, s3 = run_preference(zs, z.cuda(), ids, starts, None, refs, weight, beta=beta,
                                 kind=kind_of(zs, kind), smoothing=smoothing, mean=mean)
         assert torch.equal(l3, loss) and torch.equal(s3, seq)
@@ -374,6 +380,15 @@ def test_preference_starts_out_of_range_stay_inside(zs):
     loss, seq = run_preference(zs, z.cuda(), ids, [-5, 8, 1 << 30], grad, beta=0.1)
     l2, s2 = run_preference(zs, z.cuda(), ids, [0, 8, 20], torch.empty_like(z).cuda(), beta=0.1)
     assert torch.equal(loss, l2) and torch.equal(seq, s2) and whole()
+
+
+def test_preference_without_pairs_clears(zs):
+    z, ids, _ = problem(7, 90, BF16)
+    grad = torch.full_like(z, 7.0).cuda()
+    run_preference(zs, z.cuda(), ids, [3], grad, beta=0.1)
+    assert bool((grad == 7.0).all())
+    run_preference(zs, z.cuda(), ids, [3], grad, beta=0.1, clear=True)
+    assert not grad.any()
 
 
 def test_preference_without_rows(zs):

@@ -41,7 +41,7 @@ def calls(zs):
         "preference": (lib.zs_preference, dict(
             **common, starts=far(2), pairs=2, tau=1.0, ref=far(3), kind=0, beta=0.1, smooth=0.0,
             mean=0, weight=far(4), scale=1.0, dev=None, seq=far(5), loss=far(6), grad=far(7),
-            gld=100, **ws)),
+            gld=100, clear=0, **ws)),
     }
 
 
