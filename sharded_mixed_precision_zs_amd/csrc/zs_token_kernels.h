@@ -10,9 +10,15 @@
  * where a student is sure of its token, taking q[a] from 1 would leave
  * rounding; log q[a] is then log1p of the same ratio.
  *
- * Terms as in the distillation loss: 2^(z c - I), I whole.
+ * Terms are 2^(z c - I), c = log2(e) / tau and I the whole number next to the
+ * token's own z c: no pass over the row has to find its maximum first, and a
+ * term is added as its logit arrives. Where that lets the sum leave 2^60 (a
+ * token that has less than e^-41 of the mass) it is formed again by the row's
+ * maximum. The rounding of an exponent is relative to its size, which is that
+ * of the log-probability.
  *
- * Bound by HBM.
+ * Bound by HBM: the policy loss reads a row once, into a block's registers,
+ * the preference loss twice, for a row's gradient needs its whole pair.
  */
 #ifndef ZS_TOKEN_KERNELS_H
 #define ZS_TOKEN_KERNELS_H
@@ -21,18 +27,19 @@
 
 namespace zs {
 
-/* Statistics of one part of a row: its maximum, and the sum of its terms but
- * the token's. */
+/* Statistics of one part of a row: the sum of its terms but the token's, and
+ * the logit that their shift is from. */
 struct TokenPart {
   double rest;
-  float max, pad;
+  float from, pad;
 };
 
 /* What a row's gradient is made of: term * factor, and `own` for token id. */
 struct TokenPlan {
-  float max, factor, own;
-  int32_t id;      /* < 0: zeros, and the logits are not read */
+  float from, factor, own;
+  int32_t id;      /* kNoToken: zeros, and the logits are not read; kOutside: not written */
 };
+constexpr int32_t kNoToken = -1, kOutside = -2;
 
 struct TokenArgs {
   const void *z;
@@ -53,12 +60,19 @@ struct TokenArgs {
 
   void *grad;                      /* optional */
   TokenPart *ws;                   /* [rows][parts] */
-  TokenPlan *plan;                 /* [rows] */
-  float *own;                      /* [rows]: the tokens' logits */
+  TokenPlan *plan;                 /* [rows]; of pairs first with the total and the rest
+                                    * for `factor` and `own` */
+  double *lp;                      /* [rows]: log-probabilities, of pairs */
+  float *own;                      /* [rows]: the tokens' logits, of rows in parts */
   uint64_t ld, gld;
   uint32_t rows, vocab, parts, part_vecs;
+  uint32_t row0, blocks;           /* gradient: a launch's first row, blocks of a row */
   float log2_scale, inv_tau, scale;   /* log2_scale = log2(e) / tau */
 };
+
+__device__ __forceinline__ int32_t load_scalar(const int32_t *p, uint32_t i) {
+  return __float_as_int(load_scalar(reinterpret_cast<const float *>(p), i));
+}
 
 /* Rows of the sequences, first and one past the last. */
 struct TokenSpan {
@@ -71,7 +85,8 @@ __device__ __forceinline__ uint32_t row_of(int32_t start, uint32_t rows) {
 
 __device__ __forceinline__ TokenSpan token_span(const TokenArgs &a) {
   if (!a.starts) return {0, a.rows};
-  return {row_of(a.starts[0], a.rows), row_of(a.starts[2 * a.pairs], a.rows)};
+  return {row_of(load_scalar(a.starts, 0), a.rows),
+          row_of(load_scalar(a.starts, 2 * a.pairs), a.rows)};
 }
 
 __device__ __forceinline__ bool token_live(const TokenArgs &a, uint32_t row, int32_t id) {
@@ -106,6 +121,24 @@ __device__ __forceinline__ TokenMass token_mass(double rest, float z, const Shif
   return m;
 }
 
+/* The same in fp32, where a row's logits hold the registers: the logarithm is
+ * off by half a unit in its last place, as the result's own rounding is. */
+struct TokenMass32 {
+  float rest, total, logp;
+};
+
+__device__ __forceinline__ TokenMass32 token_mass32(double rest, float z, const Shift &s) {
+  TokenMass32 m;
+  const float own = term(z, s);
+  m.rest = (float)rest;
+  m.total = (float)(rest + (double)own);
+  if (m.rest <= own && own > 0.0f)
+    m.logp = -log1pf(m.rest / own);
+  else   /* NaN: comes here */
+    m.logp = fmaf(z, s.c, -s.whole) * 0.69314718f - logf(m.total);
+  return m;
+}
+
 /* exp(d) - 1 - d, by its series near 0, where the difference would leave
  * rounding. */
 __device__ __forceinline__ float exp_rest(float d) {
@@ -121,43 +154,62 @@ struct Slope {
   float loss, slope;   /* slope: of the loss in the log-probability */
 };
 
-__device__ __forceinline__ Slope policy_slope(const TokenArgs &a, uint32_t row, double logp,
-                                              float weight) {
-  const float adv = a.advantage[row];
-  const float r = a.old_logp ? expf((float)(logp - (double)a.old_logp[row])) : 1.0f;
+/* What a row's policy loss takes in, loaded ahead of its use. */
+struct PolicyIn {
+  float advantage, old_logp, ref_logp, weight;
+};
+
+__device__ __forceinline__ PolicyIn policy_in(const TokenArgs &a, uint32_t row) {
+  PolicyIn p;
+  p.advantage = load_scalar(a.advantage, row);
+  p.old_logp = a.old_logp ? load_scalar(a.old_logp, row) : 0.0f;
+  p.ref_logp = a.ref_logp ? load_scalar(a.ref_logp, row) : 0.0f;
+  p.weight = a.weight ? load_scalar(a.weight, row) : 1.0f;
+  return p;
+}
+
+template <class T>
+__device__ __forceinline__ Slope policy_slope(const TokenArgs &a, const PolicyIn &in, T logp) {
+  const float adv = in.advantage;
+  const float r = a.old_logp ? expf((float)(logp - (T)in.old_logp)) : 1.0f;
   const float low = 1.0f - a.clip_low, high = 1.0f + a.clip_high;
   const bool above = adv > 0.0f && r > high, below = adv < 0.0f && r < low;
   Slope s;
   s.loss = -(above ? high : below ? low : r) * adv;
   s.slope = above || below ? 0.0f : -r * adv;
   if (a.ref_logp) {
-    const float d = (float)((double)a.ref_logp[row] - logp), rest = exp_rest(d);
+    const float d = (float)((T)in.ref_logp - logp), rest = exp_rest(d);
     s.loss = fmaf(a.kl_weight, rest, s.loss);
     s.slope = fmaf(-a.kl_weight, d + rest, s.slope);
   }
-  s.loss *= weight;
-  s.slope *= weight;
+  s.loss *= in.weight;
+  s.slope *= in.weight;
   return s;
 }
 
-/* A row's plan from its mass and the slope times loss scale and 1 / tau. */
-__device__ __forceinline__ TokenPlan make_plan(const TokenMass &m, float max, float slope,
+/* Loss scale over the temperature. */
+__device__ __forceinline__ float grad_scale(const TokenArgs &a) {
+  return (a.dev ? load_scalar(&a.dev->scale, 0) : a.scale) * a.inv_tau;
+}
+
+/* A row's plan from its sums and the slope times loss scale and 1 / tau. */
+__device__ __forceinline__ TokenPlan make_plan(double rest, double total, float from, float slope,
                                                int32_t id) {
   TokenPlan p;
-  p.max = max;
-  p.factor = (float)(-(double)slope / m.total);
-  p.own = (float)((double)slope * (m.rest / m.total));
-  p.id = slope == 0.0f ? -1 : id;
+  p.from = from;
+  p.factor = (float)(-(double)slope / total);
+  p.own = (float)((double)slope * (rest / total));
+  p.id = slope == 0.0f ? kNoToken : id;
   return p;
 }
 
 /* ------------------------------------------------------------------------
- * Statistics: a block per part of a row, each thread with a maximum and sum
- * of its own that follow the vectors as they come, U of them under way at a
- * time, so that each logit is read once; then joined. A thread's sums of
- * U vectors are fp32, what they are added to binary64.
+ * Statistics: a block per part of a row, U vectors of a thread under way at a
+ * time. A thread's sums of U vectors are fp32, what they are added to
+ * binary64.
  * ---------------------------------------------------------------------- */
 constexpr int kTokenAhead = 4;
+constexpr float kTokenTop = 1.15292150e18f;   /* 2^60 */
 
 template <int DT>
 __device__ __forceinline__ void leave_out(const RowShape &s, int32_t id, uint32_t v,
@@ -169,17 +221,28 @@ __device__ __forceinline__ void leave_out(const RowShape &s, int32_t id, uint32_
   for (uint32_t j = 0; j < ve; ++j) e[j] = at == j ? -INFINITY : e[j];
 }
 
-/* The row's results, where one block has seen all of it: log-probability,
- * policy loss and plan, as far as they are asked for. One thread. */
+/* The row's results, where one thread knows all of it: log-probability,
+ * policy loss and plan, as far as they are asked for. */
 __device__ __forceinline__ void finish_token(const TokenArgs &a, uint32_t row, double rest,
-                                             float max, float z, int32_t id) {
-  const TokenMass m = token_mass(rest, z, shift_of(max, a.log2_scale));
+                                             float from, float z, int32_t id) {
+  const TokenMass m = token_mass(rest, z, shift_of(from, a.log2_scale));
   if (a.logp) a.logp[row] = (float)m.logp;
+  if (a.starts) {
+    a.lp[row] = m.logp;
+    a.plan[row] = {from, (float)m.total, (float)m.rest, id};   /* until its pair gives a slope */
+    return;
+  }
   if (!a.loss) return;
-  const Slope s = policy_slope(a, row, m.logp, a.weight ? a.weight[row] : 1.0f);
+  const Slope s = policy_slope(a, policy_in(a, row), m.logp);
   a.loss[row] = s.loss;
-  if (a.grad)
-    a.plan[row] = make_plan(m, max, s.slope * (a.dev ? a.dev->scale : a.scale) * a.inv_tau, id);
+  if (a.grad) a.plan[row] = make_plan(m.rest, m.total, from, s.slope * grad_scale(a), id);
+}
+
+/* A row without a token, or without weight. */
+__device__ __forceinline__ void dead_token(const TokenArgs &a, uint32_t row) {
+  if (a.logp) a.logp[row] = 0.0f;
+  if (a.loss && !a.starts) a.loss[row] = 0.0f;
+  if (a.plan) a.plan[row] = {0.0f, 0.0f, 0.0f, kNoToken};
 }
 
 template <int DT, int NT>
@@ -187,20 +250,18 @@ __global__ __launch_bounds__(NT) void token_stats_kernel(TokenArgs a) {
   constexpr uint32_t ve = kVecElems<DT>, esz = DT == ZS_FP32 ? 4 : 2;
   constexpr int U = kTokenAhead;
   __shared__ float fpart[NT / 64];
-  __shared__ double dpart[NT / 64];
+  __shared__ double dpart[2][NT / 64];
   const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x;
   const TokenSpan span = token_span(a);
-  if (row < span.first || row >= span.last) return;
-  const int32_t id = a.ids[row];
-  const bool live = token_live(a, row, id), says = part == 0 && t == 0;
-  if (says) {
-    if (a.plan) a.plan[row] = {0.0f, 0.0f, 0.0f, -1};
-    if (!live) {
-      if (a.logp) a.logp[row] = 0.0f;
-      if (a.loss && !a.starts) a.loss[row] = 0.0f;
-    }
+  if (row < span.first || row >= span.last) {
+    if (part == 0 && t == 0) a.plan[row] = {0.0f, 0.0f, 0.0f, a.clear ? kNoToken : kOutside};
+    return;
   }
-  if (!live) return;
+  const int32_t id = load_scalar(a.ids, row);
+  if (!token_live(a, row, id)) {
+    if (part == 0 && t == 0) dead_token(a, row);
+    return;
+  }
   const char *z = static_cast<const char *>(a.z) + (uint64_t)row * a.ld * esz;
   const RowShape sh = row_shape<DT>(z, a.vocab);
   const u32x4 *zv = reinterpret_cast<const u32x4 *>(z + sh.head * esz);
@@ -208,66 +269,68 @@ __global__ __launch_bounds__(NT) void token_stats_kernel(TokenArgs a) {
   const uint32_t v1 = v0 + a.part_vecs < sh.vecs ? v0 + a.part_vecs : sh.vecs;
   const uint32_t edge = edge_index<DT>(sh, t, part == 0, part == a.parts - 1, a.vocab);
   const float own = load1<DT>(z, id);
-  float max = edge < a.vocab ? load1<DT>(z, edge) : -INFINITY;
-  Shift shift = shift_of(max, a.log2_scale);
-  double sum = edge < a.vocab && edge != (uint32_t)id ? (double)term(max, shift) : 0.0;
-  for (uint32_t v = v0 + t; v < v1; v += U * NT) {
-    u32x4 x[U];
+  const float single = edge < a.vocab && edge != (uint32_t)id ? load1<DT>(z, edge) : -INFINITY;
+  float from = own;
+  double sum;
+  for (bool again = false;; again = true) {
+    const Shift shift = shift_of(from, a.log2_scale);
+    sum = (double)term(single, shift);
+    for (uint32_t v = v0 + t; v < v1; v += U * NT) {
+      u32x4 x[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      x[i] = v + i * NT < v1 ? zv[v + i * NT] : empty_vec<DT>();
-    VecMax<DT> top;
+      for (int i = 0; i < U; ++i)
+        x[i] = v + i * NT < v1 ? __builtin_nontemporal_load(zv + v + i * NT) : empty_vec<DT>();
+      float some = 0.0f;
 #pragma unroll
-    for (int i = 0; i < U; ++i) top.add(x[i]);
-    if (top.get() > max) {
-      const Shift to = shift_of(top.get(), a.log2_scale);
-      sum *= shift_factor(max, shift, to);
-      max = top.get();
-      shift = to;
+      for (int i = 0; i < U; ++i) {
+        float e[ve];
+        unpack_vec<DT>(x[i], e);
+        leave_out<DT>(sh, id, v + i * NT, e);
+#pragma unroll
+        for (uint32_t j = 0; j < ve; ++j) some += term(e[j], shift);
+      }
+      sum += (double)some;
     }
-    float some = 0.0f;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
+    reduce_put(sum, SumOf{}, dpart[again]);
+    __syncthreads();
+    sum = reduce_get<NT>(SumOf{}, dpart[again]);
+    if (again || sum < (double)kTokenTop) break;   /* the same for the whole block */
+    float max = single;
+    for (uint32_t v = v0 + t; v < v1; v += NT) {
       float e[ve];
-      unpack_vec<DT>(x[i], e);
-      leave_out<DT>(sh, id, v + i * NT, e);
+      unpack_vec<DT>(zv[v], e);
 #pragma unroll
-      for (uint32_t j = 0; j < ve; ++j) some += term(e[j], shift);
+      for (uint32_t j = 0; j < ve; ++j) max = fmaxf(max, e[j]);
     }
-    sum += (double)some;
+    reduce_put(max, MaxOf{}, fpart);
+    __syncthreads();
+    from = reduce_get<NT>(MaxOf{}, fpart);
   }
-  reduce_put(max, MaxOf{}, fpart);
-  __syncthreads();
-  const float top = reduce_get<NT>(MaxOf{}, fpart);
-  sum *= shift_factor(max, shift, shift_of(top, a.log2_scale));
-  reduce_put(sum, SumOf{}, dpart);
-  __syncthreads();
-  sum = reduce_get<NT>(SumOf{}, dpart);
   if (t != 0) return;
-  if (part == 0 && a.own) a.own[row] = own;
-  if (a.parts == 1 && !a.starts) finish_token(a, row, sum, top, own, id);
-  else a.ws[(uint64_t)row * a.parts + part] = {sum, top, 0.0f};
+  if (a.parts == 1) {
+    finish_token(a, row, sum, from, own, id);
+  } else {
+    a.ws[(uint64_t)row * a.parts + part] = {sum, from, 0.0f};
+    if (part == 0) a.own[row] = own;
+  }
 }
 
-/* All of a row's parts. */
-__device__ __forceinline__ TokenPart join_parts(const TokenArgs &a, uint32_t row) {
-  const TokenPart *w = a.ws + (uint64_t)row * a.parts;
-  TokenPart r{0.0, -INFINITY, 0.0f};
-  for (uint32_t i = 0; i < a.parts; ++i) r.max = fmaxf(r.max, w[i].max);
-  const Shift to = shift_of(r.max, a.log2_scale);
-  for (uint32_t i = 0; i < a.parts; ++i)
-    r.rest += w[i].rest * shift_factor(w[i].max, shift_of(w[i].max, a.log2_scale), to);
-  return r;
-}
-
-/* Rows in parts: a thread per row joins them. */
+/* Rows in parts: a thread per row joins them, by the largest of the logits
+ * that their shifts are from. */
 __global__ __launch_bounds__(64) void token_finish_kernel(TokenArgs a) {
   const uint32_t row = blockIdx.x * 64 + threadIdx.x;
-  if (row >= a.rows) return;
+  const TokenSpan span = token_span(a);
+  if (row < span.first || row >= span.last) return;
   const int32_t id = a.ids[row];
   if (!token_live(a, row, id)) return;
-  const TokenPart p = join_parts(a, row);
-  finish_token(a, row, p.rest, p.max, a.own[row], id);
+  const TokenPart *w = a.ws + (uint64_t)row * a.parts;
+  float from = -INFINITY;
+  for (uint32_t i = 0; i < a.parts; ++i) from = fmaxf(from, w[i].from);
+  const Shift to = shift_of(from, a.log2_scale);
+  double rest = 0.0;
+  for (uint32_t i = 0; i < a.parts; ++i)
+    rest += w[i].rest * shift_factor(w[i].from, shift_of(w[i].from, a.log2_scale), to);
+  finish_token(a, row, rest, from, a.own[row], id);
 }
 
 /* ------------------------------------------------------------------------
@@ -300,17 +363,18 @@ __global__ __launch_bounds__(kPairThreads) void token_pair_kernel(TokenArgs a) {
   constexpr int NT = kPairThreads;
   __shared__ double part[4][NT / 64];
   const uint32_t pair = blockIdx.x;
-  double sum[2], count[2];
+  double sum[2] = {0.0, 0.0}, count[2] = {0.0, 0.0};
   TokenSpan seq[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < 2; ++k)
     seq[k] = {row_of(a.starts[2 * pair + k], a.rows), row_of(a.starts[2 * pair + k + 1], a.rows)};
-    sum[k] = count[k] = 0.0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
     for (uint64_t row = (uint64_t)seq[k].first + threadIdx.x; row < seq[k].last; row += NT) {
       const int32_t id = a.ids[row];
+      const double lp = a.lp[row];   /* not written where there is no token */
       if (!token_live(a, row, id)) continue;
-      const TokenPart p = join_parts(a, row);
-      sum[k] += token_mass(p.rest, a.own[row], shift_of(p.max, a.log2_scale)).logp;
+      sum[k] += lp;
       count[k] += 1.0;
     }
     reduce_put(sum[k], SumOf{}, part[2 * k]);
@@ -342,73 +406,226 @@ __global__ __launch_bounds__(kPairThreads) void token_pair_kernel(TokenArgs a) {
   for (int k = 0; k < 2; ++k) {
     const float slope = (float)((k ? -up : up) * each[k]);
     for (uint64_t row = (uint64_t)seq[k].first + threadIdx.x; row < seq[k].last; row += NT) {
-      const int32_t id = a.ids[row];
-      if (!token_live(a, row, id)) continue;
-      const TokenPart p = join_parts(a, row);
-      const TokenMass m = token_mass(p.rest, a.own[row], shift_of(p.max, a.log2_scale));
-      a.plan[row] = make_plan(m, p.max, slope, id);
+      const TokenPlan p = a.plan[row];
+      if (p.id >= 0) a.plan[row] = make_plan(p.own, p.factor, p.from, slope, p.id);
     }
   }
 }
 
 /* ------------------------------------------------------------------------
- * The gradient of a part of a row, from its plan: read once, written once;
- * rows whose gradient is zero are not read.
+ * The gradient from the rows' plans: a vector per thread and blocks that live
+ * as long as that takes, the shape in which a copy is fastest here. Rows whose
+ * gradient is zero are not read.
  * ---------------------------------------------------------------------- */
 template <int DT>
 struct __attribute__((packed, aligned(DT == ZS_FP32 ? 4 : 2))) LooseVec { uint32_t w[4]; };
 
+/* By the scalar unit: the one thing that a block waits for before its logits. */
+__device__ __forceinline__ TokenPlan load_plan(const TokenPlan *p, uint32_t row) {
+  const float *f = reinterpret_cast<const float *>(p + row);
+  return {load_scalar(f, 0), load_scalar(f, 1), load_scalar(f, 2),
+          __float_as_int(load_scalar(f, 3))};
+}
+
 template <int DT, int NT>
 __global__ __launch_bounds__(NT) void token_grad_kernel(TokenArgs a) {
   constexpr uint32_t ve = kVecElems<DT>, esz = DT == ZS_FP32 ? 4 : 2;
-  constexpr int U = kTokenAhead;
-  const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x;
-  const TokenSpan span = token_span(a);
-  const bool inside = row >= span.first && row < span.last;
-  if (!inside && !a.clear) return;
-  const TokenPlan p = inside ? a.plan[row] : TokenPlan{0.0f, 0.0f, 0.0f, -1};
+  const uint32_t row = a.row0 + blockIdx.x / a.blocks, block = blockIdx.x % a.blocks;
   const char *z = static_cast<const char *>(a.z) + (uint64_t)row * a.ld * esz;
   char *g = static_cast<char *>(a.grad) + (uint64_t)row * a.gld * esz;
   const RowShape sh = row_shape<DT>(z, a.vocab);
-  const u32x4 *zv = reinterpret_cast<const u32x4 *>(z + sh.head * esz);
-  const uint32_t v0 = part * a.part_vecs;
-  const uint32_t v1 = v0 + a.part_vecs < sh.vecs ? v0 + a.part_vecs : sh.vecs;
-  const uint32_t edge = edge_index<DT>(sh, t, part == 0, part == a.parts - 1, a.vocab);
-  const bool live = p.id >= 0, vec = ((uintptr_t)(g + sh.head * esz) & 15) == 0;
-  const Shift shift = shift_of(p.max, a.log2_scale);
+  const TokenPlan p = load_plan(a.plan, row);
+  if (p.id == kOutside) return;
+  const bool live = p.id >= 0;
+  const Shift shift = shift_of(p.from, a.log2_scale);
+  const uint32_t edge = block == 0 ? edge_index<DT>(sh, threadIdx.x, true, true, a.vocab) : a.vocab;
   if (edge < a.vocab) {
     float x = 0.0f;
     if (live) x = edge == (uint32_t)p.id ? p.own : term(load1<DT>(z, edge), shift) * p.factor;
     store1<DT>(g, edge, x);
   }
-  auto put = [&](uint32_t v, const u32x4 &w) {
-    char *to = g + sh.head * esz + (uint64_t)v * 16;
-    if (vec) __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(to));
-    else *reinterpret_cast<LooseVec<DT> *>(to) = LooseVec<DT>{{w.x, w.y, w.z, w.w}};
-  };
-  if (!live) {
-    for (uint32_t v = v0 + t; v < v1; v += NT) put(v, u32x4{0, 0, 0, 0});
-    return;
+  const uint32_t v = block * NT + threadIdx.x;
+  if (v >= sh.vecs) return;
+  u32x4 w = {0, 0, 0, 0};
+  if (live) {
+    float e[ve];
+    unpack_vec<DT>(__builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(z + sh.head * esz) + v), e);
+#pragma unroll
+    for (uint32_t j = 0; j < ve; ++j) e[j] = term(e[j], shift) * p.factor;
+    const uint32_t at = (uint32_t)p.id - sh.head - v * ve;
+    if (at < ve) {
+#pragma unroll
+      for (uint32_t j = 0; j < ve; ++j) e[j] = at == j ? p.own : e[j];
+    }
+    w = pack_vec<DT>(e);
   }
-  for (uint32_t v = v0 + t; v < v1; v += U * NT) {
-    u32x4 x[U];
+  char *to = g + sh.head * esz + (uint64_t)v * 16;
+  if (((uintptr_t)(g + sh.head * esz) & 15) == 0)
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(to));
+  else
+    *reinterpret_cast<LooseVec<DT> *>(to) = LooseVec<DT>{{w.x, w.y, w.z, w.w}};
+}
+
+/* ------------------------------------------------------------------------
+ * The policy loss of rows that a block's registers hold: ITEMS 16-byte vectors
+ * per thread and, in a few threads, one single element. A block walks rows
+ * blockIdx, + gridDim, ..., and while it writes a row's gradient it fetches
+ * the next row into the registers that fall free; its terms are added as they
+ * arrive, and one reduction parts the two sweeps.
+ * ---------------------------------------------------------------------- */
+constexpr int kTokenStore = 2;   /* non-temporal: read by a later call, in whole lines */
+
+struct TokenIn {
+  const char *z;
+  RowShape shape;
+  uint32_t edge;
+  int32_t id;
+  PolicyIn policy;
+  bool live;
+};
+
+template <int DT>
+__device__ __forceinline__ TokenIn open_token(const TokenArgs &a, uint32_t row) {
+  constexpr uint64_t esz = DT == ZS_FP32 ? 4 : 2;
+  TokenIn r;
+  r.z = static_cast<const char *>(a.z) + (uint64_t)row * a.ld * esz;
+  r.shape = row_shape<DT>(r.z, a.vocab);
+  r.id = load_scalar(a.ids, row);
+  r.policy = policy_in(a, row);
+  r.live = (uint32_t)r.id < a.vocab && r.policy.weight != 0.0f;
+  r.edge = edge_index<DT>(r.shape, threadIdx.x, true, true, a.vocab);
+  return r;
+}
+
+/* A row without a token is not read: its buffer is empty. */
+template <int DT>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t token_buffer(const TokenIn &r) {
+  return bounded(r.z + r.shape.head * (DT == ZS_FP32 ? 4 : 2), r.live ? r.shape.vecs * 16 : 0);
+}
+
+/* The vector at byte `at`, or the row's last for a thread past it, which the
+ * sum leaves out. */
+__device__ __forceinline__ u32x4 token_vec(__amdgpu_buffer_rsrc_t row, const TokenIn &r,
+                                           uint32_t at) {
+  const uint32_t last = (r.shape.vecs - 1) * 16, mine = at + threadIdx.x * 16;
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                       row, (int)(mine < last ? mine : last), 0, 0));
+}
+
+template <int DT>
+__device__ __forceinline__ void token_singles(const TokenArgs &a, const TokenIn &r, uint32_t &own,
+                                              uint32_t &single) {
+  own = single = empty_vec<DT>()[0];
+  if (!r.live) return;
+  own = load_raw<DT>(r.z, r.id);
+  if (r.edge < a.vocab && r.edge != (uint32_t)r.id) single = load_raw<DT>(r.z, r.edge);
+}
+
+template <int DT, int NT, int ITEMS>
+__global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(TokenArgs a) {
+  constexpr uint32_t ve = kVecElems<DT>, esz = DT == ZS_FP32 ? 4 : 2;
+  __shared__ double dpart[2][2][NT / 64];
+  __shared__ float fpart[2][NT / 64];
+  const uint32_t t = threadIdx.x;
+  const float scale = grad_scale(a);
+  uint32_t row = blockIdx.x, turn = 0;
+  TokenIn in = open_token<DT>(a, row);
+  uint32_t raw_own, raw_single;
+  token_singles<DT>(a, in, raw_own, raw_single);
+  u32x4 x[ITEMS];
+  {
+    const __amdgpu_buffer_rsrc_t buf = token_buffer<DT>(in);
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      x[i] = v + i * NT < v1 ? zv[v + i * NT] : u32x4{0, 0, 0, 0};
+    for (int i = 0; i < ITEMS; ++i) x[i] = token_vec(buf, in, i * (NT * 16));
+  }
+  for (;; turn ^= 1) {
+    /* rows are told apart by a scalar that the compiler cannot follow: it would
+     * keep a pointer of its own in vector registers for every use */
+    asm volatile("" : "+s"(row));
+    const uint32_t next = row + gridDim.x;
+    const bool more = next < a.rows;
+    const TokenIn after = open_token<DT>(a, more ? next : row);
+    TokenPlan plan{0.0f, 0.0f, 0.0f, kNoToken};
+    float single = -INFINITY;
+    if (in.live) {   /* uniform over the block */
+      const float own = raw_value<DT>(raw_own);
+      single = raw_value<DT>(raw_single);
+      float from = own;
+      double rest;
+      for (bool again = false;; again = true) {
+        const Shift s = shift_of(from, a.log2_scale);
+        float sum = term(single, s);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (v + i * NT >= v1) break;
+        for (int i = 0; i < ITEMS; ++i) {
+          float e[ve];
+          asm volatile("" : "+v"(x[i]));   /* unpacked anew each time */
+          unpack_vec<DT>(x[i], e);
+          leave_out<DT>(in.shape, in.id, i * NT + t, e);
+          float some = 0.0f;
+#pragma unroll
+          for (uint32_t j = 0; j < ve; ++j) some += term(e[j], s);
+          sum += (int)t < (int)in.shape.vecs - i * NT ? some : 0;
+          asm volatile("" : "+v"(sum));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        reduce_put((double)sum, SumOf{}, dpart[turn][again]);
+        __syncthreads();
+        rest = reduce_get<NT>(SumOf{}, dpart[turn][again]);
+        if (again || rest < (double)kTokenTop) break;   /* uniform over the block */
+        VecMax<DT> max;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) max.add(x[i]);
+        reduce_put(fmaxf(max.get(), single), MaxOf{}, fpart[turn]);
+        __syncthreads();
+        from = reduce_get<NT>(MaxOf{}, fpart[turn]);
+      }
+      const TokenMass32 m = token_mass32(rest, own, shift_of(from, a.log2_scale));
+      const Slope s = policy_slope(a, in.policy, m.logp);
+      if (t == 0) {
+        if (a.logp) a.logp[row] = m.logp;
+        a.loss[row] = s.loss;
+      }
+      const float slope = s.slope * scale;
+      plan = {from, -slope / m.total, slope * (m.rest / m.total),
+              slope == 0.0f ? kNoToken : in.id};
+    } else if (t == 0) {
+      if (a.logp) a.logp[row] = 0.0f;
+      a.loss[row] = 0.0f;
+    }
+    if (plan.id < 0) {   /* zeros: terms of -inf */
+      plan = {0.0f, 0.0f, 0.0f, kNoToken};
+      single = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) x[i] = empty_vec<DT>();
+    }
+    const Shift shift = shift_of(plan.from, a.log2_scale);
+    char *g = static_cast<char *>(a.grad) + (uint64_t)row * a.gld * esz;
+    const __amdgpu_buffer_rsrc_t to = bounded(g + in.shape.head * esz, in.shape.vecs * 16);
+    const __amdgpu_buffer_rsrc_t from_next = token_buffer<DT>(after);
+    if (in.edge < a.vocab)
+      store1<DT>(g, in.edge,
+                 in.edge == (uint32_t)plan.id ? plan.own : term(single, shift) * plan.factor);
+    if (more) token_singles<DT>(a, after, raw_own, raw_single);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
       float e[ve];
+      asm volatile("" : "+v"(x[i]));   /* unpacked anew, not kept since the sum */
       unpack_vec<DT>(x[i], e);
 #pragma unroll
-      for (uint32_t j = 0; j < ve; ++j) e[j] = term(e[j], shift) * p.factor;
-      const uint32_t at = (uint32_t)p.id - sh.head - (v + i * NT) * ve;
-      if (at < ve) {
+      for (uint32_t j = 0; j < ve; ++j) e[j] = term(e[j], shift) * plan.factor;
+      const uint32_t at = (uint32_t)plan.id - in.shape.head - (i * NT + t) * ve;
+      if (plan.id >= 0 && at < ve) {
 #pragma unroll
-        for (uint32_t j = 0; j < ve; ++j) e[j] = at == j ? p.own : e[j];
+        for (uint32_t j = 0; j < ve; ++j) e[j] = at == j ? plan.own : e[j];
       }
-      put(v + i * NT, pack_vec<DT>(e));
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, pack_vec<DT>(e)), to,
+                                             (int)(t * 16 + i * (NT * 16)), 0, kTokenStore);
+      x[i] = token_vec(from_next, after, i * (NT * 16));   /* past the last row: not used */
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if (!more) return;
+    row = next;
+    in = after;
   }
 }
 

@@ -19,18 +19,19 @@ namespace {
 using namespace zs;
 using namespace zs_ops;
 
-constexpr int kTokenThreads = 256;
+/* How a row's statistics are cut into parts: whole, a block for each row, up
+ * to 256 KB; of longer rows, where there are too few to occupy the GPU, into
+ * such parts. */
+constexpr uint32_t kPartVecs = 16384;
 
-/* How a row is cut into parts: whole, but where few rows leave the GPU idle;
- * then into some 1024 parts in all, of a vector or more for every thread. */
 struct TokenSplit {
   uint32_t parts, part_vecs;
 };
 
 TokenSplit token_split(uint64_t rows, uint64_t vocab, int dtype) {
   const uint64_t vecs = vocab * esize(dtype) / 16;
-  uint64_t parts = rows < 1024 ? 1024 / rows : 1;
-  const uint64_t most = (vecs + kTokenThreads - 1) / kTokenThreads;
+  uint64_t parts = (vecs + kPartVecs - 1) / kPartVecs;
+  const uint64_t most = rows < 512 ? 512 / rows : 1;
   if (parts > most) parts = most;
   if (parts < 1) parts = 1;
   const uint64_t each = vecs ? (vecs + parts - 1) / parts : 1;
@@ -40,12 +41,12 @@ TokenSplit token_split(uint64_t rows, uint64_t vocab, int dtype) {
   return {(uint32_t)parts, (uint32_t)each};
 }
 
-uint64_t token_workspace(uint64_t rows, uint64_t vocab, int dtype) {
+uint64_t token_workspace(uint64_t rows, uint64_t vocab, int dtype, bool pairs) {
   if (rows == 0 || rows >> 31 || vocab == 0 || vocab > kMaxVocab || !valid_any(dtype) ||
       matrix_too_big(rows, vocab))
     return 0;
   return rows * (token_split(rows, vocab, dtype).parts * sizeof(TokenPart) + sizeof(TokenPlan) +
-                 sizeof(float));
+                 sizeof(float) + (pairs ? sizeof(double) : 0));
 }
 
 /* What the three entry points put into `a` alike. */
@@ -61,41 +62,93 @@ void token_args(TokenArgs &a, const void *logits, int dtype, uint64_t rows, uint
   a.part_vecs = sp.part_vecs;
   a.log2_scale = (float)(1.4426950408889634 / temperature);
   a.inv_tau = 1.0f / temperature;
-  char *w = static_cast<char *>(workspace);
-  a.ws = reinterpret_cast<TokenPart *>(w);
-  a.plan = reinterpret_cast<TokenPlan *>(w + rows * sp.parts * sizeof(TokenPart));
+  a.ws = static_cast<TokenPart *>(workspace);
+  a.plan = reinterpret_cast<TokenPlan *>(a.ws + rows * sp.parts);
   a.own = reinterpret_cast<float *>(a.plan + rows);
 }
 
+/* Threads of a block for a part's statistics: a wave for short rows; as many
+ * as there are where few rows leave the GPU idle. */
 template <class F>
-void with_token_threads(uint32_t part_vecs, F f) {
-  if (part_vecs <= 512) f(Tag<64>{});
-  else f(Tag<kTokenThreads>{});
+void with_token_threads(const TokenArgs &a, F f) {
+  if (a.part_vecs <= 512) f(Tag<64>{});
+  else if (a.rows * (uint64_t)a.parts >= 1024 || a.part_vecs <= 1024) f(Tag<256>{});
+  else f(Tag<1024>{});
 }
 
 int launch_stats(const TokenArgs &a, int dtype, hipStream_t s) {
   with_any(dtype, [&](auto dt) {
-    with_token_threads(a.part_vecs, [&](auto nt) {
+    with_token_threads(a, [&](auto nt) {
       hipLaunchKernelGGL((token_stats_kernel<decltype(dt)::value, decltype(nt)::value>),
                          dim3(a.rows * a.parts), dim3(decltype(nt)::value), 0, s, a);
     });
   });
+  if (int rc = launch_result()) return rc;
+  if (a.parts == 1) return ZS_OK;
+  hipLaunchKernelGGL(token_finish_kernel, dim3((a.rows + 63) / 64), dim3(64), 0, s, a);
   return launch_result();
 }
 
-int launch_grad(const TokenArgs &a, int dtype, hipStream_t s) {
+/* Logits of more than 2^32 vectors take several launches. */
+int launch_grad(TokenArgs a, int dtype, hipStream_t s) {
+  const uint64_t vecs = (uint64_t)a.vocab * esize(dtype) / 16;
+  int rc = ZS_OK;
+  auto launch = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    a.blocks = vecs > NT ? (uint32_t)((vecs + NT - 1) / NT) : 1;
+    const uint64_t most = 0xffffffffull / ((uint64_t)a.blocks * NT);   /* seven rows at least */
+    for (a.row0 = 0; a.row0 < a.rows && !rc; a.row0 += (uint32_t)most) {
+      const uint64_t n = a.rows - a.row0 < most ? a.rows - a.row0 : most;
+      with_any(dtype, [&](auto dt) {
+        hipLaunchKernelGGL((token_grad_kernel<decltype(dt)::value, NT>),
+                           dim3((unsigned)(n * a.blocks)), dim3(NT), 0, s, a);
+      });
+      rc = launch_result();
+      if (n < most) break;   /* the row's number could wrap */
+    }
+  };
+  if (vecs <= 64) launch(Tag<64>{});
+  else launch(Tag<256>{});
+  return rc;
+}
+
+/* Rows that a block's registers hold, and as many blocks as fit at the
+ * registers the kernel is held to. */
+constexpr int kPolicyItems = 32;
+
+template <int DT, int NT, int ITEMS>
+void launch_policy_rows(const TokenArgs &a, hipStream_t s) {
+  const uint64_t fit = (uint64_t)cu_count() * (ITEMS <= 16 ? 16 : 8) / (NT / 64);
+  hipLaunchKernelGGL((policy_row_kernel<DT, NT, ITEMS>),
+                     dim3((unsigned)(a.rows < fit ? a.rows : fit)), dim3(NT), 0, s, a);
+}
+
+bool policy_in_rows(const TokenArgs &a, int dtype) {
+  const uint64_t vecs = (uint64_t)a.vocab * esize(dtype) / 16;
+  /* two vectors' worth of elements hold one, whatever the row's alignment */
+  return a.grad && vecs >= 2 && vecs <= 512 * kPolicyItems &&
+         (((uintptr_t)a.grad ^ (uintptr_t)a.z) & 15) == 0 &&
+         (a.gld - a.ld) * esize(dtype) % 16 == 0;
+}
+
+int launch_policy(const TokenArgs &a, int dtype, hipStream_t s) {
+  const uint64_t vecs = (uint64_t)a.vocab * esize(dtype) / 16;
   with_any(dtype, [&](auto dt) {
-    with_token_threads(a.part_vecs, [&](auto nt) {
-      hipLaunchKernelGGL((token_grad_kernel<decltype(dt)::value, decltype(nt)::value>),
-                         dim3(a.rows * a.parts), dim3(decltype(nt)::value), 0, s, a);
-    });
+    constexpr int DT = decltype(dt)::value;
+    if (vecs <= 128) launch_policy_rows<DT, 64, 2>(a, s);
+    else if (vecs <= 512) launch_policy_rows<DT, 64, 8>(a, s);
+    else if (vecs <= 1024) launch_policy_rows<DT, 64, 16>(a, s);
+    else if (vecs <= 2048) launch_policy_rows<DT, 128, 16>(a, s);
+    else if (vecs <= 4096) launch_policy_rows<DT, 256, 16>(a, s);
+    else if (vecs <= 8192) launch_policy_rows<DT, 512, 16>(a, s);
+    else launch_policy_rows<DT, 512, kPolicyItems>(a, s);
   });
   return launch_result();
 }
 
 /* Whether the launches of a call stay below 2^32 threads. */
 bool token_launch_fits(uint64_t rows, const TokenSplit &sp) {
-  return rows < 1ull << 31 && fits(rows * sp.parts, kTokenThreads);
+  return rows < 1ull << 31 && fits(rows * sp.parts, 256);
 }
 
 /* Checks of logits, tokens, temperature and gradient. Names: one message per
@@ -129,7 +182,7 @@ int alias_check(const void *const *outs, const uint64_t *out_bytes, int n_outs,
 extern "C" {
 
 uint64_t zs_logprob_workspace(uint64_t rows, uint64_t vocab, int dtype) {
-  return token_workspace(rows, vocab, dtype);
+  return token_workspace(rows, vocab, dtype, false);
 }
 
 int zs_logprob(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
@@ -142,7 +195,7 @@ int zs_logprob(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   if (!logits || !ids || !logp) return fail(ZS_ERR_INVALID_ARG, "zs_logprob: null pointer%s");
   if (!token_launch_fits(rows, token_split(rows, vocab, dtype)))
     return fail(ZS_ERR_UNSUPPORTED, "zs_logprob: too many rows%s");
-  const uint64_t esz = esize(dtype), need = token_workspace(rows, vocab, dtype);
+  const uint64_t esz = esize(dtype), need = token_workspace(rows, vocab, dtype, false);
   if (!workspace || workspace_bytes < need)
     return fail(ZS_ERR_INVALID_ARG, "zs_logprob: workspace too small%s");
   if (!aligned(logits, esz) || !aligned(ids, 4) || !aligned(logp, 4) || !aligned(workspace, 16))
@@ -159,14 +212,11 @@ int zs_logprob(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   token_args(a, logits, dtype, rows, vocab, ld, ids, temperature, workspace);
   a.logp = logp;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (int rc = launch_stats(a, dtype, s)) return rc;
-  if (a.parts == 1) return ZS_OK;
-  hipLaunchKernelGGL(token_finish_kernel, dim3((a.rows + 63) / 64), dim3(64), 0, s, a);
-  return launch_result();
+  return launch_stats(a, dtype, s);
 }
 
 uint64_t zs_policy_workspace(uint64_t rows, uint64_t vocab, int dtype) {
-  return token_workspace(rows, vocab, dtype);
+  return token_workspace(rows, vocab, dtype, false);
 }
 
 int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
@@ -187,7 +237,7 @@ int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint
     return fail(ZS_ERR_INVALID_ARG, "zs_policy: null pointer%s");
   if (!token_launch_fits(rows, token_split(rows, vocab, dtype)))
     return fail(ZS_ERR_UNSUPPORTED, "zs_policy: too many rows%s");
-  const uint64_t esz = esize(dtype), need = token_workspace(rows, vocab, dtype);
+  const uint64_t esz = esize(dtype), need = token_workspace(rows, vocab, dtype, false);
   if (!workspace || workspace_bytes < need)
     return fail(ZS_ERR_INVALID_ARG, "zs_policy: workspace too small%s");
   if (!aligned(logits, esz) || !aligned(ids, 4) || !aligned(advantage, 4) ||
@@ -221,16 +271,13 @@ int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint
   a.grad = grad;
   a.gld = grad_ld;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (policy_in_rows(a, dtype)) return launch_policy(a, dtype, s);
   if (int rc = launch_stats(a, dtype, s)) return rc;
-  if (a.parts > 1) {
-    hipLaunchKernelGGL(token_finish_kernel, dim3((a.rows + 63) / 64), dim3(64), 0, s, a);
-    if (int rc = launch_result()) return rc;
-  }
   return grad ? launch_grad(a, dtype, s) : ZS_OK;
 }
 
 uint64_t zs_preference_workspace(uint64_t rows, uint64_t vocab, int dtype) {
-  return token_workspace(rows, vocab, dtype);
+  return token_workspace(rows, vocab, dtype, true);
 }
 
 int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
@@ -257,7 +304,7 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
   const TokenSplit sp = rows ? token_split(rows, vocab, dtype) : TokenSplit{1, 1};
   if (!token_launch_fits(rows, sp))
     return fail(ZS_ERR_UNSUPPORTED, "zs_preference: too many rows%s");
-  const uint64_t esz = esize(dtype), need = token_workspace(rows, vocab, dtype);
+  const uint64_t esz = esize(dtype), need = token_workspace(rows, vocab, dtype, true);
   if (need && (!workspace || workspace_bytes < need))
     return fail(ZS_ERR_INVALID_ARG, "zs_preference: workspace too small%s");
   if (!aligned(logits, esz) || !aligned(ids, 4) || !aligned(starts, 4) || !aligned(ref_logp, 4) ||
@@ -275,8 +322,12 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
                            "zs_preference: two outputs overlap%s"))
     return rc;
   TokenArgs a{};
-  if (rows)
+  if (rows) {
     token_args(a, logits, dtype, rows, vocab, ld, ids, temperature, workspace);
+    /* behind the plans, 16 bytes each: the doubles stay aligned */
+    a.lp = reinterpret_cast<double *>(a.plan + rows);
+    a.own = reinterpret_cast<float *>(a.lp + rows);
+  }
   a.starts = starts;
   a.pairs = (uint32_t)pairs;
   a.ref_seq = ref_logp;
@@ -293,7 +344,7 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
   a.grad = grad;
   a.gld = grad_ld;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (rows && pairs) {
+  if (rows && (pairs || clear)) {
     if (int rc = launch_stats(a, dtype, s)) return rc;
   }
   if (pairs) {

@@ -179,9 +179,12 @@ def test_policy_head_and_its_logprobs(zs):
     adv = torch.randn(ROWS, generator=g).cuda()
     old = head.logprobs(params, x, res, ids).clone()
     loss = head.step(params, x, res, ids, adv, old_logp=old, loss_scale=64.0)
-    # the ratio is 1: the loss is the advantage's, and log-probabilities are the sampler's
-    assert torch.equal(head.logp, old)
-    assert bool(((loss + adv).abs() <= 1e-5 * adv.abs()).all())
+    # the ratio is 1: the loss is the advantage's, and log-probabilities are the sampler's. The two
+    # kernels add a row's terms in orders of their own: each is within 2 (2 D + 38) 2^-24 of the
+    # exact one, D the row's spread, and these rows' is below 16 (7 standard deviations of 0.7
+    # either way): 1.7e-5 between the two, and as much of the ratio
+    assert bool(((head.logp - old).abs() <= 1.7e-5).all())
+    assert bool(((loss + adv).abs() <= 2e-5 * adv.abs()).all())
     assert torch.isfinite(head.grads.float()).all() and head.grads.float().abs().max() > 0
 
 

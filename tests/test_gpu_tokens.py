@@ -405,8 +405,9 @@ def test_token_losses_captured_and_replayed(zs):
         dz, di = z.cuda(), ids.cuda()
         starts = torch.tensor([0, rows // 4, rows // 2, rows], dtype=torch.int32).cuda()
         starts = torch.cat([starts, starts[-1:]])       # an empty last sequence
-        ws = torch.empty(zs.zs_policy_workspace(rows, vocab, zs.ZS_BF16), dtype=torch.uint8,
-                         device="cuda")
+        ws = torch.empty(max(zs.zs_policy_workspace(rows, vocab, zs.ZS_BF16),
+                             zs.zs_preference_workspace(rows, vocab, zs.ZS_BF16)),
+                         dtype=torch.uint8, device="cuda")
         outs = [torch.empty_like(dz), torch.empty_like(dz), torch.empty(rows, device="cuda"),
                 torch.empty(rows, device="cuda"), torch.empty(2, device="cuda")]
 
