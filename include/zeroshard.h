@@ -837,7 +837,7 @@ int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint
  * The logits are read twice: a row's gradient needs its whole pair's loss.
  * Further errors: ZS_ERR_INVALID_ARG (kind, beta not finite and > 0, smoothing
  * outside [0, 1] or with another kind than the sigmoid), ZS_ERR_UNSUPPORTED
- * (2^24 pairs or more). */
+ * (2^22 pairs or more). */
 typedef enum {
   ZS_PREFERENCE_SIGMOID = 0,
   ZS_PREFERENCE_HINGE = 1,

@@ -8,6 +8,7 @@
 
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "zeroshard.h"
 
@@ -37,6 +38,42 @@ int drop_args(const zs_dropout_rule *rule, DropArgs &d, const char *bad_p, const
   d.factor64 = d.threshold < 65536 ? 65536.0 / (65536 - d.threshold) : 0.0;
   d.factor = (float)d.factor64;
   return ZS_OK;
+}
+
+/* Whether a float has at most 13 significant bits, and is no extreme one whose
+ * products with 16-bit numbers could leave fp32's normal range unseen. */
+bool short_float(float x) {
+  uint32_t b;
+  memcpy(&b, &x, sizeof b);
+  return (b & 0x7ff) == 0 && (x == 0.0f || (fabsf(x) >= 0x1p-10f && fabsf(x) <= 0x1p10f));
+}
+
+template <class F>
+void with_block_shape(uint64_t padded, F f) {
+  if (padded <= 512) f(Tag<64>{}, Tag<1>{});
+  else if (padded <= 1024) f(Tag<64>{}, Tag<2>{});
+  else if (padded <= 2048) f(Tag<128>{}, Tag<2>{});
+  else if (padded <= 4096) f(Tag<128>{}, Tag<4>{});
+  else if (padded <= 8192) f(Tag<256>{}, Tag<4>{});
+  else if (padded <= 16384) f(Tag<512>{}, Tag<4>{});
+  else f(Tag<1024>{}, Tag<8>{});
+}
+
+template <class F>
+void with_block_grad_shape(uint64_t padded, F f) {
+  if (padded <= 512) f(Tag<64>{}, Tag<1>{});
+  else if (padded <= 1024) f(Tag<128>{}, Tag<1>{});
+  else if (padded <= 2048) f(Tag<256>{}, Tag<1>{});
+  else if (padded <= 4096) f(Tag<512>{}, Tag<1>{});
+  else if (padded <= 8192) f(Tag<1024>{}, Tag<1>{});
+  else if (padded <= 16384) f(Tag<1024>{}, Tag<2>{});
+  else f(Tag<1024>{}, Tag<8>{});
+}
+
+uint32_t block_parts(uint64_t rows, uint64_t cols) {
+  const uint64_t fit = cols <= 2048 ? 1024 : cols <= 4096 ? 512 : 256;
+  const uint64_t want = rows / 4 < 256 ? 256 : rows / 4 > fit ? fit : rows / 4;
+  return (uint32_t)(rows < want ? rows : want);
 }
 
 constexpr uint64_t kMaxDropRows = 1ull << 32;   /* a counter's word */
@@ -151,6 +188,8 @@ int zs_block_norm_forward(const void *x, const void *residual, const void *post_
   a.inv_cols = 1.0 / (double)cols;
   a.residual_scale = residual_scale;
   a.branch_scale = branch_scale;
+  /* 13 bits of it times 11 of the residual's are 24 */
+  a.near_dropped = short_float(residual_scale) ? 0.0f : 0x1p-22f;
   const bool al = cols % 8 == 0 && aligned(x, 16) && aligned(residual, 16) &&
                   aligned(post_gain, 16) && aligned(gate, 16) && aligned(gain, 16) &&
                   aligned(h, 16) && aligned(y, 16);
@@ -158,8 +197,8 @@ int zs_block_norm_forward(const void *x, const void *residual, const void *post_
   int rc = ZS_OK;
   with16(dtype, [&](auto dt) {
     with_bool(al, [&](auto v) {
-      with_norm_shape(padded, [&](auto g, auto items) {
-        constexpr int G = decltype(g)::value, block = G < 256 ? 256 : G, per = block / G;
+      with_block_shape(padded, [&](auto g, auto items) {
+        constexpr int G = decltype(g)::value, block = G < 128 ? 256 : G, per = block / G;
         const uint64_t blocks = (rows + per - 1) / per;
         if (!fits(blocks, block)) {
           rc = fail(ZS_ERR_UNSUPPORTED, "zs_block_norm_forward: too many rows for one launch%s");
@@ -176,7 +215,7 @@ int zs_block_norm_forward(const void *x, const void *residual, const void *post_
 }
 
 uint64_t zs_block_norm_backward_workspace(uint64_t rows, uint64_t cols) {
-  return cols > kMaxNormCols ? 0 : (uint64_t)norm_parts(rows) * cols * 8;
+  return cols > kMaxNormCols ? 0 : (uint64_t)block_parts(rows, cols) * cols * 8;
 }
 
 int zs_block_norm_backward(const void *dy, const void *h, const float *rstd, const void *gain,
@@ -238,7 +277,7 @@ int zs_block_norm_backward(const void *dy, const void *h, const float *rstd, con
           return fail(ZS_ERR_ALIAS, "zs_block_norm_backward: two outputs overlap%s");
     }
   }
-  const uint32_t parts = norm_parts(rows);
+  const uint32_t parts = block_parts(rows, cols);
   a.dy = dy;
   a.h = h;
   a.gain = gain;
@@ -263,8 +302,8 @@ int zs_block_norm_backward(const void *dy, const void *h, const float *rstd, con
   if (rows) {
     with16(dtype, [&](auto dt) {
       with_bool(al, [&](auto v) {
-        with_norm_shape(padded_of(cols), [&](auto g, auto items) {
-          constexpr int G = decltype(g)::value, block = G < 256 ? 256 : G, per = block / G;
+        with_block_grad_shape(padded_of(cols), [&](auto g, auto items) {
+          constexpr int G = decltype(g)::value, block = G < 128 ? 256 : G, per = block / G;
           hipLaunchKernelGGL((block_grad_kernel<decltype(dt)::value, decltype(v)::value, G,
                                                 decltype(items)::value>),
                              dim3((parts + per - 1) / per), dim3(block), 0, s, a);

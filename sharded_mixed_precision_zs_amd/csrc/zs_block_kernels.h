@@ -23,6 +23,7 @@
 #ifndef ZS_BLOCK_KERNELS_H
 #define ZS_BLOCK_KERNELS_H
 
+#include "zs_logits.h"
 #include "zs_norm_rows.h"
 #include "zs_philox.h"
 
@@ -37,6 +38,7 @@ struct BlockArgs {
   uint32_t cols, padded;
   float eps;
   double inv_cols, residual_scale, branch_scale;
+  float near_dropped;   /* 0 where residual_scale times 16 bits is exact, else 2^-22 */
   DropArgs drop;
 };
 
@@ -51,12 +53,90 @@ __device__ __forceinline__ float odd_float(double v) {
   return __int_as_float(__builtin_amdgcn_classf(rest, kFiniteNotZero) ? odd : b);
 }
 
+/* Eight sums l r + c p rounded once to 16 bits. In fp32 a sum is off by at most
+ * kNear times |l r| + |sum|: c p by 2^-24 for c's rounding, and as much for p's
+ * in fp16, l r, the sum and its ends by 2^-24 each; or by nothing where p is 0
+ * and l r exact. Where both ends of that have the same 16 bits, those are the
+ * exact sum's. Where they differ, in some 2^-12 of bf16 sums and 2^-9 of fp16's,
+ * the two of a word are formed in binary64. (Short scales without a first norm
+ * make ties, and go that way more often.) */
+template <int DT>
+constexpr float kNear = DT == ZS_FP16 ? 0x1p-22f : 0x1.8p-23f;
+
+template <int DT>
+__device__ __forceinline__ u32x4 sums16(const float (&p)[8], const float (&low)[8],
+                                        const float (&r)[8], const float (&near)[8], double c,
+                                        double l, const RandomWords &words, uint32_t threshold) {
+  const float cf = (float)c, lf = (float)l;
+  /* a scale that is no number reaches what is kept alone */
+  const uint32_t always = fabsf(cf) < INFINITY ? 0 : 1;
+  u32x4 w;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    float up[2], down[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float lr = lf * r[j + k], sum = fmaf(cf, p[j + k], lr), size = fabsf(lr) + fabsf(sum);
+      up[k] = fmaf(size, near[j + k], sum);
+      down[k] = fmaf(size, -near[j + k], sum);
+    }
+    w[j / 2] = pack2<DT>(up[0], up[1]);
+    if ((w[j / 2] ^ pack2<DT>(down[0], down[1])) | always) {
+      float o[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const double lr = l * (double)r[j + k];   /* exact: 35 bits */
+        double whole = p[j + k];
+        if constexpr (DT == ZS_FP16) whole += (double)low[j + k];
+        const double sum = fma(c, whole, lr);
+        o[k] = odd_float(!threshold || kept(words, j + k, threshold) ? sum : lr);
+      }
+      w[j / 2] = pack2<DT>(o[0], o[1]);
+    }
+  }
+  return w;
+}
+
+/* Eight products hg (hi + lo), so that their 16 or 8 bits are the exact ones'.
+ * To nearest in fp32 does, but where that makes a tie of what is none (or a
+ * power of two, a block's scale): then its low 12 bits are 0, in one of 4096,
+ * and the eight are rounded to odd. */
+__device__ __forceinline__ void times8(const float (&hg)[8], const RowScale &s, float (&y)[8]) {
+  uint32_t low = ~0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    y[j] = fmaf(hg[j], s.hi, hg[j] * s.lo);
+    const uint32_t b = __float_as_uint(y[j]) & 0xfffu;
+    low = low < b ? low : b;
+  }
+  if (low == 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = times_odd(hg[j], s);
+  }
+}
+
+/* Sum over the G threads of a row's group, on all of them, in a fixed tree: by
+ * lane moves within 16 lanes, which cost no LDS. `part`: G / 64 values in LDS
+ * that nothing else uses before the next barrier. */
+template <int G, class T>
+__device__ __forceinline__ T row_sum(T v, T *part) {
+  v = wave_reduce(v, SumOf{}, 64);
+  if constexpr (G > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64 % (G / 64)] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < G / 64; ++w) v += part[w];
+  }
+  return v;
+}
+
 /* As norm_kernel: a row per group of G threads, ITEMS vectors of eight each.
- * The sum that becomes h is binary64 and rounded once, so that h is the 64-bit
- * result's own, and with it what the second norm and its codes see. */
+ * The sum that becomes h is rounded once, so that h is the 64-bit result's
+ * own, and with it what the second norm and its codes see. */
 template <int DT, bool AL, int G, int ITEMS>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void block_kernel(BlockArgs a) {
-  constexpr int kRows = G < 256 ? 256 / G : 1;
+__global__ __launch_bounds__(G < 128 ? 256 : G) void block_kernel(BlockArgs a) {
+  constexpr int kRows = G < 128 ? 256 / G : 1;
   __shared__ double part[2][G / 64];
   const uint32_t t = threadIdx.x % G;
   const uint64_t row = (uint64_t)blockIdx.x * kRows + threadIdx.x / G;
@@ -73,6 +153,13 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void block_kernel(BlockArgs a) {
     settle8<AL>(xr[i], (i * G + t) * 8, a.cols);
     settle8<AL>(rr[i], (i * G + t) * 8, a.cols);
   }
+  /* the vectors too, before anything waits: they come from the caches */
+  Raw16<8> gr[ITEMS], tr[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    if (a.post_gain) gr[i] = load8_raw<AL>(a.post_gain, (uint64_t)(i * G + t) * 8, a.cols);
+    if (a.gate) tr[i] = load8_raw<AL>(a.gate, (uint64_t)(i * G + t) * 8, a.cols);
+  }
   double scale = a.branch_scale;
   if (a.post_gain) {
     double ss = 0.0;
@@ -83,7 +170,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void block_kernel(BlockArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fma((double)e[j], (double)e[j], ss);
     }
-    const double r1 = row_scale64(group_sum<G>(ss, part[0]), a.inv_cols, a.eps);
+    const double r1 = row_scale64(row_sum<G>(ss, part[0]), a.inv_cols, a.eps);
     if (a.post_rstd && t == 0) a.post_rstd[row] = (float)r1;
     scale *= r1;
   }
@@ -94,50 +181,59 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void block_kernel(BlockArgs a) {
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const uint32_t v = i * G + t;
-    float e[8], r[8];
-    upcast<8, DT>(xr[i], e);
+    float p[8], low[8] = {}, r[8], g[8];
+    upcast<8, DT>(xr[i], p);
     upcast<8, DT>(rr[i], r);
-    float g1[8], gate[8];
     if (a.post_gain) {
-      load8<DT, AL>(a.post_gain, (uint64_t)v * 8, a.cols, g1);
+      upcast<8, DT>(gr[i], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] *= g1[j];   /* exact: 22 bits at most */
+      for (int j = 0; j < 8; ++j) p[j] *= g[j];   /* exact: 22 bits at most */
     }
-    double d[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) d[j] = e[j];
     if (a.gate) {
-      load8<DT, AL>(a.gate, (uint64_t)v * 8, a.cols, gate);
+      upcast<8, DT>(tr[i], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] *= (double)gate[j];   /* exact: 33 bits at most */
+      for (int j = 0; j < 8; ++j) {
+        const float q = p[j] * g[j];   /* exact in bf16, 33 bits in fp16 */
+        if constexpr (DT == ZS_FP16) low[j] = fmaf(p[j], g[j], -q);
+        p[j] = q;
+      }
     }
+    RandomWords words{};
+    float near[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double l = a.residual_scale * (double)r[j];   /* exact: 35 bits */
-      d[j] = fma(scale, d[j], l);
-    }
+    for (int j = 0; j < 8; ++j) near[j] = kNear<DT>;
     if (a.drop.threshold) {
-      const RandomWords w = random_words(a.drop, offset, v, (uint32_t)row);
+      words = random_words(a.drop, offset, v, (uint32_t)row);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        d[j] = kept(w, j, a.drop.threshold) ? d[j] : a.residual_scale * (double)r[j];
+      for (int j = 0; j < 8; ++j) {
+        const bool stays = kept(words, j, a.drop.threshold);
+        p[j] = stays ? p[j] : 0.0f;
+        near[j] = stays ? kNear<DT> : a.near_dropped;
+        if constexpr (DT == ZS_FP16) low[j] = stays ? low[j] : 0.0f;
+      }
+    }
+    u32x4 w = sums16<DT>(p, low, r, near, scale, a.residual_scale, words,
+                         a.drop.threshold);
+    if (!AL || v * 8 >= a.cols) {
+      /* past the row's end x and res are 0, and so is h, but 0 * inf is not */
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (v * 8 + 2 * j >= a.cols) w[j] = 0;
+        else if (v * 8 + 2 * j + 1 >= a.cols) w[j] &= 0xffffu;
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const uint32_t w = pack2<DT>(odd_float(d[j]), odd_float(d[j + 1]));
-      h[i][j] = up_lo<DT>(w);
-      h[i][j + 1] = up_hi<DT>(w);
+    for (int j = 0; j < 4; ++j) {
+      h[i][2 * j] = up_lo<DT>(w[j]);
+      h[i][2 * j + 1] = up_hi<DT>(w[j]);
     }
-    /* past the row's end x and res are 0, and so is h, but 0 * inf is not */
-    if (v * 8 + 8 > a.cols) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = v * 8 + j < a.cols ? h[i][j] : 0.0f;
-    }
-    store8<DT, AL, true>(a.h + row * a.cols, (uint64_t)v * 8, a.cols, h[i]);
+    store8_raw<AL, true>(a.h + row * a.cols, (uint64_t)v * 8, a.cols, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fma((double)h[i][j], (double)h[i][j], ss);
   }
-  ss = group_sum<G>(ss, part[1]);
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) gr[i] = load8_raw<AL>(a.gain, (uint64_t)(i * G + t) * 8, a.cols);
+  ss = row_sum<G>(ss, part[1]);
   const RowScale rstd = row_scale(ss, a.inv_cols, a.eps);
   if (a.rstd && t == 0) a.rstd[row] = rstd.hi;
 #pragma unroll
@@ -145,14 +241,14 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void block_kernel(BlockArgs a) {
     const uint32_t v = i * G + t;
     if (v * 8 >= a.padded) break;   /* whole quads: padded is a multiple of 128 */
     float g[8], y[8];
-    load8<DT, AL>(a.gain, (uint64_t)v * 8, a.cols, g);
+    upcast<8, DT>(gr[i], g);
     uint32_t top = 0;
     const RowScale s = v * 8 < a.cols ? rstd : RowScale{0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      y[j] = times_odd(h[i][j] * g[j], s);
-      top = umax(top, mag_bits(y[j]));
-    }
+    for (int j = 0; j < 8; ++j) g[j] *= h[i][j];
+    times8(g, s, y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = umax(top, mag_bits(y[j]));
     if (a.y) store8<DT, AL>(a.y + row * a.cols, (uint64_t)v * 8, a.cols, y);
     if (a.codes) {
       const uint32_t byte = mx_scale_byte<ZS_MX_E4M3>(quad_max(top));
@@ -175,38 +271,29 @@ struct BlockGradArgs {
   DropArgs drop;
 };
 
-template <int ITEMS>
-struct BlockGradRow {
-  Raw16<8> dy[ITEMS], h[ITEMS], dres[ITEMS], x[ITEMS];
-  float rstd, post_rstd;
-};
-
+/* A thread's vectors of a row. */
 template <bool AL, int G, int ITEMS>
-__device__ __forceinline__ void load_block_row(const BlockGradArgs &a, uint64_t row, uint32_t t,
-                                               BlockGradRow<ITEMS> &r) {
-  const uint64_t at = row * a.cols;
+__device__ __forceinline__ void load_grad(const void *m, uint64_t at, uint32_t t, uint32_t cols,
+                                          Raw16<8> (&r)[ITEMS]) {
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const uint32_t c = (i * G + t) * 8;
-    r.dy[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols);
-    r.h[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.h) + at, c, a.cols);
-    if (a.dres)
-      r.dres[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols);
-    if (a.x) r.x[i] = load8_ahead<AL>(static_cast<const uint16_t *>(a.x) + at, c, a.cols);
-  }
-  r.rstd = a.rstd[row];
-  r.post_rstd = a.post_rstd ? a.post_rstd[row] : 1.0f;
+  for (int i = 0; i < ITEMS; ++i)
+    r[i] = load8_ahead<AL>(static_cast<const uint16_t *>(m) + at, (i * G + t) * 8, cols);
 }
 
 /* As norm_grad_kernel: `parts` groups walk the rows and keep their shares of
  * both sums over rows in registers; block_gain_kernel adds the shares in
- * order. Two barriers a row, one for each of its two dot products. */
+ * order. Two barriers a row, one for each of its two dot products. What the
+ * first needs of the next row is fetched as soon as its registers are free,
+ * the rest while the row's own first sum is joined: in registers for no more
+ * than a row, two blocks share a CU's. */
 template <int DT, bool AL, int G, int ITEMS>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void block_grad_kernel(BlockGradArgs a) {
-  constexpr int kRows = G < 256 ? 256 / G : 1;
+__global__ __launch_bounds__(G < 128 ? 256 : G, 4) void block_grad_kernel(BlockGradArgs a) {
+  constexpr int kRows = G < 128 ? 256 / G : 1;   /* several only without barriers */
   __shared__ float sums[2][2][G / 64];
   const uint32_t t = threadIdx.x % G;
-  const uint32_t p = blockIdx.x * kRows + threadIdx.x / G;
+  /* the same for a whole wave: its rows' addresses are scalars */
+  const uint32_t p =
+      (uint32_t)__builtin_amdgcn_readfirstlane((int)(blockIdx.x * kRows + threadIdx.x / G));
   if (p >= a.parts) return;
   float dg[ITEMS][8], du[ITEMS][8], g[ITEMS][8], q[ITEMS][8];   /* q: g1 gate, exact */
 #pragma unroll
@@ -225,71 +312,78 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void block_grad_kernel(BlockGrad
   const uint64_t offset = a.drop.threshold ? drop_offset(a.drop) : 0;
   const float scale = a.drop.threshold ? a.branch_scale * a.drop.factor : a.branch_scale;
   const float inv_cols = 1.0f / (float)a.cols;
-  BlockGradRow<ITEMS> r, next;
-  load_block_row<AL, G>(a, p, t, r);
+  Raw16<8> rdy[ITEMS], rh[ITEMS], rdres[ITEMS], rx[ITEMS];
+  load_grad<AL, G>(a.dy, (uint64_t)p * a.cols, t, a.cols, rdy);
+  load_grad<AL, G>(a.h, (uint64_t)p * a.cols, t, a.cols, rh);
   int turn = 0;
   for (uint64_t row = p; row < a.rows; row += a.parts, turn ^= 1) {
-    const bool more = row + a.parts < a.rows;
-    if (more) load_block_row<AL, G>(a, row + a.parts, t, next);
+    const uint64_t at = row * a.cols;
+    if (a.dres) load_grad<AL, G>(a.dres, at, t, a.cols, rdres);
+    if (a.x) load_grad<AL, G>(a.x, at, t, a.cols, rx);
+    const float rstd = a.rstd[row], post_rstd = a.post_rstd ? a.post_rstd[row] : 1.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       float h[8], d[8];
-      settle8<AL>(r.dy[i], (i * G + t) * 8, a.cols);
-      settle8<AL>(r.h[i], (i * G + t) * 8, a.cols);
-      if (a.dres) settle8<AL>(r.dres[i], (i * G + t) * 8, a.cols);
-      if (a.x) settle8<AL>(r.x[i], (i * G + t) * 8, a.cols);
-      upcast<8, DT>(r.dy[i], d);
-      upcast<8, DT>(r.h[i], h);
+      settle8<AL>(rdy[i], (i * G + t) * 8, a.cols);
+      settle8<AL>(rh[i], (i * G + t) * 8, a.cols);
+      upcast<8, DT>(rdy[i], d);
+      upcast<8, DT>(rh[i], h);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dg[i][j] = fmaf(d[j], h[j] * r.rstd, dg[i][j]);
+        dg[i][j] = fmaf(d[j], h[j] * rstd, dg[i][j]);
         dot = fmaf(d[j] * g[i][j], h[j], dot);
       }
     }
-    const float s = group_sum<G>(dot, sums[turn][0]) * inv_cols * r.rstd * r.rstd;
+    const float s = row_sum<G>(dot, sums[turn][0]) * inv_cols * rstd * rstd;
     float dn[ITEMS][8];
     dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       float h[8], d[8], o[8] = {}, x[8] = {};
-      upcast<8, DT>(r.dy[i], d);
-      upcast<8, DT>(r.h[i], h);
-      if (a.dres) upcast<8, DT>(r.dres[i], o);
-      if (a.x) upcast<8, DT>(r.x[i], x);
+      asm volatile("" : "+v"(rdy[i].w[0]), "+v"(rh[i].w[0]));   /* unpacked anew, not kept */
+      if (a.dres) settle8<AL>(rdres[i], (i * G + t) * 8, a.cols);
+      if (a.x) settle8<AL>(rx[i], (i * G + t) * 8, a.cols);
+      upcast<8, DT>(rdy[i], d);
+      upcast<8, DT>(rh[i], h);
+      if (a.dres) upcast<8, DT>(rdres[i], o);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        o[j] = fmaf(r.rstd, fmaf(-h[j], s, d[j] * g[i][j]), o[j]);   /* dh */
+        o[j] = fmaf(rstd, fmaf(-h[j], s, d[j] * g[i][j]), o[j]);   /* dh */
         d[j] = o[j] * a.residual_scale;
         o[j] *= scale;
       }
-      store8<DT, AL, true>(a.dresidual + row * a.cols, (uint64_t)(i * G + t) * 8, a.cols, d);
+      store8<DT, AL, true>(a.dresidual + at, (uint64_t)(i * G + t) * 8, a.cols, d);
       if (a.drop.threshold) {
         const RandomWords w = random_words(a.drop, offset, i * G + t, (uint32_t)row);
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = kept(w, j, a.drop.threshold) ? o[j] : 0.0f;
       }
+      if (a.x) upcast<8, DT>(rx[i], x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        du[i][j] = fmaf(o[j], x[j] * r.post_rstd, du[i][j]);
+        du[i][j] = fmaf(o[j], x[j] * post_rstd, du[i][j]);
         dn[i][j] = o[j] * q[i][j];
         dot = fmaf(dn[i][j], x[j], dot);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (row + a.parts < a.rows) {
+      load_grad<AL, G>(a.dy, at + (uint64_t)a.parts * a.cols, t, a.cols, rdy);
+      load_grad<AL, G>(a.h, at + (uint64_t)a.parts * a.cols, t, a.cols, rh);
     }
     float s1 = 0.0f;
-    if (a.post_gain)
-      s1 = group_sum<G>(dot, sums[turn][1]) * inv_cols * r.post_rstd * r.post_rstd;
+    if (a.post_gain) s1 = row_sum<G>(dot, sums[turn][1]) * inv_cols * post_rstd * post_rstd;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       if (a.post_gain) {
         float x[8];
-        upcast<8, DT>(r.x[i], x);
+        upcast<8, DT>(rx[i], x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dn[i][j] = r.post_rstd * fmaf(-x[j], s1, dn[i][j]);
+        for (int j = 0; j < 8; ++j) dn[i][j] = post_rstd * fmaf(-x[j], s1, dn[i][j]);
       }
-      store8<DT, AL, true>(a.dx + row * a.cols, (uint64_t)(i * G + t) * 8, a.cols, dn[i]);
+      store8<DT, AL, true>(a.dx + at, (uint64_t)(i * G + t) * 8, a.cols, dn[i]);
     }
-    if (more) r = next;
   }
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i)

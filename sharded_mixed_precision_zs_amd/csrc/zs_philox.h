@@ -36,6 +36,11 @@ __device__ __forceinline__ uint64_t drop_offset(const DropArgs &d) {
   return d.offset + (d.dev_offset ? *d.dev_offset : 0);
 }
 
+/* a ^ b ^ c in one instruction */
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return (uint32_t)__builtin_amdgcn_bitop3_b32((int)a, (int)b, (int)c, 0x96);
+}
+
 __device__ __forceinline__ RandomWords random_words(const DropArgs &d, uint64_t offset,
                                                     uint32_t block, uint32_t row) {
   uint32_t c0 = block, c1 = row, c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
@@ -43,9 +48,9 @@ __device__ __forceinline__ RandomWords random_words(const DropArgs &d, uint64_t 
 #pragma unroll
   for (int i = 0; i < 7; ++i) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c0 = xor3((uint32_t)(b >> 32), c1, k0);
     c1 = (uint32_t)b;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c2 = xor3((uint32_t)(a >> 32), c3, k1);
     c3 = (uint32_t)a;
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
@@ -53,10 +58,11 @@ __device__ __forceinline__ RandomWords random_words(const DropArgs &d, uint64_t 
   return RandomWords{{c0, c1, c2, c3}};
 }
 
-/* Whether element j of the eight stays. */
+/* Whether element j of the eight stays, where something may be dropped: its
+ * bits are not below the threshold, compared as 16-bit numbers. */
 __device__ __forceinline__ bool kept(const RandomWords &r, int j, uint32_t threshold) {
   const uint32_t w = r.w[j / 2];
-  return (j & 1 ? w >> 16 : w & 0xffffu) >= threshold;
+  return (uint16_t)(j & 1 ? w >> 16 : w) > (uint16_t)(threshold - 1);
 }
 
 }  // namespace zs

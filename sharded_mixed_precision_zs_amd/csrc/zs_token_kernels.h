@@ -315,29 +315,36 @@ __global__ __launch_bounds__(NT) void token_stats_kernel(TokenArgs a) {
   }
 }
 
-/* Rows in parts: a thread per row joins them, by the largest of the logits
- * that their shifts are from. */
+/* All of a row's parts, 64 at most, by a wave: in order of a fixed tree, by the
+ * largest of the logits that their shifts are from. */
+constexpr uint32_t kMaxParts = 64;
+
+__device__ __forceinline__ TokenPart join_parts(const TokenArgs &a, uint32_t row) {
+  const uint32_t lane = threadIdx.x & 63;
+  TokenPart p{0.0, -INFINITY, 0.0f};
+  if (lane < a.parts) p = a.ws[(uint64_t)row * a.parts + lane];
+  const float from = wave_reduce(p.from, MaxOf{}, 64);
+  const double f = shift_factor(p.from, shift_of(p.from, a.log2_scale),
+                                shift_of(from, a.log2_scale));
+  return {wave_reduce(p.rest * f, SumOf{}, 64), from, 0.0f};
+}
+
+/* Rows in parts: a wave per row. */
 __global__ __launch_bounds__(64) void token_finish_kernel(TokenArgs a) {
-  const uint32_t row = blockIdx.x * 64 + threadIdx.x;
+  const uint32_t row = blockIdx.x;
   const TokenSpan span = token_span(a);
   if (row < span.first || row >= span.last) return;
-  const int32_t id = a.ids[row];
+  const int32_t id = load_scalar(a.ids, row);
   if (!token_live(a, row, id)) return;
-  const TokenPart *w = a.ws + (uint64_t)row * a.parts;
-  float from = -INFINITY;
-  for (uint32_t i = 0; i < a.parts; ++i) from = fmaxf(from, w[i].from);
-  const Shift to = shift_of(from, a.log2_scale);
-  double rest = 0.0;
-  for (uint32_t i = 0; i < a.parts; ++i)
-    rest += w[i].rest * shift_factor(w[i].from, shift_of(w[i].from, a.log2_scale), to);
-  finish_token(a, row, rest, from, a.own[row], id);
+  const TokenPart p = join_parts(a, row);
+  if (threadIdx.x == 0) finish_token(a, row, p.rest, p.from, a.own[row], id);
 }
 
 /* ------------------------------------------------------------------------
  * Pairs: a block per pair sums its sequences' log-probabilities, in binary64
  * and in a fixed order, forms the loss and gives every row its plan.
  * ---------------------------------------------------------------------- */
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 1024;
 
 struct PairSlope {
   double loss, slope;   /* slope: of the loss in the difference of log ratios */
@@ -427,14 +434,30 @@ __device__ __forceinline__ TokenPlan load_plan(const TokenPlan *p, uint32_t row)
           __float_as_int(load_scalar(f, 3))};
 }
 
-template <int DT, int NT>
+template <int DT, int NT, bool JOIN>
 __global__ __launch_bounds__(NT) void token_grad_kernel(TokenArgs a) {
   constexpr uint32_t ve = kVecElems<DT>, esz = DT == ZS_FP32 ? 4 : 2;
   const uint32_t row = a.row0 + blockIdx.x / a.blocks, block = blockIdx.x % a.blocks;
   const char *z = static_cast<const char *>(a.z) + (uint64_t)row * a.ld * esz;
   char *g = static_cast<char *>(a.grad) + (uint64_t)row * a.gld * esz;
   const RowShape sh = row_shape<DT>(z, a.vocab);
-  const TokenPlan p = load_plan(a.plan, row);
+  TokenPlan p;
+  if constexpr (JOIN) {   /* few rows, whose parts every block joins for itself */
+    const int32_t id = load_scalar(a.ids, row);
+    p = {0.0f, 0.0f, 0.0f, kNoToken};
+    if (token_live(a, row, id)) {
+      const TokenPart w = join_parts(a, row);
+      const TokenMass m = token_mass(w.rest, load_scalar(a.own, row), shift_of(w.from, a.log2_scale));
+      const Slope k = policy_slope(a, policy_in(a, row), m.logp);
+      p = make_plan(m.rest, m.total, w.from, k.slope * grad_scale(a), id);
+      if (block == 0 && threadIdx.x == 0) {
+        if (a.logp) a.logp[row] = (float)m.logp;
+        a.loss[row] = k.loss;
+      }
+    }
+  } else {
+    p = load_plan(a.plan, row);
+  }
   if (p.id == kOutside) return;
   const bool live = p.id >= 0;
   const Shift shift = shift_of(p.from, a.log2_scale);

@@ -19,10 +19,10 @@ namespace {
 using namespace zs;
 using namespace zs_ops;
 
-/* How a row's statistics are cut into parts: whole, a block for each row, up
- * to 256 KB; of longer rows, where there are too few to occupy the GPU, into
- * such parts. */
-constexpr uint32_t kPartVecs = 16384;
+/* How a row's statistics are cut into parts: whole, a block for each row, but
+ * where few rows would leave most of the CUs idle; then into parts of a vector
+ * or more for each of 256 threads, some 512 in all. */
+constexpr uint64_t kFewRows = 64;
 
 struct TokenSplit {
   uint32_t parts, part_vecs;
@@ -30,9 +30,9 @@ struct TokenSplit {
 
 TokenSplit token_split(uint64_t rows, uint64_t vocab, int dtype) {
   const uint64_t vecs = vocab * esize(dtype) / 16;
-  uint64_t parts = (vecs + kPartVecs - 1) / kPartVecs;
-  const uint64_t most = rows < 512 ? 512 / rows : 1;
-  if (parts > most) parts = most;
+  uint64_t parts = rows <= kFewRows ? 512 / rows : 1;
+  if (parts > kMaxParts) parts = kMaxParts;
+  if (parts > vecs / 256) parts = vecs / 256;
   if (parts < 1) parts = 1;
   const uint64_t each = vecs ? (vecs + parts - 1) / parts : 1;
   /* as many as have vectors; a row that is not aligned has one vector fewer,
@@ -83,14 +83,18 @@ int launch_stats(const TokenArgs &a, int dtype, hipStream_t s) {
                          dim3(a.rows * a.parts), dim3(decltype(nt)::value), 0, s, a);
     });
   });
-  if (int rc = launch_result()) return rc;
+  return launch_result();
+}
+
+/* Joins the parts of rows that have some, where no gradient kernel does. */
+int launch_finish(const TokenArgs &a, hipStream_t s) {
   if (a.parts == 1) return ZS_OK;
-  hipLaunchKernelGGL(token_finish_kernel, dim3((a.rows + 63) / 64), dim3(64), 0, s, a);
+  hipLaunchKernelGGL(token_finish_kernel, dim3(a.rows), dim3(64), 0, s, a);
   return launch_result();
 }
 
 /* Logits of more than 2^32 vectors take several launches. */
-int launch_grad(TokenArgs a, int dtype, hipStream_t s) {
+int launch_grad(TokenArgs a, int dtype, bool join, hipStream_t s) {
   const uint64_t vecs = (uint64_t)a.vocab * esize(dtype) / 16;
   int rc = ZS_OK;
   auto launch = [&](auto nt) {
@@ -100,8 +104,10 @@ int launch_grad(TokenArgs a, int dtype, hipStream_t s) {
     for (a.row0 = 0; a.row0 < a.rows && !rc; a.row0 += (uint32_t)most) {
       const uint64_t n = a.rows - a.row0 < most ? a.rows - a.row0 : most;
       with_any(dtype, [&](auto dt) {
-        hipLaunchKernelGGL((token_grad_kernel<decltype(dt)::value, NT>),
-                           dim3((unsigned)(n * a.blocks)), dim3(NT), 0, s, a);
+        with_bool(join, [&](auto j) {
+          hipLaunchKernelGGL((token_grad_kernel<decltype(dt)::value, NT, decltype(j)::value>),
+                             dim3((unsigned)(n * a.blocks)), dim3(NT), 0, s, a);
+        });
       });
       rc = launch_result();
       if (n < most) break;   /* the row's number could wrap */
@@ -212,7 +218,8 @@ int zs_logprob(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   token_args(a, logits, dtype, rows, vocab, ld, ids, temperature, workspace);
   a.logp = logp;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return launch_stats(a, dtype, s);
+  if (int rc = launch_stats(a, dtype, s)) return rc;
+  return launch_finish(a, s);
 }
 
 uint64_t zs_policy_workspace(uint64_t rows, uint64_t vocab, int dtype) {
@@ -271,9 +278,10 @@ int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint
   a.grad = grad;
   a.gld = grad_ld;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (policy_in_rows(a, dtype)) return launch_policy(a, dtype, s);
+  if (a.parts == 1 && policy_in_rows(a, dtype)) return launch_policy(a, dtype, s);
   if (int rc = launch_stats(a, dtype, s)) return rc;
-  return grad ? launch_grad(a, dtype, s) : ZS_OK;
+  if (grad) return launch_grad(a, dtype, a.parts > 1, s);
+  return launch_finish(a, s);
 }
 
 uint64_t zs_preference_workspace(uint64_t rows, uint64_t vocab, int dtype) {
@@ -297,7 +305,7 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
                 "zs_preference: smoothing must lie in [0, 1], and be 0 but for the sigmoid%s");
   if (!dev && (!(loss_scale > 0.0f) || !isfinite(loss_scale)))
     return fail(ZS_ERR_INVALID_ARG, "zs_preference: loss_scale must be finite and > 0%s");
-  if (pairs >> 24) return fail(ZS_ERR_UNSUPPORTED, "zs_preference: 2^24 pairs or more%s");
+  if (pairs >> 22) return fail(ZS_ERR_UNSUPPORTED, "zs_preference: 2^22 pairs or more%s");
   if (pairs == 0 && !(clear && grad && rows)) return ZS_OK;
   if (!starts || (pairs && !loss) || (rows && (!logits || !ids)))
     return fail(ZS_ERR_INVALID_ARG, "zs_preference: null pointer%s");
@@ -346,12 +354,13 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (rows && (pairs || clear)) {
     if (int rc = launch_stats(a, dtype, s)) return rc;
+    if (int rc = launch_finish(a, s)) return rc;
   }
   if (pairs) {
     hipLaunchKernelGGL(token_pair_kernel, dim3(a.pairs), dim3(kPairThreads), 0, s, a);
     if (int rc = launch_result()) return rc;
   }
-  return rows && grad ? launch_grad(a, dtype, s) : ZS_OK;
+  return rows && grad ? launch_grad(a, dtype, false, s) : ZS_OK;
 }
 
 }  /* extern "C" */

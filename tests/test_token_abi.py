@@ -75,7 +75,7 @@ BAD = [(name, *c) for name in ("logprob", "policy", "preference") for c in COMMO
     ("preference", dict(beta=0.0), INVALID), ("preference", dict(beta=math.nan), INVALID),
     ("preference", dict(smooth=1.5), INVALID), ("preference", dict(smooth=0.1, kind=1), INVALID),
     ("preference", dict(smooth=math.nan), INVALID), ("preference", dict(scale=-1.0), INVALID),
-    ("preference", dict(gld=99), INVALID), ("preference", dict(pairs=1 << 24), UNSUPPORTED),
+    ("preference", dict(gld=99), INVALID), ("preference", dict(pairs=1 << 22), UNSUPPORTED),
     ("preference", dict(starts=far(2, 2)), UNSUPPORTED), ("preference", dict(ref=far(3, 2)), UNSUPPORTED),
     ("preference", dict(weight=far(4, 1)), UNSUPPORTED), ("preference", dict(seq=far(5, 2)), UNSUPPORTED),
     ("preference", dict(loss=far(6, 2)), UNSUPPORTED), ("preference", dict(grad=far(7, 1)), UNSUPPORTED),
