@@ -287,7 +287,7 @@ __device__ __forceinline__ void load_grad(const void *m, uint64_t at, uint32_t t
  * the rest while the row's own first sum is joined: in registers for no more
  * than a row, two blocks share a CU's. */
 template <int DT, bool AL, int G, int ITEMS>
-__global__ __launch_bounds__(G < 128 ? 256 : G, 4) void block_grad_kernel(BlockGradArgs a) {
+__global__ __launch_bounds__(G < 128 ? 256 : G, G == 512 && ITEMS > 1 ? 2 : 4) void block_grad_kernel(BlockGradArgs a) {
   constexpr int kRows = G < 128 ? 256 / G : 1;   /* several only without barriers */
   __shared__ float sums[2][2][G / 64];
   const uint32_t t = threadIdx.x % G;
@@ -295,20 +295,35 @@ __global__ __launch_bounds__(G < 128 ? 256 : G, 4) void block_grad_kernel(BlockG
   const uint32_t p =
       (uint32_t)__builtin_amdgcn_readfirstlane((int)(blockIdx.x * kRows + threadIdx.x / G));
   if (p >= a.parts) return;
-  float dg[ITEMS][8], du[ITEMS][8], g[ITEMS][8], q[ITEMS][8];   /* q: g1 gate, exact */
+  /* both sums' shares: in registers, or where a block of 1024 threads has two
+   * vectors each, in LDS, a word of its own for each of a thread's */
+  constexpr bool kInLds = G == 1024 && ITEMS == 2;
+  __shared__ float acc[kInLds ? ITEMS * 16 * G : 1];
+  float shares[kInLds ? 1 : ITEMS][2][8];
+  auto share = [&](int i, int which, int j) -> float & {
+    if constexpr (kInLds) return acc[((i * 2 + which) * 8 + j) * G + t];
+    else return shares[i][which][j];
+  };
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    load8<DT, AL>(a.gain, (uint64_t)(i * G + t) * 8, a.cols, g[i]);
+  for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dg[i][j] = du[i][j] = 0.0f, q[i][j] = 1.0f;
-    if (a.post_gain) load8<DT, AL>(a.post_gain, (uint64_t)(i * G + t) * 8, a.cols, q[i]);
+    for (int j = 0; j < 8; ++j) share(i, 0, j) = share(i, 1, j) = 0.0f;
+  /* gain, and g1 gate (exact): held where a thread has one vector, else from
+   * the caches for every row */
+  float g0[8], q0[8];
+  auto vectors = [&](int i, float (&g)[8], float (&q)[8]) {
+    load8<DT, AL>(a.gain, (uint64_t)(i * G + t) * 8, a.cols, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = 1.0f;
+    if (a.post_gain) load8<DT, AL>(a.post_gain, (uint64_t)(i * G + t) * 8, a.cols, q);
     if (a.gate) {
       float gate[8];
       load8<DT, AL>(a.gate, (uint64_t)(i * G + t) * 8, a.cols, gate);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[i][j] *= gate[j];
+      for (int j = 0; j < 8; ++j) q[j] *= gate[j];
     }
-  }
+  };
+  vectors(0, g0, q0);
   const uint64_t offset = a.drop.threshold ? drop_offset(a.drop) : 0;
   const float scale = a.drop.threshold ? a.branch_scale * a.drop.factor : a.branch_scale;
   const float inv_cols = 1.0f / (float)a.cols;
@@ -329,10 +344,11 @@ __global__ __launch_bounds__(G < 128 ? 256 : G, 4) void block_grad_kernel(BlockG
       settle8<AL>(rh[i], (i * G + t) * 8, a.cols);
       upcast<8, DT>(rdy[i], d);
       upcast<8, DT>(rh[i], h);
+      if constexpr (ITEMS > 1) load8<DT, AL>(a.gain, (uint64_t)(i * G + t) * 8, a.cols, g0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dg[i][j] = fmaf(d[j], h[j] * rstd, dg[i][j]);
-        dot = fmaf(d[j] * g[i][j], h[j], dot);
+        share(i, 0, j) = fmaf(d[j], h[j] * rstd, share(i, 0, j));
+        dot = fmaf(d[j] * g0[j], h[j], dot);
       }
     }
     const float s = row_sum<G>(dot, sums[turn][0]) * inv_cols * rstd * rstd;
@@ -347,9 +363,10 @@ __global__ __launch_bounds__(G < 128 ? 256 : G, 4) void block_grad_kernel(BlockG
       upcast<8, DT>(rdy[i], d);
       upcast<8, DT>(rh[i], h);
       if (a.dres) upcast<8, DT>(rdres[i], o);
+      if constexpr (ITEMS > 1) vectors(i, g0, q0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        o[j] = fmaf(rstd, fmaf(-h[j], s, d[j] * g[i][j]), o[j]);   /* dh */
+        o[j] = fmaf(rstd, fmaf(-h[j], s, d[j] * g0[j]), o[j]);   /* dh */
         d[j] = o[j] * a.residual_scale;
         o[j] *= scale;
       }
@@ -362,8 +379,8 @@ __global__ __launch_bounds__(G < 128 ? 256 : G, 4) void block_grad_kernel(BlockG
       if (a.x) upcast<8, DT>(rx[i], x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        du[i][j] = fmaf(o[j], x[j] * post_rstd, du[i][j]);
-        dn[i][j] = o[j] * q[i][j];
+        share(i, 1, j) = fmaf(o[j], x[j] * post_rstd, share(i, 1, j));
+        dn[i][j] = o[j] * q0[j];
         dot = fmaf(dn[i][j], x[j], dot);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -391,8 +408,8 @@ __global__ __launch_bounds__(G < 128 ? 256 : G, 4) void block_grad_kernel(BlockG
     for (int j = 0; j < 8; ++j) {
       const uint32_t c = (i * G + t) * 8 + j;
       if (c < a.cols) {
-        a.part[(uint64_t)p * 2 * a.cols + c] = dg[i][j];
-        if (a.x) a.part[((uint64_t)p * 2 + 1) * a.cols + c] = du[i][j];
+        a.part[(uint64_t)p * 2 * a.cols + c] = share(i, 0, j);
+        if (a.x) a.part[((uint64_t)p * 2 + 1) * a.cols + c] = share(i, 1, j);
       }
     }
 }
