@@ -82,21 +82,26 @@ struct Epilogue {
     }
   }
 
-  /* Eight neighbouring sums of a row, their bias given, to memory. */
+  /* Eight neighbouring sums of a row, their bias and residual given, to memory. */
   template <int CDT>
   __device__ __forceinline__ void store(uint64_t row, uint32_t col, uint32_t n, float (&x)[8],
-                                        const float (&b)[8], uint16_t *c, uint64_t ldc) const {
+                                        const float (&b)[8], const Raw16<8> &residual, uint16_t *c,
+                                        uint64_t ldc) const {
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] += b[j];
     if (pre) store8<CDT, false>(pre + row * n, col, n, x);
     apply(x);
     if (res) {
       float r[8];
-      load8<CDT, false>(static_cast<const uint16_t *>(res) + row * ldr, col, n, r);
+      upcast<8, CDT>(residual, r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] += r[j];
     }
     store8<CDT, false>(c + row * ldc, col, n, x);
+  }
+
+  __device__ __forceinline__ Raw16<8> load(uint64_t row, uint32_t col, uint32_t n) const {
+    return load8_raw<false>(static_cast<const uint16_t *>(res) + row * ldr, col, n);
   }
 
   /* One sum. */
@@ -112,58 +117,6 @@ struct Epilogue {
     c[row * ldc + col] = pack1<CDT>(v[0]);
   }
 };
-
-/* ------------------------------------------------------------------------
- * The gradient of bias and activation: dpre = dc act'(pre), and dpre's sum
- * over the rows. A block is kAcross vectors of eight columns by kDown rows at
- * a time, and walks a share of the rows; a thread keeps its columns' sums,
- * unrounded, in registers, and the shares are joined in order. Bound by HBM.
- * ---------------------------------------------------------------------- */
-struct ActGradArgs {
-  const void *dc, *pre;   /* pre optional: no activation */
-  uint16_t *dpre;         /* optional */
-  float *part;            /* [parts][cols], optional */
-  uint64_t rows;
-  uint32_t cols, parts;
-};
-
-template <int DT, bool AL, int ACT, int ACROSS>
-__global__ __launch_bounds__(kBlock) void act_grad_kernel(ActGradArgs a) {
-  constexpr uint32_t kDown = kBlock / ACROSS;
-  const uint32_t v = blockIdx.x * ACROSS + threadIdx.x % ACROSS;
-  const uint32_t p = blockIdx.y * kDown + threadIdx.x / ACROSS;
-  const uint64_t col = (uint64_t)v * 8;
-  if (p >= a.parts || col >= a.cols) return;
-  const uint16_t *dc = static_cast<const uint16_t *>(a.dc);
-  const uint16_t *pre = static_cast<const uint16_t *>(a.pre);
-  float sum[8] = {};
-  Raw16<8> d = load8_raw<AL, true>(dc + (uint64_t)p * a.cols, col, a.cols), s = {};
-  if constexpr (ACT != ZS_ACT_NONE) s = load8_raw<AL, true>(pre + (uint64_t)p * a.cols, col, a.cols);
-  for (uint64_t row = p; row < a.rows; row += a.parts) {
-    const uint64_t next = row + a.parts;
-    Raw16<8> d1 = {}, s1 = {};
-    if (next < a.rows) {
-      d1 = load8_raw<AL, true>(dc + next * a.cols, col, a.cols);
-      if constexpr (ACT != ZS_ACT_NONE) s1 = load8_raw<AL, true>(pre + next * a.cols, col, a.cols);
-    }
-    float x[8], y[8];
-    upcast<8, DT>(d, x);
-    if constexpr (ACT != ZS_ACT_NONE) {
-      upcast<8, DT>(s, y);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= slope_of<ACT>(y[j]);
-    }
-    if (a.dpre) store8<DT, AL>(a.dpre + row * a.cols, col, a.cols, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += x[j];
-    d = d1;
-    s = s1;
-  }
-  if (!a.part) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (col + j < a.cols) a.part[(uint64_t)p * a.cols + col + j] = sum[j];
-}
 
 }  // namespace zs
 #endif  // ZS_EPILOGUE_H

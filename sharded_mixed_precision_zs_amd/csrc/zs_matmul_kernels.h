@@ -467,8 +467,26 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs
     ldc = p.n;
   }
   const bool vec = ((uintptr_t)c & 15) == 0 && ldc * kEsz % 16 == 0;
+  /* An epilogue's lane: eight columns of every kRows-th row; its residual's
+   * vectors of a strip are on their way while the strip is turned. */
+  constexpr uint32_t kAhead = FN * 4, kRows = 64 / kAhead, kStrips = 32 / kRows;
+  const uint32_t pc = lane % kAhead, col = n0 + tn + pc * 8;
+  float bias[8] = {};
+  if constexpr (E::kOn) {
+    if (epilogue.bias) load8<CDT, false>(epilogue.bias, col, p.n, bias);
+  }
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
+    Raw16<8> residual[kStrips];
+    if constexpr (E::kOn) {
+      if (epilogue.res) {
+#pragma unroll
+        for (uint32_t k = 0; k < kStrips; ++k) {
+          const uint32_t row = m0 + tm + i * 32 + k * kRows + lane / kAhead;
+          residual[k] = epilogue.load(row < p.m ? row : p.m - 1, col, p.n);
+        }
+      }
+    }
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -481,12 +499,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs
     __builtin_amdgcn_wave_barrier();
     const uint32_t col0 = n0 + tn;
     if constexpr (E::kOn) {
-      constexpr uint32_t kAhead = FN * 4, kRows = 64 / kAhead;   /* lanes to a row, rows at once */
-      const uint32_t pc = lane % kAhead, col = col0 + pc * 8;
-      float bias[8] = {};
-      if (epilogue.bias) load8<CDT, false>(epilogue.bias, col, p.n, bias);
 #pragma unroll
-      for (uint32_t k = 0; k < 32 / kRows; ++k) {
+      for (uint32_t k = 0; k < kStrips; ++k) {
         const uint32_t lr = k * kRows + lane / kAhead, row = m0 + tm + i * 32 + lr;
         float v[8];
 #pragma unroll
@@ -499,7 +513,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void matmul_tile_kernel(MatmulArgs
           v[4 * h + 3] = w.w;
         }
         if (row < p.m)
-          epilogue.template store<CDT>(row, col, p.n, v, bias, static_cast<uint16_t *>(p.c), p.ldc);
+          epilogue.template store<CDT>(row, col, p.n, v, bias, residual[k],
+                                       static_cast<uint16_t *>(p.c), p.ldc);
       }
       __builtin_amdgcn_wave_barrier();
       continue;
