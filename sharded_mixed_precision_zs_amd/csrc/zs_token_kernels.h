@@ -208,7 +208,6 @@ __device__ __forceinline__ TokenPlan make_plan(double rest, double total, float 
  * time. A thread's sums of U vectors are fp32, what they are added to
  * binary64.
  * ---------------------------------------------------------------------- */
-constexpr int kTokenAhead = 4;
 constexpr float kTokenTop = 1.15292150e18f;   /* 2^60 */
 
 template <int DT>
@@ -248,7 +247,7 @@ __device__ __forceinline__ void dead_token(const TokenArgs &a, uint32_t row) {
 template <int DT, int NT>
 __global__ __launch_bounds__(NT) void token_stats_kernel(TokenArgs a) {
   constexpr uint32_t ve = kVecElems<DT>, esz = DT == ZS_FP32 ? 4 : 2;
-  constexpr int U = kTokenAhead;
+  constexpr int U = 4;
   __shared__ float fpart[NT / 64];
   __shared__ double dpart[2][NT / 64];
   const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x;
@@ -329,17 +328,6 @@ __device__ __forceinline__ TokenPart join_parts(const TokenArgs &a, uint32_t row
   return {wave_reduce(p.rest * f, SumOf{}, 64), from, 0.0f};
 }
 
-/* Rows in parts: a wave per row. */
-__global__ __launch_bounds__(64) void token_finish_kernel(TokenArgs a) {
-  const uint32_t row = blockIdx.x;
-  const TokenSpan span = token_span(a);
-  if (row < span.first || row >= span.last) return;
-  const int32_t id = load_scalar(a.ids, row);
-  if (!token_live(a, row, id)) return;
-  const TokenPart p = join_parts(a, row);
-  if (threadIdx.x == 0) finish_token(a, row, p.rest, p.from, a.own[row], id);
-}
-
 /* ------------------------------------------------------------------------
  * Pairs: a block per pair sums its sequences' log-probabilities, in binary64
  * and in a fixed order, forms the loss and gives every row its plan.
@@ -374,7 +362,8 @@ __global__ __launch_bounds__(kPairThreads) void token_pair_kernel(TokenArgs a) {
   TokenSpan seq[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    seq[k] = {row_of(a.starts[2 * pair + k], a.rows), row_of(a.starts[2 * pair + k + 1], a.rows)};
+    seq[k] = {row_of(load_scalar(a.starts, 2 * pair + k), a.rows),
+              row_of(load_scalar(a.starts, 2 * pair + k + 1), a.rows)};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     for (uint64_t row = (uint64_t)seq[k].first + threadIdx.x; row < seq[k].last; row += NT) {
@@ -544,6 +533,38 @@ __device__ __forceinline__ void token_singles(const TokenArgs &a, const TokenIn 
   if (r.edge < a.vocab && r.edge != (uint32_t)r.id) single = load_raw<DT>(r.z, r.edge);
 }
 
+/* Where a row's token lies among a block's vectors: the same for all threads,
+ * so that one item of one thread is looked at, and not each for every element. */
+struct TokenPlace {
+  uint32_t item, thread, elem;   /* item: none of them if the token is a single element */
+};
+
+template <int DT, int NT>
+__device__ __forceinline__ TokenPlace token_place(const TokenIn &r) {
+  constexpr uint32_t ve = kVecElems<DT>;
+  const uint32_t at = (uint32_t)r.id - r.shape.head, v = at / ve;   /* wraps for the head's */
+  return {at < r.shape.vecs * ve ? v / NT : ~0u, v % NT, at % ve};
+}
+
+/* Element j of a vector in memory's form; j is the same for all threads. */
+template <int DT>
+__device__ __forceinline__ void set_element(u32x4 &x, uint32_t j, uint32_t bits) {
+  if constexpr (DT == ZS_FP32) {
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) x[k] = j == k ? bits : x[k];
+  } else {
+    const uint32_t keep = j & 1 ? 0xffffu : 0xffff0000u, put = j & 1 ? bits << 16 : bits & 0xffffu;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) x[k] = j / 2 == k ? (x[k] & keep) | put : x[k];
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t raw_bits(float x) {
+  if constexpr (DT == ZS_FP32) return __float_as_uint(x);
+  else return pack1<DT>(x);
+}
+
 template <int DT, int NT, int ITEMS>
 __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(TokenArgs a) {
   constexpr uint32_t ve = kVecElems<DT>, esz = DT == ZS_FP32 ? 4 : 2;
@@ -569,12 +590,18 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
     const bool more = next < a.rows;
     const TokenIn after = open_token<DT>(a, more ? next : row);
     TokenPlan plan{0.0f, 0.0f, 0.0f, kNoToken};
+    const TokenPlace place = token_place<DT, NT>(in);
     float single = -INFINITY;
     if (in.live) {   /* uniform over the block */
       const float own = raw_value<DT>(raw_own);
       single = raw_value<DT>(raw_single);
       float from = own;
       double rest;
+      /* the token's own term is left out of the sum, and its gradient put in below */
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i)
+        if (place.item == (uint32_t)i && t == place.thread)
+          set_element<DT>(x[i], place.elem, empty_vec<DT>()[0]);
       for (bool again = false;; again = true) {
         const Shift s = shift_of(from, a.log2_scale);
         float sum = term(single, s);
@@ -583,7 +610,6 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
           float e[ve];
           asm volatile("" : "+v"(x[i]));   /* unpacked anew each time */
           unpack_vec<DT>(x[i], e);
-          leave_out<DT>(in.shape, in.id, i * NT + t, e);
           float some = 0.0f;
 #pragma unroll
           for (uint32_t j = 0; j < ve; ++j) some += term(e[j], s);
@@ -636,12 +662,10 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
       unpack_vec<DT>(x[i], e);
 #pragma unroll
       for (uint32_t j = 0; j < ve; ++j) e[j] = term(e[j], shift) * plan.factor;
-      const uint32_t at = (uint32_t)plan.id - in.shape.head - (i * NT + t) * ve;
-      if (plan.id >= 0 && at < ve) {
-#pragma unroll
-        for (uint32_t j = 0; j < ve; ++j) e[j] = at == j ? plan.own : e[j];
-      }
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, pack_vec<DT>(e)), to,
+      u32x4 w = pack_vec<DT>(e);
+      if (place.item == (uint32_t)i && t == place.thread)
+        set_element<DT>(w, place.elem, raw_bits<DT>(plan.own));
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), to,
                                              (int)(t * 16 + i * (NT * 16)), 0, kTokenStore);
       x[i] = token_vec(from_next, after, i * (NT * 16));   /* past the last row: not used */
       __builtin_amdgcn_sched_barrier(0);

@@ -20,17 +20,19 @@ using namespace zs;
 using namespace zs_ops;
 
 /* How a row's statistics are cut into parts: whole, a block for each row, but
- * where few rows would leave most of the CUs idle; then into parts of a vector
- * or more for each of 256 threads, some 512 in all. */
-constexpr uint64_t kFewRows = 64;
+ * for the policy's gradient of few long rows, which would leave most of the CUs
+ * idle; then into parts of a vector or more for each of 256 threads, some 512
+ * in all, which every block of the gradient joins for itself (13 x 50257 bf16
+ * 8.4 us, a block for each row 12; but 13 x 4096 6.4 and 4.8). */
+constexpr uint64_t kFewRows = 64, kLongRow = 2048;
 
 struct TokenSplit {
   uint32_t parts, part_vecs;
 };
 
-TokenSplit token_split(uint64_t rows, uint64_t vocab, int dtype) {
+TokenSplit token_split(uint64_t rows, uint64_t vocab, int dtype, bool cut) {
   const uint64_t vecs = vocab * esize(dtype) / 16;
-  uint64_t parts = rows <= kFewRows ? 512 / rows : 1;
+  uint64_t parts = cut && rows <= kFewRows && vecs >= kLongRow ? 512 / rows : 1;
   if (parts > kMaxParts) parts = kMaxParts;
   if (parts > vecs / 256) parts = vecs / 256;
   if (parts < 1) parts = 1;
@@ -41,23 +43,25 @@ TokenSplit token_split(uint64_t rows, uint64_t vocab, int dtype) {
   return {(uint32_t)parts, (uint32_t)each};
 }
 
-uint64_t token_workspace(uint64_t rows, uint64_t vocab, int dtype, bool pairs) {
+/* `cut`: with room for parts; `pairs`: for pairs' log-probabilities. */
+uint64_t token_workspace(uint64_t rows, uint64_t vocab, int dtype, bool cut, bool pairs) {
   if (rows == 0 || rows >> 31 || vocab == 0 || vocab > kMaxVocab || !valid_any(dtype) ||
       matrix_too_big(rows, vocab))
     return 0;
-  return rows * (token_split(rows, vocab, dtype).parts * sizeof(TokenPart) + sizeof(TokenPlan) +
-                 sizeof(float) + (pairs ? sizeof(double) : 0));
+  return rows * (token_split(rows, vocab, dtype, cut).parts * sizeof(TokenPart) +
+                 sizeof(TokenPlan) + sizeof(float) + (pairs ? sizeof(double) : 0));
 }
 
 /* What the three entry points put into `a` alike. */
 void token_args(TokenArgs &a, const void *logits, int dtype, uint64_t rows, uint64_t vocab,
-                uint64_t ld, const int32_t *ids, float temperature, void *workspace) {
+                uint64_t ld, const int32_t *ids, float temperature, bool cut,
+                void *workspace) {
   a.z = logits;
   a.ids = ids;
   a.ld = ld;
   a.rows = (uint32_t)rows;
   a.vocab = (uint32_t)vocab;
-  const TokenSplit sp = token_split(rows, vocab, dtype);
+  const TokenSplit sp = token_split(rows, vocab, dtype, cut);
   a.parts = sp.parts;
   a.part_vecs = sp.part_vecs;
   a.log2_scale = (float)(1.4426950408889634 / temperature);
@@ -83,13 +87,6 @@ int launch_stats(const TokenArgs &a, int dtype, hipStream_t s) {
                          dim3(a.rows * a.parts), dim3(decltype(nt)::value), 0, s, a);
     });
   });
-  return launch_result();
-}
-
-/* Joins the parts of rows that have some, where no gradient kernel does. */
-int launch_finish(const TokenArgs &a, hipStream_t s) {
-  if (a.parts == 1) return ZS_OK;
-  hipLaunchKernelGGL(token_finish_kernel, dim3(a.rows), dim3(64), 0, s, a);
   return launch_result();
 }
 
@@ -129,8 +126,12 @@ void launch_policy_rows(const TokenArgs &a, hipStream_t s) {
                      dim3((unsigned)(a.rows < fit ? a.rows : fit)), dim3(NT), 0, s, a);
 }
 
+/* Whether they do. Not where a row takes a CU to itself and there are fewer
+ * rows than CUs: two passes over all CUs are faster then (65 x 128000 bf16 18
+ * us, 21 in rows; 256 rows 33 and 38). */
 bool policy_in_rows(const TokenArgs &a, int dtype) {
   const uint64_t vecs = (uint64_t)a.vocab * esize(dtype) / 16;
+  if (vecs > 8192 && a.rows <= 256) return false;
   /* two vectors' worth of elements hold one, whatever the row's alignment */
   return a.grad && vecs >= 2 && vecs <= 512 * kPolicyItems &&
          (((uintptr_t)a.grad ^ (uintptr_t)a.z) & 15) == 0 &&
@@ -188,7 +189,7 @@ int alias_check(const void *const *outs, const uint64_t *out_bytes, int n_outs,
 extern "C" {
 
 uint64_t zs_logprob_workspace(uint64_t rows, uint64_t vocab, int dtype) {
-  return token_workspace(rows, vocab, dtype, false);
+  return token_workspace(rows, vocab, dtype, false, false);
 }
 
 int zs_logprob(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
@@ -199,9 +200,9 @@ int zs_logprob(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
   ZS_TOKEN_CHECKS("zs_logprob");
   if (rows == 0) return ZS_OK;
   if (!logits || !ids || !logp) return fail(ZS_ERR_INVALID_ARG, "zs_logprob: null pointer%s");
-  if (!token_launch_fits(rows, token_split(rows, vocab, dtype)))
+  if (!token_launch_fits(rows, token_split(rows, vocab, dtype, false)))
     return fail(ZS_ERR_UNSUPPORTED, "zs_logprob: too many rows%s");
-  const uint64_t esz = esize(dtype), need = token_workspace(rows, vocab, dtype, false);
+  const uint64_t esz = esize(dtype), need = zs_logprob_workspace(rows, vocab, dtype);
   if (!workspace || workspace_bytes < need)
     return fail(ZS_ERR_INVALID_ARG, "zs_logprob: workspace too small%s");
   if (!aligned(logits, esz) || !aligned(ids, 4) || !aligned(logp, 4) || !aligned(workspace, 16))
@@ -215,15 +216,14 @@ int zs_logprob(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
                            "zs_logprob: two outputs overlap%s"))
     return rc;
   TokenArgs a{};
-  token_args(a, logits, dtype, rows, vocab, ld, ids, temperature, workspace);
+  token_args(a, logits, dtype, rows, vocab, ld, ids, temperature, false, workspace);
   a.logp = logp;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (int rc = launch_stats(a, dtype, s)) return rc;
-  return launch_finish(a, s);
+  return launch_stats(a, dtype, s);
 }
 
 uint64_t zs_policy_workspace(uint64_t rows, uint64_t vocab, int dtype) {
-  return token_workspace(rows, vocab, dtype, false);
+  return token_workspace(rows, vocab, dtype, true, false);
 }
 
 int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
@@ -242,9 +242,9 @@ int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint
   if (rows == 0) return ZS_OK;
   if (!logits || !ids || !advantage || !loss)
     return fail(ZS_ERR_INVALID_ARG, "zs_policy: null pointer%s");
-  if (!token_launch_fits(rows, token_split(rows, vocab, dtype)))
+  if (!token_launch_fits(rows, token_split(rows, vocab, dtype, true)))
     return fail(ZS_ERR_UNSUPPORTED, "zs_policy: too many rows%s");
-  const uint64_t esz = esize(dtype), need = token_workspace(rows, vocab, dtype, false);
+  const uint64_t esz = esize(dtype), need = zs_policy_workspace(rows, vocab, dtype);
   if (!workspace || workspace_bytes < need)
     return fail(ZS_ERR_INVALID_ARG, "zs_policy: workspace too small%s");
   if (!aligned(logits, esz) || !aligned(ids, 4) || !aligned(advantage, 4) ||
@@ -263,7 +263,7 @@ int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint
                            "zs_policy: two outputs overlap%s"))
     return rc;
   TokenArgs a{};
-  token_args(a, logits, dtype, rows, vocab, ld, ids, temperature, workspace);
+  token_args(a, logits, dtype, rows, vocab, ld, ids, temperature, grad != nullptr, workspace);
   a.weight = row_weight;
   a.dev = dev;
   a.advantage = advantage;
@@ -280,12 +280,11 @@ int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (a.parts == 1 && policy_in_rows(a, dtype)) return launch_policy(a, dtype, s);
   if (int rc = launch_stats(a, dtype, s)) return rc;
-  if (grad) return launch_grad(a, dtype, a.parts > 1, s);
-  return launch_finish(a, s);
+  return grad ? launch_grad(a, dtype, a.parts > 1, s) : ZS_OK;
 }
 
 uint64_t zs_preference_workspace(uint64_t rows, uint64_t vocab, int dtype) {
-  return token_workspace(rows, vocab, dtype, true);
+  return token_workspace(rows, vocab, dtype, false, true);
 }
 
 int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint64_t ld,
@@ -309,10 +308,10 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
   if (pairs == 0 && !(clear && grad && rows)) return ZS_OK;
   if (!starts || (pairs && !loss) || (rows && (!logits || !ids)))
     return fail(ZS_ERR_INVALID_ARG, "zs_preference: null pointer%s");
-  const TokenSplit sp = rows ? token_split(rows, vocab, dtype) : TokenSplit{1, 1};
+  const TokenSplit sp = rows ? token_split(rows, vocab, dtype, false) : TokenSplit{1, 1};
   if (!token_launch_fits(rows, sp))
     return fail(ZS_ERR_UNSUPPORTED, "zs_preference: too many rows%s");
-  const uint64_t esz = esize(dtype), need = token_workspace(rows, vocab, dtype, true);
+  const uint64_t esz = esize(dtype), need = zs_preference_workspace(rows, vocab, dtype);
   if (need && (!workspace || workspace_bytes < need))
     return fail(ZS_ERR_INVALID_ARG, "zs_preference: workspace too small%s");
   if (!aligned(logits, esz) || !aligned(ids, 4) || !aligned(starts, 4) || !aligned(ref_logp, 4) ||
@@ -331,7 +330,7 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
     return rc;
   TokenArgs a{};
   if (rows) {
-    token_args(a, logits, dtype, rows, vocab, ld, ids, temperature, workspace);
+    token_args(a, logits, dtype, rows, vocab, ld, ids, temperature, false, workspace);
     /* behind the plans, 16 bytes each: the doubles stay aligned */
     a.lp = reinterpret_cast<double *>(a.plan + rows);
     a.own = reinterpret_cast<float *>(a.lp + rows);
@@ -354,7 +353,6 @@ int zs_preference(const void *logits, int dtype, uint64_t rows, uint64_t vocab, 
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (rows && (pairs || clear)) {
     if (int rc = launch_stats(a, dtype, s)) return rc;
-    if (int rc = launch_finish(a, s)) return rc;
   }
   if (pairs) {
     hipLaunchKernelGGL(token_pair_kernel, dim3(a.pairs), dim3(kPairThreads), 0, s, a);
