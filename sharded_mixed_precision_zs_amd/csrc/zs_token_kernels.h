@@ -605,6 +605,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
       for (bool again = false;; again = true) {
         const Shift s = shift_of(from, a.log2_scale);
         float sum = term(single, s);
+        double sum64 = 0.0;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
           float e[ve];
@@ -614,10 +615,14 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
 #pragma unroll
           for (uint32_t j = 0; j < ve; ++j) some += term(e[j], s);
           sum += (int)t < (int)in.shape.vecs - i * NT ? some : 0;
-          asm volatile("" : "+v"(sum));
+          if (i % 4 == 3 || i == ITEMS - 1) {   /* a few of them in fp32, the rest in binary64 */
+            sum64 += (double)sum;
+            sum = 0.0f;
+            asm volatile("" : "+v"(sum64));
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
-        reduce_put((double)sum, SumOf{}, dpart[turn][again]);
+        reduce_put(sum64, SumOf{}, dpart[turn][again]);
         __syncthreads();
         rest = reduce_get<NT>(SumOf{}, dpart[turn][again]);
         if (again || rest < (double)kTokenTop) break;   /* uniform over the block */

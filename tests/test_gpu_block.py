@@ -367,3 +367,51 @@ def test_block_on_another_stream_and_in_a_graph(zs):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_more_than_32_bits_of_elements(zs):
+    """A matrix of more than 2^32 elements: its last rows have the mask of their own numbers."""
+    rows, cols = (1 << 20) + 3, 4104
+    x = torch.ones(rows, cols, dtype=BF16, device="cuda")
+    zs.zs_dropout(x, x, (0.5, SEED, OFFSET))
+    for r in (0, 1, rows - 2):
+        want = torch.empty(cols, dtype=F64)
+        for b in range(cols // 8):
+            w = ref.philox((b, r, OFFSET & ref.LOW, OFFSET >> 32), (SEED & ref.LOW, SEED >> 32))
+            for j in range(8):
+                want[8 * b + j] = 2.0 * ((w[j // 2] >> 16 * (j % 2) & 0xFFFF) >= 32768)
+        assert torch.equal(x[r].double().cpu(), want)
+
+
+def test_block_wide_rows_and_their_gradient(zs):
+    """Rows that take every launch shape up to the widest. (The 64-bit forms run
+    on the CPU: torch.ldexp on the GPU is not exact.)"""
+    for r, c in ((3, 1000), (5, 2040), (3, 6000), (4, 12296), (2, 20001), (3, 40000), (2, 65536)):
+        announce(f"block wide {r}x{c}")
+        v, _ = problem(r, c, BF16, True, True, 0.0)
+        d = {k: t.cuda() for k, t in v.items()}
+        h, post_rstd, rstd, y, *_ = run_forward(zs, v, BF16, 0.0)
+        want = ref.block(*(dbl(v[k]) for k in ("x", "res", "post_gain", "gate", "gain")),
+                         float(torch.tensor(1e-5)), 0.875, float(torch.tensor(0.55)),
+                         torch.ones(r, c, dtype=F64), BF16)
+        assert torch.equal(h.cpu().double(), want[0])
+        assert torch.equal(y.cpu().double(), ref.rounded(want[4], BF16))
+        g = gen("w", r, c)
+        dy = (0.1 * randn(g, r, c)).to(BF16).cuda()
+        dx, dr = torch.empty_like(h), torch.empty_like(h)
+        s3 = [torch.empty(c, device="cuda") for _ in range(3)]
+        ws = torch.empty(zs.zs_block_norm_backward_workspace(r, c), dtype=torch.uint8, device="cuda")
+        zs.zs_block_norm_backward(dy, h, rstd, d["gain"], dx, dr, s3[0], ws, x=d["x"],
+                                  post_gain=d["post_gain"], post_rstd=post_rstd, gate=d["gate"],
+                                  dpost_gain=s3[1], dgate=s3[2], residual_scale=0.875,
+                                  branch_scale=0.55)
+        w, mag = ref.block_grad(dbl(dy.cpu()), dbl(h.cpu()), dbl(rstd.cpu()), dbl(v["gain"]), None,
+                                dbl(v["x"]), dbl(post_rstd.cpu()), dbl(v["post_gain"]), dbl(v["gate"]),
+                                0.875, float(torch.tensor(0.55)), torch.ones(r, c, dtype=F64))
+        # as above: 64 elements of a thread, 6 levels of lanes, 16 waves, ten roundings
+        chain = (64 + 6 + 16 + 10) * 2.0 ** -24
+        for k, got in (("dx", dx), ("dresidual", dr)):
+            inner = (2 if k == "dx" else 1) * chain * mag[k]
+            close(got, w[k], U[BF16] * (w[k].abs() + inner) + inner + TINY[BF16], k)
+        for k, got in zip(("dgain", "dpost_gain", "dgate"), s3):
+            close(got, w[k], (70 * 2.0 ** -24 + chain) * mag[k] + TINY[FP32], k)

@@ -430,3 +430,74 @@ def test_token_losses_captured_and_replayed(zs):
             torch.cuda.synchronize()
             for a, b in zip(got, outs):
                 assert torch.equal(a, b)
+
+
+def test_rows_past_32_bits(zs):
+    """Rows 2^31 elements apart."""
+    ld, vocab = 1 << 31, 1000
+    base = torch.empty(2 * ld + vocab, dtype=BF16, device="cuda")
+    view = base.as_strided((3, vocab), (ld, 1))
+    z, ids, _ = problem(3, vocab, BF16)
+    view.copy_(z)
+    adv = torch.tensor([1.0, -1.0, 0.5])
+    want, got = torch.empty_like(z).cuda(), torch.empty_like(z).cuda()
+    l0, s0 = run_policy(zs, z.cuda(), ids, 1.0, adv, None, None, None, 8.0, want)
+    l1, s1 = run_policy(zs, view, ids, 1.0, adv, None, None, None, 8.0, got)
+    assert torch.equal(l0, l1) and torch.equal(s0, s1) and torch.equal(got, want)
+    run_policy(zs, view, ids, 1.0, adv, None, None, None, 8.0, view)
+    assert torch.equal(view, want)
+    view.copy_(z)
+    a, _ = run_preference(zs, z.cuda(), ids, [0, 1, 3], want, beta=0.1)
+    b, _ = run_preference(zs, view, ids, [0, 1, 3], view, beta=0.1)
+    assert torch.equal(a, b) and torch.equal(view, want)
+
+
+def test_two_streams_at_once(zs):
+    """Calls side by side, each with a workspace of its own, give what they give alone."""
+    jobs = []
+    for k, (rows, vocab) in enumerate(((300, 9000), (40, 50257))):
+        z, ids, g = problem(rows, vocab, BF16)
+        adv, o, r, w = (cu(t) for t in policy_inputs(z, ids, g, 1.0, True, True, False))
+        starts = torch.tensor([0, rows // 3, rows], dtype=torch.int32).cuda()
+        out = [torch.empty_like(z).cuda() for _ in range(2)] + [torch.empty(rows, device="cuda"),
+                                                                torch.empty(1, device="cuda")]
+        need = max(zs.zs_policy_workspace(rows, vocab, zs.ZS_BF16),
+                   zs.zs_preference_workspace(rows, vocab, zs.ZS_BF16))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        jobs.append((z.cuda(), ids.cuda(), adv, o, r, starts, out, ws, torch.cuda.Stream()))
+
+    def run(z, ids, adv, o, r, starts, out, ws, stream):
+        zs.zs_policy(z, ids, adv, out[2], old_logp=o, ref_logp=r, kl_weight=0.1, grad=out[0],
+                     workspace=ws, stream=stream)
+        zs.zs_preference(z, ids, starts, 0.1, out[3], grad=out[1], workspace=ws, stream=stream)
+
+    want = []
+    for job in jobs:
+        torch.cuda.synchronize()
+        run(*job)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in job[6]])
+        for t in job[6]:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for job in jobs:
+            run(*job)
+    torch.cuda.synchronize()
+    for job, w in zip(jobs, want):
+        for a, b in zip(job[6], w):
+            assert torch.equal(a, b)
+
+
+def test_one_token_and_many_equal_ones(zs):
+    """A vocabulary of one, every logit alike, the same token in every row."""
+    for vocab in (1, 2, 700, 20000):
+        z = torch.full((5, vocab), 3.0).to(BF16)
+        ids = torch.full((5,), vocab - 1, dtype=torch.int32)
+        grad = torch.empty_like(z).cuda()
+        logp, loss = run_policy(zs, z.cuda(), ids, 1.0, torch.ones(5), None, None, None, 1.0, grad)
+        want = ref.logprob(z.double(), ids, 1.0)[0]
+        assert bool(((logp.cpu().double() - want).abs() <= 2.0 ** -20 * want.abs()).all())
+        q = torch.full((5, vocab), 1.0 / vocab, dtype=F64)
+        g = ref.logit_grad(q, ids, torch.full((5,), -1.0, dtype=F64))
+        check(grad, g, U[BF16] * g.abs() * 1.001 + 2.0 ** -20 * g.abs(), "grad")
