@@ -509,8 +509,9 @@ class _Torch:
         self.codes32 = {**self.codes, torch.float32: ZS_FP32}
         try:    # the current stream's handle without an object around it
             raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-            self.stream = lambda: raw(device())
+            self.stream, self.device = lambda: raw(device()), device
         except AttributeError:
+            self.device = torch.cuda.current_device
             self.stream = lambda: torch.cuda.current_stream().cuda_stream
 
 
@@ -528,6 +529,17 @@ def _raw_stream(stream):
     if stream is None:
         return _t().stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _here(stream, *tensors):
+    """The stream's handle, where all tensors are on the current device: the kernels run there."""
+    device = _t().device()
+    for x in tensors:
+        if x is not None and x.get_device() != device:
+            raise ValueError(f"tensor on {x.device}, but the current device is {device}")
+    if getattr(stream, "device_index", device) != device:
+        raise ValueError(f"stream of device {stream.device_index}, but the current is {device}")
+    return _raw_stream(stream)
 
 
 def _float_code(t, what, fp32=False):
@@ -707,6 +719,8 @@ def _rule(dropout):
     dev = more[0] if more else None
     if dev is not None and (not dev.is_cuda or dev.element_size() != 8 or dev.numel() != 1):
         raise ValueError("dev_offset: CUDA tensor of one 64-bit element expected")
+    if dev is not None:
+        _here(0, dev)
     mask = (1 << 64) - 1
     return zs_dropout_rule(p, seed & mask, offset & mask, None if dev is None else dev.data_ptr())
 
@@ -720,7 +734,7 @@ def zs_dropout(x, out, rule, residual=None, stream=None):
     _check("zs_dropout", _lib.zs_dropout(
         _dense(x, shape, dt, "x"), _dense(residual, shape, dt, "residual"),
         _float_code(x, "x", fp32=True), *shape, _rule(rule), _dense(out, shape, dt, "out"),
-        _raw_stream(stream)))
+        _here(stream, x, residual, out)))
 
 
 def zs_block_norm_forward(x, residual, gain, eps, h, rstd=None, post_gain=None, post_rstd=None,
@@ -743,7 +757,8 @@ def zs_block_norm_forward(x, residual, gain, eps, h, rstd=None, post_gain=None, 
         _dense(gain, shape[1:], dt, "gain"), _float_code(x, "x"), *shape, eps, residual_scale,
         branch_scale, _rule(dropout), _dense(h, shape, dt, "h"),
         _dense(post_rstd, shape[:1], f32, "post_rstd"), _dense(rstd, shape[:1], f32, "rstd"),
-        cp, sp, _dense(y, shape, dt, "y"), _raw_stream(stream)))
+        cp, sp, _dense(y, shape, dt, "y"),
+        _here(stream, x, residual, post_gain, gate, gain, h, post_rstd, rstd, codes, scales, y)))
 
 
 def zs_block_norm_backward_workspace(rows, cols):
@@ -770,7 +785,9 @@ def zs_block_norm_backward(dy, h, rstd, gain, dx, dresidual, dgain, workspace, x
         _float_code(dy, "dy"), *shape, residual_scale, branch_scale, _rule(dropout),
         _dense(dx, shape, dt, "dx"), _dense(dresidual, shape, dt, "dresidual"),
         _dense(dgain, shape[1:], f32, "dgain"), _dense(dpost_gain, shape[1:], f32, "dpost_gain"),
-        _dense(dgate, shape[1:], f32, "dgate"), wp, wb, _raw_stream(stream)))
+        _dense(dgate, shape[1:], f32, "dgate"), wp, wb,
+        _here(stream, dy, h, rstd, gain, dres, x, post_rstd, post_gain, gate, dx, dresidual, dgain,
+              dpost_gain, dgate, workspace)))
 
 
 def zs_mx_linear(a_codes, a_scales, a_format, b_codes, b_scales, out, k, bias=None,
@@ -790,7 +807,7 @@ def zs_mx_linear(a_codes, a_scales, a_format, b_codes, b_scales, out, k, bias=No
     _check("zs_mx_linear", _lib.zs_mx_linear(
         ac, asc, a_format, bc, bsc, m, n, k, _dense(bias, (n,), dt, "bias"), activation, rp, rld,
         _dense(pre, (m, n), dt, "pre"), p, _float_code(out, "out"), ld, wp, wb,
-        _raw_stream(stream)))
+        _here(stream, a_codes, a_scales, b_codes, b_scales, bias, residual, pre, out, workspace)))
 
 
 def zs_activation_backward_workspace(rows, cols):
@@ -809,10 +826,18 @@ def zs_activation_backward(dout, pre, activation, dpre=None, dbias=None, workspa
     _check("zs_activation_backward", _lib.zs_activation_backward(
         _dense(dout, shape, dt, "dout"), _dense(pre, shape, dt, "pre"), activation,
         _float_code(dout, "dout"), *shape, _dense(dpre, shape, dt, "dpre"),
-        _dense(dbias, shape[1:], _t().f32, "dbias"), wp, wb, _raw_stream(stream)))
+        _dense(dbias, shape[1:], _t().f32, "dbias"), wp, wb,
+        _here(stream, dout, pre, dpre, dbias, workspace)))
 
 
 # ---- losses on the log-probabilities of given tokens ---------------------------
+
+def _scaler(dev):
+    """Address of a device scaler on the current device (None stays None)."""
+    if dev is not None and not isinstance(dev, int):
+        _here(0, dev)
+    return None if dev is None else _dev_scaler_ptr(dev)
+
 
 def _grad_rows(grad, logits, rows, vocab):
     """(address, row stride) of a gradient of the logits' shape and type; (None, 0) without."""
@@ -836,7 +861,7 @@ def zs_logprob(logits, ids, logp, temperature=1.0, workspace=None, stream=None):
     _check("zs_logprob", _lib.zs_logprob(
         p, _float_code(logits, "logits", fp32=True), rows, vocab, ld,
         _dense(ids, (rows,), _t().i32, "ids"), temperature, _dense(logp, (rows,), _t().f32, "logp"),
-        wp, wb, _raw_stream(stream)))
+        wp, wb, _here(stream, logits, ids, logp, workspace)))
 
 
 def zs_policy_workspace(rows, vocab, dtype):
@@ -861,8 +886,10 @@ def zs_policy(logits, ids, advantage, loss, temperature=1.0, old_logp=None, ref_
         _dense(ids, (rows,), _t().i32, "ids"), temperature, per_row["advantage"],
         per_row["old_logp"], per_row["ref_logp"], clip_low, clip_high, kl_weight,
         per_row["row_weight"], loss_scale,
-        None if dev_scaler is None else _dev_scaler_ptr(dev_scaler), per_row["logp"],
-        per_row["loss"], gp, gld, wp, wb, _raw_stream(stream)))
+        _scaler(dev_scaler), per_row["logp"],
+        per_row["loss"], gp, gld, wp, wb,
+        _here(stream, logits, ids, advantage, old_logp, ref_logp, row_weight, logp, loss, grad,
+              workspace)))
 
 
 def zs_preference_workspace(rows, vocab, dtype):
@@ -888,6 +915,8 @@ def zs_preference(logits, ids, starts, beta, loss, kind=ZS_PREFERENCE_SIGMOID, s
         _dense(ids, (rows,), i32, "ids"), _dense(starts, (2 * pairs + 1,), i32, "starts"), pairs,
         temperature, _dense(ref_logp, (2 * pairs,), f32, "ref_logp"), kind, beta, smoothing,
         1 if mean else 0, _dense(pair_weight, (pairs,), f32, "pair_weight"), loss_scale,
-        None if dev_scaler is None else _dev_scaler_ptr(dev_scaler),
+        _scaler(dev_scaler),
         _dense(seq_logp, (2 * pairs,), f32, "seq_logp"), _dense(loss, (pairs,), f32, "loss"), gp,
-        gld, 1 if clear else 0, wp, wb, _raw_stream(stream)))
+        gld, 1 if clear else 0, wp, wb,
+        _here(stream, logits, ids, starts, ref_logp, pair_weight, seq_logp, loss, grad,
+              workspace)))

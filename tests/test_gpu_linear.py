@@ -236,3 +236,65 @@ def test_activation_backward_ends(zs):
     none = torch.empty(0, 9, dtype=BF16, device="cuda")
     zs.zs_activation_backward(none, none, zs.ZS_ACT_GELU, none, dbias=dbias)
     assert not dbias.any()
+
+
+def test_more_than_32_bits_of_elements(zs):
+    """pre and c of more than 2^32 elements, and rows that are 2^31 apart."""
+    m, n, k = 65600, 65544, 64
+    g = gen("large")
+    # codes of +-1, and scales of 1: every sum is a whole number that bf16 has
+    a = torch.randint(0, 2, (m, k), generator=g) * 2.0 - 1
+    b = torch.randint(0, 2, (n, k), generator=g) * 2.0 - 1
+    a8, b4 = zs.mx_empty(m, k, zs.ZS_MX_E4M3), zs.mx_empty(n, k, zs.ZS_MX_E2M1)
+    zs.zs_mx_quantize(a.to(BF16).cuda(), zs.ZS_MX_E4M3, *a8)
+    zs.zs_mx_quantize(b.to(BF16).cuda(), zs.ZS_MX_E2M1, *b4)
+    out, pre = (torch.empty(m, n, dtype=BF16, device="cuda") for _ in range(2))
+    zs.zs_mx_linear(*a8, zs.ZS_MX_E4M3, *b4, out, k, activation=zs.ZS_ACT_RELU, pre=pre)
+    for rows in (slice(0, 3), slice(32767, 32770), slice(m - 65, m)):
+        want = a[rows] @ b.t()
+        assert torch.equal(pre[rows].float().cpu(), want)
+        assert torch.equal(out[rows].float().cpu(), want.clamp(min=0))
+    del out
+    dpre, dbias = torch.empty_like(pre), torch.empty(n, device="cuda")
+    ws = torch.empty(zs.zs_activation_backward_workspace(m, n), dtype=torch.uint8, device="cuda")
+    zs.zs_activation_backward(pre, pre, zs.ZS_ACT_RELU, dpre, dbias, ws)
+    assert torch.equal(dpre[-65:].float().cpu(), (a[-65:] @ b.t()).clamp(min=0))
+    del pre, dpre
+    ld, few = 1 << 31, 3
+    raw = torch.empty(2 * (few - 1) * ld + 2 * n, dtype=BF16, device="cuda")
+    out, res = (raw[i * n:].as_strided((few, n), (2 * ld, 1)) for i in range(2))
+    res.fill_(4.0)
+    a8 = zs.mx_empty(few, k, zs.ZS_MX_E4M3)
+    zs.zs_mx_quantize(a[:few].to(BF16).cuda(), zs.ZS_MX_E4M3, *a8)
+    with pytest.raises(zs.ZsError):     # the extents cross each other
+        zs.zs_mx_linear(*a8, zs.ZS_MX_E4M3, *b4, out, k, residual=res)
+    zs.zs_mx_linear(*a8, zs.ZS_MX_E4M3, *b4, res, k, residual=res)
+    assert torch.equal(res.float().cpu(), a[:few] @ b.t() + 4)
+
+
+def test_tensors_of_another_device_are_refused(zs, monkeypatch):
+    """Every entry point looks at its tensors' device before it queues anything."""
+    x = torch.zeros(4, 64, dtype=BF16, device="cuda")
+    v, r = x[0].clone(), torch.zeros(4, device="cuda")
+    ids = torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    a8, b4 = zs.mx_empty(4, 64, zs.ZS_MX_E4M3), zs.mx_empty(64, 64, zs.ZS_MX_E2M1)
+    out = [torch.full_like(x, 7.0) for _ in range(3)]
+    calls = {
+        "dropout": lambda: zs.zs_dropout(x, out[0], (0.5, 1, 2)),
+        "block": lambda: zs.zs_block_norm_forward(x, x, v, 1e-5, out[0], y=out[1]),
+        "block back": lambda: zs.zs_block_norm_backward(x, x, r, v, out[0], out[1],
+                                                        torch.zeros(64, device="cuda"), ws),
+        "linear": lambda: zs.zs_mx_linear(*a8, zs.ZS_MX_E4M3, *b4, out[0], 64),
+        "act": lambda: zs.zs_activation_backward(x, x, zs.ZS_ACT_GELU, out[0]),
+        "logprob": lambda: zs.zs_logprob(x, ids, torch.empty_like(r), workspace=ws),
+        "policy": lambda: zs.zs_policy(x, ids, r, torch.empty_like(r), grad=out[0], workspace=ws),
+        "preference": lambda: zs.zs_preference(x, ids, ids[:3], 0.1, r[:1].clone(), grad=out[0],
+                                               workspace=ws),
+    }
+    monkeypatch.setattr(zs._t(), "device", lambda: 1)
+    for name, call in calls.items():
+        with pytest.raises(ValueError, match="current device is 1"):
+            call()
+    torch.cuda.synchronize()
+    assert all(bool((o == 7).all()) for o in out)

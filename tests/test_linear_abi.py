@@ -101,6 +101,21 @@ def test_python_checks(zs):
         zs.zs_activation_backward(x[0], x[0], zs.ZS_ACT_GELU, x[0])
 
 
+def test_device_of_tensors_and_stream(zs, monkeypatch):
+    class Stub:
+        def __init__(self, index):
+            self.device, self.device_index, self.cuda_stream = f"cuda:{index}", index, 5
+
+        def get_device(self):
+            return self.device_index
+
+    monkeypatch.setattr(zs._t(), "device", lambda: 1)
+    assert zs._here(Stub(1), Stub(1), None, Stub(1)) == 5 and zs._here(3, Stub(1)) == 3
+    for stream, tensors in ((3, (Stub(1), Stub(0))), (Stub(0), (Stub(1),))):
+        with pytest.raises(ValueError, match="device"):
+            zs._here(stream, *tensors)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
 def test_activations_against_torch_and_differences(act):
     x = torch.cat([torch.linspace(-9, 9, 400, dtype=F64), torch.tensor([-40.0, 40.0, 0.3], dtype=F64)])
