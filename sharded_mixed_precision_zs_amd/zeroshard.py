@@ -513,6 +513,8 @@ class _Torch:
         except AttributeError:
             self.device = torch.cuda.current_device
             self.stream = lambda: torch.cuda.current_stream().cuda_stream
+        if not torch.cuda.is_available():   # then no tensor is on it
+            self.device = lambda: 0
 
 
 _names = None
@@ -537,6 +539,8 @@ def _here(stream, *tensors):
     for x in tensors:
         if x is not None and x.get_device() != device:
             raise ValueError(f"tensor on {x.device}, but the current device is {device}")
+    if stream is None:
+        return _t().stream()
     if getattr(stream, "device_index", device) != device:
         raise ValueError(f"stream of device {stream.device_index}, but the current is {device}")
     return _raw_stream(stream)
@@ -551,10 +555,20 @@ def _float_code(t, what, fp32=False):
     return code
 
 
-def _rows(x, what, shape=None):
-    """(address, rows, cols, row stride) of a 2-D CUDA tensor with contiguous rows."""
-    if not x.is_cuda:
-        raise ValueError(f"{what}: CUDA tensor expected")
+def _elsewhere(x, device):
+    """Whether x is not on the GPU (device: None) or not on that one."""
+    return not x.is_cuda if device is None else x.get_device() != device
+
+
+def _where(x, device):
+    return x.device if device is None else f"{x.device}, the current device is {device}"
+
+
+def _rows(x, what, shape=None, device=None):
+    """(address, rows, cols, row stride) of a 2-D CUDA tensor with contiguous rows; with
+    `device`, on that one."""
+    if _elsewhere(x, device):
+        raise ValueError(f"{what}: CUDA tensor expected, got one on {_where(x, device)}")
     if x.dim() != 2 or (shape is not None and x.shape != shape):
         raise ValueError(f"{what}: {'2-D' if shape is None else shape} tensor expected, "
                          f"got {tuple(x.shape)}")
@@ -567,21 +581,24 @@ def _rows(x, what, shape=None):
     return x.data_ptr(), r, c, ld
 
 
-def _dense(x, shape, dtype, what):
-    """Address of a contiguous CUDA tensor of that shape and type (None stays None)."""
+def _dense(x, shape, dtype, what, device=None):
+    """Address of a contiguous CUDA tensor of that shape and type (None stays None); with
+    `device`, on that one."""
     if x is None:
         return None
-    if x.shape != shape or x.dtype != dtype or not x.is_cuda or not x.is_contiguous():
+    if (x.shape != shape or x.dtype is not dtype or not x.is_contiguous()
+            or (not x.is_cuda if device is None else x.get_device() != device)):
         raise ValueError(f"{what}: contiguous {dtype} CUDA tensor of shape {tuple(shape)} "
-                         f"expected, got {x.dtype} {tuple(x.shape)} on {x.device}")
+                         f"expected, got {x.dtype} {tuple(x.shape)} on {_where(x, device)}")
     return x.data_ptr()
 
 
-def _workspace(x):
+def _workspace(x, device=None):
     if x is None:
         return None, 0
-    if not x.is_cuda or not x.is_contiguous():
-        raise ValueError("workspace: contiguous CUDA tensor expected")
+    if _elsewhere(x, device) or not x.is_contiguous():
+        raise ValueError(f"workspace: contiguous CUDA tensor expected, got one on "
+                         f"{_where(x, device)}")
     return x.data_ptr(), x.nbytes
 
 
@@ -603,10 +620,11 @@ def mx_empty(rows, k, fmt, device="cuda"):
                  for s in mx_shapes(rows, k, fmt))
 
 
-def _mx_ptrs(codes, scales, rows, k, fmt, what):
+def _mx_ptrs(codes, scales, rows, k, fmt, what, device=None):
     cs, ss = mx_shapes(rows, k, fmt)
     u8 = _t().u8
-    return (_dense(codes, cs, u8, f"{what} codes"), _dense(scales, ss, u8, f"{what} scales"))
+    return (_dense(codes, cs, u8, f"{what} codes", device),
+            _dense(scales, ss, u8, f"{what} scales", device))
 
 
 def zs_mx_quantize(src, fmt, codes, scales, columns=False, values=None, stream=None):
@@ -730,11 +748,11 @@ def zs_dropout(x, out, rule, residual=None, stream=None):
     out may be x or residual."""
     if x.dim() != 2:
         raise ValueError("x: 2-D tensor expected")
-    shape, dt = x.shape, x.dtype
+    shape, dt, here = x.shape, x.dtype, _t().device()
     _check("zs_dropout", _lib.zs_dropout(
-        _dense(x, shape, dt, "x"), _dense(residual, shape, dt, "residual"),
-        _float_code(x, "x", fp32=True), *shape, _rule(rule), _dense(out, shape, dt, "out"),
-        _here(stream, x, residual, out)))
+        _dense(x, shape, dt, "x", here), _dense(residual, shape, dt, "residual", here),
+        _float_code(x, "x", fp32=True), *shape, _rule(rule), _dense(out, shape, dt, "out", here),
+        _here(stream)))
 
 
 def zs_block_norm_forward(x, residual, gain, eps, h, rstd=None, post_gain=None, post_rstd=None,
@@ -745,20 +763,21 @@ def zs_block_norm_forward(x, residual, gain, eps, h, rstd=None, post_gain=None, 
     taken as it is, without gate the gate is 1; dropout: (p, seed, offset[, dev_offset])."""
     if x.dim() != 2:
         raise ValueError("x: 2-D tensor expected")
-    shape, dt, f32 = x.shape, x.dtype, _t().f32
+    names = _t()
+    shape, dt, f32, here = x.shape, x.dtype, names.f32, names.device()
+    row, col = shape[:1], shape[1:]
     cp = sp = None
     if codes is not None or scales is not None:
         if codes is None or scales is None:
             raise ValueError("codes and scales go together")
-        cp, sp = _mx_ptrs(codes, scales, *shape, ZS_MX_E4M3, "y")
+        cp, sp = _mx_ptrs(codes, scales, *shape, ZS_MX_E4M3, "y", here)
     _check("zs_block_norm_forward", _lib.zs_block_norm_forward(
-        _dense(x, shape, dt, "x"), _dense(residual, shape, dt, "residual"),
-        _dense(post_gain, shape[1:], dt, "post_gain"), _dense(gate, shape[1:], dt, "gate"),
-        _dense(gain, shape[1:], dt, "gain"), _float_code(x, "x"), *shape, eps, residual_scale,
-        branch_scale, _rule(dropout), _dense(h, shape, dt, "h"),
-        _dense(post_rstd, shape[:1], f32, "post_rstd"), _dense(rstd, shape[:1], f32, "rstd"),
-        cp, sp, _dense(y, shape, dt, "y"),
-        _here(stream, x, residual, post_gain, gate, gain, h, post_rstd, rstd, codes, scales, y)))
+        _dense(x, shape, dt, "x", here), _dense(residual, shape, dt, "residual", here),
+        _dense(post_gain, col, dt, "post_gain", here), _dense(gate, col, dt, "gate", here),
+        _dense(gain, col, dt, "gain", here), _float_code(x, "x"), *shape, eps, residual_scale,
+        branch_scale, _rule(dropout), _dense(h, shape, dt, "h", here),
+        _dense(post_rstd, row, f32, "post_rstd", here), _dense(rstd, row, f32, "rstd", here), cp,
+        sp, _dense(y, shape, dt, "y", here), _here(stream)))
 
 
 def zs_block_norm_backward_workspace(rows, cols):
@@ -774,40 +793,41 @@ def zs_block_norm_backward(dy, h, rstd, gain, dx, dresidual, dgain, workspace, x
     dpost_gain and dgate. dres: what h receives from elsewhere."""
     if dy.dim() != 2:
         raise ValueError("dy: 2-D tensor expected")
-    shape, dt, f32 = dy.shape, dy.dtype, _t().f32
-    wp, wb = _workspace(workspace)
+    names = _t()
+    shape, dt, f32, here = dy.shape, dy.dtype, names.f32, names.device()
+    row, col = shape[:1], shape[1:]
+    wp, wb = _workspace(workspace, here)
     _check("zs_block_norm_backward", _lib.zs_block_norm_backward(
-        _dense(dy, shape, dt, "dy"), _dense(h, shape, dt, "h"),
-        _dense(rstd, shape[:1], f32, "rstd"), _dense(gain, shape[1:], dt, "gain"),
-        _dense(dres, shape, dt, "dres"), _dense(x, shape, dt, "x"),
-        _dense(post_rstd, shape[:1], f32, "post_rstd"),
-        _dense(post_gain, shape[1:], dt, "post_gain"), _dense(gate, shape[1:], dt, "gate"),
+        _dense(dy, shape, dt, "dy", here), _dense(h, shape, dt, "h", here),
+        _dense(rstd, row, f32, "rstd", here), _dense(gain, col, dt, "gain", here),
+        _dense(dres, shape, dt, "dres", here), _dense(x, shape, dt, "x", here),
+        _dense(post_rstd, row, f32, "post_rstd", here),
+        _dense(post_gain, col, dt, "post_gain", here), _dense(gate, col, dt, "gate", here),
         _float_code(dy, "dy"), *shape, residual_scale, branch_scale, _rule(dropout),
-        _dense(dx, shape, dt, "dx"), _dense(dresidual, shape, dt, "dresidual"),
-        _dense(dgain, shape[1:], f32, "dgain"), _dense(dpost_gain, shape[1:], f32, "dpost_gain"),
-        _dense(dgate, shape[1:], f32, "dgate"), wp, wb,
-        _here(stream, dy, h, rstd, gain, dres, x, post_rstd, post_gain, gate, dx, dresidual, dgain,
-              dpost_gain, dgate, workspace)))
+        _dense(dx, shape, dt, "dx", here), _dense(dresidual, shape, dt, "dresidual", here),
+        _dense(dgain, col, f32, "dgain", here), _dense(dpost_gain, col, f32, "dpost_gain", here),
+        _dense(dgate, col, f32, "dgate", here), wp, wb, _here(stream)))
 
 
 def zs_mx_linear(a_codes, a_scales, a_format, b_codes, b_scales, out, k, bias=None,
                  activation=ZS_ACT_NONE, residual=None, pre=None, workspace=None, stream=None):
     """out[m][n] = residual + act(A B^T + bias): A m microscaled rows of k elements in a_format,
     B n in ZS_MX_E2M1. pre: what the activation is applied to, 16 bits. out may be residual."""
-    p, m, n, ld = _rows(out, "out")
+    here = _t().device()
+    p, m, n, ld = _rows(out, "out", device=here)
     dt = out.dtype
-    ac, asc = _mx_ptrs(a_codes, a_scales, m, k, a_format, "A")
-    bc, bsc = _mx_ptrs(b_codes, b_scales, n, k, ZS_MX_E2M1, "B")
+    ac, asc = _mx_ptrs(a_codes, a_scales, m, k, a_format, "A", here)
+    bc, bsc = _mx_ptrs(b_codes, b_scales, n, k, ZS_MX_E2M1, "B", here)
     rp, rld = None, 0
     if residual is not None:
         if residual.dtype != dt:
             raise ValueError("residual: out's dtype expected")
-        rp, _, _, rld = _rows(residual, "residual", (m, n))
-    wp, wb = _workspace(workspace)
+        rp, _, _, rld = _rows(residual, "residual", (m, n), here)
+    wp, wb = _workspace(workspace, here)
     _check("zs_mx_linear", _lib.zs_mx_linear(
-        ac, asc, a_format, bc, bsc, m, n, k, _dense(bias, (n,), dt, "bias"), activation, rp, rld,
-        _dense(pre, (m, n), dt, "pre"), p, _float_code(out, "out"), ld, wp, wb,
-        _here(stream, a_codes, a_scales, b_codes, b_scales, bias, residual, pre, out, workspace)))
+        ac, asc, a_format, bc, bsc, m, n, k, _dense(bias, (n,), dt, "bias", here), activation, rp,
+        rld, _dense(pre, (m, n), dt, "pre", here), p, _float_code(out, "out"), ld, wp, wb,
+        _here(stream)))
 
 
 def zs_activation_backward_workspace(rows, cols):
@@ -821,13 +841,12 @@ def zs_activation_backward(dout, pre, activation, dpre=None, dbias=None, workspa
     (None without an activation). dpre may be dout or pre."""
     if dout.dim() != 2:
         raise ValueError("dout: 2-D tensor expected")
-    shape, dt = dout.shape, dout.dtype
-    wp, wb = _workspace(workspace)
+    shape, dt, here = dout.shape, dout.dtype, _t().device()
+    wp, wb = _workspace(workspace, here)
     _check("zs_activation_backward", _lib.zs_activation_backward(
-        _dense(dout, shape, dt, "dout"), _dense(pre, shape, dt, "pre"), activation,
-        _float_code(dout, "dout"), *shape, _dense(dpre, shape, dt, "dpre"),
-        _dense(dbias, shape[1:], _t().f32, "dbias"), wp, wb,
-        _here(stream, dout, pre, dpre, dbias, workspace)))
+        _dense(dout, shape, dt, "dout", here), _dense(pre, shape, dt, "pre", here), activation,
+        _float_code(dout, "dout"), *shape, _dense(dpre, shape, dt, "dpre", here),
+        _dense(dbias, shape[1:], _t().f32, "dbias", here), wp, wb, _here(stream)))
 
 
 # ---- losses on the log-probabilities of given tokens ---------------------------
@@ -839,13 +858,13 @@ def _scaler(dev):
     return None if dev is None else _dev_scaler_ptr(dev)
 
 
-def _grad_rows(grad, logits, rows, vocab):
+def _grad_rows(grad, logits, rows, vocab, here=None):
     """(address, row stride) of a gradient of the logits' shape and type; (None, 0) without."""
     if grad is None:
         return None, 0
     if grad.dtype != logits.dtype:
         raise ValueError("grad: the logits' dtype expected")
-    gp, _, _, gld = _rows(grad, "grad", (rows, vocab))
+    gp, _, _, gld = _rows(grad, "grad", (rows, vocab), here)
     return gp, gld
 
 
@@ -856,12 +875,14 @@ def zs_logprob_workspace(rows, vocab, dtype):
 
 def zs_logprob(logits, ids, logp, temperature=1.0, workspace=None, stream=None):
     """Log-probability of each row's token ids[row] (0 where that is no token)."""
-    p, rows, vocab, ld = _rows(logits, "logits")
-    wp, wb = _workspace(workspace)
+    names = _t()
+    here = names.device()
+    p, rows, vocab, ld = _rows(logits, "logits", device=here)
+    wp, wb = _workspace(workspace, here)
     _check("zs_logprob", _lib.zs_logprob(
         p, _float_code(logits, "logits", fp32=True), rows, vocab, ld,
-        _dense(ids, (rows,), _t().i32, "ids"), temperature, _dense(logp, (rows,), _t().f32, "logp"),
-        wp, wb, _here(stream, logits, ids, logp, workspace)))
+        _dense(ids, (rows,), names.i32, "ids", here), temperature,
+        _dense(logp, (rows,), names.f32, "logp", here), wp, wb, _here(stream)))
 
 
 def zs_policy_workspace(rows, vocab, dtype):
@@ -874,22 +895,21 @@ def zs_policy(logits, ids, advantage, loss, temperature=1.0, old_logp=None, ref_
               dev_scaler=None, logp=None, grad=None, workspace=None, stream=None):
     """Clipped policy loss per row and, with grad, the logits' gradient times the loss scale
     (loss_scale, or dev_scaler's). grad may be logits itself."""
-    p, rows, vocab, ld = _rows(logits, "logits")
-    f32 = _t().f32
-    gp, gld = _grad_rows(grad, logits, rows, vocab)
-    wp, wb = _workspace(workspace)
-    per_row = {name: _dense(t, (rows,), f32, name) for name, t in
-               (("advantage", advantage), ("old_logp", old_logp), ("ref_logp", ref_logp),
-                ("row_weight", row_weight), ("logp", logp), ("loss", loss))}
+    names = _t()
+    f32, here = names.f32, names.device()
+    p, rows, vocab, ld = _rows(logits, "logits", device=here)
+    gp, gld = _grad_rows(grad, logits, rows, vocab, here)
+    wp, wb = _workspace(workspace, here)
+    each = (rows,)
     _check("zs_policy", _lib.zs_policy(
         p, _float_code(logits, "logits", fp32=True), rows, vocab, ld,
-        _dense(ids, (rows,), _t().i32, "ids"), temperature, per_row["advantage"],
-        per_row["old_logp"], per_row["ref_logp"], clip_low, clip_high, kl_weight,
-        per_row["row_weight"], loss_scale,
-        _scaler(dev_scaler), per_row["logp"],
-        per_row["loss"], gp, gld, wp, wb,
-        _here(stream, logits, ids, advantage, old_logp, ref_logp, row_weight, logp, loss, grad,
-              workspace)))
+        _dense(ids, each, names.i32, "ids", here), temperature,
+        _dense(advantage, each, f32, "advantage", here),
+        _dense(old_logp, each, f32, "old_logp", here),
+        _dense(ref_logp, each, f32, "ref_logp", here), clip_low, clip_high, kl_weight,
+        _dense(row_weight, each, f32, "row_weight", here), loss_scale, _scaler(dev_scaler),
+        _dense(logp, each, f32, "logp", here), _dense(loss, each, f32, "loss", here), gp, gld, wp,
+        wb, _here(stream)))
 
 
 def zs_preference_workspace(rows, vocab, dtype):
@@ -905,18 +925,19 @@ def zs_preference(logits, ids, starts, beta, loss, kind=ZS_PREFERENCE_SIGMOID, s
     pair p prefers sequence 2p) and, with grad, the logits' gradient times the loss scale. grad
     may be logits itself; its rows outside all sequences are left as they were, or with clear
     filled with zeros."""
-    p, rows, vocab, ld = _rows(logits, "logits")
-    f32, i32 = _t().f32, _t().i32
+    names = _t()
+    f32, i32, here = names.f32, names.i32, names.device()
+    p, rows, vocab, ld = _rows(logits, "logits", device=here)
     pairs = loss.shape[0] if loss.dim() == 1 else -1
-    gp, gld = _grad_rows(grad, logits, rows, vocab)
-    wp, wb = _workspace(workspace)
+    gp, gld = _grad_rows(grad, logits, rows, vocab, here)
+    wp, wb = _workspace(workspace, here)
+    each, sequences = (pairs,), (2 * pairs,)
     _check("zs_preference", _lib.zs_preference(
         p, _float_code(logits, "logits", fp32=True), rows, vocab, ld,
-        _dense(ids, (rows,), i32, "ids"), _dense(starts, (2 * pairs + 1,), i32, "starts"), pairs,
-        temperature, _dense(ref_logp, (2 * pairs,), f32, "ref_logp"), kind, beta, smoothing,
-        1 if mean else 0, _dense(pair_weight, (pairs,), f32, "pair_weight"), loss_scale,
-        _scaler(dev_scaler),
-        _dense(seq_logp, (2 * pairs,), f32, "seq_logp"), _dense(loss, (pairs,), f32, "loss"), gp,
-        gld, 1 if clear else 0, wp, wb,
-        _here(stream, logits, ids, starts, ref_logp, pair_weight, seq_logp, loss, grad,
-              workspace)))
+        _dense(ids, (rows,), i32, "ids", here),
+        _dense(starts, (2 * pairs + 1,), i32, "starts", here), pairs, temperature,
+        _dense(ref_logp, sequences, f32, "ref_logp", here), kind, beta, smoothing,
+        1 if mean else 0, _dense(pair_weight, each, f32, "pair_weight", here), loss_scale,
+        _scaler(dev_scaler), _dense(seq_logp, sequences, f32, "seq_logp", here),
+        _dense(loss, each, f32, "loss", here), gp, gld, 1 if clear else 0, wp, wb,
+        _here(stream)))
