@@ -32,23 +32,26 @@ void with_act(int act, F f) {
   else f(Tag<ZS_ACT_NONE>{});
 }
 
-/* A block's vectors of a row, all of a row's where they are 256 or fewer, and
- * its rows at a time; blocks that share the rows, some eight rows to a thread
- * and 1024 in all (8192 x 16384 with gelu: 134 us; with 2048 blocks 153). */
+/* A block's vectors of a row, 512 bytes of it or all, and its rows at a time
+ * (32768 x 1600 with gelu 62 us, with 1024 bytes 67; rows that are no whole
+ * vectors straddle lines at both ends of that: 16384 x 4095 97 us with 1024
+ * bytes, 107 with 512). Parts of the rows: what a block takes at once, but 1024
+ * at most. */
 struct ActShape {
   uint32_t vecs, across, down, stripes, parts;
+  uint64_t each;
 };
 
 ActShape act_shape(uint64_t rows, uint64_t cols) {
   ActShape s;
   s.vecs = (uint32_t)((cols + 7) / 8);
-  s.across = s.vecs < kBlock ? s.vecs : kBlock;
-  s.down = kBlock / s.across;
+  const uint32_t most_across = cols % 8 ? 64 : 32;
+  s.across = s.vecs < most_across ? s.vecs : most_across;
+  s.down = kActThreads / s.across;
   s.stripes = (s.vecs + s.across - 1) / s.across;
-  const uint64_t each = 8ull * s.down, most = (rows + each - 1) / each;
-  uint64_t parts = 1024 / s.stripes;
-  if (parts > most) parts = most;
-  s.parts = (uint32_t)(parts < 1 ? 1 : parts);
+  const uint64_t once = (uint64_t)kActRows * s.down, most = (rows + once - 1) / once;
+  s.each = (most + 1023) / 1024 * once;
+  s.parts = (uint32_t)((rows + s.each - 1) / s.each);
   return s;
 }
 
@@ -159,16 +162,18 @@ int zs_activation_backward(const void *dc, const void *pre, int activation, int 
     const ActShape sh = act_shape(rows, cols);
     parts = sh.parts;
     const ActGradArgs a{dc, need_pre ? pre : nullptr, static_cast<uint16_t *>(dpre),
-                        dbias ? static_cast<float *>(workspace) : nullptr, rows, (uint32_t)cols,
-                        sh.vecs, parts, sh.across, sh.down};
+                        dbias ? static_cast<float *>(workspace) : nullptr, rows, sh.each,
+                        (uint32_t)cols, sh.vecs, sh.across, sh.down};
     const bool al = cols % 8 == 0 && aligned(dc, 16) && aligned(a.pre, 16) && aligned(dpre, 16);
+    if (!fits(sh.stripes, kActThreads))
+      return fail(ZS_ERR_UNSUPPORTED, "zs_activation_backward: too many columns for one launch%s");
     const dim3 grid(sh.stripes, parts);
     with16(dtype, [&](auto dt) {
       with_bool(al, [&](auto v) {
         with_act(activation, [&](auto act) {
           hipLaunchKernelGGL((act_grad_kernel<decltype(dt)::value, decltype(v)::value,
                                               decltype(act)::value>),
-                             grid, dim3(kBlock), 0, s, a);
+                             grid, dim3(kActThreads), 0, s, a);
         });
       });
     });
