@@ -555,11 +555,6 @@ def _float_code(t, what, fp32=False):
     return code
 
 
-def _elsewhere(x, device):
-    """Whether x is not on the GPU (device: None) or not on that one."""
-    return not x.is_cuda if device is None else x.get_device() != device
-
-
 def _where(x, device):
     return x.device if device is None else f"{x.device}, the current device is {device}"
 
@@ -567,7 +562,7 @@ def _where(x, device):
 def _rows(x, what, shape=None, device=None):
     """(address, rows, cols, row stride) of a 2-D CUDA tensor with contiguous rows; with
     `device`, on that one."""
-    if _elsewhere(x, device):
+    if not x.is_cuda if device is None else x.get_device() != device:
         raise ValueError(f"{what}: CUDA tensor expected, got one on {_where(x, device)}")
     if x.dim() != 2 or (shape is not None and x.shape != shape):
         raise ValueError(f"{what}: {'2-D' if shape is None else shape} tensor expected, "
@@ -596,7 +591,8 @@ def _dense(x, shape, dtype, what, device=None):
 def _workspace(x, device=None):
     if x is None:
         return None, 0
-    if _elsewhere(x, device) or not x.is_contiguous():
+    if (not x.is_contiguous()
+            or (not x.is_cuda if device is None else x.get_device() != device)):
         raise ValueError(f"workspace: contiguous CUDA tensor expected, got one on "
                          f"{_where(x, device)}")
     return x.data_ptr(), x.nbytes
