@@ -67,8 +67,9 @@ void with_block_shape(uint64_t padded, F f) {
 
 /* The gradient's: one vector per thread as far as a block goes, for a thread
  * holds four tensors' and the sums (16384 x 4096: 151 us with 512 threads of one,
- * 203 with 256 of two). Beyond 16384 elements it keeps a part of them in scratch
- * memory. */
+ * 203 with 256 of two). Beyond 16384 elements it reads a row twice. */
+constexpr uint64_t kHeldGrad = 16384;
+
 template <class F>
 void with_block_grad_shape(uint64_t padded, F f) {
   if (padded <= 512) f(Tag<64>{}, Tag<1>{});
@@ -76,9 +77,7 @@ void with_block_grad_shape(uint64_t padded, F f) {
   else if (padded <= 2048) f(Tag<256>{}, Tag<1>{});
   else if (padded <= 4096) f(Tag<512>{}, Tag<1>{});
   else if (padded <= 8192) f(Tag<1024>{}, Tag<1>{});
-  else if (padded <= 16384) f(Tag<1024>{}, Tag<2>{});
-  else if (padded <= 32768) f(Tag<512>{}, Tag<8>{});
-  else f(Tag<1024>{}, Tag<8>{});
+  else f(Tag<1024>{}, Tag<2>{});
 }
 
 /* Groups that share the rows: as many as are resident at a time, but some four
@@ -315,6 +314,11 @@ int zs_block_norm_backward(const void *dy, const void *h, const float *rstd, con
   if (rows) {
     with16(dtype, [&](auto dt) {
       with_bool(al, [&](auto v) {
+        if (padded_of(cols) > kHeldGrad) {
+          hipLaunchKernelGGL((block_grad_wide_kernel<decltype(dt)::value, decltype(v)::value>),
+                             dim3(parts), dim3(1024), 0, s, a);
+          return;
+        }
         with_block_grad_shape(padded_of(cols), [&](auto g, auto items) {
           constexpr int G = decltype(g)::value, block = G < 128 ? 256 : G, per = block / G;
           hipLaunchKernelGGL((block_grad_kernel<decltype(dt)::value, decltype(v)::value, G,

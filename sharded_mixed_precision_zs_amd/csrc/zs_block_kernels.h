@@ -288,7 +288,7 @@ __device__ __forceinline__ void load_grad(const void *m, uint64_t at, uint32_t t
  * the rest while the row's own first sum is joined: in registers for no more
  * than a row, two blocks share a CU's. */
 template <int DT, bool AL, int G, int ITEMS>
-__global__ __launch_bounds__(G < 128 ? 256 : G, G == 512 && ITEMS > 1 ? 2 : 4) void block_grad_kernel(BlockGradArgs a) {
+__global__ __launch_bounds__(G < 128 ? 256 : G, 4) void block_grad_kernel(BlockGradArgs a) {
   constexpr int kRows = G < 128 ? 256 / G : 1;   /* several only without barriers */
   __shared__ float sums[2][2][G / 64];
   const uint32_t t = threadIdx.x % G;
@@ -413,6 +413,99 @@ __global__ __launch_bounds__(G < 128 ? 256 : G, G == 512 && ITEMS > 1 ? 2 : 4) v
         if (a.x) a.part[((uint64_t)p * 2 + 1) * a.cols + c] = share(i, 1, j);
       }
     }
+}
+
+/* A thread's eight elements of a row, from memory. */
+template <int DT, bool AL>
+struct BlockGradVec {
+  float d[8], h[8], g[8], e[8], x[8], q[8];   /* e: dres + r2 g2 dy; q: g1 gate */
+  bool kept[8];
+
+  __device__ __forceinline__ BlockGradVec(const BlockGradArgs &a, uint64_t row, uint32_t v,
+                                          float rstd, uint64_t offset) {
+    const uint64_t at = row * a.cols, c = (uint64_t)v * 8;
+    load8<DT, AL>(static_cast<const uint16_t *>(a.dy) + at, c, a.cols, d);
+    load8<DT, AL>(static_cast<const uint16_t *>(a.h) + at, c, a.cols, h);
+    load8<DT, AL>(a.gain, c, a.cols, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = x[j] = 0.0f, q[j] = 1.0f, kept[j] = true;
+    if (a.dres) load8<DT, AL>(static_cast<const uint16_t *>(a.dres) + at, c, a.cols, e);
+    if (a.x) load8<DT, AL>(static_cast<const uint16_t *>(a.x) + at, c, a.cols, x);
+    if (a.post_gain) load8<DT, AL>(a.post_gain, c, a.cols, q);
+    if (a.gate) {
+      float gate[8];
+      load8<DT, AL>(a.gate, c, a.cols, gate);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] *= gate[j];
+    }
+    if (a.drop.threshold) {
+      const RandomWords w = random_words(a.drop, offset, v, (uint32_t)row);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) kept[j] = zs::kept(w, j, a.drop.threshold);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = fmaf(rstd, d[j] * g[j], e[j]);
+  }
+};
+
+/* Rows whose vectors and shares a block's registers and LDS do not hold: read
+ * twice, and their shares added to in memory, a word of its own for each of a
+ * thread's (2048 x 32768 bf16 403 us; held as above, for the most part in
+ * scratch memory, 1262). One reduction a row: with dh = e - h c,
+ * mean(q x) = (sum(q k e x) - c sum(q k h x)) a / cols. */
+template <int DT, bool AL>
+__global__ __launch_bounds__(1024) void block_grad_wide_kernel(BlockGradArgs a) {
+  constexpr int G = 1024;
+  __shared__ float sums[2][3][G / 64];
+  const uint32_t t = threadIdx.x, p = blockIdx.x, vecs = (a.cols + 7) / 8;
+  const uint64_t offset = a.drop.threshold ? drop_offset(a.drop) : 0;
+  const float scale = a.drop.threshold ? a.branch_scale * a.drop.factor : a.branch_scale;
+  const float inv_cols = 1.0f / (float)a.cols;
+  float *own = a.part + (uint64_t)p * 2 * a.cols;
+  int turn = 0;
+  for (uint64_t row = p; row < a.rows; row += a.parts, turn ^= 1) {
+    const float rstd = a.rstd[row], post_rstd = a.post_rstd ? a.post_rstd[row] : 1.0f;
+    float dot = 0.0f, dot_e = 0.0f, dot_h = 0.0f;
+    for (uint32_t v = t; v < vecs; v += G) {
+      const BlockGradVec<DT, AL> m(a, row, v, rstd, offset);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dot = fmaf(m.d[j] * m.g[j], m.h[j], dot);
+        dot_e = fmaf(m.kept[j] ? scale * m.e[j] * m.q[j] : 0.0f, m.x[j], dot_e);
+        dot_h = fmaf(m.kept[j] ? scale * m.h[j] * m.q[j] : 0.0f, m.x[j], dot_h);
+      }
+    }
+    const float c = row_sum<G>(dot, sums[turn][0]) * inv_cols * rstd * rstd * rstd;
+    float s1 = 0.0f;
+    if (a.post_gain) {
+      dot_e = row_sum<G>(dot_e, sums[turn][1]);
+      dot_h = row_sum<G>(dot_h, sums[turn][2]);
+      s1 = fmaf(-c, dot_h, dot_e) * inv_cols * post_rstd * post_rstd;
+    }
+    for (uint32_t v = t; v < vecs; v += G) {
+      const BlockGradVec<DT, AL> m(a, row, v, rstd, offset);
+      const uint64_t at = row * a.cols;
+      const bool first = row == p;
+      float r[8], dn[8], sg[8] = {}, su[8] = {};
+      if (!first) {
+        load8<ZS_FP32, false>(own, (uint64_t)v * 8, a.cols, sg);
+        if (a.x) load8<ZS_FP32, false>(own + a.cols, (uint64_t)v * 8, a.cols, su);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float dh = fmaf(-m.h[j], c, m.e[j]), o = m.kept[j] ? scale * dh : 0.0f;
+        r[j] = dh * a.residual_scale;
+        dn[j] = o * m.q[j];
+        if (a.post_gain) dn[j] = post_rstd * fmaf(-m.x[j], s1, dn[j]);
+        sg[j] = fmaf(m.d[j], m.h[j] * rstd, sg[j]);
+        su[j] = fmaf(o, m.x[j] * post_rstd, su[j]);
+      }
+      store8f<false, false>(own, (uint64_t)v * 8, a.cols, sg);
+      if (a.x) store8f<false, false>(own + a.cols, (uint64_t)v * 8, a.cols, su);
+      store8<DT, AL, true>(a.dresidual + at, (uint64_t)v * 8, a.cols, r);
+      store8<DT, AL, true>(a.dx + at, (uint64_t)v * 8, a.cols, dn);
+    }
+  }
 }
 
 /* The shares joined in order, as norm_gain_kernel does: blockIdx.y 0 for dg2,

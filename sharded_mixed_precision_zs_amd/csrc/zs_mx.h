@@ -163,6 +163,32 @@ __device__ __forceinline__ void load8(const void *row, uint64_t col, uint64_t co
   }
 }
 
+/* Eight floats of a row; LATER as below. */
+template <bool AL, bool LATER>
+__device__ __forceinline__ void store8f(float *row, uint64_t col, uint64_t cols,
+                                        const float (&x)[8]) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  if constexpr (AL) {
+    if (col >= cols) return;
+    f32x4 *p = reinterpret_cast<f32x4 *>(row + col);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const f32x4 w = {x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+      if constexpr (LATER) __builtin_nontemporal_store(w, p + j);
+      else p[j] = w;
+    }
+  } else if (col + 8 <= cols) {
+    Loose32 w;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w.x[j] = x[j];
+    *reinterpret_cast<Loose32 *>(row + col) = w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < cols) row[col + j] = x[j];
+  }
+}
+
 /* Eight 16-bit elements of a row; LATER: stored non-temporally, past the
  * caches, which what is read next keeps then. */
 template <bool AL, bool LATER = false>

@@ -415,3 +415,43 @@ def test_block_wide_rows_and_their_gradient(zs):
             close(got, w[k], U[BF16] * (w[k].abs() + inner) + inner + TINY[BF16], k)
         for k, got in zip(("dgain", "dpost_gain", "dgate"), s3):
             close(got, w[k], (70 * 2.0 ** -24 + chain) * mag[k] + TINY[FP32], k)
+        dy2, h2, again = dy.clone(), h.clone(), [torch.empty_like(t) for t in s3]
+        zs.zs_block_norm_backward(dy2, h2, rstd, d["gain"], h2, dy2, again[0], ws, x=d["x"],
+                                  post_gain=d["post_gain"], post_rstd=post_rstd, gate=d["gate"],
+                                  dpost_gain=again[1], dgate=again[2], residual_scale=0.875,
+                                  branch_scale=0.55)
+        assert torch.equal(h2, dx) and torch.equal(dy2, dr)
+        assert all(torch.equal(a, b) for a, b in zip(again, s3))
+
+
+def test_block_wide_rows_shares(zs):
+    """More rows than shares, with dropout, where the shares are added to in memory."""
+    r, c = 600, 16392
+    g = gen("shares")
+    v = dict(x=randn(g, r, c).to(BF16), gain=(1 + 0.1 * randn(g, c)).to(BF16),
+             post_gain=(1 + 0.1 * randn(g, c)).to(BF16), gate=(0.3 + 0.2 * randn(g, c)).to(BF16))
+    h, dy, dres = randn(g, r, c).to(BF16), (0.1 * randn(g, r, c)).to(BF16), randn(g, r, c).to(BF16)
+    d = {k: t.cuda() for k, t in v.items()}
+    rstd = 1 / torch.sqrt(h.double().square().mean(1) + 1e-5)
+    post_rstd = 1 / torch.sqrt(v["x"].double().square().mean(1) + 1e-5)
+    rstd, post_rstd = rstd.float(), post_rstd.float()
+    mask = torch.ones(r, c, dtype=BF16, device="cuda")
+    zs.zs_dropout(mask, mask, (0.5, SEED, OFFSET))     # its bits are tested above: 0 and 2
+    dx, dr = torch.empty_like(mask), torch.empty_like(mask)
+    s3 = [torch.empty(c, device="cuda") for _ in range(3)]
+    ws = torch.empty(zs.zs_block_norm_backward_workspace(r, c), dtype=torch.uint8, device="cuda")
+    zs.zs_block_norm_backward(dy.cuda(), h.cuda(), rstd.cuda(), d["gain"], dx, dr, s3[0], ws,
+                              x=d["x"], post_gain=d["post_gain"], post_rstd=post_rstd.cuda(),
+                              gate=d["gate"], dpost_gain=s3[1], dgate=s3[2], dres=dres.cuda(),
+                              branch_scale=0.5, dropout=(0.5, SEED, OFFSET))
+    w, mag = ref.block_grad(dbl(dy), dbl(h), dbl(rstd), dbl(v["gain"]), dbl(dres), dbl(v["x"]),
+                            dbl(post_rstd), dbl(v["post_gain"]), dbl(v["gate"]), 1.0, 0.5,
+                            dbl(mask.cpu()))
+    # a mean's chain: 24 elements of a thread, 6 levels of lanes, 16 waves; ten roundings
+    chain = (24 + 6 + 16 + 10) * 2.0 ** -24
+    for k, got in (("dx", dx), ("dresidual", dr)):
+        inner = (2 if k == "dx" else 1) * chain * mag[k]
+        close(got, w[k], U[BF16] * (w[k].abs() + inner) + inner + TINY[BF16], k)
+    for k, got in zip(("dgain", "dpost_gain", "dgate"), s3):
+        # a share's three rows, 8 of 32 shares at a time, 32 runs
+        close(got, w[k], ((3 + 32 + 32 + 3) * 2.0 ** -24 + chain) * mag[k] + TINY[FP32], k)
