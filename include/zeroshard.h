@@ -710,6 +710,7 @@ int zs_block_norm_forward(const void *x, const void *residual, const void *post_
  *          post_gain or gate, NULL otherwise; zeros when rows == 0.
  *   workspace: zs_block_norm_backward_workspace(rows, cols) bytes, 4-byte
  *          aligned.
+ * Rows above 16384 elements are read twice (2.5 times the time and more).
  * Errors: as zs_block_norm_forward; a workspace too small is
  * ZS_ERR_INVALID_ARG, 2^32 rows or more ZS_ERR_UNSUPPORTED. */
 uint64_t zs_block_norm_backward_workspace(uint64_t rows, uint64_t cols);

