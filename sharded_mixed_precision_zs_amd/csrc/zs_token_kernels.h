@@ -586,7 +586,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) x[i] = token_vec(buf, in, i * (NT * 16));
   }
-  for (;; turn ^= 1) {
+  for (;;) {
     /* rows are told apart by a scalar that the compiler cannot follow: it would
      * keep a pointer of its own in vector registers for every use */
     asm volatile("" : "+s"(row));
@@ -680,6 +680,11 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
       __builtin_amdgcn_sched_barrier(0);
     }
     if (!more) return;
+    /* A wave may still read a row's sums while another is at the next row: that
+     * one has the other half of them, and no wave reaches the row after it before
+     * all have passed its barrier. A row without a token has no barrier, and so
+     * takes no half: the next one's would be the one that is still read. */
+    if (in.live) turn ^= 1;
     row = next;
     in = after;
   }

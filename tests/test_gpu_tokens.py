@@ -501,3 +501,72 @@ def test_one_token_and_many_equal_ones(zs):
         q = torch.full((5, vocab), 1.0 / vocab, dtype=F64)
         g = ref.logit_grad(q, ids, torch.full((5,), -1.0, dtype=F64))
         check(grad, g, U[BF16] * g.abs() * 1.001 + 2.0 ** -20 * g.abs(), "grad")
+
+
+# ---- rows that a block walks -----------------------------------------------------
+
+def gpu_close(got, want, tol, what):
+    """As check, of finite values, where they lie."""
+    err = (got.double() - want).abs()
+    bad = ~(err <= tol)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {err.numel()} off; rows " \
+        f"{torch.nonzero(bad)[:4].tolist()}"
+
+
+# rows, vocabulary, type, threads of a block, rows of 64 threads that a CU holds
+WALKS = [(600, 66000, BF16, 512, 8), (1100, 35001, FP16, 512, 16), (2100, 9001, FP32, 256, 16),
+         (4200, 8301, BF16, 128, 16), (8300, 4200, BF16, 64, 16), (8300, 2049, FP16, 64, 16)]
+
+
+@pytest.mark.parametrize("rows,vocab,dtype,threads,held", WALKS,
+                         ids=[f"{w[0]}x{w[1]}" for w in WALKS])
+def test_policy_rows_walked(zs, rows, vocab, dtype, threads, held):
+    """Blocks that take a third row and more, whose second has a token, none, or no weight: a
+    row without a token passes no barrier between the sums of those around it. Some tokens have
+    less than e^-41 of the mass, so that their row is summed again. The 64-bit forms run on the
+    GPU: products, exponentials and sums alone."""
+    announce(f"policy walk {dtype} {rows}x{vocab}")
+    blocks = torch.cuda.get_device_properties(0).multi_processor_count * held * 64 // threads
+    z, ids, g = problem(rows, vocab, dtype)
+    at = torch.arange(rows)
+    ids = (ids % vocab).int()
+    ids[(at // blocks % 2 == 1) & (at % 4 == 0)] = -1
+    weight = torch.rand(rows, generator=g) + 0.5
+    weight[(at // blocks % 2 == 1) & (at % 4 == 1)] = 0
+    z, ids, weight = z.cuda(), ids.cuda(), weight.cuda()
+    for first in (0, 1, 2, 3):           # of the first and the third turn, and one of the second
+        rare = torch.arange(first, rows, 2 * blocks)[:4].cuda()
+        z[rare, ids[rare].clamp(min=0).long()] = -60
+    z[blocks + 2, ids[blocks + 2].long()] = -60
+    adv = torch.randn(rows, generator=g).cuda()
+    lp = ref.logprob(z.double(), ids, 1.0)[0]
+    drift = torch.tensor([0.05, 0.4, -0.4, 0.1, -0.1, 0.3, -0.3])[at % 7].cuda()
+    old, refs = (lp - drift.double()).float(), (lp + 0.3 * torch.randn(rows, generator=g).cuda()).float()
+    logp, loss = torch.full((2, rows), 9.0, device="cuda")
+    grad = torch.full_like(z, 7.0)
+    ws = torch.empty(zs.zs_policy_workspace(rows, vocab, code(zs, dtype)), dtype=torch.uint8,
+                     device="cuda")
+
+    def run(z, logp, loss, grad):
+        zs.zs_policy(z, ids, adv, loss, old_logp=old, ref_logp=refs, clip_low=0.2, clip_high=0.28,
+                     kl_weight=0.05, row_weight=weight, loss_scale=64.0, logp=logp, grad=grad,
+                     workspace=ws)
+
+    run(z, logp, loss, grad)
+    low, high, kl = (float(torch.tensor(v)) for v in (0.2, 0.28, 0.05))
+    lp, want, wg, mag = ref.policy(z.double(), ids, 1.0, adv.double(), old.double(), refs.double(),
+                                   low, high, kl, weight.double(), 64.0)
+    delta, dlogp = errors(z, 1.0, lp)
+    gpu_close(logp, lp, dlogp + 1e-45, "logp")
+    gpu_close(loss, want, (mag / 64 + want.abs()) * (2 * dlogp + 2.0 ** -20) + 1e-45, "loss")
+    q = torch.softmax(z.double(), 1)
+    live = (ids >= 0) & (ids < vocab)
+    mine = ids.clamp(0, vocab - 1).long().unsqueeze(1)
+    share = q.scatter(1, mine, torch.where(live, q.scatter(1, mine, 0.0).sum(1),
+                                           q.gather(1, mine).squeeze(1)).unsqueeze(1))
+    inner = (wg.abs() * (3 * delta.unsqueeze(1) + 2.0 ** -22)
+             + share * (mag * (2 * dlogp + 2.0 ** -20)).unsqueeze(1))
+    gpu_close(grad, wg, U[dtype] * (wg.abs() + inner) + inner + TINY[dtype], "grad")
+    l2, s2 = torch.full((2, rows), 9.0, device="cuda")
+    run(z, l2, s2, z)
+    assert torch.equal(l2, logp) and torch.equal(s2, loss) and torch.equal(z, grad)
