@@ -779,9 +779,10 @@ int zs_activation_backward(const void *dc, const void *pre, int activation, int 
  *            may be the logits' own buffer.
  *   workspace: the entry point's _workspace(rows, vocab, dtype) bytes, 16-byte
  *            aligned.
- * Logits of -inf are tokens that cannot be chosen; a NaN, +inf or a row of
- * -inf gives a NaN row. A row's result depends on the row, on how it is aligned
- * to 16 bytes and, in a sum's last bits, on the number of rows. Errors of all three:
+ * Logits of -inf are tokens that cannot be chosen, logp -inf if the row's own
+ * is one; a NaN, +inf or a row of -inf gives a NaN row. A row's result depends
+ * on the row, on how it is aligned to 16 bytes and, in a sum's last bits, on
+ * the number of rows. Errors of all three:
  * ZS_ERR_INVALID_ARG (null pointers, dtype, temperature not finite or below
  * 2^-126, loss_scale not finite and > 0, vocab 0 or above 2^31 - 1, rows
  * closer than vocab, workspace too small), ZS_ERR_UNSUPPORTED (2^31 rows or

@@ -13,9 +13,10 @@
  * Terms are 2^(z c - I), c = log2(e) / tau and I the whole number next to the
  * token's own z c: no pass over the row has to find its maximum first, and a
  * term is added as its logit arrives. Where that lets the sum leave 2^60 (a
- * token that has less than e^-41 of the mass) it is formed again by the row's
- * maximum. The rounding of an exponent is relative to its size, which is that
- * of the log-probability.
+ * token that has less than e^-41 of the mass), or where the token's logit is
+ * -inf and no place to count from, it is formed again by the row's maximum; so
+ * a part that is counted from -inf holds nothing but -inf. The rounding of an
+ * exponent is relative to its size, which is that of the log-probability.
  *
  * Bound by HBM: the policy loss reads a row once, into a block's registers,
  * the preference loss twice, for a row's gradient needs its whole pair.
@@ -294,7 +295,8 @@ __global__ __launch_bounds__(NT) void token_stats_kernel(TokenArgs a) {
     reduce_put(sum, SumOf{}, dpart[again]);
     __syncthreads();
     sum = reduce_get<NT>(SumOf{}, dpart[again]);
-    if (again || sum < (double)kTokenTop) break;   /* the same for the whole block */
+    /* the same for the whole block */
+    if (again || (sum < (double)kTokenTop && own != -INFINITY)) break;
     float max = single;
     for (uint32_t v = v0 + t; v < v1; v += NT) {
       float e[ve];
@@ -629,7 +631,8 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
         reduce_put(sum64, SumOf{}, dpart[turn][again]);
         __syncthreads();
         rest = reduce_get<NT>(SumOf{}, dpart[turn][again]);
-        if (again || rest < (double)kTokenTop) break;   /* uniform over the block */
+        /* uniform over the block */
+        if (again || (rest < (double)kTokenTop && own != -INFINITY)) break;
         VecMax<DT> max;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) max.add(x[i]);

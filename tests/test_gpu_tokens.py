@@ -570,3 +570,57 @@ def test_policy_rows_walked(zs, rows, vocab, dtype, threads, held):
     l2, s2 = torch.full((2, rows), 9.0, device="cuda")
     run(z, l2, s2, z)
     assert torch.equal(l2, logp) and torch.equal(s2, loss) and torch.equal(z, grad)
+
+
+# ---- tokens that cannot be chosen -------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+@pytest.mark.parametrize("tau", [1.0, 0.7])
+def test_tokens_that_cannot_be_chosen(zs, dtype, tau):
+    """A token whose logit is -inf, among ordinary others, others far below and far above 0, and
+    a single other one: its log-probability is -inf and the row's gradient the definition's, by
+    rows, in parts, and in two passes."""
+    for rows, vocab in ((5, 9), (5, 1000), (5, 20000), (6, 50257), (5, 140001), (70, 50257),
+                        (70, 140001)):
+        announce(f"-inf token {dtype} {rows}x{vocab}")
+        z, ids, g = problem(rows, vocab, dtype)
+        ids = (ids % vocab).int()
+        at = torch.arange(4)
+        z[1] -= 200
+        z[3] += 200
+        z[2] = -math.inf
+        z[2, (int(ids[2]) + vocab // 2 + 1) % vocab] = -7
+        z[at, ids[:4].long()] = -math.inf
+        want, q, _ = ref.logprob(z.double(), ids, float(torch.tensor(tau)))
+        assert bool((want[:4] == -math.inf).all()) and bool(torch.isfinite(want[4:]).all())
+        finite = torch.where(torch.isfinite(want), want, 0.0)
+        delta, dlogp = errors(z, tau, finite)
+        out = torch.full((rows,), 9.0, device="cuda")
+        ws = torch.empty(zs.zs_logprob_workspace(rows, vocab, code(zs, dtype)), dtype=torch.uint8,
+                         device="cuda")
+        zs.zs_logprob(z.cuda(), ids.cuda(), out, temperature=tau, workspace=ws)
+        check(out, want, dlogp + 1e-45, "logp alone")
+        # without the sampler's the ratio is 1, and the slope -A
+        adv = torch.tensor([1.0, -0.7])[torch.arange(rows) % 2]
+        grad = torch.full_like(z, 7.0).cuda()
+        logp, loss = run_policy(zs, z.cuda(), ids, tau, adv, None, None, None, 64.0, grad)
+        check(logp, want, dlogp + 1e-45, "logp")
+        assert torch.equal(loss.cpu(), -adv)
+        slope = -adv.double() * 64 / float(torch.tensor(tau))
+        check_grad(grad, ref.logit_grad(q, ids, slope), z, ids, tau, delta,
+                   slope.abs() * 2.0 ** -20, dtype, "grad")
+        # with it the ratio is 0: clipped below for A < 0, no slope either way
+        old = (finite - 0.05).float()
+        logp, loss = run_policy(zs, z.cuda(), ids, tau, adv, old, None, None, 64.0, grad)
+        low = 1 - float(torch.tensor(0.2))
+        clipped = torch.tensor([0.0, 0.7 * low])[torch.arange(4) % 2]
+        check(loss[:4], clipped, 1e-6, "loss")
+        assert not grad[:4].any() and torch.isfinite(grad.float()).all()
+        # a preferred sequence with such a token: its loss is inf, its slope -beta
+        grad.fill_(7.0)
+        l2, s2 = run_preference(zs, z.cuda(), ids, [0, 1, 1], grad, None, beta=0.25,
+                                temperature=tau)
+        assert s2[0] == -math.inf and s2[1] == 0 and l2[0] == math.inf
+        slope = torch.full((1,), -0.25 / float(torch.tensor(tau)), dtype=F64)
+        check_grad(grad[:1], ref.logit_grad(q[:1], ids[:1], slope), z[:1], ids[:1], tau, delta[:1],
+                   slope.abs() * 2.0 ** -20, dtype, "pair grad")
