@@ -201,7 +201,7 @@ int zs_block_norm_forward(const void *x, const void *residual, const void *post_
   a.residual_scale = residual_scale;
   a.branch_scale = branch_scale;
   /* 13 bits of it times 11 of the residual's are 24 */
-  a.near_dropped = short_float(residual_scale) ? 0.0f : 0x1p-22f;
+  a.near_dropped = short_float(residual_scale) ? 0x1p-100f : 0x1p-22f;
   const bool al = cols % 8 == 0 && aligned(x, 16) && aligned(residual, 16) &&
                   aligned(post_gain, 16) && aligned(gate, 16) && aligned(gain, 16) &&
                   aligned(h, 16) && aligned(y, 16);

@@ -40,7 +40,7 @@ struct BlockArgs {
   uint32_t cols, padded;
   float eps;
   double inv_cols, residual_scale, branch_scale;
-  float near_dropped;   /* 0 where residual_scale times 16 bits is exact, else 2^-22 */
+  float near_dropped;   /* 2^-100 where residual_scale times 16 bits is exact, else 2^-22 */
   DropArgs drop;
 };
 
@@ -58,7 +58,8 @@ __device__ __forceinline__ float odd_float(double v) {
 /* Eight sums l r + c p rounded once to 16 bits. In fp32 a sum is off by at most
  * kNear times |l r| + |sum|: c p by 2^-24 for c's rounding, and as much for p's
  * in fp16, l r, the sum and its ends by 2^-24 each; or by nothing where p is 0
- * and l r exact. Where both ends of that have the same 16 bits, those are the
+ * and l r exact, and `near` so small that both ends are the sum (0 would make
+ * NaN of an infinite size, at both ends alike). Where both ends of that have the same 16 bits, those are the
  * exact sum's. Where they differ, in some 2^-12 of bf16 sums and 2^-9 of fp16's,
  * the two of a word are formed in binary64. (Short scales without a first norm
  * make ties, and go that way more often. Where a sum is below fp32's normal

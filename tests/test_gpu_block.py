@@ -455,3 +455,26 @@ def test_block_wide_rows_shares(zs):
     for k, got in zip(("dgain", "dpost_gain", "dgate"), s3):
         # a share's three rows, 8 of 32 shares at a time, 32 runs
         close(got, w[k], ((3 + 32 + 32 + 3) * 2.0 ** -24 + chain) * mag[k] + TINY[FP32], k)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=str)
+@pytest.mark.parametrize("rs", [1.0, 0.875, 0.3])
+def test_block_infinite_residual_stays_infinite(zs, dtype, rs):
+    """An infinite residual under a dropped and a kept element: h has the infinity, and the norm
+    behind it is NaN there and 0 in the rest of the row. A very large one stays what it is."""
+    for c in (96, 1001, 4096):
+        announce(f"block inf {dtype} {rs} {c}")
+        v, f = problem(5, c, dtype, True, True, 0.25)
+        for row, sign, keeps in ((1, 1, False), (2, -1, False), (3, 1, True)):
+            at = int(torch.nonzero((f[row] > 0) == keeps)[7])
+            v["res"][row, at] = sign * math.inf
+        # finite, but not its size twice
+        v["res"][4, int(torch.nonzero(f[4] == 0)[5])] = 2e38 if dtype is BF16 else 6e4
+        h, post_rstd, rstd, y, *_ = run_forward(zs, v, dtype, 0.25, rs=rs)
+        want = ref.block(*(dbl(v[k]) for k in ("x", "res", "post_gain", "gate", "gain")),
+                         float(torch.tensor(1e-5)), float(torch.tensor(rs)),
+                         float(torch.tensor(0.55)), f, dtype)
+        assert torch.equal(h.cpu().double(), want[0])
+        close(rstd, want[3], 2.0 ** -23 * want[3], "rstd")
+        close(y, want[4], U[dtype] * want[4].abs() * 1.01 + TINY[dtype], "y")
+        assert int(torch.isnan(y.float()).sum()) == 3
