@@ -141,14 +141,22 @@ __device__ __forceinline__ TokenMass32 token_mass32(double rest, float z, const 
 }
 
 /* exp(d) - 1 - d, by its series near 0, where the difference would leave
- * rounding. */
-__device__ __forceinline__ float exp_rest(float d) {
-  if (d == INFINITY) return d;   /* not the difference of two infinities */
-  if (!(fabsf(d) < 1.0f)) return expf(d) - 1.0f - d;
+ * rounding; and its slope exp(d) - 1, from the series too there, but not
+ * elsewhere: of a d far below 0 the sum with d would leave nothing of the 1. */
+struct ExpRest {
+  float rest, slope;
+};
+
+__device__ __forceinline__ ExpRest exp_rest(float d) {
+  if (!(fabsf(d) < 1.0f)) {
+    const float e = expf(d) - 1.0f;
+    return {d == INFINITY ? d : e - d, e};   /* not the difference of two infinities */
+  }
   float s = 1.0f + d * (1.0f / 12.0f);
 #pragma unroll
   for (int k = 11; k > 2; --k) s = fmaf(d * (1.0f / (float)k), s, 1.0f);
-  return 0.5f * d * d * s;
+  const float rest = 0.5f * d * d * s;
+  return {rest, d + rest};
 }
 
 struct Slope {
@@ -179,9 +187,9 @@ __device__ __forceinline__ Slope policy_slope(const TokenArgs &a, const PolicyIn
   s.loss = -(above ? high : below ? low : r) * adv;
   s.slope = above || below ? 0.0f : -r * adv;
   if (a.ref_logp) {
-    const float d = (float)((T)in.ref_logp - logp), rest = exp_rest(d);
-    s.loss = fmaf(a.kl_weight, rest, s.loss);
-    s.slope = fmaf(-a.kl_weight, d + rest, s.slope);
+    const ExpRest k = exp_rest((float)((T)in.ref_logp - logp));
+    s.loss = fmaf(a.kl_weight, k.rest, s.loss);
+    s.slope = fmaf(-a.kl_weight, k.slope, s.slope);
   }
   s.loss *= in.weight;
   s.slope *= in.weight;

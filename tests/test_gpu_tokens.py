@@ -624,3 +624,25 @@ def test_tokens_that_cannot_be_chosen(zs, dtype, tau):
         slope = torch.full((1,), -0.25 / float(torch.tensor(tau)), dtype=F64)
         check_grad(grad[:1], ref.logit_grad(q[:1], ids[:1], slope), z[:1], ids[:1], tau, delta[:1],
                    slope.abs() * 2.0 ** -20, dtype, "pair grad")
+
+
+# the values that d takes are far from 0, where exp(d) - 1 - d and exp(d) - 1 part
+KL_SHAPES = [(6, 1000), (6, 140001), (70, 140001)]
+
+
+def test_policy_far_from_the_reference(zs):
+    """A reference that gives a token nothing, or far less than the student: the KL term's slope
+    is that of exp(d) - 1, -1 in the end, and keeps its precision."""
+    for rows, vocab in KL_SHAPES:
+        announce(f"policy far from the reference {rows}x{vocab}")
+        z, ids, g = problem(rows, vocab, FP32)
+        ids = (ids % vocab).int()
+        lp = ref.logprob(z.double(), ids, 1.0)[0]
+        d = torch.tensor([-math.inf, -3e7, -1000.5, -20.0, -1.0, 1.0])[torch.arange(rows) % 6]
+        refs = (lp + d.double()).float()
+        for adv in (torch.zeros(rows), torch.full((rows,), 0.5)):
+            grad = torch.full_like(z, 7.0).cuda()
+            logp, loss = run_policy(zs, z.cuda(), ids, 1.0, adv, None, refs, None, 64.0, grad)
+            check_policy(z, ids, 1.0, adv, None, refs, None, 64.0, logp, loss, grad,
+                         f"{rows}x{vocab}")
+            assert torch.isfinite(grad).all()
