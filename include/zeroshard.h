@@ -803,7 +803,8 @@ int zs_logprob(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uin
  * clipped (A > 0 and r > 1 + clip_high, or A < 0 and r < 1 - clip_low).
  *   advantage: fp32[rows], A.
  *   old_logp : fp32[rows], the sampler's; NULL: r is 1 (its slope is A's).
- *   ref_logp : fp32[rows], the reference model's; NULL: no KL term.
+ *   ref_logp : fp32[rows], the reference model's; NULL, or a kl_weight of 0: no
+ *              KL term.
  *   row_weight: NULL (all 1), or fp32[rows]. A row of weight 0 gives logp and
  *              loss 0 and a zero gradient, whatever its logits.
  *   logp     : NULL, or fp32[rows]; loss: fp32[rows]; 0 for rows without a

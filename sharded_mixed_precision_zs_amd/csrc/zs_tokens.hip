@@ -270,7 +270,7 @@ int zs_policy(const void *logits, int dtype, uint64_t rows, uint64_t vocab, uint
   a.dev = dev;
   a.advantage = advantage;
   a.old_logp = old_logp;
-  a.ref_logp = ref_logp;
+  a.ref_logp = kl_weight != 0.0f ? ref_logp : nullptr;   /* 0 times an infinity is no term */
   a.clip_low = clip_low;
   a.clip_high = clip_high;
   a.kl_weight = kl_weight;

@@ -646,3 +646,18 @@ def test_policy_far_from_the_reference(zs):
             check_policy(z, ids, 1.0, adv, None, refs, None, 64.0, logp, loss, grad,
                          f"{rows}x{vocab}")
             assert torch.isfinite(grad).all()
+
+
+def test_policy_without_kl_weight_has_no_kl_term(zs):
+    """A weight of 0 is no term, also where exp(d) is beyond fp32 or d is not finite."""
+    for rows, vocab in KL_SHAPES:
+        announce(f"policy kl 0 {rows}x{vocab}")
+        z, ids, g = problem(rows, vocab, BF16)
+        ids = (ids % vocab).int()
+        adv, o, _, _ = policy_inputs(z, ids, g, 1.0, True, False, False)
+        refs = torch.tensor([-math.inf, 100.0, 3e38, -3.0, math.inf, math.nan])[torch.arange(rows) % 6]
+        a, b = torch.full((2,) + tuple(z.shape), 7.0, dtype=BF16, device="cuda")
+        want = run_policy(zs, z.cuda(), ids, 1.0, adv, o, None, None, 64.0, a, kl=0.0)
+        got = run_policy(zs, z.cuda(), ids, 1.0, adv, o, refs, None, 64.0, b, kl=0.0)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(a, b)
+        assert torch.isfinite(got[1]).all()
