@@ -182,7 +182,8 @@ __device__ __forceinline__ Slope policy_slope(const TokenArgs &a, const PolicyIn
   const float adv = in.advantage;
   const float r = a.old_logp ? expf((float)(logp - (T)in.old_logp)) : 1.0f;
   const float low = 1.0f - a.clip_low, high = 1.0f + a.clip_high;
-  const bool above = adv > 0.0f && r > high, below = adv < 0.0f && r < low;
+  /* without an advantage r is clipped too: it may lie beyond fp32, times 0 */
+  const bool above = adv >= 0.0f && r > high, below = adv < 0.0f && r < low;
   Slope s;
   s.loss = -(above ? high : below ? low : r) * adv;
   s.slope = above || below ? 0.0f : -r * adv;

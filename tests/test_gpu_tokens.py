@@ -661,3 +661,22 @@ def test_policy_without_kl_weight_has_no_kl_term(zs):
         got = run_policy(zs, z.cuda(), ids, 1.0, adv, o, refs, None, 64.0, b, kl=0.0)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(a, b)
         assert torch.isfinite(got[1]).all()
+
+
+def test_policy_without_advantage(zs):
+    """An advantage of 0 gives a loss of 0 and no slope, also where the ratio is beyond fp32."""
+    for rows, vocab in KL_SHAPES:
+        announce(f"policy advantage 0 {rows}x{vocab}")
+        z, ids, g = problem(rows, vocab, BF16)
+        ids = (ids % vocab).int()
+        lp = ref.logprob(z.double(), ids, 1.0)[0]
+        adv = torch.tensor([0.0, -0.0, 0.7])[torch.arange(rows) % 3]
+        old = (lp - 100).float()                       # a ratio of e^100
+        grad = torch.full_like(z, 7.0).cuda()
+        logp, loss = run_policy(zs, z.cuda(), ids, 1.0, adv, old, None, None, 64.0, grad)
+        clipped = -(1 + float(torch.tensor(0.28))) * adv.double()
+        check(loss, clipped, 2.0 ** -22 * clipped.abs(), "loss")
+        assert not grad.any()
+        z[0] = math.nan
+        logp, loss = run_policy(zs, z.cuda(), ids, 1.0, adv, old, None, None, 64.0, grad)
+        assert torch.isnan(loss[0]) and torch.isnan(grad[0].float()).all()
