@@ -356,8 +356,10 @@ __device__ __forceinline__ PairSlope pair_slope(const TokenArgs &a, double delta
   if (a.kind == ZS_PREFERENCE_SIGMOID) {
     const double eps = a.smoothing, small = log1p(exp(-fabs(m)));
     const double up = m > 0.0 ? m : 0.0, down = m > 0.0 ? 0.0 : -m;   /* NaN: small is one */
-    return {(1.0 - eps) * (small + down) + eps * (small + up),
-            beta * (eps / (1.0 + exp(-m)) - (1.0 - eps) / (1.0 + exp(m)))};
+    /* a term of weight 0 is none, also of an infinite difference */
+    const double yes = eps < 1.0 ? (1.0 - eps) * (small + down) : 0.0;
+    const double no = eps > 0.0 ? eps * (small + up) : 0.0;
+    return {yes + no, beta * (eps / (1.0 + exp(-m)) - (1.0 - eps) / (1.0 + exp(m)))};
   }
   if (a.kind == ZS_PREFERENCE_HINGE) {
     const double l = 1.0 - m;

@@ -680,3 +680,27 @@ def test_policy_without_advantage(zs):
         z[0] = math.nan
         logp, loss = run_policy(zs, z.cuda(), ids, 1.0, adv, old, None, None, 64.0, grad)
         assert torch.isnan(loss[0]) and torch.isnan(grad[0].float()).all()
+
+
+def test_preference_of_tokens_that_cannot_be_chosen(zs):
+    """A sequence with a token that cannot be chosen, against one without: with no smoothing the
+    side that it is right on costs nothing, the other one is infinite with a finite slope."""
+    z, ids, _ = problem(8, 600, FP32)
+    ids = (ids % 600).int()
+    z[5, ids[5].long()] = -math.inf
+    for starts, delta in (([0, 4, 8], math.inf), ([4, 8, 8], -math.inf)):
+        for kind, smoothing in (("sigmoid", 0.0), ("sigmoid", 1.0), ("sigmoid", 0.25), ("hinge", 0.0)):
+            grad = torch.full_like(z, 7.0).cuda()
+            loss, seq = run_preference(zs, z.cuda(), ids, starts, grad, None, beta=0.25,
+                                       kind=kind_of(zs, kind), smoothing=smoothing, loss_scale=16.0)
+            good = smoothing if delta < 0 else 1 - smoothing     # weight of the term that is 0
+            assert float(loss) == (0.0 if kind == "hinge" and delta > 0 or
+                                   kind == "sigmoid" and good == 1 else math.inf)
+            k = {"sigmoid": 0.25 * (smoothing if delta > 0 else smoothing - 1),
+                 "hinge": 0.0 if delta > 0 else -0.25}[kind] * 16
+            _, q, _ = ref.logprob(z.double(), ids, 1.0)
+            slope = torch.zeros(8, dtype=F64)
+            slope[starts[0]:starts[1]], slope[starts[1]:starts[2]] = k, -k
+            wg = ref.logit_grad(q, ids, slope)
+            inside = slice(starts[0], starts[2])
+            check(grad[inside], wg[inside], 1e-4 * wg[inside].abs() + TINY[FP32], "grad")
