@@ -110,7 +110,22 @@ struct TokenMass {
   double rest, total, logp;
 };
 
-__device__ __forceinline__ TokenMass token_mass(double rest, float z, const Shift &s) {
+constexpr float kTokenTop = 1.15292150e18f;   /* 2^60 */
+
+/* Whether z's exponent does not give its log-probability: where the shift's
+ * logit lies beyond the exponents' range, so that terms have another c than the
+ * row's, or z itself does, so that its product could overflow. */
+__device__ __forceinline__ bool token_far(float z, const Shift &s, float c) {
+  return s.c != c || !(fabsf(z * c) < kTokenTop);
+}
+
+/* Then its distance from that logit does, whose term is 1, or as near to it as
+ * a distance of 2^60 tells. */
+__device__ __forceinline__ double far_log(float z, const Shift &s, float c) {
+  return ((double)z - (double)s.max) * ((double)c * 0.69314718055994531);
+}
+
+__device__ __forceinline__ TokenMass token_mass(double rest, float z, const Shift &s, float c) {
   TokenMass m;
   const double own = (double)term(z, s);
   m.rest = rest;
@@ -118,7 +133,10 @@ __device__ __forceinline__ TokenMass token_mass(double rest, float z, const Shif
   if (rest <= own && own > 0.0)
     m.logp = -log1p(rest / own);
   else   /* NaN: comes here */
-    m.logp = fma((double)z, (double)s.c, -(double)s.whole) * 0.69314718055994531 - log(m.total);
+    m.logp = (token_far(z, s, c)
+                  ? far_log(z, s, c)
+                  : fma((double)z, (double)s.c, -(double)s.whole) * 0.69314718055994531) -
+             log(m.total);
   return m;
 }
 
@@ -128,7 +146,8 @@ struct TokenMass32 {
   float rest, total, logp;
 };
 
-__device__ __forceinline__ TokenMass32 token_mass32(double rest, float z, const Shift &s) {
+__device__ __forceinline__ TokenMass32 token_mass32(double rest, float z, const Shift &s,
+                                                    float c) {
   TokenMass32 m;
   const float own = term(z, s);
   m.rest = (float)rest;
@@ -136,7 +155,9 @@ __device__ __forceinline__ TokenMass32 token_mass32(double rest, float z, const 
   if (m.rest <= own && own > 0.0f)
     m.logp = -log1pf(m.rest / own);
   else   /* NaN: comes here */
-    m.logp = fmaf(z, s.c, -s.whole) * 0.69314718f - logf(m.total);
+    m.logp = (token_far(z, s, c) ? (float)far_log(z, s, c)
+                                 : fmaf(z, s.c, -s.whole) * 0.69314718f) -
+             logf(m.total);
   return m;
 }
 
@@ -219,8 +240,6 @@ __device__ __forceinline__ TokenPlan make_plan(double rest, double total, float 
  * binary64. 8192 x 128000 bf16 306 us, 6.9 TB/s; rows of 1000 are held up by
  * their one thread's binary64 logarithm (65536 of them 46 us, 2.8 TB/s).
  * ---------------------------------------------------------------------- */
-constexpr float kTokenTop = 1.15292150e18f;   /* 2^60 */
-
 template <int DT>
 __device__ __forceinline__ void leave_out(const RowShape &s, int32_t id, uint32_t v,
                                           float (&e)[kVecElems<DT>]) {
@@ -235,7 +254,7 @@ __device__ __forceinline__ void leave_out(const RowShape &s, int32_t id, uint32_
  * policy loss and plan, as far as they are asked for. */
 __device__ __forceinline__ void finish_token(const TokenArgs &a, uint32_t row, double rest,
                                              float from, float z, int32_t id) {
-  const TokenMass m = token_mass(rest, z, shift_of(from, a.log2_scale));
+  const TokenMass m = token_mass(rest, z, shift_of(from, a.log2_scale), a.log2_scale);
   if (a.logp) a.logp[row] = (float)m.logp;
   if (a.starts) {
     a.lp[row] = m.logp;
@@ -452,7 +471,8 @@ __global__ __launch_bounds__(NT) void token_grad_kernel(TokenArgs a) {
     p = {0.0f, 0.0f, 0.0f, kNoToken};
     if (token_live(a, row, id)) {
       const TokenPart w = join_parts(a, row);
-      const TokenMass m = token_mass(w.rest, load_scalar(a.own, row), shift_of(w.from, a.log2_scale));
+      const TokenMass m = token_mass(w.rest, load_scalar(a.own, row),
+                                     shift_of(w.from, a.log2_scale), a.log2_scale);
       const Slope k = policy_slope(a, policy_in(a, row), m.logp);
       p = make_plan(m.rest, m.total, w.from, k.slope * grad_scale(a), id);
       if (block == 0 && threadIdx.x == 0) {
@@ -651,7 +671,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
         __syncthreads();
         from = reduce_get<NT>(MaxOf{}, fpart[turn]);
       }
-      const TokenMass32 m = token_mass32(rest, own, shift_of(from, a.log2_scale));
+      const TokenMass32 m = token_mass32(rest, own, shift_of(from, a.log2_scale), a.log2_scale);
       const Slope s = policy_slope(a, in.policy, m.logp);
       if (t == 0) {
         if (a.logp) a.logp[row] = m.logp;

@@ -704,3 +704,39 @@ def test_preference_of_tokens_that_cannot_be_chosen(zs):
             wg = ref.logit_grad(q, ids, slope)
             inside = slice(starts[0], starts[2])
             check(grad[inside], wg[inside], 1e-4 * wg[inside].abs() + TINY[FP32], "grad")
+
+
+def test_logits_far_below_the_others(zs):
+    """Tokens whose logit is the type's lowest value, or far below the largest of a row that is
+    itself beyond the exponents' range: the log-probability is their distance over tau."""
+    for rows, vocab in ((6, 1000), (6, 140001), (70, 140001), (70, 50257)):
+        for dtype in (BF16, FP32):
+            for tau in (1.0, 1.7):
+                announce(f"far logits {dtype} {tau} {rows}x{vocab}")
+                z, ids, g = problem(rows, vocab, dtype)
+                ids = (ids % vocab).int()
+                mine = ids[:6].long()
+                top = (mine + vocab // 2 + 1) % vocab
+                z[0, mine[0]] = torch.finfo(dtype).min
+                z[1, mine[1]], z[1, top[1]] = 1e30, 1e31
+                z[2, mine[2]], z[2, top[2]] = -1e25, 1e25
+                z[3, mine[3]], z[3, top[3]] = 3.0, 2e19
+                z[4] = torch.finfo(dtype).min
+                z[4, top[4]] = -1e30
+                z[5] = torch.finfo(dtype).min
+                want, q, _ = ref.logprob(z.double(), ids, float(torch.tensor(tau)))
+                tol = errors(z.clamp(-60, 60), tau, want)[1] + 2.0 ** -22 * want.abs()
+                out = torch.full((rows,), 9.0, device="cuda")
+                ws = torch.empty(zs.zs_logprob_workspace(rows, vocab, code(zs, dtype)),
+                                 dtype=torch.uint8, device="cuda")
+                zs.zs_logprob(z.cuda(), ids.cuda(), out, temperature=tau, workspace=ws)
+                check(out, want.float(), tol, "logp alone")
+                grad = torch.full_like(z, 7.0).cuda()
+                adv = torch.full((rows,), 0.5)
+                logp, loss = run_policy(zs, z.cuda(), ids, tau, adv, None, None, None, 64.0, grad)
+                check(logp, want.float(), tol, "logp")
+                slope = torch.full((rows,), -32.0 / float(torch.tensor(tau)), dtype=F64)
+                wg = ref.logit_grad(q, ids, slope)
+                delta = errors(z.clamp(-60, 60), tau, want)[0]
+                inner = wg.abs() * (3 * delta.unsqueeze(1) + 2.0 ** -20)
+                check(grad, wg, U[dtype] * (wg.abs() + inner) + inner + TINY[dtype], "grad")
