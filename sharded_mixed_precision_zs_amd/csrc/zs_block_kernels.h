@@ -72,8 +72,10 @@ __device__ __forceinline__ u32x4 sums16(const float (&p)[8], const float (&low)[
                                         const float (&r)[8], const float (&near)[8], double c,
                                         double l, const RandomWords &words, uint32_t threshold) {
   const float cf = (float)c, lf = (float)l;
-  /* a scale that is no number reaches what is kept alone */
-  const uint32_t always = fabsf(cf) < INFINITY ? 0 : 1;
+  /* a scale that is no number reaches what is kept alone; and one below fp32's
+   * normal range is off by more than 2^-24 */
+  const uint32_t always =
+      c == 0.0 || (fabsf(cf) >= 0x1p-126f && fabsf(cf) < INFINITY) ? 0 : 1;
   u32x4 w;
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {

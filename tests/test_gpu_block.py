@@ -478,3 +478,19 @@ def test_block_infinite_residual_stays_infinite(zs, dtype, rs):
         close(rstd, want[3], 2.0 ** -23 * want[3], "rstd")
         close(y, want[4], U[dtype] * want[4].abs() * 1.01 + TINY[dtype], "y")
         assert int(torch.isnan(y.float()).sum()) == 3
+
+
+def test_block_scales_below_fp32s_range(zs):
+    """Rows so large, and branch scales so small, that the branch's whole factor is no normal
+    fp32 number: h is still the 64-bit sum rounded once."""
+    for size, bs in ((2e38, 1.0), (2e38, 0.003), (1e35, 0.001), (1e20, 2.0 ** -60), (1.0, 0.0)):
+        for p in (0.0, 0.25):
+            announce(f"block small scale {size} {bs} {p}")
+            v, f = problem(20, 1000, BF16, True, True, p)
+            v["x"] = ((0.5 + 0.5 * torch.rand(20, 1000, generator=gen("sub"))) * size).to(BF16)
+            v["post_gain"] = (0.4 + 0.5 * torch.rand(1000, generator=gen("g"))).to(BF16)
+            v["res"] = (v["res"].float() * bs).to(BF16)
+            h, *_ = run_forward(zs, v, BF16, p, bs=bs)
+            want = ref.block(*(dbl(v[k]) for k in ("x", "res", "post_gain", "gate", "gain")),
+                             float(torch.tensor(1e-5)), 0.875, float(torch.tensor(bs)), f, BF16)
+            assert torch.equal(h.cpu().double(), want[0])
