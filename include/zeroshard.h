@@ -700,7 +700,7 @@ int zs_block_norm_forward(const void *x, const void *residual, const void *post_
  *        a post_gain)
  *   dgain = sum over rows of dy * h * rstd
  *   dpost_gain = gate * u, dgate = post_gain * u,
- *        u = sum over rows of t * x * post_rstd
+ *        u = sum over rows of t * x * post_rstd, without the dropped elements
  *   dy, h, rstd, gain, x, post_rstd, post_gain, gate, dropout and the scales:
  *          as in the forward call; x may be NULL without post_gain and gate.
  *   dres : dtype[rows][cols], what h receives from elsewhere, or NULL.

@@ -377,12 +377,16 @@ __global__ __launch_bounds__(G < 128 ? 256 : G, 4) void block_grad_kernel(BlockG
         o[j] *= scale;
       }
       store8<DT, AL, true>(a.dresidual + at, (uint64_t)(i * G + t) * 8, a.cols, d);
+      if (a.x) upcast<8, DT>(rx[i], x);
       if (a.drop.threshold) {
         const RandomWords w = random_words(a.drop, offset, i * G + t, (uint32_t)row);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = kept(w, j, a.drop.threshold) ? o[j] : 0.0f;
+        for (int j = 0; j < 8; ++j) {   /* x too: 0 times what was replaced could be NaN */
+          const bool stays = kept(w, j, a.drop.threshold);
+          o[j] = stays ? o[j] : 0.0f;
+          x[j] = stays ? x[j] : 0.0f;
+        }
       }
-      if (a.x) upcast<8, DT>(rx[i], x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         share(i, 1, j) = fmaf(o[j], x[j] * post_rstd, share(i, 1, j));
@@ -476,8 +480,10 @@ __global__ __launch_bounds__(1024) void block_grad_wide_kernel(BlockGradArgs a) 
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dot = fmaf(m.d[j] * m.g[j], m.h[j], dot);
-        dot_e = fmaf(m.kept[j] ? scale * m.e[j] * m.q[j] : 0.0f, m.x[j], dot_e);
-        dot_h = fmaf(m.kept[j] ? scale * m.h[j] * m.q[j] : 0.0f, m.x[j], dot_h);
+        if (m.kept[j]) {   /* else x may be no number */
+          dot_e = fmaf(scale * m.e[j] * m.q[j], m.x[j], dot_e);
+          dot_h = fmaf(scale * m.h[j] * m.q[j], m.x[j], dot_h);
+        }
       }
     }
     const float c = row_sum<G>(dot, sums[turn][0]) * inv_cols * rstd * rstd * rstd;
@@ -503,7 +509,7 @@ __global__ __launch_bounds__(1024) void block_grad_wide_kernel(BlockGradArgs a) 
         dn[j] = o * m.q[j];
         if (a.post_gain) dn[j] = post_rstd * fmaf(-m.x[j], s1, dn[j]);
         sg[j] = fmaf(m.d[j], m.h[j] * rstd, sg[j]);
-        su[j] = fmaf(o, m.x[j] * post_rstd, su[j]);
+        su[j] = fmaf(o, m.kept[j] ? m.x[j] * post_rstd : 0.0f, su[j]);
       }
       store8f<false, false>(own, (uint64_t)v * 8, a.cols, sg);
       if (a.x) store8f<false, false>(own + a.cols, (uint64_t)v * 8, a.cols, su);

@@ -494,3 +494,37 @@ def test_block_scales_below_fp32s_range(zs):
             want = ref.block(*(dbl(v[k]) for k in ("x", "res", "post_gain", "gate", "gain")),
                              float(torch.tensor(1e-5)), 0.875, float(torch.tensor(bs)), f, BF16)
             assert torch.equal(h.cpu().double(), want[0])
+
+
+def test_block_backward_masked_places(zs):
+    """What dropout replaced has no part in the gate's gradient, whatever it was: as if it had
+    been 0. dx is 0 there."""
+    for r, c in ((6, 96), (600, 1001), (3, 16392)):
+        announce(f"block backward masked {r}x{c}")
+        g = gen("bm", r, c)
+        x, gate = randn(g, r, c).to(BF16), (0.3 + 0.2 * randn(g, c)).to(BF16)
+        h, dy = randn(g, r, c).to(BF16), (0.1 * randn(g, r, c)).to(BF16)
+        gain = (1 + 0.1 * randn(g, c)).to(BF16)
+        rstd = (1 / torch.sqrt(h.double().square().mean(1) + 1e-5)).float()
+        mask = torch.ones(r, c, dtype=BF16, device="cuda")
+        zs.zs_dropout(mask, mask, (0.25, SEED, OFFSET))
+        gone = mask.cpu() == 0
+        clean = torch.where(gone, 0.0, x.float()).to(BF16)
+        spoilt = x.clone()
+        spoilt[gone] = torch.tensor([math.nan, math.inf, -math.inf]).to(BF16)[
+            torch.arange(int(gone.sum())) % 3]
+        outs = []
+        for t in (clean, spoilt):
+            dx, dr = torch.empty(r, c, dtype=BF16, device="cuda"), torch.empty(r, c, dtype=BF16,
+                                                                               device="cuda")
+            s2 = [torch.empty(c, device="cuda") for _ in range(2)]
+            ws = torch.empty(zs.zs_block_norm_backward_workspace(r, c), dtype=torch.uint8,
+                             device="cuda")
+            zs.zs_block_norm_backward(dy.cuda(), h.cuda(), rstd.cuda(), gain.cuda(), dx, dr, s2[0],
+                                      ws, x=t.cuda(), gate=gate.cuda(), dgate=s2[1],
+                                      dropout=(0.25, SEED, OFFSET))
+            assert not dx[gone.cuda()].any()
+            outs.append((dx, dr, *s2))
+        assert torch.isfinite(outs[0][3]).all()
+        for a, b in zip(*outs):
+            assert torch.equal(a, b)
