@@ -460,8 +460,10 @@ struct BlockGradVec {
 /* Rows whose vectors and shares a block's registers and LDS do not hold: read
  * twice, and their shares added to in memory, a word of its own for each of a
  * thread's (2048 x 32768 bf16 403 us; held as above, for the most part in
- * scratch memory, 1262). One reduction a row: with dh = e - h c,
- * mean(q x) = (sum(q k e x) - c sum(q k h x)) a / cols. */
+ * scratch memory, 1262). One reduction a row: with n = h r2 and dh = e - n c,
+ * mean(q x) = (sum(q k e x) - c sum(q k n x)) a / cols. With n
+ * in place of h c has dh's size: h's c is r2 times that, and its sum 1 / r2
+ * times, which leave fp32 for bf16 rows beyond 1e19 or below 1e-19. */
 template <int DT, bool AL>
 __global__ __launch_bounds__(1024) void block_grad_wide_kernel(BlockGradArgs a) {
   constexpr int G = 1024;
@@ -479,14 +481,15 @@ __global__ __launch_bounds__(1024) void block_grad_wide_kernel(BlockGradArgs a) 
       const BlockGradVec<DT, AL> m(a, row, v, rstd, offset);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dot = fmaf(m.d[j] * m.g[j], m.h[j], dot);
+        const float n = m.h[j] * rstd;
+        dot = fmaf(m.d[j] * m.g[j], n, dot);
         if (m.kept[j]) {   /* else x may be no number */
           dot_e = fmaf(scale * m.e[j] * m.q[j], m.x[j], dot_e);
-          dot_h = fmaf(scale * m.h[j] * m.q[j], m.x[j], dot_h);
+          dot_h = fmaf(scale * n * m.q[j], m.x[j], dot_h);
         }
       }
     }
-    const float c = row_sum<G>(dot, sums[turn][0]) * inv_cols * rstd * rstd * rstd;
+    const float c = row_sum<G>(dot, sums[turn][0]) * inv_cols * rstd;
     float s1 = 0.0f;
     if (a.post_gain) {
       dot_e = row_sum<G>(dot_e, sums[turn][1]);
@@ -504,11 +507,11 @@ __global__ __launch_bounds__(1024) void block_grad_wide_kernel(BlockGradArgs a) 
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float dh = fmaf(-m.h[j], c, m.e[j]), o = m.kept[j] ? scale * dh : 0.0f;
+        const float n = m.h[j] * rstd, dh = fmaf(-n, c, m.e[j]), o = m.kept[j] ? scale * dh : 0.0f;
         r[j] = dh * a.residual_scale;
         dn[j] = o * m.q[j];
         if (a.post_gain) dn[j] = post_rstd * fmaf(-m.x[j], s1, dn[j]);
-        sg[j] = fmaf(m.d[j], m.h[j] * rstd, sg[j]);
+        sg[j] = fmaf(m.d[j], n, sg[j]);
         su[j] = fmaf(o, m.kept[j] ? m.x[j] * post_rstd : 0.0f, su[j]);
       }
       store8f<false, false>(own, (uint64_t)v * 8, a.cols, sg);

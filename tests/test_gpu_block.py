@@ -528,3 +528,36 @@ def test_block_backward_masked_places(zs):
         assert torch.isfinite(outs[0][3]).all()
         for a, b in zip(*outs):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("c", [1000, 12001, 16392, 20001])
+def test_block_backward_of_large_and_small_rows(zs, c):
+    """bf16 rows beyond 1e19 and below 1e-19, whose squares and cubes of scales leave fp32."""
+    for hs, xs, ds in ((1e25, 1e-10, 1.0), (1e25, 1e20, 1e8), (1e-20, 1.0, 1e-3), (1e-25, 1e10, 1e-10),
+                       (1e30, 1.0, 1e5)):
+        announce(f"block backward {c} h {hs} x {xs} dy {ds}")
+        r, g = 3, gen("size", c)
+        x, h = (randn(g, r, c) * xs).to(BF16), (randn(g, r, c) * hs).to(BF16)
+        dy, dres = (0.1 * randn(g, r, c) * ds).to(BF16), (0.1 * randn(g, r, c) * ds / hs).to(BF16)
+        gain, post_gain = ((1 + 0.1 * randn(g, c)).to(BF16) for _ in range(2))
+        gate = (0.3 + 0.2 * randn(g, c)).to(BF16)
+        rstd = (1 / torch.sqrt(h.double().square().mean(1))).float()
+        post_rstd = (1 / torch.sqrt(x.double().square().mean(1))).float()
+        dx, dr = (torch.empty(r, c, dtype=BF16, device="cuda") for _ in range(2))
+        s3 = [torch.empty(c, device="cuda") for _ in range(3)]
+        ws = torch.empty(zs.zs_block_norm_backward_workspace(r, c), dtype=torch.uint8, device="cuda")
+        zs.zs_block_norm_backward(dy.cuda(), h.cuda(), rstd.cuda(), gain.cuda(), dx, dr, s3[0], ws,
+                                  x=x.cuda(), post_gain=post_gain.cuda(), post_rstd=post_rstd.cuda(),
+                                  gate=gate.cuda(), dpost_gain=s3[1], dgate=s3[2], dres=dres.cuda(),
+                                  branch_scale=0.5)
+        w, mag = ref.block_grad(dbl(dy), dbl(h), dbl(rstd), dbl(gain), dbl(dres), dbl(x),
+                                dbl(post_rstd), dbl(post_gain), dbl(gate), 1.0, 0.5,
+                                torch.ones(r, c, dtype=F64))
+        # as for wide rows: 64 elements of a thread, 6 levels of lanes, 16 waves, ten roundings;
+        # a value below fp32's normal range is off by 2^-150 at each of some ten steps
+        chain = (64 + 6 + 16 + 10) * 2.0 ** -24
+        for k, got in (("dx", dx), ("dresidual", dr)):
+            inner = (2 if k == "dx" else 1) * chain * mag[k] + 10 * 2.0 ** -150
+            close(got, w[k], U[BF16] * (w[k].abs() + inner) + inner + TINY[BF16], k)
+        for k, got in zip(("dgain", "dpost_gain", "dgate"), s3):
+            close(got, w[k], (70 * 2.0 ** -24 + chain) * mag[k] + TINY[FP32], k)
