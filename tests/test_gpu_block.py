@@ -561,3 +561,43 @@ def test_block_backward_of_large_and_small_rows(zs, c):
             close(got, w[k], U[BF16] * (w[k].abs() + inner) + inner + TINY[BF16], k)
         for k, got in zip(("dgain", "dpost_gain", "dgate"), s3):
             close(got, w[k], (70 * 2.0 ** -24 + chain) * mag[k] + TINY[FP32], k)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=str)
+def test_block_backward_rows_walked(zs, dtype):
+    """Groups of one wave up to sixteen that take a third row, with its next row's loads and both
+    sums' shares in registers and in LDS."""
+    r = 600
+    for c in (500, 1000, 1999, 4000, 4095, 8000, 8191, 12001, 16384):
+        announce(f"block backward walk {dtype} {r}x{c}")
+        g = gen("walk", c)
+        x, h = (randn(g, r, c) * (0.2 + torch.rand(r, 1, generator=g))).to(dtype), randn(g, r, c).to(dtype)
+        gain, post_gain = ((1 + 0.1 * randn(g, c)).to(dtype) for _ in range(2))
+        gate = (0.3 + 0.2 * randn(g, c)).to(dtype)
+        dy, dres = (0.1 * randn(g, r, c)).to(dtype), (0.1 * randn(g, r, c)).to(dtype)
+        rstd = (1 / torch.sqrt(h.double().square().mean(1) + 1e-5)).float()
+        post_rstd = (1 / torch.sqrt(x.double().square().mean(1) + 1e-5)).float()
+        mask = torch.ones(r, c, dtype=dtype, device="cuda")
+        zs.zs_dropout(mask, mask, (0.5, SEED, OFFSET))     # its bits are tested above: 0 and 2
+        for post in (True, False):
+            dx, dr = (torch.empty(r, c, dtype=dtype, device="cuda") for _ in range(2))
+            s3 = [torch.empty(c, device="cuda") for _ in range(3)]
+            ws = torch.empty(zs.zs_block_norm_backward_workspace(r, c), dtype=torch.uint8,
+                             device="cuda")
+            more = dict(post_gain=post_gain.cuda(), post_rstd=post_rstd.cuda(),
+                        dpost_gain=s3[2]) if post else {}
+            zs.zs_block_norm_backward(dy.cuda(), h.cuda(), rstd.cuda(), gain.cuda(), dx, dr, s3[0],
+                                      ws, x=x.cuda(), gate=gate.cuda(), dgate=s3[1],
+                                      dres=dres.cuda(), branch_scale=0.5,
+                                      dropout=(0.5, SEED, OFFSET), **more)
+            w, mag = ref.block_grad(dbl(dy), dbl(h), dbl(rstd), dbl(gain), dbl(dres), dbl(x),
+                                    dbl(post_rstd), dbl(post_gain) if post else None, dbl(gate),
+                                    1.0, 0.5, dbl(mask.cpu()))
+            # a mean's chain: 16 elements of a thread, 6 levels of lanes, 16 waves; ten roundings
+            chain = (16 + 6 + 16 + 10) * 2.0 ** -24
+            for k, got in (("dx", dx), ("dresidual", dr)):
+                inner = (2 if k == "dx" else 1) * chain * mag[k]
+                close(got, w[k], U[dtype] * (w[k].abs() + inner) + inner + TINY[dtype], k)
+            for k, got in zip(("dgain", "dgate", "dpost_gain"), s3):
+                if k in w:   # a share's three rows, 8 of 32 shares at a time, 32 runs
+                    close(got, w[k], ((3 + 32 + 32 + 3) * 2.0 ** -24 + chain) * mag[k] + TINY[FP32], k)
