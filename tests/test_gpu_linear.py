@@ -298,3 +298,34 @@ def test_tensors_of_another_device_are_refused(zs, monkeypatch):
             call()
     torch.cuda.synchronize()
     assert all(bool((o == 7).all()) for o in out)
+
+
+@pytest.mark.parametrize("dtype,act,r,c", [(BF16, "gelu", 70000, 264), (FP16, "silu", 33000, 513),
+                                           (BF16, "none", 2100000, 8), (FP16, "relu", 70001, 257)],
+                         ids=str)
+def test_activation_backward_rows_walked(zs, dtype, act, r, c):
+    """So many rows that a block takes several turns of them."""
+    announce(f"activation backward walk {dtype} {act} {r}x{c}")
+    g = gen("aw", r, c)
+    dc = torch.randn(r, c, generator=g).to(dtype)
+    pre = (2 * torch.randn(r, c, generator=g)).to(dtype)
+    s, bound = ref.slope(pre.double(), act)
+    w = ref.logistic_argument(pre.double(), act)[0].abs() * math.log2(math.e)
+    inner = dc.double().abs() * ((bound * (w.clamp(max=160) + 6) * 2.0 ** -22
+                                  if act in ("gelu", "silu") else 0) + 2.0 ** -24 * s.abs())
+    # the exponential gives 0 below 2^-126, and so p, which is off by as much: the slope p (1 +
+    # x q w') by |1 + x q w'| times that (of gelu's at -10 some 200 times)
+    p = torch.sigmoid(ref.logistic_argument(pre.double(), act)[0])
+    inner = inner + 2.0 ** -126 * (1 + dc.double().abs() * (bound / p.clamp(min=1e-300)
+                                                            if act in ("gelu", "silu") else 0))
+    want = dc.double() * s
+    dpre = torch.empty_like(dc).cuda()
+    dbias = torch.empty(c, device="cuda")
+    ws = torch.empty(zs.zs_activation_backward_workspace(r, c), dtype=torch.uint8, device="cuda")
+    zs.zs_activation_backward(dc.cuda(), None if act == "none" else pre.cuda(), act_of(zs, act), dpre,
+                              dbias=dbias, workspace=ws)
+    check(dpre, want, U[dtype] * (want.abs() + inner) + inner + TINY[dtype], "dpre")
+    # a thread takes four rows a turn, two turns here; a block's rows join in at most ten halvings,
+    # 1024 shares in 32 runs of 32
+    chain = (8 + 10 + 32 + 32) * 2.0 ** -24
+    check(dbias, want.sum(0), chain * want.abs().sum(0) + inner.sum(0) + 1e-40, "dbias")
