@@ -21,12 +21,16 @@ using namespace zs;
  * that split along K into pieces of 1024 elements or more, as far as the
  * workspace holds their sums.
  * ---------------------------------------------------------------------- */
-inline int too_large() { return fail(ZS_ERR_UNSUPPORTED, "zs_mx_matmul: too large for one launch%s"); }
+template <class E>
+int too_large() {
+  return fail(ZS_ERR_UNSUPPORTED, E::kOn ? "zs_mx_linear: too large for one launch%s"
+                                         : "zs_mx_matmul: too large for one launch%s");
+}
 
 template <int AF, int CDT, int BM, int BN, int NW, class E>
 int launch_tile(const MatmulArgs &a, uint32_t splits, const E &e, hipStream_t s) {
   const uint64_t tiles = (uint64_t)((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN);
-  if (!fits(tiles, 64 * NW)) return too_large();
+  if (!fits(tiles, 64 * NW)) return too_large<E>();
   hipLaunchKernelGGL((matmul_tile_kernel<AF, CDT, BM, BN, NW, E>), dim3((unsigned)tiles, splits),
                      dim3(64 * NW), 0, s, a, e);
   return launch_result();
@@ -75,7 +79,7 @@ int launch_matmul(MatmulArgs a, const E &e, float *workspace, uint64_t workspace
     /* four results of a lane in one store */
     const int vec = aligned(a.c, 4 * esz) && a.ldc % 4 == 0;
     const uint32_t blocks = (a.n + 31) / 32;
-    if (!fits(blocks, 64 * kThinWaves)) return too_large();
+    if (!fits(blocks, 64 * kThinWaves)) return too_large<E>();
     /* both halves of an 8-bit A in one instruction: 1 x 32000 x 4096 15.6 us,
      * in two 18.9; 4 rows 18.0 and 19.3; 16 rows 26.6 and 22.5 */
     if (AF == ZS_MX_E4M3 && a.m <= 4)

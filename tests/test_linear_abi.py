@@ -93,6 +93,15 @@ def test_workspace(zs):
     assert zs.zs_activation_backward_workspace(8, 1 << 31) == 0
 
 
+def test_too_large_is_said_by_its_name(zs):
+    """A product of more tiles than a launch takes is refused, in the entry point's own words."""
+    fn, args = calls(zs)["linear"]
+    size, apart = 1 << 20, {k: P((i + 1) << 48) for i, k in enumerate(("a", "as_", "b", "bs", "c"))}
+    args = {**args, **apart, "m": size, "n": size, "ldc": size, "bias": None, "res": None, "pre": None}
+    assert fn(*args.values()) == UNSUPPORTED
+    assert zs.zs_last_error().startswith("zs_mx_linear: too large")
+
+
 def test_python_checks(zs):
     x = torch.zeros(4, 8, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
