@@ -52,12 +52,7 @@ def train(steps=40, pairs=8, length=32, width=256, hidden=512, vocab=1000, lr=1e
     starts = torch.arange(0, rows + 1, length, device="cuda", dtype=torch.int32)
     weight = torch.full((pairs,), 1.0 / pairs, device="cuda")
     # the reference: the student before its first step, without dropout
-    keep, student.block.dropout = student.block.dropout, 0.0
-    logits = student.forward(st.params, x, res)
-    logp, ws = torch.empty(rows, device="cuda"), student.head._ws
-    zs.zs_logprob(logits, ids, logp, workspace=ws)
-    ref = logp.view(2 * pairs, length).sum(1)
-    student.block.dropout = keep
+    ref = student.logprobs(st.params, x, res, ids).view(2 * pairs, length).sum(1)
     losses = []
     for i in range(steps):
         student.step(st.params, x, res, offset=i, ids=ids, starts=starts, ref_logp=ref,

@@ -68,8 +68,9 @@ class MlpBlock:
         return out
 
     def _rule(self, offset):
-        """offset: a number of the step's own, or (number, CUDA int64 tensor added to it)."""
-        if not self.dropout:
+        """offset: a number of the step's own, or (number, CUDA int64 tensor added to it); None:
+        no dropout."""
+        if not self.dropout or offset is None:
             return None
         return (self.dropout, self.seed, *(offset if isinstance(offset, tuple) else (offset,)))
 
@@ -134,22 +135,28 @@ class MlpBlock:
 class BlockStudent:
     """An MlpBlock and a head (DistillHead, PolicyHead or PreferenceHead) of the same rows and
     width, their parameters one after the other in the flat buffers. grads: the flat 16-bit
-    gradient that step() fills; dx: the gradient of its x and residual."""
+    gradient that step() fills; dx: the gradient of its x and residual; logp: fp32 per row, what
+    logprobs() fills."""
 
     def __init__(self, block, head):
         if (block.rows, block.width, block._code) != (head.rows, head.width, head._code):
             raise ValueError("block and head differ in rows, width or dtype")
         self.block, self.head = block, head
         self.phi = block.phi + head.phi
-        self.grads = torch.zeros(self.phi, dtype=head.grads.dtype, device=head.grads.device)
+        device = head.grads.device
+        self.grads = torch.zeros(self.phi, dtype=head.grads.dtype, device=device)
         self.dx = block.dx
+        self.logp = torch.empty(head.rows, dtype=torch.float32, device=device)
+        need = zs.zs_logprob_workspace(head.rows, head.vocab, head._code)
+        self._ws = head._ws if head._ws.numel() >= need else \
+            torch.empty(need, dtype=torch.uint8, device=device)
 
     def split(self, flat):
         """(the block's, the head's) part of a flat buffer."""
         return flat[:self.block.phi], flat[self.block.phi:self.phi]
 
     def forward(self, params, x, residual, offset=0, stream=None):
-        """Logits of a batch, in head.logits, with the step's dropout."""
+        """Logits of a batch, in head.logits, with the step's dropout (offset None: without)."""
         mine, heads = self.split(params)
         gain, weight = self.head.split(heads)
         h = self.head
@@ -157,6 +164,16 @@ class BlockStudent:
                            stream=stream)
         h._product(weight, dict(stream=stream))
         return h.logits
+
+    def logprobs(self, params, x, residual, ids, offset=None, stream=None):
+        """Log-probability of each row's token under the block and the head, without dropout or
+        with an offset's, fp32: what old_logp and ref_logp are made of. (The head's own is that of
+        a student without a block.)"""
+        h = self.head
+        self.forward(params, x, residual, offset, stream)
+        zs.zs_logprob(h.logits, ids, self.logp, temperature=h.temperature, workspace=self._ws,
+                      stream=stream)
+        return self.logp
 
     def step(self, params, x, residual, offset=0, stream=None, **loss):
         """Forward and backward of one batch, all queued; loss: the head's step's arguments from

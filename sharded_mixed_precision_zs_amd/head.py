@@ -139,7 +139,8 @@ class PolicyHead(_Head):
                      logp=self.logp, grad=self.logits, workspace=self._ws, **more, **s)
 
     def logprobs(self, params, x, residual, ids, stream=None):
-        """Log-probability of each row's token, fp32: what old_logp and ref_logp are made of."""
+        """Log-probability of each row's token, fp32: what old_logp and ref_logp are made of (with
+        a block in front BlockStudent.logprobs: params are the head's own here)."""
         s = dict(stream=stream)
         gain, weight = self.split(params)
         self._norm(gain, x, residual, s)

@@ -259,3 +259,29 @@ def test_block_and_head_must_match(zs):
     from sharded_mixed_precision_zs_amd.head import PolicyHead
     with pytest.raises(ValueError):
         BlockStudent(MlpBlock(8, 64, 64), PolicyHead(8, 128, 100))
+
+
+@pytest.mark.parametrize("kind", ["policy", "preference", "distill"])
+def test_students_logprobs(zs, kind):
+    """Of block and head together, without dropout or with an offset's: the 64-bit
+    log-probabilities of the logits that forward() leaves."""
+    from sharded_mixed_precision_zs_amd.block import BlockStudent, MlpBlock
+    from sharded_mixed_precision_zs_amd.head import DistillHead
+    student = parts(zs, kind) if kind != "distill" else BlockStudent(
+        MlpBlock(ROWS, WIDTH, HIDDEN, dropout=0.25, seed=77), DistillHead(ROWS, WIDTH, VOCAB, 4))
+    params, x, res, ids, _ = problem(student.block, student.head)
+    args = (params.cuda(), x.cuda(), res.cuda())
+    seen = []
+    for offset in (None, 5):
+        got = student.logprobs(*args, ids.cuda(), **({} if offset is None else {"offset": offset}))
+        z = student.forward(*args, offset=offset).clone()
+        assert torch.equal(z, student.head.logits)
+        want = tok.logprob(back(z), ids, 1.0)[0]
+        # each is within 2 (2 D + 38) 2^-24, D the row's spread, here below 40
+        near(got, want, torch.full_like(want, 1.5e-5) + 2.0 ** -23 * want.abs(), "logp")
+        assert not got.cpu()[ids < 0].any()
+        seen.append(z)
+    keep, student.block.dropout = student.block.dropout, 0.0
+    assert torch.equal(student.forward(*args, offset=5), seen[0])
+    student.block.dropout = keep
+    assert not torch.equal(seen[0], seen[1])
