@@ -673,7 +673,9 @@ int zs_dropout(const void *x, const void *residual, int dtype, uint64_t rows, ui
  *   h = R16(residual_scale * residual + branch_scale * k * gate * n)
  *   y = h * rstd * gain,            rstd = 1 / sqrt(mean(h^2) + eps)
  * per row, k as in zs_dropout. h is rounded once, from more than fp32; what y
- * and its 8 bits are made of is the rounded h, as in zs_rmsnorm_forward.
+ * and its 8 bits are made of is the rounded h, as in zs_rmsnorm_forward. The
+ * products x * post_gain * gate and h * gain are formed first and must lie in
+ * fp32's range.
  *   x, residual: dtype (bf16, fp16)[rows][cols], both needed.
  *   post_gain  : dtype[cols], or NULL: no first norm (n = x).
  *   gate       : dtype[cols], one for all rows, or NULL (1).
