@@ -201,7 +201,7 @@ struct SlotSums {
 /* This thread's share; weights w = exp(t / tau - ref) take the logits' place.
  * All ids are in LDS before this. With a tail the exponent is formed in
  * binary64: what it is off by goes into 1 - mass whole. */
-template <bool TAIL, int NT>
+template <int DT, bool TAIL, int NT>
 __device__ __forceinline__ SlotSums<TAIL> slot_weights(const DistillArgs &a, float ref,
                                                        const Shift &sh, const SlotLds &s) {
   SlotSums<TAIL> r{0, 0.0f, 0.0};
@@ -222,7 +222,7 @@ __device__ __forceinline__ SlotSums<TAIL> slot_weights(const DistillArgs &a, flo
       r.mass += w;
       if (!(w == 0.0f)) r.cross += w * (u - (zk - sh.max) * a.inv_tau);
       if constexpr (TAIL) {
-        if (!slot_seen(s, k, id)) r.terms += (double)term(zk, sh);
+        if (!slot_seen(s, k, id)) r.terms += (double)term<DT>(zk, sh);
       }
     }
     s.w[k] = w;
@@ -287,7 +287,7 @@ __device__ __forceinline__ void store_slots(const DistillArgs &a, void *g, const
     if (id < 0 || (uint32_t)id < first || (uint32_t)id >= last) continue;
     const float w = slot_weight(s, a.slots, id);
     const float p = TAIL ? w : w / mass;
-    store1<DT>(g, id, (term(s.z[k], sh) / total - p) * coef);
+    store1<DT>(g, id, (term<DT>(s.z[k], sh) / total - p) * coef);
   }
 }
 
@@ -488,13 +488,13 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
       reduce_put(top.top, MaxOf{}, red.part[1]);
       reduce_put(top.any, MaxOf{}, red.part[2]);
       __syncthreads();
-      shift = shift_of(reduce_get<NT>(MaxOf{}, red.part[0]), a.log2_scale);
+      shift = shift_of<DT>(reduce_get<NT>(MaxOf{}, red.part[0]), a.log2_scale);
       const float highest = reduce_get<NT>(MaxOf{}, red.part[1]);
       const float ref = TAIL ? in.lse : highest;
       const bool live = TAIL ? reduce_get<NT>(MaxOf{}, red.part[2]) > 0.0f : highest > -INFINITY;
       off = shift;
       auto sum_terms = [&] {
-        float sum = in.edge < a.vocab ? term(single, off) : 0.0f;
+        float sum = in.edge < a.vocab ? term<DT>(single, off) : 0.0f;
         if constexpr (TAIL) {
           if (in.edge < a.vocab && marks[kMarks] >> t & 1) sum = 0.0f;
         }
@@ -512,7 +512,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
             }
           }
 #pragma unroll
-          for (uint32_t j = 0; j < ve; ++j) some += term(e[j], off);
+          for (uint32_t j = 0; j < ve; ++j) some += term<DT>(e[j], off);
           sum += (int)t < (int)in.shape.vecs - i * NT ? some : 0;
           if constexpr (TAIL) asm volatile("" : "+v"(sum));   /* now, not behind the next branch */
           __builtin_amdgcn_sched_barrier(0);
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
         return sum;
       };
       reduce_put((double)sum_terms(), SumOf{}, red.dpart[1]);
-      sums = slot_weights<TAIL, NT>(a, ref, shift, lds);
+      sums = slot_weights<DT, TAIL, NT>(a, ref, shift, lds);
       put_mass<NT>(sums.mass, red);
       reduce_put(sums.cross, SumOf{}, red.part[3]);
       if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.dpart[2]);
@@ -548,7 +548,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
     }
     if (!f.live) {   /* zeros: terms of -inf */
       off.c = 1.0f;
-      off.whole = f.factor = 0.0f;
+      off.whole = off.frac = f.factor = 0.0f;
       f.up = 1.0f;
       single = -INFINITY;
 #pragma unroll
@@ -560,7 +560,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
     const __amdgpu_buffer_rsrc_t from = row_buffer<DT>(after);
     if (more) slots_ahead(next, after, slot);
     const uint32_t edge = edge_index<DT>(in.shape, t, true, true, a.vocab);
-    if (a.grad && edge < a.vocab) store1<DT>(g, edge, off_slots<TAIL>(term(single, off), f));
+    if (a.grad && edge < a.vocab) store1<DT>(g, edge, off_slots<TAIL>(term<DT>(single, off), f));
     if (more) raw_single = fetch_edge<DT>(a, after);
     if (!a.grad) {
 #pragma unroll
@@ -572,7 +572,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void distill_row_kernel(Di
         asm volatile("" : "+v"(x[i]));   /* unpacked anew, not kept since the sum */
         unpack_vec<DT>(x[i], e);
 #pragma unroll
-        for (uint32_t j = 0; j < ve; ++j) e[j] = off_slots<TAIL>(term(e[j], off), f);
+        for (uint32_t j = 0; j < ve; ++j) e[j] = off_slots<TAIL>(term<DT>(e[j], off), f);
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, pack_vec<DT>(e)), to,
                                                (int)(t * 16 + i * (NT * 16)), 0,
                                                NT > 64 ? kNonTemporal : 0);
@@ -662,11 +662,11 @@ __global__ __launch_bounds__(NT) void distill_stats_kernel(DistillArgs a) {
   if constexpr (TAIL) {
     if (edge < a.vocab) leave_slots_out(lds, a.slots, edge, single);
   }
-  Shift off = shift_of(max, a.log2_scale);
+  Shift off = shift_of<DT>(max, a.log2_scale);
   double sum;
   bool lifted = false;
   for (;;) {
-    sum = edge < a.vocab ? (double)term(single[0], off) : 0.0;
+    sum = edge < a.vocab ? (double)term<DT>(single[0], off) : 0.0;
     for (uint32_t v = v0 + threadIdx.x; v < v1; v += NT) {
       float x[ve];
       unpack_vec<DT>(zv[v], x);
@@ -675,7 +675,7 @@ __global__ __launch_bounds__(NT) void distill_stats_kernel(DistillArgs a) {
           leave_slots_out(lds, a.slots, sh.head + v * ve, x);
       }
 #pragma unroll
-      for (uint32_t j = 0; j < ve; ++j) sum += (double)term(x[j], off);
+      for (uint32_t j = 0; j < ve; ++j) sum += (double)term<DT>(x[j], off);
     }
     reduce_put(sum, SumOf{}, dpart[lifted]);
     __syncthreads();
@@ -692,15 +692,11 @@ __global__ __launch_bounds__(NT) void distill_stats_kernel(DistillArgs a) {
   }
 }
 
-/* What turns a part's terms into the row's. They are by its own whole
- * number, so the factor is a power of two and exact; where the two scale
- * differently (beyond 2^60) the part has no terms worth the name. A part of
- * nothing but -inf has the sum 0, one with a NaN or +inf off the slots a NaN. */
+/* What turns a part's terms into the row's. A part of nothing but -inf has the
+ * sum 0, one with a NaN or +inf off the slots a NaN. */
+template <int DT>
 __device__ __forceinline__ double part_factor(const DistillPart &w, const Shift &row, float c) {
-  const Shift own = shift_of(w.max, c);
-  const float by = own.whole - row.whole;
-  const bool some = w.max != -INFINITY && own.c == row.c && by > -800.0f;
-  return __hiloint2double(some ? (1023 + (int)(by - w.lift)) << 20 : 0, 0);
+  return w.max == -INFINITY ? 0.0 : shift_factor<DT>(shift_of<DT>(w.max, c), row, w.lift);
 }
 
 template <int DT, bool TAIL, int NT>
@@ -727,10 +723,10 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
     const DistillPart *w = a.ws + row * a.parts;
     float max = -INFINITY;
     for (uint32_t i = 0; i < a.parts; ++i) max = fmaxf(max, w[i].max);
-    shift = shift_of(max, a.log2_scale);
+    shift = shift_of<DT>(max, a.log2_scale);
     double sum = 0.0;
     for (uint32_t i = 0; i < a.parts; ++i)
-      sum += w[i].sum * part_factor(w[i], shift, a.log2_scale);
+      sum += w[i].sum * part_factor<DT>(w[i], shift, a.log2_scale);
     off = shift;
     bool lifted = false;
     if constexpr (TAIL) {
@@ -745,7 +741,7 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
     const float highest = reduce_get<NT>(MaxOf{}, red.part[1]);
     const float ref = TAIL ? a.lse[row] : highest;
     const bool live = TAIL ? reduce_get<NT>(MaxOf{}, red.part[2]) > 0.0f : highest > -INFINITY;
-    sums = slot_weights<TAIL, NT>(a, ref, shift, lds);
+    sums = slot_weights<DT, TAIL, NT>(a, ref, shift, lds);
     put_mass<NT>(sums.mass, red);
     reduce_put(sums.cross, SumOf{}, red.part[3]);
     if constexpr (TAIL) reduce_put(sums.terms, SumOf{}, red.dpart[2]);
@@ -761,13 +757,13 @@ __global__ __launch_bounds__(NT) void distill_grad_kernel(DistillArgs a, uint32_
   if (!g) return;
   const u32x4 *zv = reinterpret_cast<const u32x4 *>(z + sh.head * esz);
   if (edge < a.vocab)
-    store1<DT>(g, edge, f.live ? off_slots<TAIL>(term(load1<DT>(z, edge), off), f) : 0.0f);
+    store1<DT>(g, edge, f.live ? off_slots<TAIL>(term<DT>(load1<DT>(z, edge), off), f) : 0.0f);
   for (uint32_t v = v0 + threadIdx.x; v < v1; v += NT) {
     float x[ve];
     if (f.live) {
       unpack_vec<DT>(zv[v], x);
 #pragma unroll
-      for (uint32_t j = 0; j < ve; ++j) x[j] = off_slots<TAIL>(term(x[j], off), f);
+      for (uint32_t j = 0; j < ve; ++j) x[j] = off_slots<TAIL>(term<DT>(x[j], off), f);
     } else {
 #pragma unroll
       for (uint32_t j = 0; j < ve; ++j) x[j] = 0.0f;

@@ -159,26 +159,61 @@ __device__ __forceinline__ T reduce_get(Op op, const T *part) {
 
 /* ------------------------------------------------------------------------
  * Terms. A maximum of -inf (nothing but -inf) counts as 0, so that such
- * terms are 0 and a NaN stays one. Beyond 2^60 in exponent units, where
- * z c could overflow, neighbouring values lie so far apart that any c gives
- * terms of 1 and 0: 2^-4 does.
+ * terms are 0 and a NaN stays one.
+ *
+ * From 2^24 exponent units on, reached by large logits or a small temperature,
+ * fp32 has no whole number next to max c: they lie up to 2^(e - 24) apart, and
+ * terms would be off by half of that in their exponents. Neighbouring 16-bit
+ * values lie 2^12 units and more apart there, so that terms are 1 or 0 by any
+ * c: one that is a power of two and makes max c a whole number of 24 bits
+ * does. Of fp32's, whose neighbours may lie 1 apart, the difference is taken
+ * off each exponent; from 2^32 on they too are 2^8 apart.
  * ---------------------------------------------------------------------- */
 struct Shift {
   float max, c, whole;
-  float rest;   /* ln 2 * (max c - whole) */
+  float frac;   /* of fp32's exponents, off each: max c - whole from 2^24 on, else 0 */
+  float rest;   /* ln 2 * (max c - whole - frac) */
 };
 
+template <int DT>
 __device__ __forceinline__ Shift shift_of(float max, float c) {
+  constexpr float kWhole = 16777216.0f, kFar = DT == ZS_FP32 ? 4294967296.0f : kWhole;
+  constexpr uint32_t kTop = DT == ZS_FP32 ? 32 : 23;   /* max c lies in [2^kTop, 2^(kTop + 1)) then */
   Shift s;
   s.max = max == -INFINITY ? 0.0f : max;
-  s.c = fabsf(s.max * c) < 1.15292150e18f ? c : 0.0625f;
-  s.whole = rintf(s.max * s.c);
-  s.rest = fmaf(s.max, s.c, -s.whole) * 0.69314718f;
+  s.c = c;
+  s.frac = 0.0f;
+  if (fabsf(s.max * c) < kFar) {
+    s.whole = rintf(s.max * c);
+    if (DT == ZS_FP32 && fabsf(s.whole) >= kWhole) s.frac = fmaf(s.max, c, -s.whole);
+  } else {   /* c is below 2^127, so that a max of fp32 is above 2^-95; or it is no number */
+    s.c = __uint_as_float((254 + kTop - (__float_as_uint(s.max) >> 23 & 255)) << 23);
+    s.whole = s.max * s.c;
+  }
+  s.rest = (fmaf(s.max, s.c, -s.whole) - s.frac) * 0.69314718f;
   return s;
 }
 
+template <int DT>
 __device__ __forceinline__ float term(float z, const Shift &s) {
-  return exp2_fast(fmaf(z, s.c, -s.whole));
+  const float e = fmaf(z, s.c, -s.whole);
+  return exp2_fast(DT == ZS_FP32 ? e - s.frac : e);
+}
+
+/* What turns a sum of terms by shift `own`, 2^lift too large, into one by shift
+ * `to`: a power of two, but for a difference of fracs; 0 where the two have
+ * another c, and so no terms in common, or lie too far apart. */
+template <int DT>
+__device__ __forceinline__ double shift_factor(const Shift &own, const Shift &to, float lift) {
+  float by = own.whole - to.whole - lift, part = 0.0f;
+  if constexpr (DT == ZS_FP32) {
+    by += own.frac - to.frac;
+    part = by;
+    by = floorf(by);
+    part -= by;
+  }
+  const double f = __hiloint2double(own.c == to.c && by > -900.0f ? (1023 + (int)by) << 20 : 0, 0);
+  return DT == ZS_FP32 ? f * (double)exp2_fast(part) : f;
 }
 
 template <int DT>

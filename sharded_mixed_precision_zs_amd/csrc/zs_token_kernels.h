@@ -94,14 +94,6 @@ __device__ __forceinline__ bool token_live(const TokenArgs &a, uint32_t row, int
   return (uint32_t)id < a.vocab && (!a.weight || a.weight[row] != 0.0f);
 }
 
-/* What turns a sum of terms by shift `own` into one by shift `to`, a power of
- * two; 0 where the two scale differently or lie too far apart. */
-__device__ __forceinline__ double shift_factor(float max, const Shift &own, const Shift &to) {
-  const float by = own.whole - to.whole;
-  const bool some = max != -INFINITY && own.c == to.c && by > -800.0f;
-  return __hiloint2double(some ? (1023 + (int)by) << 20 : 0, 0);
-}
-
 /* ------------------------------------------------------------------------
  * A row's token: its share of the softmax and its log-probability. `rest` and
  * `own` are the sums of the other terms and its own.
@@ -125,9 +117,10 @@ __device__ __forceinline__ double far_log(float z, const Shift &s, float c) {
   return ((double)z - (double)s.max) * ((double)c * 0.69314718055994531);
 }
 
+template <int DT>
 __device__ __forceinline__ TokenMass token_mass(double rest, float z, const Shift &s, float c) {
   TokenMass m;
-  const double own = (double)term(z, s);
+  const double own = (double)term<DT>(z, s);
   m.rest = rest;
   m.total = rest + own;
   if (rest <= own && own > 0.0)
@@ -135,7 +128,8 @@ __device__ __forceinline__ TokenMass token_mass(double rest, float z, const Shif
   else   /* NaN: comes here */
     m.logp = (token_far(z, s, c)
                   ? far_log(z, s, c)
-                  : fma((double)z, (double)s.c, -(double)s.whole) * 0.69314718055994531) -
+                  : (fma((double)z, (double)s.c, -(double)s.whole) - (double)s.frac) *
+                        0.69314718055994531) -
              log(m.total);
   return m;
 }
@@ -146,17 +140,18 @@ struct TokenMass32 {
   float rest, total, logp;
 };
 
+template <int DT>
 __device__ __forceinline__ TokenMass32 token_mass32(double rest, float z, const Shift &s,
                                                     float c) {
   TokenMass32 m;
-  const float own = term(z, s);
+  const float own = term<DT>(z, s);
   m.rest = (float)rest;
   m.total = (float)(rest + (double)own);
   if (m.rest <= own && own > 0.0f)
     m.logp = -log1pf(m.rest / own);
   else   /* NaN: comes here */
     m.logp = (token_far(z, s, c) ? (float)far_log(z, s, c)
-                                 : fmaf(z, s.c, -s.whole) * 0.69314718f) -
+                                 : (fmaf(z, s.c, -s.whole) - s.frac) * 0.69314718f) -
              logf(m.total);
   return m;
 }
@@ -252,9 +247,10 @@ __device__ __forceinline__ void leave_out(const RowShape &s, int32_t id, uint32_
 
 /* The row's results, where one thread knows all of it: log-probability,
  * policy loss and plan, as far as they are asked for. */
+template <int DT>
 __device__ __forceinline__ void finish_token(const TokenArgs &a, uint32_t row, double rest,
                                              float from, float z, int32_t id) {
-  const TokenMass m = token_mass(rest, z, shift_of(from, a.log2_scale), a.log2_scale);
+  const TokenMass m = token_mass<DT>(rest, z, shift_of<DT>(from, a.log2_scale), a.log2_scale);
   if (a.logp) a.logp[row] = (float)m.logp;
   if (a.starts) {
     a.lp[row] = m.logp;
@@ -302,8 +298,8 @@ __global__ __launch_bounds__(NT) void token_stats_kernel(TokenArgs a) {
   float from = own;
   double sum;
   for (bool again = false;; again = true) {
-    const Shift shift = shift_of(from, a.log2_scale);
-    sum = (double)term(single, shift);
+    const Shift shift = shift_of<DT>(from, a.log2_scale);
+    sum = (double)term<DT>(single, shift);
     for (uint32_t v = v0 + t; v < v1; v += U * NT) {
       u32x4 x[U];
 #pragma unroll
@@ -316,7 +312,7 @@ __global__ __launch_bounds__(NT) void token_stats_kernel(TokenArgs a) {
         unpack_vec<DT>(x[i], e);
         leave_out<DT>(sh, id, v + i * NT, e);
 #pragma unroll
-        for (uint32_t j = 0; j < ve; ++j) some += term(e[j], shift);
+        for (uint32_t j = 0; j < ve; ++j) some += term<DT>(e[j], shift);
       }
       sum += (double)some;
     }
@@ -338,7 +334,7 @@ __global__ __launch_bounds__(NT) void token_stats_kernel(TokenArgs a) {
   }
   if (t != 0) return;
   if (a.parts == 1) {
-    finish_token(a, row, sum, from, own, id);
+    finish_token<DT>(a, row, sum, from, own, id);
   } else {
     a.ws[(uint64_t)row * a.parts + part] = {sum, from, 0.0f};
     if (part == 0) a.own[row] = own;
@@ -349,13 +345,17 @@ __global__ __launch_bounds__(NT) void token_stats_kernel(TokenArgs a) {
  * largest of the logits that their shifts are from. */
 constexpr uint32_t kMaxParts = 64;
 
+template <int DT>
 __device__ __forceinline__ TokenPart join_parts(const TokenArgs &a, uint32_t row) {
   const uint32_t lane = threadIdx.x & 63;
   TokenPart p{0.0, -INFINITY, 0.0f};
   if (lane < a.parts) p = a.ws[(uint64_t)row * a.parts + lane];
   const float from = wave_reduce(p.from, MaxOf{}, 64);
-  const double f = shift_factor(p.from, shift_of(p.from, a.log2_scale),
-                                shift_of(from, a.log2_scale));
+  /* a part from -inf has nothing else */
+  const double f = p.from == -INFINITY
+                       ? 0.0
+                       : shift_factor<DT>(shift_of<DT>(p.from, a.log2_scale),
+                                          shift_of<DT>(from, a.log2_scale), 0.0f);
   return {wave_reduce(p.rest * f, SumOf{}, 64), from, 0.0f};
 }
 
@@ -470,9 +470,9 @@ __global__ __launch_bounds__(NT) void token_grad_kernel(TokenArgs a) {
     const int32_t id = load_scalar(a.ids, row);
     p = {0.0f, 0.0f, 0.0f, kNoToken};
     if (token_live(a, row, id)) {
-      const TokenPart w = join_parts(a, row);
-      const TokenMass m = token_mass(w.rest, load_scalar(a.own, row),
-                                     shift_of(w.from, a.log2_scale), a.log2_scale);
+      const TokenPart w = join_parts<DT>(a, row);
+      const TokenMass m = token_mass<DT>(w.rest, load_scalar(a.own, row),
+                                     shift_of<DT>(w.from, a.log2_scale), a.log2_scale);
       const Slope k = policy_slope(a, policy_in(a, row), m.logp);
       p = make_plan(m.rest, m.total, w.from, k.slope * grad_scale(a), id);
       if (block == 0 && threadIdx.x == 0) {
@@ -485,11 +485,11 @@ __global__ __launch_bounds__(NT) void token_grad_kernel(TokenArgs a) {
   }
   if (p.id == kOutside) return;
   const bool live = p.id >= 0;
-  const Shift shift = shift_of(p.from, a.log2_scale);
+  const Shift shift = shift_of<DT>(p.from, a.log2_scale);
   const uint32_t edge = block == 0 ? edge_index<DT>(sh, threadIdx.x, true, true, a.vocab) : a.vocab;
   if (edge < a.vocab) {
     float x = 0.0f;
-    if (live) x = edge == (uint32_t)p.id ? p.own : term(load1<DT>(z, edge), shift) * p.factor;
+    if (live) x = edge == (uint32_t)p.id ? p.own : term<DT>(load1<DT>(z, edge), shift) * p.factor;
     store1<DT>(g, edge, x);
   }
   const uint32_t v = block * NT + threadIdx.x;
@@ -499,7 +499,7 @@ __global__ __launch_bounds__(NT) void token_grad_kernel(TokenArgs a) {
     float e[ve];
     unpack_vec<DT>(__builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(z + sh.head * esz) + v), e);
 #pragma unroll
-    for (uint32_t j = 0; j < ve; ++j) e[j] = term(e[j], shift) * p.factor;
+    for (uint32_t j = 0; j < ve; ++j) e[j] = term<DT>(e[j], shift) * p.factor;
     const uint32_t at = (uint32_t)p.id - sh.head - v * ve;
     if (at < ve) {
 #pragma unroll
@@ -640,8 +640,8 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
         if (place.item == (uint32_t)i && t == place.thread)
           set_element<DT>(x[i], place.elem, empty_vec<DT>()[0]);
       for (bool again = false;; again = true) {
-        const Shift s = shift_of(from, a.log2_scale);
-        float sum = term(single, s);
+        const Shift s = shift_of<DT>(from, a.log2_scale);
+        float sum = term<DT>(single, s);
         double sum64 = 0.0;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
@@ -650,7 +650,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
           unpack_vec<DT>(x[i], e);
           float some = 0.0f;
 #pragma unroll
-          for (uint32_t j = 0; j < ve; ++j) some += term(e[j], s);
+          for (uint32_t j = 0; j < ve; ++j) some += term<DT>(e[j], s);
           sum += (int)t < (int)in.shape.vecs - i * NT ? some : 0;
           if (i % 4 == 3 || i == ITEMS - 1) {   /* a few of them in fp32, the rest in binary64 */
             sum64 += (double)sum;
@@ -671,7 +671,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
         __syncthreads();
         from = reduce_get<NT>(MaxOf{}, fpart[turn]);
       }
-      const TokenMass32 m = token_mass32(rest, own, shift_of(from, a.log2_scale), a.log2_scale);
+      const TokenMass32 m = token_mass32<DT>(rest, own, shift_of<DT>(from, a.log2_scale), a.log2_scale);
       const Slope s = policy_slope(a, in.policy, m.logp);
       if (t == 0) {
         if (a.logp) a.logp[row] = m.logp;
@@ -690,13 +690,13 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) x[i] = empty_vec<DT>();
     }
-    const Shift shift = shift_of(plan.from, a.log2_scale);
+    const Shift shift = shift_of<DT>(plan.from, a.log2_scale);
     char *g = static_cast<char *>(a.grad) + (uint64_t)row * a.gld * esz;
     const __amdgpu_buffer_rsrc_t to = bounded(g + in.shape.head * esz, in.shape.vecs * 16);
     const __amdgpu_buffer_rsrc_t from_next = token_buffer<DT>(after);
     if (in.edge < a.vocab)
       store1<DT>(g, in.edge,
-                 in.edge == (uint32_t)plan.id ? plan.own : term(single, shift) * plan.factor);
+                 in.edge == (uint32_t)plan.id ? plan.own : term<DT>(single, shift) * plan.factor);
     if (more) token_singles<DT>(a, after, raw_own, raw_single);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
@@ -704,7 +704,7 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
       asm volatile("" : "+v"(x[i]));   /* unpacked anew, not kept since the sum */
       unpack_vec<DT>(x[i], e);
 #pragma unroll
-      for (uint32_t j = 0; j < ve; ++j) e[j] = term(e[j], shift) * plan.factor;
+      for (uint32_t j = 0; j < ve; ++j) e[j] = term<DT>(e[j], shift) * plan.factor;
       u32x4 w = pack_vec<DT>(e);
       if (place.item == (uint32_t)i && t == place.thread)
         set_element<DT>(w, place.elem, raw_bits<DT>(plan.own));

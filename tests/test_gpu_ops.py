@@ -733,3 +733,33 @@ def test_operators_in_a_graph(zs):
         graph.replay()
         torch.cuda.synchronize()
         assert same(out, want), f"replay {i}"
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16, FP32], ids=str)
+def test_distill_small_temperatures_and_large_logits(zs, dt):
+    """Exponents far beyond 2^24 units: the largest logit's neighbours have nothing, but of fp32
+    some, and ties share. A term's exponent is off by 2^-24 of itself, and of 128 where its whole
+    number is as far away: 2^-15 of the terms that matter; below 2^-126 they are 0."""
+    sizes = [(1e-6, 1), (1e-8, 1), (1e-9, 1), (1e-12, 1), (1e-18, 1)]
+    if dt is not FP16:
+        sizes += [(1.0, 3e7), (1.0, 1e9), (1.0, 1e13), (1.0, 1e17)]
+    for r, v in ((5, 1000), (3, 70000), (2, 140001)):
+        for tau, size in sizes:
+            announce(f"distill cold {dt} {tau} {size} {r}x{v}")
+            g = gen("cold", r, v, tau, size)
+            z = (2 * size * torch.randn(r, v, generator=g)).to(dt)
+            if dt is FP32:
+                z[1, torch.randint(0, v, (3,), generator=g)] = torch.nextafter(
+                    z[1].max(), torch.tensor(-math.inf))
+            ids = torch.stack([torch.randperm(v, generator=g)[:5] for _ in range(r)]).int()
+            ids[0, 2], ids[1, 0] = int(z[0].float().argmax()), int(z[1].float().argmax())
+            t = torch.stack([torch.randperm(8, generator=g)[:5] * 0.5 for _ in range(r)]).to(dt)
+            tau32, scale = float(torch.tensor(tau)), 64.0 / float(torch.tensor(tau))
+            loss, grad, bound = ref.distill(z, ids, t, tau32, None, None, scale=scale)
+            ol, og = torch.full((r,), 9.0, device="cuda"), torch.full_like(z, 7.0).cuda()
+            ws = torch.empty(max(16, zs.zs_distill_workspace(r, v, 5, zs._float_code(z, "z", True))),
+                             dtype=torch.uint8, device="cuda")
+            zs.zs_distill(z.cuda(), ids.cuda(), t.cuda(), tau, ol, grad=og, loss_scale=scale,
+                          workspace=ws)
+            close(og, grad, U[dt] * grad.abs() + 2.0 ** -14 * bound + 64 * 2.0 ** -125, "grad")
+            close(ol, loss, 2.0 ** -18 * loss.abs() + tau32 ** 2 * 2.0 ** -13, "loss")

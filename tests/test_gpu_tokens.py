@@ -740,3 +740,65 @@ def test_logits_far_below_the_others(zs):
                 delta = errors(z.clamp(-60, 60), tau, want)[0]
                 inner = wg.abs() * (3 * delta.unsqueeze(1) + 2.0 ** -20)
                 check(grad, wg, U[dtype] * (wg.abs() + inner) + inner + TINY[dtype], "grad")
+
+
+def cold_logits(rows, vocab, size, dtype, g):
+    """Logits, tokens that are a row's largest in every other row, and in fp32 rows that have
+    others next to the largest."""
+    z = (2 * size * torch.randn(rows, vocab, generator=g)).to(dtype)
+    ids = torch.randint(0, vocab, (rows,), generator=g, dtype=torch.int32)
+    ids[::2] = z[::2].float().argmax(1).int()
+    if dtype is FP32:
+        for r in (1, 2):
+            z[r, torch.randint(0, vocab, (3,), generator=g)] = torch.nextafter(
+                z[r].max(), torch.tensor(-math.inf))
+        ids[1] = int(z[1].argmax())
+    return z, ids
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+def test_small_temperatures_and_large_logits(zs, dtype):
+    """Exponents far beyond 2^24 units: the largest logit's neighbours have nothing, but of fp32
+    some, and ties share.
+
+    Tolerance: an exponent e of a term has errors of 2^-24 |e| from c and from its own rounding,
+    and of 2^-24 128 where it is formed by a whole number up to 128 away: with those terms that
+    matter within 128 of the largest, 2^-15 of a term; a log-probability 2^-21 of itself beside
+    that. An exponential below 2^-126 is 0."""
+    sizes = [(1e-6, 1), (1e-7, 1), (3e-9, 1), (1e-9, 1), (1e-10, 1), (1e-13, 1), (1e-17, 1),
+             (1e-18, 1), (1e-20, 1), (1e-30, 1), (2.0 ** -126, 1)]
+    if dtype is not FP16:
+        sizes += [(1.0, 3e7), (1.0, 1e9), (1.0, 1e13), (1.0, 1e17), (0.5, 1e30)]
+    for rows, vocab in ((6, 1000), (6, 70000), (70, 20000)):
+        for tau, size in sizes:
+            announce(f"cold {dtype} {tau} {size} {rows}x{vocab}")
+            z, ids = cold_logits(rows, vocab, size, dtype, gen("cold", rows, vocab, tau, size))
+            tau32 = float(torch.tensor(tau))
+            want, q, _ = ref.logprob(z.double(), ids, tau32)
+            tol = 2.0 ** -15 + 2.0 ** -21 * want.abs()
+            out = torch.full((rows,), 9.0, device="cuda")
+            ws = torch.empty(zs.zs_logprob_workspace(rows, vocab, code(zs, dtype)),
+                             dtype=torch.uint8, device="cuda")
+            zs.zs_logprob(z.cuda(), ids.cuda(), out, temperature=tau, workspace=ws)
+            check(out, want.float(), tol, "logp alone")
+            grad = torch.full_like(z, 7.0).cuda()
+            logp, loss = run_policy(zs, z.cuda(), ids, tau, torch.ones(rows), None, None, None,
+                                    64 * tau32, grad)
+            check(logp, want.float(), tol, "logp")
+            assert bool((loss == -1).all())
+
+            def near(got, slope, what):
+                wg = ref.logit_grad(q[:len(slope)], ids[:len(slope)], slope)
+                check(got, wg, (U[dtype] + 2.0 ** -14) * wg.abs() + 64 * 2.0 ** -125, what)
+
+            near(grad, torch.full((rows,), -64.0, dtype=F64), "grad")
+            if tau32 < 1e-17 or size > 1e17:
+                continue
+            # a pair's slope is beta's, whatever its difference of up to 1e19
+            grad.fill_(7.0)
+            loss, seq = run_preference(zs, z.cuda(), ids, [0, 2, 4], grad, None, beta=1e-30,
+                                       kind=zs.ZS_PREFERENCE_HINGE, temperature=tau,
+                                       loss_scale=64e30 * tau32)
+            sums = torch.stack([want[:2].sum(), want[2:4].sum()])
+            check(seq, sums, 2 * (2.0 ** -15 + 2.0 ** -21 * want[:4].abs().max()), "seq_logp")
+            near(grad[:4], torch.tensor([-64.0, -64.0, 64.0, 64.0], dtype=F64), "pair grad")
