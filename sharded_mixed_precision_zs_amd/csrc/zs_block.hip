@@ -52,7 +52,8 @@ bool short_float(float x) {
  * 2048 elements half as many threads as the norm's, for there are two sums a
  * row to join (32768 x 2048: 90 us, with 256 threads 102; 4096 x 12288: 89 with
  * 512 of four vectors, 123 with 1024 of two; 16384 x 4096 91 with 256, 94 with
- * 128). */
+ * 128). Above 32768, eight vectors a thread, 204 to 420 bytes of them are in
+ * scratch memory. */
 template <class F>
 void with_block_shape(uint64_t padded, F f) {
   if (padded <= 512) f(Tag<64>{}, Tag<1>{});
@@ -67,7 +68,9 @@ void with_block_shape(uint64_t padded, F f) {
 
 /* The gradient's: one vector per thread as far as a block goes, for a thread
  * holds four tensors' and the sums (16384 x 4096: 151 us with 512 threads of one,
- * 203 with 256 of two). Beyond 16384 elements it reads a row twice. */
+ * 203 with 256 of two). Beyond 16384 elements it reads a row twice. 1024 threads
+ * of two vectors keep 120 to 156 bytes each in scratch memory; threads of rows
+ * that are not whole vectors 20 to 132 with one vector and up to 308 with two. */
 constexpr uint64_t kHeldGrad = 16384;
 
 template <class F>

@@ -459,11 +459,11 @@ struct BlockGradVec {
 
 /* Rows whose vectors and shares a block's registers and LDS do not hold: read
  * twice, and their shares added to in memory, a word of its own for each of a
- * thread's (2048 x 32768 bf16 403 us; held as above, for the most part in
+ * thread's (2048 x 32768 bf16 400 us; held as above, for the most part in
  * scratch memory, 1262). One reduction a row: with n = h r2 and dh = e - n c,
- * mean(q x) = (sum(q k e x) - c sum(q k n x)) a / cols. With n
- * in place of h c has dh's size: h's c is r2 times that, and its sum 1 / r2
- * times, which leave fp32 for bf16 rows beyond 1e19 or below 1e-19. */
+ * mean(q x) = (sum(q k e x) - c sum(q k n x)) a / cols. With n in place of h
+ * c has dh's size: h's c is r2 times that, and its sum 1 / r2 times, which leave
+ * fp32 for bf16 rows beyond 1e19 or below 1e-19. */
 template <int DT, bool AL>
 __global__ __launch_bounds__(1024) void block_grad_wide_kernel(BlockGradArgs a) {
   constexpr int G = 1024;
