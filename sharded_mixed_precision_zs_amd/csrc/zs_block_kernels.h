@@ -59,11 +59,12 @@ __device__ __forceinline__ float odd_float(double v) {
  * kNear times |l r| + |sum|: c p by 2^-24 for c's rounding, and as much for p's
  * in fp16, l r, the sum and its ends by 2^-24 each; or by nothing where p is 0
  * and l r exact, and `near` so small that both ends are the sum (0 would make
- * NaN of an infinite size, at both ends alike). Where both ends of that have the same 16 bits, those are the
- * exact sum's. Where they differ, in some 2^-12 of bf16 sums and 2^-9 of fp16's,
- * the two of a word are formed in binary64. (Short scales without a first norm
- * make ties, and go that way more often. Where a sum is below fp32's normal
- * range, 2^-150 more may be off, 2^-17 of bf16's step there.) */
+ * NaN of an infinite size, at both ends alike). Where both ends of that have the
+ * same 16 bits, those are the exact sum's. Where they differ, in some 2^-12 of
+ * bf16 sums and 2^-9 of fp16's, the two of a word are formed in binary64. (Short
+ * scales without a first norm make ties, and go that way more often. Where a sum
+ * is below fp32's normal range, 2^-150 more may be off, 2^-17 of bf16's step
+ * there.) */
 template <int DT>
 constexpr float kNear = DT == ZS_FP16 ? 0x1p-22f : 0x1.8p-23f;
 

@@ -36,8 +36,8 @@ __device__ __forceinline__ float activate(float x) {
 
 /* d act / d x. With p the logistic function of w and q = 1 - p, formed without
  * the difference: p (1 + x q w'). Beyond 30 the slope is 0 or 1 in any type
- * here, and w' of such x would leave fp32. The exponential is 0 below 2^-126: so
- * are slopes below some 2^-118 (gelu's from -10 on), with 16 bits or 8 of them. */
+ * here, and w' of such x would leave fp32. The exponential is 0 below 2^-126, and
+ * so are slopes below some 2^-118 (gelu's left of -10). */
 template <int ACT>
 __device__ __forceinline__ float slope_of(float x) {
   if constexpr (ACT == ZS_ACT_RELU) return x > 0.0f ? 1.0f : x == x ? 0.0f : x;

@@ -178,7 +178,7 @@ struct Shift {
 template <int DT>
 __device__ __forceinline__ Shift shift_of(float max, float c) {
   constexpr float kWhole = 16777216.0f, kFar = DT == ZS_FP32 ? 4294967296.0f : kWhole;
-  constexpr uint32_t kTop = DT == ZS_FP32 ? 32 : 23;   /* max c lies in [2^kTop, 2^(kTop + 1)) then */
+  constexpr uint32_t kTop = DT == ZS_FP32 ? 32 : 23;   /* |max c| in [2^kTop, 2^(kTop + 1)) then */
   Shift s;
   s.max = max == -INFINITY ? 0.0f : max;
   s.c = c;

@@ -671,7 +671,8 @@ __global__ __launch_bounds__(NT, ITEMS <= 16 ? 4 : 2) void policy_row_kernel(Tok
         __syncthreads();
         from = reduce_get<NT>(MaxOf{}, fpart[turn]);
       }
-      const TokenMass32 m = token_mass32<DT>(rest, own, shift_of<DT>(from, a.log2_scale), a.log2_scale);
+      const TokenMass32 m =
+          token_mass32<DT>(rest, own, shift_of<DT>(from, a.log2_scale), a.log2_scale);
       const Slope s = policy_slope(a, in.policy, m.logp);
       if (t == 0) {
         if (a.logp) a.logp[row] = m.logp;
